@@ -13,8 +13,15 @@ from .binding import (  # noqa: F401
     fa2_backward_dq,
     fa2_backward_preprocess,
     fa2_backward_workspace_size,
+    fa2_decode,
+    fa2_decode_workspace_size,
     fa2_device_status,
     fa2_forward,
+    fa2_kv_append,
+    fa2_kv_read,
+    fa2_rope,
+    fa2_rope_backward,
+    fa2_rope_frequencies,
     fa2_status_string,
     library,
     psa_merge_attn_nchw,

@@ -41,6 +41,13 @@ EXPORTS = (
     "fa2_watchdog_selftest",
     "fa2_status_string",
     "fa2_last_launch_info",
+    "fa2_rope_frequencies",
+    "fa2_rope",
+    "fa2_rope_backward",
+    "fa2_kv_append",
+    "fa2_kv_read",
+    "fa2_decode_workspace_size",
+    "fa2_decode",
 )
 
 
@@ -58,6 +65,7 @@ _c_ptr = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 
 
 class LaunchInfo(ctypes.Structure):
@@ -65,6 +73,18 @@ class LaunchInfo(ctypes.Structure):
     _fields_ = [("fwd_key_ranges", ctypes.c_int32), ("bwd_one_pass", ctypes.c_int32),
                 ("bwd_dkv_query_ranges", ctypes.c_int32), ("bwd_dq_key_ranges", ctypes.c_int32),
                 ("bwd_key_tiles_per_cta", ctypes.c_int32)]
+
+
+class KvCache(ctypes.Structure):
+    """fa2_kv_cache of include/fa2.h."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("slot_stride", ctypes.c_int64), ("n_kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("type", ctypes.c_int)]
+
+
+CACHE_SAME, CACHE_E4M3 = 0, 1
+ROPE_SCALINGS = ("plain", "linear", "base", "turns", "ramp")  # fa2_rope_scaling's values in order
 
 
 def _declare(lib):
@@ -92,7 +112,16 @@ def _declare(lib):
         "fa2_watchdog_selftest": (ctypes.c_int, [_c_ptr]),
         "fa2_status_string": (ctypes.c_char_p, [ctypes.c_int]),
         "fa2_last_launch_info": (ctypes.c_int, [ctypes.POINTER(LaunchInfo)]),
+        "fa2_rope_frequencies": (ctypes.c_int, [_c_ptr, _c_ptr, _i32, _f64, ctypes.c_int, _f64, _f64, _f64, _f64]),
+        "fa2_rope": (ctypes.c_int, [_c_ptr, _c_ptr, _c_ptr, _i64, _c_ptr, _i64, _i64, _i64, _i32, _i32, _c_ptr, _c_ptr, _i32,
+                                    _f32, _i32, _c_ptr]),
+        "fa2_kv_append": (ctypes.c_int, [_c_ptr] * 5 + [_c_ptr, _i64, _i64, _c_ptr, _c_ptr, _i64, _i64, _i32, _c_ptr]),
+        "fa2_kv_read": (ctypes.c_int, [_c_ptr] * 4 + [_c_ptr, _i64, _i64, _c_ptr, _i64, _i64, _i32, _c_ptr]),
+        "fa2_decode_workspace_size": (ctypes.c_size_t, [_i64, _i32, _i32, _i32]),
+        "fa2_decode": (ctypes.c_int, [_c_ptr] * 5 + [_c_ptr, _i64, _i64, _c_ptr, _i64, _i32, _i64, _c_ptr, ctypes.c_size_t,
+                                                     _i32, _f32, _c_ptr]),
     }
+    sig["fa2_rope_backward"] = sig["fa2_rope"]
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
         fn.restype = res
@@ -112,7 +141,8 @@ def library(path: str | None = None):
 
 
 _MESSAGES = {0: "ok", 1: "invalid argument", 2: "unsupported", 3: "misaligned pointer",
-             4: "CUDA error", 5: "device wait timed out", 6: "bad workspace", 7: "too large for the fixed scratch"}
+             4: "CUDA error", 5: "device wait timed out", 6: "bad workspace", 7: "too large for the fixed scratch",
+             8: "bad page number or length"}
 
 
 def fa2_status_string(status: int) -> str:
@@ -156,7 +186,7 @@ def _require_f32(where, **tensors):
             raise TypeError(f"{where}: {name} must be float32, got {t.dtype}")
 
 
-def _dev(t, name, ndim=None):
+def _on_current_device(t, name):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     import torch
@@ -164,6 +194,10 @@ def _dev(t, name, ndim=None):
     if t.device.index != current:
         # the library launches on the current device; another device's memory is not its to read
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{current}")
+
+
+def _dev(t, name, ndim=None):
+    _on_current_device(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if ndim is not None and t.dim() != ndim:
@@ -384,3 +418,192 @@ def fa2_last_launch_info() -> dict:
 def fa2_watchdog_selftest(stream=None) -> None:
     """Launch the bounded-wait self-test (a wait that gives up after about a second)."""
     _check(library().fa2_watchdog_selftest(_stream(stream)), "fa2_watchdog_selftest")
+
+
+# ---------------------------------------------------------------------------- rotary positions and the paged cache
+
+
+def _strided(t, name, ndim):
+    """Pointer of a tensor whose last dimension is contiguous; the library takes its other strides."""
+    _on_current_device(t, name)
+    if t.dim() != ndim:
+        raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise ValueError(f"{name}'s last dimension must be contiguous")
+    return ctypes.c_void_p(t.data_ptr())
+
+
+def _int64s(values):
+    values = tuple(values)
+    return (ctypes.c_int64 * len(values))(*values)
+
+
+def _require_dtype(where, dtype, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.dtype != dtype:
+            raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+
+
+def fa2_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
+                         original_len: float = 0.0, low: float = 1.0, high: float = 32.0):
+    """(inv_freq, magnitude) for fa2_rope: a float64 CPU tensor [rot_dim / 2] and a float.  `scaling`, one of
+    ROPE_SCALINGS, slows the frequencies down for contexts `factor` times as long as `original_len` (fa2.h)."""
+    import torch
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling must be one of {ROPE_SCALINGS}, got {scaling!r}")
+    inv_freq = torch.empty(max(0, int(rot_dim) // 2), dtype=torch.float64)
+    magnitude = ctypes.c_float()
+    _check(library().fa2_rope_frequencies(ctypes.c_void_p(inv_freq.data_ptr()), ctypes.byref(magnitude), int(rot_dim),
+                                          float(base), ROPE_SCALINGS.index(scaling), float(factor), float(original_len),
+                                          float(low), float(high)), "fa2_rope_frequencies")
+    return inv_freq, float(magnitude.value)
+
+
+def _rope(where, x, y, inv_freq, positions, interleaved, magnitude, stream):
+    import torch
+    if x.dim() != 4 or y.shape != x.shape:
+        raise ValueError(f"{where}: the tensors are [B, H, N, d], both of one shape")
+    b, h, n, d = x.shape
+    _same_dtype(where, x, y=y)
+    _require_dtype(where, torch.float64, inv_freq=inv_freq)
+    _require_dtype(where, torch.int32, positions=positions)
+    position_stride, pos_ptr = 0, None
+    if positions is not None:
+        if positions.shape not in ((n,), (1, n), (b, n)):
+            raise ValueError(f"{where}: positions must be [N], [1, N] or [B, N], got {tuple(positions.shape)}")
+        pos_ptr = _strided(positions, "positions", positions.dim())
+        position_stride = positions.stride(0) if positions.dim() == 2 and positions.shape[0] > 1 else 0
+    st = getattr(library(), where)(_strided(x, "x", 4), _strided(y, "y", 4), pos_ptr, position_stride,
+                                   _dev(inv_freq, "inv_freq", 1), b, h, n, d, 2 * inv_freq.numel(), _int64s(x.stride()[:3]),
+                                   _int64s(y.stride()[:3]), int(bool(interleaved)), float(magnitude), _dtype_code(x),
+                                   _stream(stream))
+    _check(st, where)
+
+
+def fa2_rope(x, y, inv_freq, positions=None, interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """Rotary positions: x, y [B, H, N, d] (any strides, d contiguous; y may be x); inv_freq float64 [rot_dim / 2];
+    positions int32 [B, N] or [N] (None: 0 .. N - 1)."""
+    _rope("fa2_rope", x, y, inv_freq, positions, interleaved, magnitude, stream)
+
+
+def fa2_rope_backward(dy, dx, inv_freq, positions=None, interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
+    """Gradient of fa2_rope: dx from dy, the other arguments as for the forward call."""
+    _rope("fa2_rope_backward", dy, dx, inv_freq, positions, interleaved, magnitude, stream)
+
+
+def _cache(where, k_pages, v_pages, k_exp, v_exp, row_dtype):
+    """The sizes and strides of the fa2_kv_cache of two page pools [num_pages, n_kv_heads, page_size, d] (any strides, d
+    contiguous), after checking them; _cache_pointers adds the rest."""
+    import torch
+    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+        raise ValueError(f"{where}: k_pages and v_pages are [num_pages, n_kv_heads, page_size, d], both of one shape")
+    # the stride of a dimension of one element means nothing
+    for size, a, b in zip(k_pages.shape[:3], k_pages.stride()[:3], v_pages.stride()[:3]):
+        if size > 1 and a != b:
+            raise ValueError(f"{where}: k_pages and v_pages must have the same strides")
+    _same_dtype(where, k_pages, v_pages=v_pages)
+    pages, heads, page_size, d = k_pages.shape
+    c = KvCache()
+    if k_pages.dtype == torch.float8_e4m3fn:
+        if k_exp is None or v_exp is None:
+            raise ValueError(f"{where}: an e4m3 cache has scale bytes, k_exp and v_exp")
+        _require_dtype(where, torch.uint8, k_exp=k_exp, v_exp=v_exp)
+        for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
+            if t.shape != (pages, heads, page_size):
+                raise ValueError(f"{where}: {name} must be [num_pages, n_kv_heads, page_size]")
+        c.type = CACHE_E4M3
+    else:
+        if k_exp is not None or v_exp is not None:
+            raise ValueError(f"{where}: k_exp and v_exp belong to an e4m3 cache")
+        if k_pages.dtype != row_dtype:
+            raise TypeError(f"{where}: the pages are {k_pages.dtype}, expected {row_dtype} or float8_e4m3fn")
+        c.type = CACHE_SAME
+    c.num_pages, c.n_kv_heads, c.page_size, c.head_dim = pages, heads, page_size, d
+    c.page_stride, c.head_stride, c.slot_stride = k_pages.stride()[:3]
+    return c
+
+
+def _cache_pointers(c, k_pages, v_pages, k_exp, v_exp):
+    c.k, c.v = _strided(k_pages, "k_pages", 4), _strided(v_pages, "v_pages", 4)
+    if c.type == CACHE_E4M3:
+        c.k_exp, c.v_exp = _dev(k_exp, "k_exp", 3), _dev(v_exp, "v_exp", 3)
+    return ctypes.byref(c)
+
+
+def _check_table(where, block_table, seq_lens):
+    import torch
+    _require_dtype(where, torch.int32, block_table=block_table, seq_lens=seq_lens)
+    if block_table.dim() != 2 or seq_lens.shape != (block_table.shape[0],):
+        raise ValueError(f"{where}: block_table is [batch, pages_per_seq] and seq_lens [batch]")
+    return block_table.shape[0]
+
+
+def _table(block_table):
+    """Pointer, row stride and pages per sequence of a block table."""
+    batch, pages = block_table.shape
+    return _strided(block_table, "block_table", 2), block_table.stride(0) if batch > 1 else pages, pages
+
+
+def fa2_kv_append(k_pages, v_pages, k, v, block_table, seq_lens, cu_new=None, k_exp=None, v_exp=None, stream=None) -> None:
+    """Write new keys and values k, v [tokens, n_kv_heads, d] into the pages [num_pages, n_kv_heads, page_size, d] (the
+    rows' dtype, or float8_e4m3fn with scale bytes k_exp, v_exp).  seq_lens counts the new tokens in; cu_new int32
+    [batch + 1] says which rows are whose (None: one a sequence)."""
+    import torch
+    where = "fa2_kv_append"
+    c = _cache(where, k_pages, v_pages, k_exp, v_exp, k.dtype)
+    if k.dim() != 3 or v.shape != k.shape or k.shape[1:] != (c.n_kv_heads, c.head_dim):
+        raise ValueError(f"{where}: k and v are [tokens, n_kv_heads, d]")
+    _same_dtype(where, k, v=v)
+    batch = _check_table(where, block_table, seq_lens)
+    if cu_new is not None:
+        _require_dtype(where, torch.int32, cu_new=cu_new)
+        if cu_new.shape != (batch + 1,):
+            raise ValueError(f"{where}: cu_new must be [batch + 1]")
+    cache = _cache_pointers(c, k_pages, v_pages, k_exp, v_exp)
+    st = library().fa2_kv_append(cache, _strided(k, "k", 3), _strided(v, "v", 3), _int64s(k.stride()[:2]),
+                                 _int64s(v.stride()[:2]), *_table(block_table),
+                                 None if cu_new is None else _dev(cu_new, "cu_new", 1), _dev(seq_lens, "seq_lens", 1), batch,
+                                 k.shape[0], _dtype_code(k), _stream(stream))
+    _check(st, where)
+
+
+def fa2_kv_read(k_pages, v_pages, k_out, v_out, block_table, seq_lens, k_exp=None, v_exp=None, stream=None) -> None:
+    """Copy the cached rows out: k_out, v_out [batch, n_kv_heads, max_len, d]; positions past a sequence's length stay."""
+    where = "fa2_kv_read"
+    c = _cache(where, k_pages, v_pages, k_exp, v_exp, k_out.dtype)
+    batch = _check_table(where, block_table, seq_lens)
+    if k_out.dim() != 4 or v_out.shape != k_out.shape or (k_out.shape[0], k_out.shape[1], k_out.shape[3]) != (
+            batch, c.n_kv_heads, c.head_dim):
+        raise ValueError(f"{where}: k_out and v_out are [batch, n_kv_heads, max_len, d]")
+    for size, a, b in zip(k_out.shape[:3], k_out.stride()[:3], v_out.stride()[:3]):
+        if size > 1 and a != b:
+            raise ValueError(f"{where}: k_out and v_out must have the same strides")
+    _same_dtype(where, k_out, v_out=v_out)
+    cache = _cache_pointers(c, k_pages, v_pages, k_exp, v_exp)
+    st = library().fa2_kv_read(cache, _strided(k_out, "k_out", 4), _strided(v_out, "v_out", 4), _int64s(k_out.stride()[:3]),
+                               *_table(block_table), _dev(seq_lens, "seq_lens", 1), batch, k_out.shape[2],
+                               _dtype_code(k_out), _stream(stream))
+    _check(st, where)
+
+
+def fa2_decode_workspace_size(batch: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
+    return int(library().fa2_decode_workspace_size(batch, n_heads, n_kv_heads, head_dim))
+
+
+def fa2_decode(q, k_pages, v_pages, o, lse, block_table, seq_lens, workspace, softmax_scale: float, window: int = 0,
+               k_exp=None, v_exp=None, stream=None) -> None:
+    """Attention of one new token a sequence over the paged cache: q, o [batch, n_heads, d], lse [batch, n_heads]
+    float32; workspace a CUDA uint8 tensor of fa2_decode_workspace_size bytes; window > 0: the last keys only."""
+    where = "fa2_decode"
+    c = _cache(where, k_pages, v_pages, k_exp, v_exp, q.dtype)
+    batch = _check_table(where, block_table, seq_lens)
+    if q.dim() != 3 or q.shape[0] != batch or q.shape[2] != c.head_dim or o.shape != q.shape or lse.shape != q.shape[:2]:
+        raise ValueError(f"{where}: q and o are [batch, n_heads, d], lse [batch, n_heads]")
+    _same_dtype(where, q, o=o)
+    _require_f32(where, lse=lse)
+    cache = _cache_pointers(c, k_pages, v_pages, k_exp, v_exp)
+    st = library().fa2_decode(_strided(q, "q", 3), _int64s(q.stride()[:2]), cache, _dev(o, "o", 3), _dev(lse, "lse", 2),
+                              *_table(block_table), _dev(seq_lens, "seq_lens", 1), batch, q.shape[1], int(window),
+                              _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _dtype_code(q),
+                              float(softmax_scale), _stream(stream))
+    _check(st, where)

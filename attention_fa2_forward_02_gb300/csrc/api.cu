@@ -5,12 +5,14 @@
 #include <atomic>
 #include <mutex>
 
+#include "common.cuh"
 #include "fa2.h"
 #include "internal.h"
 
 namespace fa2 {
 
-// Watchdog word: kernels OR kStatusTimeout into it when a bounded wait gives up.
+// Watchdog word: kernels OR kStatusTimeout into it when a bounded wait gives up, the cache's
+// kernels kStatusBadIndex when they refuse a page number or length.
 __device__ unsigned int g_watchdog_word;
 
 namespace {
@@ -34,7 +36,7 @@ EncodeTiledFn encode_fn() {
 }
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSlots = 64;
+constexpr int kMaxSlots = 80;
 std::mutex g_mu;
 unsigned int* g_status_ptr[kMaxDevices] = {};
 std::atomic<uint64_t> g_smem_done[kMaxSlots];
@@ -472,7 +474,7 @@ fa2_status fa2_device_status(void* stream) {
     if (word == 0) return FA2_OK;
     const unsigned int zero = 0;
     if (cudaMemcpyToSymbol(g_watchdog_word, &zero, sizeof(zero)) != cudaSuccess) return FA2_ERR_CUDA;
-    return FA2_ERR_DEVICE_TIMEOUT;
+    return (word & kStatusTimeout) ? FA2_ERR_DEVICE_TIMEOUT : FA2_ERR_BAD_INDEX;
 }
 
 fa2_status fa2_last_launch_info(fa2_launch_info* info) {
@@ -491,6 +493,7 @@ const char* fa2_status_string(fa2_status s) {
         case FA2_ERR_DEVICE_TIMEOUT: return "a kernel gave up a bounded wait (watchdog)";
         case FA2_ERR_WORKSPACE: return "workspace missing, misaligned or smaller than fa2_backward_workspace_size";
         case FA2_ERR_SCRATCH_LIMIT: return "problem too large for fa2_backward_noalloc's fixed 8 MiB scratch";
+        case FA2_ERR_BAD_INDEX: return "a page number or sequence length outside the key-value cache was not followed";
         default: return "unknown status";
     }
 }

@@ -17,6 +17,8 @@ namespace fa2 {
 constexpr uint64_t kWaitLimitNs = 1000ull * 1000ull * 1000ull;
 // Bit set in the watchdog word when a wait gives up.
 constexpr unsigned int kStatusTimeout = 1u;
+// Bit set in the watchdog word when a page number or length is outside the cache.
+constexpr unsigned int kStatusBadIndex = 2u;
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {
     return static_cast<uint32_t>(__cvta_generic_to_shared(p));

@@ -154,6 +154,68 @@ struct PsaParams {
     int dtype = 0;         // Dtype, for the accumulating adjoint
 };
 
+// Rotary positions over [b, h, n, d] views (strides in elements).
+struct RopeParams {
+    const void* x;
+    void* y;
+    const int32_t* positions;  // null: position n
+    int64_t position_stride;
+    const double* inv_freq;
+    int64_t b, h, n;
+    int d, rot;
+    int64_t xs[3], ys[3];
+    bool interleaved, backward;
+    float magnitude;
+    int dtype;
+};
+
+// A paged cache and the sequences that a call goes through (fa2.h, fa2_kv_cache).
+struct PagedParams {
+    char* k;
+    char* v;
+    uint8_t* k_exp;
+    uint8_t* v_exp;
+    int64_t num_pages, page_stride, head_stride, slot_stride;  // strides in bytes
+    int hkv, page_size, d;
+    bool e4m3;
+    const int32_t* table;
+    int64_t table_stride;
+    int64_t room;  // pages_per_seq * page_size, at most 2^30
+    const int32_t* lens;
+    int64_t batch;
+    int dtype;
+    unsigned int* status;
+};
+
+// Copies rows between the cache and contiguous-row tensors: append (rows [token, head]) or
+// read (rows [b, head, pos]).
+struct KvRowsParams {
+    PagedParams c;
+    char* k;
+    char* v;
+    int64_t ks[3], vs[3];  // bytes: append {token, head, 0}, read {b, head, pos}
+    const int32_t* cu_new;
+    int64_t tokens;  // append: rows of k and v; read: max_len
+    bool read;
+};
+
+struct DecodeParams {
+    PagedParams c;
+    const void* q;
+    int64_t q_batch, q_head;  // elements
+    void* o;
+    float* lse;
+    int heads;
+    int64_t window;
+    float* workspace;
+    float scale;
+};
+
+cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
+cudaError_t launch_kv_rows(const KvRowsParams& p, cudaStream_t stream);
+cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream);
+size_t decode_workspace_bytes(int heads, int hkv, int d);
+
 cudaError_t launch_fwd_tc(const FwdParams& p, cudaStream_t stream);
 cudaError_t launch_fwd_f32(const FwdParams& p, cudaStream_t stream);
 // One pass over the scores applied to two value tensors (v, v2) with outputs (o, o2).

@@ -1,0 +1,228 @@
+// kv_cache.cu - rows of keys and values into the pages of a cache, and back out.
+//
+// A row is one token's head_dim elements of one head, of K or of V. A warp takes one token (and
+// a share of its heads): the page is looked up once for all its rows, then groups of lanes move
+// one row each, 16 elements a lane to or from the 8-bit form and 8 a lane in the 16-bit form, so
+// that every access to either side is a whole 16-byte vector.
+//
+// The 8-bit form: with a the row's largest finite magnitude, the scale is 2^e for the smallest
+// e with a <= 448 2^e (448 the largest e4m3 value), from a's own exponent and fraction bits.
+// A power of two makes x / 2^e exact, so a code depends on its rounding alone and reading back
+// is exact in bfloat16. e >= -60 keeps 2^-e, 2^e and their products with sums inside float32.
+//
+// Bound by memory: each row is read once and written once.
+#include "paged.cuh"
+
+namespace fa2 {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kMinExp = -60;
+
+// e of the scale 2^e for a row whose largest finite magnitude is a.
+__device__ __forceinline__ int scale_exp(float a) {
+    if (a == 0.f) return 0;
+    const uint32_t bits = __float_as_uint(a);
+    const int k = (int)(bits >> 23) - 126;  // a = f 2^k, f in [1/2, 1) (a subnormal a reads as k = -126: clamped below)
+    // 448 = 7/8 * 2^9: a <= 448 * 2^(k - 9) exactly when f <= 7/8
+    const int e = k - 9 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+    return e < kMinExp ? kMinExp : e;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+    if constexpr (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {  // nearest even; beyond 448: 448; NaN stays
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// The cache side and the tensor side of one token.
+struct Token {
+    int64_t cache_off, exp_off;  // bytes / scale bytes, head 0
+    int64_t k_off, v_off;        // bytes, head 0
+};
+
+// Which token warp `t` of the launch moves; false: none.
+__device__ __forceinline__ bool find_token(const KvRowsParams& p, int64_t t, int b_read, Token* out) {
+    const PagedParams& c = p.c;
+    int64_t pos;
+    int b;
+    if (p.read) {
+        b = b_read;
+        pos = t;
+        if (pos >= bounded_len(c.lens[b], c.room, c.status)) return false;
+        out->k_off = b * p.ks[0] + pos * p.ks[2];
+        out->v_off = b * p.vs[0] + pos * p.vs[2];
+    } else {
+        int first = (int)t, end = (int)t + 1;
+        if (p.cu_new) {
+            // the last sequence that begins at or before row t
+            int lo = 0, hi = (int)c.batch;  // cu_new[lo] <= t < cu_new[hi], were it ascending
+            if (t < p.cu_new[0] || t >= p.cu_new[hi]) return false;
+            while (hi - lo > 1) {
+                const int mid = (lo + hi) >> 1;
+                if (p.cu_new[mid] <= t) lo = mid;
+                else hi = mid;
+            }
+            b = lo;
+            first = p.cu_new[b];
+            end = p.cu_new[b + 1];
+        } else {
+            b = (int)t;
+            if (c.lens[b] == 0) return false;
+        }
+        pos = (int64_t)c.lens[b] - end + t;
+        if (t < first || t >= end || pos < 0 || pos >= c.room) {
+            if (c.status) atomicOr(c.status, kStatusBadIndex);
+            return false;
+        }
+        out->k_off = t * p.ks[0];
+        out->v_off = t * p.vs[0];
+    }
+    const int page = c.table[b * c.table_stride + (int)pos / c.page_size];
+    const Slot s = slot_of(c, page, (int)pos % c.page_size);
+    if (s.off < 0) return false;
+    out->cache_off = s.off;
+    out->exp_off = s.exp;
+    return true;
+}
+
+// kLanes lanes a row; each warp moves rows r0, r0 + 32 / kLanes, ... of its token's 2 hkv rows
+// (heads of K, then of V), kRows of them at a time.
+template <bool kBf16, bool kE4m3, bool kRead, int kLanes, int kRows>
+__global__ void __launch_bounds__(kWarps * 32) kv_rows_kernel(const KvRowsParams p, int rows_per_warp) {
+    const PagedParams& c = p.c;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t = (int64_t)blockIdx.x * kWarps + warp;
+    if (t >= p.tokens) return;
+    Token tok;
+    if (!find_token(p, t, blockIdx.z, &tok)) return;
+    constexpr int kGroups = 32 / kLanes;
+    constexpr int kElems = kE4m3 ? 16 : 8;  // elements a lane
+    const int li = lane % kLanes;
+    const bool on = li * kElems < c.d;
+    const int total = 2 * c.hkv;
+    const int begin = blockIdx.y * rows_per_warp, stop = min(total, begin + rows_per_warp);
+    for (int r0 = begin + lane / kLanes; r0 - lane / kLanes < stop; r0 += kGroups * kRows) {
+        uint4 in[kRows][kE4m3 ? 2 : 1];
+        int byte[kRows];
+        // the rows' addresses: cache side and tensor side
+        auto cache_ptr = [&](int r) {
+            const bool v = r >= c.hkv;
+            const int h = v ? r - c.hkv : r;
+            return (v ? c.v : c.k) + tok.cache_off + h * c.head_stride + li * 16;
+        };
+        auto row_ptr = [&](int r) {
+            const bool v = r >= c.hkv;
+            const int h = v ? r - c.hkv : r;
+            return (v ? p.v + tok.v_off + h * p.vs[1] : p.k + tok.k_off + h * p.ks[1]) + li * kElems * 2;
+        };
+        auto exp_ptr = [&](int r) {
+            const bool v = r >= c.hkv;
+            const int h = v ? r - c.hkv : r;
+            return (v ? c.v_exp : c.k_exp) + tok.exp_off + (int64_t)h * c.page_size;
+        };
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i * kGroups;
+            in[i][0] = make_uint4(0, 0, 0, 0);
+            if constexpr (kE4m3) in[i][1] = make_uint4(0, 0, 0, 0);
+            byte[i] = 127;
+            if (r >= stop || !on) continue;
+            if constexpr (kRead) {
+                in[i][0] = *reinterpret_cast<const uint4*>(cache_ptr(r));
+                if constexpr (kE4m3) byte[i] = *exp_ptr(r);
+            } else {
+                const uint4* src = reinterpret_cast<const uint4*>(row_ptr(r));
+                in[i][0] = src[0];
+                if constexpr (kE4m3) in[i][1] = src[1];
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kRows; ++i) {
+            const int r = r0 + i * kGroups;
+            if constexpr (!kE4m3) {
+                if (r < stop && on) *reinterpret_cast<uint4*>(kRead ? row_ptr(r) : cache_ptr(r)) = in[i][0];
+            } else if constexpr (kRead) {
+                if (r < stop && on) {
+                    const uint32_t w[4] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w};
+                    const float scale = byte[i] ? __uint_as_float((uint32_t)byte[i] << 23) : 0x1p-127f;
+                    uint32_t o[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t h2 = e4m3x2_to_f16x2((w[j >> 1] >> (16 * (j & 1))) & 0xffffu);
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                        o[j] = pack2<kBf16>(f.x * scale, f.y * scale);
+                    }
+                    uint4* dst = reinterpret_cast<uint4*>(row_ptr(r));
+                    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+            } else {
+                const uint32_t w[8] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w,
+                                       in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
+                float2 f[8];
+                float a = 0.f;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    f[j] = widen2<kBf16>(w[j]);
+                    const float ax = fabsf(f[j].x), ay = fabsf(f[j].y);
+                    a = fmaxf(a, fmaxf(ax < INFINITY ? ax : 0.f, ay < INFINITY ? ay : 0.f));  // finite ones only
+                }
+#pragma unroll
+                for (int off = kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+                const int e = scale_exp(a);
+                const float inv = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e, e in [-60, 120]
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    o[j] = to_e4m3x2(f[2 * j].x * inv, f[2 * j].y * inv) | (to_e4m3x2(f[2 * j + 1].x * inv, f[2 * j + 1].y * inv) << 16);
+                if (r < stop && on) {
+                    *reinterpret_cast<uint4*>(cache_ptr(r)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    if (li == 0) *exp_ptr(r) = (uint8_t)(e + 127);
+                }
+            }
+        }
+    }
+}
+
+template <bool kBf16, bool kE4m3, bool kRead, int kLanes>
+cudaError_t launch_lanes(const KvRowsParams& p, cudaStream_t stream) {
+    constexpr int kGroups = 32 / kLanes, kRows = 4;
+    const int total = 2 * p.c.hkv;
+    const int64_t blocks = (p.tokens + kWarps - 1) / kWarps;
+    const int64_t batch = p.read ? p.c.batch : 1;
+    // A warp takes all rows of its token, or with few tokens one round of them.
+    int rpw = total;
+    if (blocks * batch < 152 * 8) rpw = kGroups;
+    const dim3 grid((unsigned)blocks, (unsigned)((total + rpw - 1) / rpw), (unsigned)batch);
+    if (rpw == kGroups) kv_rows_kernel<kBf16, kE4m3, kRead, kLanes, 1><<<grid, kWarps * 32, 0, stream>>>(p, rpw);
+    else kv_rows_kernel<kBf16, kE4m3, kRead, kLanes, kRows><<<grid, kWarps * 32, 0, stream>>>(p, rpw);
+    return cudaGetLastError();
+}
+
+template <bool kBf16, bool kE4m3, bool kRead>
+cudaError_t launch_type(const KvRowsParams& p, cudaStream_t stream) {
+    const int lanes = kE4m3 ? (p.c.d + 15) / 16 : (p.c.d + 7) / 8;
+    if (lanes <= 2) return launch_lanes<kBf16, kE4m3, kRead, 2>(p, stream);
+    if (lanes <= 4) return launch_lanes<kBf16, kE4m3, kRead, 4>(p, stream);
+    if (lanes <= 8) return launch_lanes<kBf16, kE4m3, kRead, 8>(p, stream);
+    return launch_lanes<kBf16, kE4m3, kRead, 16>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_kv_rows(const KvRowsParams& p, cudaStream_t stream) {
+    const bool bf = p.c.dtype == kBf16;
+    if (!p.c.e4m3)  // words are moved without a look at them
+        return p.read ? launch_type<true, false, true>(p, stream) : launch_type<true, false, false>(p, stream);
+    if (p.read) return bf ? launch_type<true, true, true>(p, stream) : launch_type<false, true, true>(p, stream);
+    return bf ? launch_type<true, true, false>(p, stream) : launch_type<false, true, false>(p, stream);
+}
+
+}  // namespace fa2

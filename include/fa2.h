@@ -53,7 +53,8 @@ typedef enum {
     FA2_ERR_CUDA = 4,            /* a CUDA runtime call or kernel launch failed */
     FA2_ERR_DEVICE_TIMEOUT = 5,  /* a kernel gave up a bounded wait (reported by fa2_device_status) */
     FA2_ERR_WORKSPACE = 6,       /* workspace pointer null/misaligned or smaller than required */
-    FA2_ERR_SCRATCH_LIMIT = 7    /* the problem needs more than fa2_backward_noalloc's fixed scratch */
+    FA2_ERR_SCRATCH_LIMIT = 7,   /* the problem needs more than fa2_backward_noalloc's fixed scratch */
+    FA2_ERR_BAD_INDEX = 8        /* a page number or length outside the cache (reported by fa2_device_status) */
 } fa2_status;
 
 typedef enum {
@@ -387,6 +388,168 @@ fa2_status psa_extract_v_backward(const void* d_v, void* d_qkv, int32_t qkv_h, i
                                   int32_t B, int32_t num_heads, fa2_dtype dtype, void* stream);
 
 /*
+ * Rotary positions.  Element pairs of each head's first rot_dim elements turn by an angle
+ * that grows with the token's position; the elements past rot_dim stay as they are:
+ *   angle_i = position * inv_freq[i],  i < rot_dim / 2,
+ *   y1 = magnitude * (x1 cos angle_i - x2 sin angle_i),
+ *   y2 = magnitude * (x2 cos angle_i + x1 sin angle_i),
+ * (x1, x2) = (x[i], x[i + rot_dim / 2]) with interleaved = 0 and (x[2 i], x[2 i + 1])
+ * otherwise.  The backward is the transposed map: the same with angle -> -angle.
+ *
+ * fa2_rope_frequencies - HOST memory: fills inv_freq[rot_dim / 2] and *magnitude (may be
+ * NULL).  f_i = base^(-2 i / rot_dim), then for contexts `factor` times as long as the
+ * original_len positions a model was trained on:
+ *   FA2_ROPE_PLAIN   f_i                                               (magnitude 1)
+ *   FA2_ROPE_LINEAR  f_i / factor                                      (magnitude 1)
+ *   FA2_ROPE_BASE    base * factor^(rot_dim / (rot_dim - 2)) as base   (magnitude 1; rot_dim > 2)
+ *   FA2_ROPE_TURNS   with t_i = original_len f_i / (2 pi) turns over the original length and
+ *                    w = clamp((t_i - low) / (high - low), 0, 1): f_i (w + (1 - w) / factor)
+ *                    (magnitude 1)
+ *   FA2_ROPE_RAMP    the same mix, w falling linearly in i between the indices at which t_i
+ *                    is high (rounded down, at least 0) and low (rounded up, at most
+ *                    rot_dim - 1); magnitude 0.1 ln(factor) + 1
+ * factor >= 1, original_len > 0 and 0 < low < high where they are used.
+ *
+ * fa2_rope / fa2_rope_backward
+ *   x, y       element (b, h, n, d) at b strides[0] + h strides[1] + n strides[2] + d, device;
+ *              strides in elements, >= 0.  x is read (a stride of 0 repeats it), y is written
+ *              and may not overlap itself.  y may be x itself, with the same strides.
+ *   positions  int32, device: the position of token n of batch entry b at
+ *              b * position_stride + n (position_stride 0: one row for all entries); any
+ *              int32 value.  NULL: position n.
+ *   inv_freq   float64 [rot_dim / 2], device, finite
+ *   magnitude  finite
+ * dtype F32, F16 or BF16; rotated in float32, one rounding to dtype.  The angle is reduced
+ * to a fraction of a turn in 64-bit fixed point (position * (inv_freq / 2 pi) modulo 1), so
+ * that far positions lose nothing; its sine and cosine are float32.
+ * head_dim in [1, 1024]; rot_dim even, in [2, head_dim]; b h <= 2^31 - 1; n <= 2^30
+ * (FA2_ERR_UNSUPPORTED past them).  16-byte vectors where rot_dim / 2, head_dim and the
+ * strides allow it, narrower accesses otherwise.
+ * Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_CUDA.
+ */
+typedef enum {
+    FA2_ROPE_PLAIN = 0,
+    FA2_ROPE_LINEAR = 1,
+    FA2_ROPE_BASE = 2,
+    FA2_ROPE_TURNS = 3,
+    FA2_ROPE_RAMP = 4
+} fa2_rope_scaling;
+fa2_status fa2_rope_frequencies(double* inv_freq, float* magnitude, int32_t rot_dim, double base,
+                                fa2_rope_scaling scaling, double factor, double original_len, double low, double high);
+fa2_status fa2_rope(const void* x, void* y, const int32_t* positions, int64_t position_stride, const double* inv_freq,
+                    int64_t b, int64_t h, int64_t n, int32_t head_dim, int32_t rot_dim, const int64_t x_strides[3],
+                    const int64_t y_strides[3], int32_t interleaved, float magnitude, fa2_dtype dtype, void* stream);
+fa2_status fa2_rope_backward(const void* dy, void* dx, const int32_t* positions, int64_t position_stride,
+                             const double* inv_freq, int64_t b, int64_t h, int64_t n, int32_t head_dim, int32_t rot_dim,
+                             const int64_t dy_strides[3], const int64_t dx_strides[3], int32_t interleaved,
+                             float magnitude, fa2_dtype dtype, void* stream);
+
+/*
+ * A paged key-value cache: two pools of pages, `page_size` tokens each, shared by any number
+ * of sequences through a block table (int32 [batch, pages_per_seq], rows table_stride entries
+ * apart): token `pos` of sequence b lies in slot pos % page_size of page
+ * block_table[b * table_stride + pos / page_size].  Entries past a sequence's length are never
+ * read.  Sequences may share pages that are only read.
+ *
+ *   k, v       element (page, head, slot, d) at page * page_stride + head * head_stride +
+ *              slot * slot_stride + d, strides in elements and whole 16-byte units: pages as
+ *              [heads, slots, d] or [slots, heads, d], or wider ones.  Rows may not overlap.
+ *   type       FA2_CACHE_SAME: rows of the call's 16-bit dtype.
+ *              FA2_CACHE_E4M3: 8-bit floats (4 exponent, 3 fraction bits), and for each row a
+ *              scale byte in k_exp, v_exp (uint8 [num_pages, n_kv_heads, page_size],
+ *              contiguous): an element stands for code * 2^(byte - 127).
+ *   head_dim   a multiple of 8 (E4M3: 16) up to 128; page_size, n_kv_heads, num_pages > 0,
+ *              n_kv_heads <= 1024, pages_per_seq * page_size <= 2^30 (FA2_ERR_UNSUPPORTED).
+ *
+ * The lengths (int32 [batch], device) and the block table are read on the device, so that a
+ * captured graph replays with new ones.  What they say is checked there: a length that is
+ * negative or passes pages_per_seq * page_size counts as 0 or as that product, a page number
+ * outside [0, num_pages) is never followed (its tokens are not written, not read back, and
+ * masked out of the attention), and either sets the status that fa2_device_status reports as
+ * FA2_ERR_BAD_INDEX.
+ */
+typedef enum { FA2_CACHE_SAME = 0, FA2_CACHE_E4M3 = 1 } fa2_cache_type;
+typedef struct fa2_kv_cache {
+    void* k;
+    void* v;
+    uint8_t* k_exp;
+    uint8_t* v_exp;
+    int64_t num_pages;
+    int64_t page_stride, head_stride, slot_stride;
+    int32_t n_kv_heads, page_size, head_dim;
+    fa2_cache_type type;
+} fa2_kv_cache;
+
+/*
+ * fa2_kv_append - writes new tokens' keys and values into the cache.
+ *
+ *   k, v      element (token, head, d) at token * strides[0] + head * strides[1] + d, dtype F16
+ *             or BF16, device, read; strides in elements, >= 0, whole 16-byte units
+ *   cu_new    int32 [batch + 1], device: the new tokens of sequence b are rows cu_new[b] to
+ *             cu_new[b + 1] - 1 of k and v (cu_new ascending).  Rows outside all of them are
+ *             not stored.  NULL: one token a sequence, row b (tokens = batch).
+ *   seq_lens  int32 [batch]: each sequence's length AFTER the append: its n_b new tokens take
+ *             positions seq_lens[b] - n_b to seq_lens[b] - 1.  A token without a valid
+ *             position or page is not stored and sets the status FA2_ERR_BAD_INDEX; with
+ *             cu_new NULL a sequence of length 0 stores nothing and is no error.
+ * FA2_CACHE_E4M3: a row's scale is 2^e, e the smallest integer with max|x| <= 448 * 2^e over
+ * the row's finite elements (0 if they are all zero), no less than -60; codes are x / 2^e
+ * (exact) rounded to nearest even; infinities become 448 * 2^e with their sign, NaN stays NaN.
+ * Two tokens may not name one slot (a page shared by two sequences that both write it): the
+ * slot's contents are then some mix of both.
+ * Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_CUDA.
+ */
+fa2_status fa2_kv_append(const fa2_kv_cache* cache, const void* k, const void* v, const int64_t k_strides[2],
+                         const int64_t v_strides[2], const int32_t* block_table, int64_t table_stride,
+                         int64_t pages_per_seq, const int32_t* cu_new, const int32_t* seq_lens, int64_t batch,
+                         int64_t tokens, fa2_dtype dtype, void* stream);
+
+/*
+ * fa2_kv_read - copies the cached rows of each sequence out of the pages.
+ *
+ *   k_out, v_out  element (b, head, pos, d) at b strides[0] + head strides[1] + pos strides[2]
+ *                 + d, dtype, device; strides in elements, whole 16-byte units, the same for
+ *                 both, rows not overlapping.  Positions 0 to min(seq_lens[b], max_len) - 1 are
+ *                 written, the others left as they were.  With [batch, heads, max_len, d]
+ *                 outputs of equal lengths, fa2_forward takes them as they are.
+ * FA2_CACHE_E4M3: code * 2^(byte - 127), rounded once to dtype (BF16: exact; F16 past 65504:
+ * infinity).  Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_CUDA.
+ */
+fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, const int64_t out_strides[3],
+                       const int32_t* block_table, int64_t table_stride, int64_t pages_per_seq,
+                       const int32_t* seq_lens, int64_t batch, int64_t max_len, fa2_dtype dtype, void* stream);
+
+/*
+ * fa2_decode - attention of one new token of each sequence over the cache.
+ *
+ * fa2_forward's formula for one query row a head, over keys j of sequence b with
+ * max(0, len_b - window) <= j < len_b (window 0: all of them):
+ *   O = sum_j softmax_j(softmax_scale q.k_j) v_j,  LSE = ln sum_j exp(softmax_scale q.k_j);
+ * an empty row gives O = 0, LSE = -inf.  Query head h reads key-value head
+ * h / (n_heads / n_kv_heads).
+ *
+ *   q          element (b, h, d) at b q_strides[0] + h q_strides[1] + d, dtype F16 / BF16
+ *   o          [batch, n_heads, head_dim] dtype, contiguous;  lse [batch, n_heads] float32
+ *   window     >= 0
+ *   workspace  fa2_decode_workspace_size bytes, 16-byte aligned, contents do not matter;
+ *              calls whose GPU work may overlap need one each
+ * float32 scores, softmax statistics and sums; the probabilities are rounded to 16 bits
+ * (FA2_CACHE_SAME: dtype; FA2_CACHE_E4M3: half) before the product with V; in half, weights
+ * below 2^-25 of the row's largest count as 0 there.
+ * The keys of all sequences and heads are divided evenly over the CTAs, whatever the lengths;
+ * a row divided between CTAs is joined from float32 partial results in a fixed order (the
+ * result is reproducible for the same lengths).
+ * n_heads a multiple of n_kv_heads, n_heads <= 65535, batch <= 65535 (FA2_ERR_UNSUPPORTED).
+ * Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_WORKSPACE,
+ *         FA2_ERR_CUDA.
+ */
+size_t fa2_decode_workspace_size(int64_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim);
+fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_cache* cache, void* o, float* lse,
+                      const int32_t* block_table, int64_t table_stride, int64_t pages_per_seq,
+                      const int32_t* seq_lens, int64_t batch, int32_t n_heads, int64_t window, void* workspace,
+                      size_t workspace_bytes, fa2_dtype dtype, float softmax_scale, void* stream);
+
+/*
  * fa2_device_status - the watchdog word of the library's kernels.
  *
  * Every wait of a kernel's threads on an mbarrier (a TMA copy landing, a tensor-core
@@ -395,7 +558,9 @@ fa2_status psa_extract_v_backward(const void* d_v, void* d_qkv, int32_t qkv_h, i
  * word, raises its CTA's abort flag, drains the copies it has in flight and returns;
  * the CTA frees its tensor memory and exits.  This call synchronises `stream`, reads
  * that word on the current device, clears it and returns FA2_OK or
- * FA2_ERR_DEVICE_TIMEOUT (FA2_ERR_CUDA if the synchronisation failed).
+ * FA2_ERR_DEVICE_TIMEOUT (FA2_ERR_CUDA if the synchronisation failed).  The cache's kernels
+ * also record there a page number or a length that they refused to follow: with no timeout
+ * beside it, this call then returns FA2_ERR_BAD_INDEX.
  *
  * What this does NOT cover, stated plainly:
  *  - A launch call (fa2_forward, fa2_backward, ...) returns FA2_OK once its kernels

@@ -13,10 +13,13 @@ Modules:
   the analytic backward (dQ, dK, dV), as explicit score matrices in float64.
 * :mod:`oracle.psa` - the PSA pack / extract / merge index maps and their
   adjoints, element-for-element.
+* :mod:`oracle.serving` - rotary positions, the paged cache and its 8-bit rows,
+  and the attention of one new token.
 
 Parity pins (tests/test_oracle.py, marked "not gpu"): brute-force evaluation on
 tiny inputs, the worked examples the pages print, closed forms and invariants,
 central finite differences for the gradients, and brute-force index loops for
-the PSA maps.  Every function here is pinned; none is "parity unpinned".
+the PSA maps.  The serving oracle is pinned in tests/test_oracle_serving.py.
+Every function here is pinned; none is "parity unpinned".
 """
-from . import attention, psa  # noqa: F401
+from . import attention, psa, serving  # noqa: F401

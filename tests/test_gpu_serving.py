@@ -1,0 +1,153 @@
+"""Rotary positions, the cache and the attention run together, as a program that generates tokens uses them."""
+import math
+
+import numpy as np
+import pytest
+
+from attention_fa2_forward_02_gb300 import binding, synth
+from oracle import attention as A
+from oracle import serving as S
+from tests import gpu_util as G
+from tests.paged import Cache
+from tests.tolerance import UNIT_ROUNDOFF
+
+pytestmark = pytest.mark.gpu
+
+HKV, GROUP, D, PAGE = 2, 3, 64, 16
+HEADS = HKV * GROUP
+
+
+class Server:
+    """Prompts of given lengths, then tokens one by one: the projections are seeded, everything after them the library's."""
+
+    def __init__(self, prompts, steps, e4m3):
+        torch = G.require_gpu()
+        self.prompts, self.steps, self.e4m3 = prompts, steps, e4m3
+        self.total = [n + steps for n in prompts]
+        self.cache = Cache("server", self.total, PAGE, HKV, D, "bf16", e4m3, stale="nan")
+        self.lens = torch.zeros(len(prompts), dtype=torch.int32, device="cuda")
+        freq, self.magnitude = binding.fa2_rope_frequencies(D, 10000.0, "ramp", 4.0, 32.0)
+        self.freq64, self.freq = freq.numpy(), freq.cuda()
+        # all tokens of all sequences: q, k, v heads side by side
+        self.qkv = [synth.tensor(f"server/{b}", (n, HEADS + 2 * HKV, D), "bf16") for b, n in enumerate(self.total)]
+        self.ws = torch.empty(binding.fa2_decode_workspace_size(len(prompts), HEADS, HKV, D), dtype=torch.uint8, device="cuda")
+        self.o = G.empty((len(prompts), HEADS, D), "bf16")
+        self.lse = torch.empty(len(prompts), HEADS, device="cuda")
+
+    def rotate(self, rows, positions):
+        """q and k heads of rows [T, heads, D] turned in place."""
+        view = rows[:, :HEADS + HKV].unsqueeze(0).transpose(1, 2)
+        binding.fa2_rope(view, view, self.freq, positions=positions.unsqueeze(0), magnitude=self.magnitude)
+
+    def prefill(self):
+        torch = G.require_gpu()
+        rows = torch.cat([G.to_device(x[:n], "bf16") for x, n in zip(self.qkv, self.prompts)])
+        pos = torch.cat([torch.arange(n, dtype=torch.int32) for n in self.prompts]).cuda()
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(self.prompts)]), dtype=torch.int32, device="cuda")
+        self.lens.copy_(torch.tensor(self.prompts, dtype=torch.int32))
+        self.rotate(rows, pos)
+        self.store(rows, cu)
+
+    def store(self, rows, cu=None):
+        c = self.cache
+        binding.fa2_kv_append(*c.pools(), rows[:, HEADS:HEADS + HKV], rows[:, HEADS + HKV:], c.table_dev, self.lens, cu_new=cu, **c.exps())
+
+    def step(self, rows):
+        """rows [batch, heads, D]: the new tokens' projections; lens already counts them in."""
+        c = self.cache
+        self.rotate(rows, self.lens - 1)
+        self.store(rows)
+        binding.fa2_decode(rows[:, :HEADS], *c.pools(), self.o, self.lse, c.table_dev, self.lens, self.ws, 1 / math.sqrt(D), **c.exps())
+
+    def new_rows(self, i):
+        return np.stack([x[n + i] for x, n in zip(self.qkv, self.prompts)])
+
+    def reference(self, i):
+        """O after step i from the unquantised float64 projections."""
+        out = []
+        for x, n in zip(self.qkv, self.prompts):
+            w = synth.widen(x[: n + i + 1], "bf16")
+            t = S.rope(w[:, :HEADS + HKV].swapaxes(0, 1)[None], np.arange(n + i + 1)[None], self.freq64, False, self.magnitude)[0]
+            k, v = t[HEADS:], w[:, HEADS + HKV:].swapaxes(0, 1)
+            q = t[:HEADS, -1].reshape(HKV, GROUP, D)
+            out.append(A.forward(q, k, v, 1 / math.sqrt(D))[0].reshape(HEADS, D))
+        return np.stack(out)
+
+
+def tolerance(e4m3):
+    """q and k rounded to bfloat16 after the rotation (2^-8 each) and, with e4m3, k and v by 2^-4: a score of |s| <= E then
+    moves by about sqrt(d) roundings of its terms, not d; with unit normal rows and scale 1 / sqrt(d), its terms' root sum of
+    squares is about 1, so a score moves by 8 * 2^-4 at 8 of Hoeffding's deviations (8 * 2^-7 without e4m3), every weight by the
+    factor exp of that, and O, an average of unit values of at most about 4, by twice that times 4 at the very most."""
+    return 2 * 4 * math.expm1(8 * (2.0 ** -4 if e4m3 else 2.0 ** -7)) / 2 ** 2
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_generation_follows_the_oracle(e4m3):
+    s = Server([33, 1, 64, 17], 20, e4m3)
+    s.prefill()
+    for i in range(s.steps):
+        s.lens += 1
+        s.step(G.to_device(s.new_rows(i), "bf16"))
+        binding.fa2_device_status()
+        ref = s.reference(i)
+        err = G.to_f64(s.o) - ref
+        assert np.max(np.abs(err)) <= tolerance(e4m3)
+        # a wrong position, page or head makes an error as large as the result itself
+        assert np.sqrt(np.mean(err ** 2)) <= (0.15 if e4m3 else 0.02) * np.sqrt(np.mean(ref ** 2))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_a_captured_step_replays_with_new_lengths(e4m3):
+    """One graph of (length + 1, rotate, store, attend) replayed for every token gives what the eager calls give."""
+    torch = G.require_gpu()
+    a, b = (Server([33, 1, 64, 17], 20, e4m3) for _ in range(2))
+    a.prefill()
+    b.prefill()
+    rows = torch.empty(4, HEADS + 2 * HKV, D, dtype=torch.bfloat16, device="cuda")
+
+    def one():
+        b.lens += 1
+        b.step(rows)
+
+    keep = [t.clone() for t in (b.lens, *[p.view(torch.uint8) for p in b.cache.pools()])]
+    rows.copy_(G.to_device(b.new_rows(0), "bf16"))
+    one()  # eager once, for the library's one-time settings
+    torch.cuda.synchronize()
+    b.lens.copy_(keep[0])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        one()
+    b.lens.copy_(keep[0])
+    for i in range(a.steps):
+        a.lens += 1
+        a.step(G.to_device(a.new_rows(i), "bf16"))
+        rows.copy_(G.to_device(b.new_rows(i), "bf16"))
+        b.o.fill_(float("nan"))
+        graph.replay()
+        assert torch.equal(a.o, b.o) and torch.equal(a.lse, b.lse), f"token {i}"
+    for x, y in zip(a.cache.pools(), b.cache.pools()):
+        assert torch.equal(x.contiguous().view(torch.uint8), y.contiguous().view(torch.uint8))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+def test_read_back_feeds_the_forward(e4m3):
+    """The cache read back, its heads' grouped queries as query rows: fa2_forward and fa2_decode agree."""
+    torch = G.require_gpu()
+    n, batch = 300, 3
+    c = Cache("feed", [n] * batch, PAGE, HKV, D, "bf16", e4m3)
+    q = G.to_device(synth.tensor("feed/q", (batch, HEADS, D), "bf16"), "bf16")
+    o, lse = torch.empty_like(q), torch.empty(batch, HEADS, device="cuda")
+    ws = torch.empty(binding.fa2_decode_workspace_size(batch, HEADS, HKV, D), dtype=torch.uint8, device="cuda")
+    binding.fa2_decode(q, *c.pools(), o, lse, c.table_dev, c.lens_dev, ws, 0.125, **c.exps())
+    k, v = (G.empty((batch, HKV, n, D), "bf16") for _ in "kv")
+    binding.fa2_kv_read(*c.pools(), k, v, c.table_dev, c.lens_dev, **c.exps())
+    rows = batch * HKV
+    o2, lse2 = torch.empty_like(q).view(rows, GROUP, D), torch.empty(rows, GROUP, device="cuda")
+    binding.fa2_forward(q.view(rows, GROUP, D), k.view(rows, n, D), v.view(rows, n, D), o2, lse2, 0.125)
+    binding.fa2_device_status()
+    a, b = G.to_f64(o).reshape(rows, GROUP, D), G.to_f64(o2)
+    v64 = np.abs(G.to_f64(v)).reshape(rows, 1, n, D).max(2)
+    # both are within two roundings of 2^-8 (weights, output) of sum P |v| <= max |v|
+    assert np.all(np.abs(a - b) <= 4 * UNIT_ROUNDOFF["bf16"] * v64 + 1e-5)
+    assert np.max(np.abs(G.to_f64(lse).reshape(rows, GROUP) - G.to_f64(lse2))) <= 2e-4

@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_NAME = "libfa2_gb300.so"
@@ -81,10 +82,6 @@ class KvCache(ctypes.Structure):
                 ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("slot_stride", ctypes.c_int64), ("n_kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
                 ("head_dim", ctypes.c_int32), ("type", ctypes.c_int)]
-
-
-CACHE_SAME, CACHE_E4M3 = 0, 1
-ROPE_SCALINGS = ("plain", "linear", "base", "turns", "ramp")  # fa2_rope_scaling's values in order
 
 
 def _declare(lib):
@@ -421,27 +418,67 @@ def fa2_watchdog_selftest(stream=None) -> None:
 
 
 # ---------------------------------------------------------------------------- rotary positions and the paged cache
+#
+# A decoding step makes these calls on tensors so small that the host's work sets the pace, so the arguments are
+# marshalled with few Python operations: pointers as plain integers, structures and stride arrays packed into bytes.
+
+CACHE_SAME, CACHE_E4M3 = 0, 1
+ROPE_SCALINGS = ("plain", "linear", "base", "turns", "ramp")  # fa2_rope_scaling's values in order
+_pack_cache = struct.Struct("@4Q4q3ii").pack  # fa2_kv_cache
+_pack2, _pack3 = struct.Struct("@2q").pack, struct.Struct("@3q").pack
+_torch_codes = {}
 
 
-def _strided(t, name, ndim):
-    """Pointer of a tensor whose last dimension is contiguous; the library takes its other strides."""
+def _row_code(t):
+    """The library's code of a tensor's type."""
+    try:
+        return _torch_codes[t.dtype]
+    except KeyError:
+        _torch_codes[t.dtype] = _dtype_code(t)  # refuses others
+        return _torch_codes[t.dtype]
+
+
+def _refuse_device(name, t):
     _on_current_device(t, name)
-    if t.dim() != ndim:
-        raise ValueError(f"{name} must have {ndim} dimensions, got {tuple(t.shape)}")
-    if t.shape[-1] > 1 and t.stride(-1) != 1:
+    raise ValueError(f"{name} is not on the current device")
+
+
+def _at(t, name, device):
+    """Pointer of a contiguous tensor."""
+    if t.get_device() != device:
+        _refuse_device(name, t)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
+
+
+def _rows_at(t, name, device, shape, strides):
+    """Pointer of a tensor whose last dimension is contiguous; the library takes its other strides."""
+    if t.get_device() != device:
+        _refuse_device(name, t)
+    if strides[-1] != 1 and shape[-1] > 1:
         raise ValueError(f"{name}'s last dimension must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
-def _int64s(values):
-    values = tuple(values)
-    return (ctypes.c_int64 * len(values))(*values)
+def _same_strides(shape, a, b):
+    """Whether two stride tuples agree (the stride of a dimension of one element means nothing)."""
+    return a == b or all(x == y or n <= 1 for n, x, y in zip(shape, a, b))
 
 
 def _require_dtype(where, dtype, **tensors):
     for name, t in tensors.items():
         if t is not None and t.dtype != dtype:
             raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
+
+
+def _now(t, stream):
+    """(current device, raw stream) of a call on `t`: the given stream, or torch's current one."""
+    import torch
+    if not t.is_cuda:
+        _refuse_device("every tensor", t)
+    device = torch.cuda.current_device()
+    return device, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
 
 
 def fa2_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -461,23 +498,33 @@ def fa2_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "pl
 
 def _rope(where, x, y, inv_freq, positions, interleaved, magnitude, stream):
     import torch
-    if x.dim() != 4 or y.shape != x.shape:
+    shape = x.shape
+    if len(shape) != 4 or y.shape != shape:
         raise ValueError(f"{where}: the tensors are [B, H, N, d], both of one shape")
-    b, h, n, d = x.shape
-    _same_dtype(where, x, y=y)
-    _require_dtype(where, torch.float64, inv_freq=inv_freq)
-    _require_dtype(where, torch.int32, positions=positions)
-    position_stride, pos_ptr = 0, None
+    b, h, n, d = shape
+    if y.dtype != x.dtype:
+        _same_dtype(where, x, y=y)
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError(f"{where}: inv_freq must be float64 [rot_dim / 2], got {inv_freq.dtype} {tuple(inv_freq.shape)}")
+    position_stride, at = 0, None
     if positions is not None:
-        if positions.shape not in ((n,), (1, n), (b, n)):
-            raise ValueError(f"{where}: positions must be [N], [1, N] or [B, N], got {tuple(positions.shape)}")
-        pos_ptr = _strided(positions, "positions", positions.dim())
-        position_stride = positions.stride(0) if positions.dim() == 2 and positions.shape[0] > 1 else 0
-    st = getattr(library(), where)(_strided(x, "x", 4), _strided(y, "y", 4), pos_ptr, position_stride,
-                                   _dev(inv_freq, "inv_freq", 1), b, h, n, d, 2 * inv_freq.numel(), _int64s(x.stride()[:3]),
-                                   _int64s(y.stride()[:3]), int(bool(interleaved)), float(magnitude), _dtype_code(x),
-                                   _stream(stream))
-    _check(st, where)
+        if positions.dtype != torch.int32:
+            raise TypeError(f"{where}: positions must be int32, got {positions.dtype}")
+        given = positions.shape
+        if given != (b, n) and given != (n,) and given != (1, n):
+            raise ValueError(f"{where}: positions must be [N], [1, N] or [B, N], got {tuple(given)}")
+    device, raw = _now(x, stream)
+    if positions is not None:
+        steps = positions.stride()
+        at = _rows_at(positions, "positions", device, given, steps)
+        if len(given) == 2 and given[0] > 1:
+            position_stride = steps[0]
+    xs, ys = x.stride(), y.stride()
+    st = getattr(library(), where)(_rows_at(x, "x", device, shape, xs), _rows_at(y, "y", device, shape, ys), at, position_stride,
+                                   _at(inv_freq, "inv_freq", device), b, h, n, d, 2 * inv_freq.numel(), _pack3(*xs[:3]),
+                                   _pack3(*ys[:3]), 1 if interleaved else 0, magnitude, _row_code(x), raw)
+    if st:
+        _check(st, where)
 
 
 def fa2_rope(x, y, inv_freq, positions=None, interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
@@ -491,57 +538,49 @@ def fa2_rope_backward(dy, dx, inv_freq, positions=None, interleaved: bool = Fals
     _rope("fa2_rope_backward", dy, dx, inv_freq, positions, interleaved, magnitude, stream)
 
 
-def _cache(where, k_pages, v_pages, k_exp, v_exp, row_dtype):
-    """The sizes and strides of the fa2_kv_cache of two page pools [num_pages, n_kv_heads, page_size, d] (any strides, d
-    contiguous), after checking them; _cache_pointers adds the rest."""
+def _cache_of(where, k_pages, v_pages, k_exp, v_exp, row_dtype, block_table, seq_lens):
+    """Checks two page pools [num_pages, n_kv_heads, page_size, d] (any strides, d contiguous), their scale bytes, the
+    block table and the lengths; (batch, n_kv_heads, d, pointers), where pointers(device) gives the packed fa2_kv_cache,
+    the table's pointer, row stride and pages per sequence, and the lengths' pointer."""
     import torch
-    if k_pages.dim() != 4 or v_pages.shape != k_pages.shape:
+    shape = k_pages.shape
+    if len(shape) != 4 or v_pages.shape != shape:
         raise ValueError(f"{where}: k_pages and v_pages are [num_pages, n_kv_heads, page_size, d], both of one shape")
-    # the stride of a dimension of one element means nothing
-    for size, a, b in zip(k_pages.shape[:3], k_pages.stride()[:3], v_pages.stride()[:3]):
-        if size > 1 and a != b:
-            raise ValueError(f"{where}: k_pages and v_pages must have the same strides")
-    _same_dtype(where, k_pages, v_pages=v_pages)
-    pages, heads, page_size, d = k_pages.shape
-    c = KvCache()
-    if k_pages.dtype == torch.float8_e4m3fn:
+    pages, heads, page_size, d = shape
+    strides, vs = k_pages.stride(), v_pages.stride()
+    if not _same_strides(shape, strides, vs):
+        raise ValueError(f"{where}: k_pages and v_pages must have the same strides")
+    kind = k_pages.dtype
+    if v_pages.dtype != kind:
+        _same_dtype(where, k_pages, v_pages=v_pages)
+    e4m3 = kind == torch.float8_e4m3fn
+    if e4m3:
         if k_exp is None or v_exp is None:
             raise ValueError(f"{where}: an e4m3 cache has scale bytes, k_exp and v_exp")
-        _require_dtype(where, torch.uint8, k_exp=k_exp, v_exp=v_exp)
-        for name, t in (("k_exp", k_exp), ("v_exp", v_exp)):
-            if t.shape != (pages, heads, page_size):
-                raise ValueError(f"{where}: {name} must be [num_pages, n_kv_heads, page_size]")
-        c.type = CACHE_E4M3
-    else:
-        if k_exp is not None or v_exp is not None:
-            raise ValueError(f"{where}: k_exp and v_exp belong to an e4m3 cache")
-        if k_pages.dtype != row_dtype:
-            raise TypeError(f"{where}: the pages are {k_pages.dtype}, expected {row_dtype} or float8_e4m3fn")
-        c.type = CACHE_SAME
-    c.num_pages, c.n_kv_heads, c.page_size, c.head_dim = pages, heads, page_size, d
-    c.page_stride, c.head_stride, c.slot_stride = k_pages.stride()[:3]
-    return c
-
-
-def _cache_pointers(c, k_pages, v_pages, k_exp, v_exp):
-    c.k, c.v = _strided(k_pages, "k_pages", 4), _strided(v_pages, "v_pages", 4)
-    if c.type == CACHE_E4M3:
-        c.k_exp, c.v_exp = _dev(k_exp, "k_exp", 3), _dev(v_exp, "v_exp", 3)
-    return ctypes.byref(c)
-
-
-def _check_table(where, block_table, seq_lens):
-    import torch
-    _require_dtype(where, torch.int32, block_table=block_table, seq_lens=seq_lens)
-    if block_table.dim() != 2 or seq_lens.shape != (block_table.shape[0],):
+        if k_exp.dtype != torch.uint8 or v_exp.dtype != torch.uint8:
+            _require_dtype(where, torch.uint8, k_exp=k_exp, v_exp=v_exp)
+        if k_exp.shape != shape[:3] or v_exp.shape != shape[:3]:
+            raise ValueError(f"{where}: k_exp and v_exp must be [num_pages, n_kv_heads, page_size]")
+    elif k_exp is not None or v_exp is not None:
+        raise ValueError(f"{where}: k_exp and v_exp belong to an e4m3 cache")
+    elif kind != row_dtype:
+        raise TypeError(f"{where}: the pages are {kind}, expected {row_dtype} or float8_e4m3fn")
+    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
+        _require_dtype(where, torch.int32, block_table=block_table, seq_lens=seq_lens)
+    table_shape = block_table.shape
+    if len(table_shape) != 2 or seq_lens.shape != table_shape[:1]:
         raise ValueError(f"{where}: block_table is [batch, pages_per_seq] and seq_lens [batch]")
-    return block_table.shape[0]
+    batch, per_seq = table_shape
 
+    def pointers(device):
+        steps = block_table.stride()
+        return (_pack_cache(_rows_at(k_pages, "k_pages", device, shape, strides), _rows_at(v_pages, "v_pages", device, shape, vs),
+                            _at(k_exp, "k_exp", device) if e4m3 else 0, _at(v_exp, "v_exp", device) if e4m3 else 0,
+                            pages, *strides[:3], heads, page_size, d, CACHE_E4M3 if e4m3 else CACHE_SAME),
+                (_rows_at(block_table, "block_table", device, table_shape, steps), steps[0] if batch > 1 else per_seq, per_seq),
+                _at(seq_lens, "seq_lens", device))
 
-def _table(block_table):
-    """Pointer, row stride and pages per sequence of a block table."""
-    batch, pages = block_table.shape
-    return _strided(block_table, "block_table", 2), block_table.stride(0) if batch > 1 else pages, pages
+    return batch, heads, d, pointers
 
 
 def fa2_kv_append(k_pages, v_pages, k, v, block_table, seq_lens, cu_new=None, k_exp=None, v_exp=None, stream=None) -> None:
@@ -550,40 +589,45 @@ def fa2_kv_append(k_pages, v_pages, k, v, block_table, seq_lens, cu_new=None, k_
     [batch + 1] says which rows are whose (None: one a sequence)."""
     import torch
     where = "fa2_kv_append"
-    c = _cache(where, k_pages, v_pages, k_exp, v_exp, k.dtype)
-    if k.dim() != 3 or v.shape != k.shape or k.shape[1:] != (c.n_kv_heads, c.head_dim):
+    batch, heads, d, pointers = _cache_of(where, k_pages, v_pages, k_exp, v_exp, k.dtype, block_table, seq_lens)
+    shape = k.shape
+    if len(shape) != 3 or v.shape != shape or shape[1] != heads or shape[2] != d:
         raise ValueError(f"{where}: k and v are [tokens, n_kv_heads, d]")
-    _same_dtype(where, k, v=v)
-    batch = _check_table(where, block_table, seq_lens)
+    if v.dtype != k.dtype:
+        _same_dtype(where, k, v=v)
     if cu_new is not None:
-        _require_dtype(where, torch.int32, cu_new=cu_new)
+        if cu_new.dtype != torch.int32:
+            _require_dtype(where, torch.int32, cu_new=cu_new)
         if cu_new.shape != (batch + 1,):
             raise ValueError(f"{where}: cu_new must be [batch + 1]")
-    cache = _cache_pointers(c, k_pages, v_pages, k_exp, v_exp)
-    st = library().fa2_kv_append(cache, _strided(k, "k", 3), _strided(v, "v", 3), _int64s(k.stride()[:2]),
-                                 _int64s(v.stride()[:2]), *_table(block_table),
-                                 None if cu_new is None else _dev(cu_new, "cu_new", 1), _dev(seq_lens, "seq_lens", 1), batch,
-                                 k.shape[0], _dtype_code(k), _stream(stream))
-    _check(st, where)
+    device, raw = _now(k, stream)
+    cache, table, lens = pointers(device)
+    ks, vs = k.stride(), v.stride()
+    st = library().fa2_kv_append(cache, _rows_at(k, "k", device, shape, ks), _rows_at(v, "v", device, shape, vs), _pack2(*ks[:2]),
+                                 _pack2(*vs[:2]), *table, None if cu_new is None else _at(cu_new, "cu_new", device), lens, batch,
+                                 shape[0], _row_code(k), raw)
+    if st:
+        _check(st, where)
 
 
 def fa2_kv_read(k_pages, v_pages, k_out, v_out, block_table, seq_lens, k_exp=None, v_exp=None, stream=None) -> None:
     """Copy the cached rows out: k_out, v_out [batch, n_kv_heads, max_len, d]; positions past a sequence's length stay."""
     where = "fa2_kv_read"
-    c = _cache(where, k_pages, v_pages, k_exp, v_exp, k_out.dtype)
-    batch = _check_table(where, block_table, seq_lens)
-    if k_out.dim() != 4 or v_out.shape != k_out.shape or (k_out.shape[0], k_out.shape[1], k_out.shape[3]) != (
-            batch, c.n_kv_heads, c.head_dim):
+    batch, heads, d, pointers = _cache_of(where, k_pages, v_pages, k_exp, v_exp, k_out.dtype, block_table, seq_lens)
+    shape = k_out.shape
+    if len(shape) != 4 or v_out.shape != shape or shape[0] != batch or shape[1] != heads or shape[3] != d:
         raise ValueError(f"{where}: k_out and v_out are [batch, n_kv_heads, max_len, d]")
-    for size, a, b in zip(k_out.shape[:3], k_out.stride()[:3], v_out.stride()[:3]):
-        if size > 1 and a != b:
-            raise ValueError(f"{where}: k_out and v_out must have the same strides")
-    _same_dtype(where, k_out, v_out=v_out)
-    cache = _cache_pointers(c, k_pages, v_pages, k_exp, v_exp)
-    st = library().fa2_kv_read(cache, _strided(k_out, "k_out", 4), _strided(v_out, "v_out", 4), _int64s(k_out.stride()[:3]),
-                               *_table(block_table), _dev(seq_lens, "seq_lens", 1), batch, k_out.shape[2],
-                               _dtype_code(k_out), _stream(stream))
-    _check(st, where)
+    strides, vs = k_out.stride(), v_out.stride()
+    if not _same_strides(shape, strides, vs):
+        raise ValueError(f"{where}: k_out and v_out must have the same strides")
+    if v_out.dtype != k_out.dtype:
+        _same_dtype(where, k_out, v_out=v_out)
+    device, raw = _now(k_out, stream)
+    cache, table, lens = pointers(device)
+    st = library().fa2_kv_read(cache, _rows_at(k_out, "k_out", device, shape, strides), _rows_at(v_out, "v_out", device, shape, vs),
+                               _pack3(*strides[:3]), *table, lens, batch, shape[2], _row_code(k_out), raw)
+    if st:
+        _check(st, where)
 
 
 def fa2_decode_workspace_size(batch: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -595,15 +639,18 @@ def fa2_decode(q, k_pages, v_pages, o, lse, block_table, seq_lens, workspace, so
     """Attention of one new token a sequence over the paged cache: q, o [batch, n_heads, d], lse [batch, n_heads]
     float32; workspace a CUDA uint8 tensor of fa2_decode_workspace_size bytes; window > 0: the last keys only."""
     where = "fa2_decode"
-    c = _cache(where, k_pages, v_pages, k_exp, v_exp, q.dtype)
-    batch = _check_table(where, block_table, seq_lens)
-    if q.dim() != 3 or q.shape[0] != batch or q.shape[2] != c.head_dim or o.shape != q.shape or lse.shape != q.shape[:2]:
+    batch, heads, d, pointers = _cache_of(where, k_pages, v_pages, k_exp, v_exp, q.dtype, block_table, seq_lens)
+    shape = q.shape
+    if len(shape) != 3 or shape[0] != batch or shape[2] != d or o.shape != shape or lse.shape != shape[:2]:
         raise ValueError(f"{where}: q and o are [batch, n_heads, d], lse [batch, n_heads]")
-    _same_dtype(where, q, o=o)
+    if o.dtype != q.dtype:
+        _same_dtype(where, q, o=o)
     _require_f32(where, lse=lse)
-    cache = _cache_pointers(c, k_pages, v_pages, k_exp, v_exp)
-    st = library().fa2_decode(_strided(q, "q", 3), _int64s(q.stride()[:2]), cache, _dev(o, "o", 3), _dev(lse, "lse", 2),
-                              *_table(block_table), _dev(seq_lens, "seq_lens", 1), batch, q.shape[1], int(window),
-                              _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), _dtype_code(q),
-                              float(softmax_scale), _stream(stream))
-    _check(st, where)
+    device, raw = _now(q, stream)
+    cache, table, lens = pointers(device)
+    qs = q.stride()
+    st = library().fa2_decode(_rows_at(q, "q", device, shape, qs), _pack2(*qs[:2]), cache, _at(o, "o", device), _at(lse, "lse", device),
+                              *table, lens, batch, shape[1], window, _at(workspace, "workspace", device),
+                              workspace.numel() * workspace.element_size(), _row_code(q), softmax_scale, raw)
+    if st:
+        _check(st, where)

@@ -226,7 +226,7 @@ fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_ca
     const fa2_status st = paged(cache, block_table, table_stride, pages_per_seq, seq_lens, batch, dtype, &p.c);
     if (st != FA2_OK) return st;
     if (n_heads % cache->n_kv_heads != 0) return FA2_ERR_INVALID_ARG;
-    if (n_heads > kMaxGrid) return FA2_ERR_UNSUPPORTED;
+    if (n_heads > kMaxGrid || batch * n_heads > INT32_MAX) return FA2_ERR_UNSUPPORTED;
     if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16)) return FA2_ERR_MISALIGNED;
     const int64_t sizes[2] = {batch, n_heads};
     for (int i = 0; i < 2; ++i)

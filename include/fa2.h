@@ -539,7 +539,8 @@ fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, cons
  * The keys of all sequences and heads are divided evenly over the CTAs, whatever the lengths;
  * a row divided between CTAs is joined from float32 partial results in a fixed order (the
  * result is reproducible for the same lengths).
- * n_heads a multiple of n_kv_heads, n_heads <= 65535, batch <= 65535 (FA2_ERR_UNSUPPORTED).
+ * n_heads a multiple of n_kv_heads; n_heads <= 65535, batch <= 65535 and their product
+ * <= 2^31 - 1 (FA2_ERR_UNSUPPORTED).
  * Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_WORKSPACE,
  *         FA2_ERR_CUDA.
  */

@@ -94,6 +94,7 @@ fa2_status paged(const fa2_kv_cache* c, const int32_t* table, int64_t table_stri
     p.num_pages = c->num_pages;
     p.page_stride = c->page_stride * eb; p.head_stride = c->head_stride * eb; p.slot_stride = c->slot_stride * eb;
     p.hkv = c->n_kv_heads; p.page_size = c->page_size; p.d = c->head_dim;
+    page_divisor(p.page_size, &p.page_mul, &p.page_shift);
     p.e4m3 = e4m3;
     p.table = table; p.table_stride = table_stride; p.room = pages_per_seq * c->page_size;
     p.lens = lens; p.batch = batch; p.dtype = (int)dtype;

@@ -177,6 +177,7 @@ struct PagedParams {
     uint8_t* v_exp;
     int64_t num_pages, page_stride, head_stride, slot_stride;  // strides in bytes
     int hkv, page_size, d;
+    uint32_t page_mul, page_shift;  // pos / page_size = (pos + high word of pos * page_mul) >> page_shift
     bool e4m3;
     const int32_t* table;
     int64_t table_stride;
@@ -186,6 +187,17 @@ struct PagedParams {
     int dtype;
     unsigned int* status;
 };
+
+// The multiplier and shift for a division by d (1 <= d <= 2^30) of numbers below 2^31: with
+// 2^s >= d > 2^(s-1) and m = floor(2^32 (2^s - d) / d) + 1, 2^32 + m lies within 2^s of 2^(32+s) / d
+// from above, so that (2^32 + m) n / 2^(32+s) has the floor of n / d for n < 2^32 (Granlund and
+// Montgomery, "Division by invariant integers using multiplication", PLDI 1994).
+inline void page_divisor(int d, uint32_t* mul, uint32_t* shift) {
+    uint32_t s = 0;
+    while (((int64_t)1 << s) < d) ++s;
+    *mul = (uint32_t)((((uint64_t)1 << 32) * (((uint64_t)1 << s) - (uint64_t)d)) / (uint64_t)d + 1);
+    *shift = s;
+}
 
 // Copies rows between the cache and contiguous-row tensors: append (rows [token, head]) or
 // read (rows [b, head, pos]).

@@ -84,8 +84,8 @@ __device__ __forceinline__ bool find_token(const KvRowsParams& p, int64_t t, int
         out->k_off = t * p.ks[0];
         out->v_off = t * p.vs[0];
     }
-    const int page = c.table[b * c.table_stride + (int)pos / c.page_size];
-    const Slot s = slot_of(c, page, (int)pos % c.page_size);
+    const int at = page_of(c, (int)pos);
+    const Slot s = slot_of(c, c.table[b * c.table_stride + at], (int)pos - at * c.page_size);
     if (s.off < 0) return false;
     out->cache_off = s.off;
     out->exp_off = s.exp;

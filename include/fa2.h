@@ -457,7 +457,8 @@ fa2_status fa2_rope_backward(const void* dy, void* dx, const int32_t* positions,
  *   type       FA2_CACHE_SAME: rows of the call's 16-bit dtype.
  *              FA2_CACHE_E4M3: 8-bit floats (4 exponent, 3 fraction bits), and for each row a
  *              scale byte in k_exp, v_exp (uint8 [num_pages, n_kv_heads, page_size],
- *              contiguous): an element stands for code * 2^(byte - 127).
+ *              contiguous): an element stands for code * 2^(byte - 127), bytes 1 to 253
+ *              (fa2_kv_append writes 67 to 247; others have no meaning).
  *   head_dim   a multiple of 8 (E4M3: 16) up to 128; page_size, n_kv_heads, num_pages > 0,
  *              n_kv_heads <= 1024, pages_per_seq * page_size <= 2^30 (FA2_ERR_UNSUPPORTED).
  *

@@ -3,11 +3,13 @@
 // fa2_forward's formula for one query row a head: O = softmax(scale q K^T) V, LSE, over the
 // sequence's cached keys. Every key and value is read once for up to 16 query heads, 4 * 16
 // FLOPs for 4 bytes at most, so memory sets the pace and the products only have to keep up:
-// they run as warp-level 16 x 8 x 16 products on registers, whose 16 rows are the query heads
-// of one key-value head. (The 128-row products of the tensor memory path would want 128 rows
-// of queries, or the keys as rows and then the probabilities through shared memory.)
+// they run as warp-level 16 x 8 x 16 products on registers. Their 16 rows are keys in the
+// first (S^T = K Q^T) and columns of V in the second (O^T = V^T P^T), their 8 columns query
+// heads of one key-value head: K and V come out of shared memory as whole left operands, and
+// up to 8 heads cost no more than one. (The 128-row products of the tensor memory path would
+// want the probabilities back through shared memory for every tile.)
 //
-// Work: the keys of every (sequence, key-value head, 16 query heads) item are cut into blocks
+// Work: the keys of every (sequence, key-value head, 8 or 16 query heads) item are cut into blocks
 // of kKeys; all blocks of all items in a row are divided evenly over the CTAs, whatever the
 // lengths, and a CTA's blocks of one item over its warps, one by one. Each warp keeps its own
 // running maximum, sum and O, and its own ring of stages filled by asynchronous 16-byte copies
@@ -32,17 +34,18 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16;         // query heads per item
-constexpr int kMergeRows = 4;     // rows the warps add up at a time at the end of an item
 constexpr int kOver = 8;          // blocks an item counts beyond its own
-constexpr int kMaxCtas = 2 * 152; // CTAs of the first kernel (a fixed number: the split depends on the lengths alone)
 constexpr int kJoinWarps = 16;
 constexpr int kJoinRows = 4;      // rows a CTA of the second kernel joins
 constexpr float kRescale = 8.0f;  // the running maximum may lag by this much (base-2 units) before O is rescaled
 constexpr float kLn2 = 0.693147180559945309f;
 
-template <int D, bool kE4m3>
+// D: the head size's kernel; kTiles: query heads per item / 8.
+template <int D, bool kE4m3, int kTiles>
 struct Cfg {
+    static constexpr int kRows = 8 * kTiles;                // query heads per item
+    static constexpr int kPerSm = kTiles == 1 ? 3 : 2;      // CTAs an SM
+    static constexpr int kMaxCtas = 152 * kPerSm;           // a fixed number: the split depends on the lengths alone
     static constexpr int kRowBytes = kE4m3 ? D : 2 * D;
     static constexpr int kKeys = kRowBytes >= 256 ? 16 : (kRowBytes == 128 ? 32 : 64);  // keys per block: 8 KB of K and V
     static constexpr int kLooks = (kKeys + 31) / 32;        // keys a lane looks up per block
@@ -51,13 +54,13 @@ struct Cfg {
     static constexpr int kInfo = kE4m3 ? kKeys * 8 : 16;    // e4m3: a float2 per key; else the keys that count, as bits
     static constexpr int kStage = 2 * kTile + kInfo;
     static constexpr int kStages = 2;
-    static constexpr bool kQRegs = true;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kQ = kRows * D * 2;                // q as the first product takes it
-    static constexpr int kPitch = D + 8;                    // floats a row at the end of an item (no bank twice)
+    static constexpr int kMergeRows = 2;                    // rows the warps add up at a time at the end of an item
+    static constexpr int kPitch = kE4m3 ? D + 8 : D + 4;    // floats a row there (no bank twice)
     static constexpr int kMerge = kWarps * kMergeRows * kPitch * 4;
     static constexpr int kSmem = kRing + kQ + kMerge + kRows * 4;
-    static_assert(kSmem <= 112 * 1024, "two CTAs an SM");
+    static_assert(kSmem + 1024 + 256 <= 228 * 1024 / kPerSm, "CTAs an SM");
 };
 
 // Position of chunk `c` of row `r` in a tile: the eight rows an ldmatrix reads at one chunk lie
@@ -84,6 +87,13 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+// The transpose of an 8 x 8 matrix of 16-bit elements, row g, columns 2t, 2t+1 in lane 4 g + t.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 template <bool kBf16>
@@ -134,7 +144,7 @@ __device__ __forceinline__ int units_of(int nb) { return nb ? nb + kOver : 0; }
 // Workspace: per CTA two partial results (its first item, if that began before it or ends after
 // it; its last item, if that ends after it), each [kRows][D] floats and then [kRows] (m, l);
 // behind all of them, per CTA, the item that begins in it and ends in a later CTA.
-template <int D>
+template <int D, int kRows>
 __device__ __forceinline__ float* partial(float* ws, int64_t cta, int which) {
     return ws + (cta * 2 + which) * (kRows * (D + 2));
 }
@@ -144,9 +154,9 @@ struct __align__(16) Torn {
     int which;     // the first CTA's partial result
     int out_row;   // row of O and LSE
 };
-template <int D>
+template <typename C, int D>
 __device__ __forceinline__ Torn* torn(float* ws, int64_t cta) {
-    return reinterpret_cast<Torn*>(partial<D>(ws, kMaxCtas, 0)) + cta;
+    return reinterpret_cast<Torn*>(partial<D, C::kRows>(ws, C::kMaxCtas, 0)) + cta;
 }
 
 // Inclusive sums over the CTA's threads in order, and the total of all. `scratch`: kWarps int64,
@@ -185,11 +195,11 @@ struct Segment {
     int item, k0, k1;
 };
 
-template <int D, bool kBf16, bool kE4m3>
-__global__ void __launch_bounds__(kThreads, 2) fa2_decode_kernel(const DecodeParams p) {
-    using C = Cfg<D, kE4m3>;
+template <int D, bool kBf16, bool kE4m3, int kTiles>
+__global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_decode_kernel(const DecodeParams p) {
+    using C = Cfg<D, kE4m3, kTiles>;
     constexpr bool kMmaBf16 = kBf16 && !kE4m3;
-    constexpr int kKeys = C::kKeys, S = C::kStages, kNt = kKeys / 8;
+    constexpr int kKeys = C::kKeys, S = C::kStages, kRows = C::kRows, kMt = kKeys / 16;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int64_t scratch[2][kWarps];
     __shared__ int64_t start_seq;
@@ -245,7 +255,7 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_decode_kernel(const DecodePar
         for (int i = threadIdx.x; i < p.heads; i += kThreads) p.lse[row0 + i] = -INFINITY;
     }
     if (!working) {
-        if (threadIdx.x == 0) torn<D>(p.workspace, blockIdx.x)->rows = 0;
+        if (threadIdx.x == 0) torn<C, D>(p.workspace, blockIdx.x)->rows = 0;
         return;
     }
     __syncthreads();
@@ -387,8 +397,8 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_decode_kernel(const DecodePar
     uint8_t* q_smem = smem + C::kRing;
     float* merge = reinterpret_cast<float*>(smem + C::kRing + C::kQ);
     float* q_scale = reinterpret_cast<float*>(smem + C::kRing + C::kQ + C::kMerge);
-    const uint32_t q_addr = smem_u32(q_smem), q_off = swizzle<D / 8>((lane & 7) + ((lane >> 3) & 1) * 8, lane >> 4) * 16;
-    const int g = lane >> 2, t = lane & 3;  // row (head) and column group in the products' fragments
+    const uint32_t q_addr = smem_u32(q_smem);
+    const int g = lane >> 2, t = lane & 3;  // row and column group in the products' fragments
     int number = 0, use = 0;                // the segment's number, the stage to use next
     bool first_item = true;
     Torn ends_later{0, 0, 0, 0};
@@ -398,9 +408,9 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_decode_kernel(const DecodePar
         const int head0 = hk * group + hb * kRows;        // first query head
         const int rows = min(kRows, group - hb * kRows);  // query heads of the item
 
-        // ---- q into shared memory: thread (row, 16 elements)
-        if (threadIdx.x < D) {
-            constexpr int kParts = D / 16;
+        // ---- q into shared memory: thread (row, 16 elements), in whole warps (they exchange)
+        constexpr int kParts = D / 16;
+        if (threadIdx.x < (kRows * kParts + 31) / 32 * 32) {
             const int r = threadIdx.x / kParts, part = threadIdx.x % kParts;
             const uint16_t* src = static_cast<const uint16_t*>(p.q) + seg.b * p.q_batch + (int64_t)(head0 + r) * p.q_head + 16 * part;
             const uint4 zero = make_uint4(0, 0, 0, 0);
@@ -426,23 +436,43 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_decode_kernel(const DecodePar
                     w[i] = pack2<false>(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
             }
             // 8-bit cache: elements 4t .. 4t+3 of 16 as columns 2t, 2t+1, 2t+8, 2t+9, the order its codes come in
-            uint4* row = reinterpret_cast<uint4*>(q_smem);
-            row[swizzle<D / 8>(r, 2 * part)] = kE4m3 ? make_uint4(w[0], w[2], w[4], w[6]) : make_uint4(w[0], w[1], w[2], w[3]);
-            row[swizzle<D / 8>(r, 2 * part + 1)] = kE4m3 ? make_uint4(w[1], w[3], w[5], w[7]) : make_uint4(w[4], w[5], w[6], w[7]);
-            if (part == 0) q_scale[r] = scale;
+            if (r < kRows) {
+                uint4* row = reinterpret_cast<uint4*>(q_smem);
+                row[swizzle<D / 8>(r, 2 * part)] = kE4m3 ? make_uint4(w[0], w[2], w[4], w[6]) : make_uint4(w[0], w[1], w[2], w[3]);
+                row[swizzle<D / 8>(r, 2 * part + 1)] = kE4m3 ? make_uint4(w[1], w[3], w[5], w[7]) : make_uint4(w[4], w[5], w[6], w[7]);
+                if (part == 0) q_scale[r] = scale;
+            }
         }
         __syncthreads();
-        const float qscale[2] = {q_scale[g], q_scale[g + 8]};
-        uint32_t qf[C::kQRegs ? D / 16 : 1][4];
-        if constexpr (C::kQRegs) {
+        // q as the first product's right operand: head g (+ 8), elements 2t, 2t+1 (and + 8) of 16
+        uint32_t qf[kTiles][D / 16][2];
+        float qscale[kTiles][2];
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) ldsm4(q_addr + (q_off ^ (uint32_t)(2 * kk * 16)), qf[kk]);
+        for (int h = 0; h < kTiles; ++h) {
+#pragma unroll
+            for (int kk = 0; kk < D / 16; kk += 2) {
+                uint32_t q4[4];
+                ldsm4(q_addr + swizzle<D / 8>(8 * h + (lane & 7), 2 * kk + (lane >> 3)) * 16, q4);
+                qf[h][kk][0] = q4[0];
+                qf[h][kk][1] = q4[1];
+                qf[h][kk + 1][0] = q4[2];
+                qf[h][kk + 1][1] = q4[3];
+            }
+            qscale[h][0] = q_scale[8 * h + 2 * t];
+            qscale[h][1] = q_scale[8 * h + 2 * t + 1];
         }
 
-        float o[D / 8][4];
+        float o[D / 16][kTiles][4];
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) o[i][0] = o[i][1] = o[i][2] = o[i][3] = 0.f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+            for (int h = 0; h < kTiles; ++h) o[i][h][0] = o[i][h][1] = o[i][h][2] = o[i][h][3] = 0.f;
+        float m[kTiles][2], l[kTiles][2];  // of heads 2t, 2t+1 (+ 8); l over this lane's keys
+#pragma unroll
+        for (int h = 0; h < kTiles; ++h) {
+            m[h][0] = m[h][1] = -INFINITY;
+            l[h][0] = l[h][1] = 0.f;
+        }
 
         for (int i = count(seg, number); i > 0; --i) {
             cp_async_wait<S - 2>();
@@ -453,143 +483,142 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_decode_kernel(const DecodePar
             const uint32_t kt = my_addr + use * C::kStage, vt = kt + C::kTile;
             const uint8_t* info = my + use * C::kStage + 2 * C::kTile;
             use = use + 1 == S ? 0 : use + 1;
-            // ---- scores: kNt column tiles of 8 keys
-            float sc[kNt][4];
+            // ---- scores, 16 keys at a time: keys g, g + 8 x heads 2t, 2t+1
+            float sc[kMt][kTiles][4];
 #pragma unroll
-            for (int j = 0; j < kNt; ++j) sc[j][0] = sc[j][1] = sc[j][2] = sc[j][3] = 0.f;
-            const int kr = (lane & 7) + (lane & 16 ? 8 : 0);
+            for (int j = 0; j < kMt; ++j)
 #pragma unroll
-            for (int kk = 0; kk < D / 16; kk += 2) {
-                uint32_t qa[2][4];
+                for (int h = 0; h < kTiles; ++h) sc[j][h][0] = sc[j][h][1] = sc[j][h][2] = sc[j][h][3] = 0.f;
+            if constexpr (!kE4m3) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if constexpr (C::kQRegs) {
+                for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) qa[h][i] = qf[kk + h][i];
-                    } else {  // the swizzle's exclusive or commutes with the constant chunk offset
-                        ldsm4(q_addr + (q_off ^ (uint32_t)(2 * (kk + h) * 16)), qa[h]);
+                    for (int j = 0; j < kMt; ++j) {
+                        uint32_t k4[4];  // (keys 0-7, 8-15) of d 0-7, of d 8-15 of this step
+                        ldsm4(kt + swizzle<C::kChunks>(16 * j + (lane & 15), 2 * kk + (lane >> 4)) * 16, k4);
+#pragma unroll
+                        for (int h = 0; h < kTiles; ++h) mma16816<kMmaBf16>(sc[j][h], k4, qf[h][kk][0], qf[h][kk][1]);
                     }
-                }
-#pragma unroll
-                for (int j = 0; j < kNt; j += 2) {
-                    if constexpr (!kE4m3) {
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t k4[4];  // (keys 0-7, 8-15) x (d 0-7, 8-15 of this step)
-                            ldsm4(kt + swizzle<C::kChunks>(8 * j + kr, 2 * (kk + h) + ((lane >> 3) & 1)) * 16, k4);
-                            mma16816<kMmaBf16>(sc[j], qa[h], k4[0], k4[1]);
-                            mma16816<kMmaBf16>(sc[j + 1], qa[h], k4[2], k4[3]);
-                        }
-                    } else {
-                        uint32_t k4[4];  // (keys 0-7, 8-15) x (16 codes, next 16 codes)
-                        ldsm4(kt + swizzle<C::kChunks>(8 * j + kr, kk + ((lane >> 3) & 1)) * 16, k4);
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t b0, b1, b2, b3;
-                            e4m3x4_to_f16x4(k4[h], b0, b1);
-                            e4m3x4_to_f16x4(k4[2 + h], b2, b3);
-                            mma16816<false>(sc[j], qa[h], b0, b1);
-                            mma16816<false>(sc[j + 1], qa[h], b2, b3);
-                        }
-                    }
-                }
-            }
-            // ---- x, the running maximum, P
-            float mx[2] = {-INFINITY, -INFINITY};
-            float rv[kNt][2];
-            if constexpr (kE4m3) {
-#pragma unroll
-                for (int j = 0; j < kNt; ++j) {
-                    const float4 f = reinterpret_cast<const float4*>(info)[4 * j + t];  // keys 8 j + 2 t, + 1
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const float ks = e ? f.z : f.x, ex = e ? f.w : f.y;
-                        // 2^-ex out of the low bits of 1.5 2^23 + 127 - ex; masked: 0
-                        rv[j][e] = __uint_as_float(__float_as_uint(12583039.f - ex) << 23);
-                        sc[j][e] = fmaf(sc[j][e] * ks, qscale[0], ex);
-                        sc[j][2 + e] = fmaf(sc[j][2 + e] * ks, qscale[1], ex);
-                    }
-                }
             } else {
 #pragma unroll
-                for (int j = 0; j < kNt; ++j)
+                for (int kk = 0; kk < D / 16; kk += 2)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) sc[j][e] *= qscale[0];
+                    for (int j = 0; j < kMt; ++j) {
+                        uint32_t k4[4];  // (keys 0-7, 8-15) of 16 codes, of the next 16: codes 4t .. 4t+3
+                        ldsm4(kt + swizzle<C::kChunks>(16 * j + (lane & 15), kk + (lane >> 4)) * 16, k4);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t a4[4];
+                            e4m3x4_to_f16x4(k4[2 * e], a4[0], a4[2]);
+                            e4m3x4_to_f16x4(k4[2 * e + 1], a4[1], a4[3]);
+#pragma unroll
+                            for (int h = 0; h < kTiles; ++h) mma16816<false>(sc[j][h], a4, qf[h][kk + e][0], qf[h][kk + e][1]);
+                        }
+                    }
+            }
+            // ---- x, the running maximum, P
+            float rv[kMt][2];  // of keys g, g + 8: 2^-(value scale's exponent)
+            if constexpr (kE4m3) {
+#pragma unroll
+                for (int j = 0; j < kMt; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 f = reinterpret_cast<const float2*>(info)[16 * j + 8 * e + g];
+                        // 2^-f.y out of the low bits of 1.5 2^23 + 127 - f.y; masked: 0
+                        rv[j][e] = __uint_as_float(__float_as_uint(12583039.f - f.y) << 23);
+#pragma unroll
+                        for (int h = 0; h < kTiles; ++h)
+#pragma unroll
+                            for (int n = 0; n < 2; ++n) sc[j][h][2 * e + n] = fmaf(sc[j][h][2 * e + n] * f.x, qscale[h][n], f.y);
+                    }
+            } else {
+#pragma unroll
+                for (int j = 0; j < kMt; ++j)
+#pragma unroll
+                    for (int h = 0; h < kTiles; ++h)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) sc[j][h][e] *= qscale[0][0];
 #pragma unroll
                 for (int w = 0; w < C::kLooks; ++w) {
                     const uint32_t counts = reinterpret_cast<const uint32_t*>(info)[w];
                     if (counts != 0xffffffffu) {
 #pragma unroll
-                        for (int j = 4 * w; j < kNt && j < 4 * w + 4; ++j)
+                        for (int j = 2 * w; j < kMt && j < 2 * w + 2; ++j)
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
-                                if (!((counts >> (8 * j + 2 * t + e - 32 * w)) & 1u)) sc[j][e] = sc[j][2 + e] = -INFINITY;
+                                if (!((counts >> (16 * (j - 2 * w) + 8 * e + g)) & 1u)) {
+#pragma unroll
+                                    for (int h = 0; h < kTiles; ++h) sc[j][h][2 * e] = sc[j][h][2 * e + 1] = -INFINITY;
+                                }
                     }
                 }
             }
-#pragma unroll
-            for (int j = 0; j < kNt; ++j) {
-                mx[0] = fmaxf(mx[0], fmaxf(sc[j][0], sc[j][1]));
-                mx[1] = fmaxf(mx[1], fmaxf(sc[j][2], sc[j][3]));
-            }
+            float mx[kTiles][2];
             bool grow = false;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-                mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
-                grow |= mx[h] > m[h] + kRescale || (m[h] == -INFINITY && mx[h] > -INFINITY);
-            }
+            for (int h = 0; h < kTiles; ++h)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    mx[h][n] = fmaxf(sc[0][h][n], sc[0][h][2 + n]);
+#pragma unroll
+                    for (int j = 1; j < kMt; ++j) mx[h][n] = fmax3(mx[h][n], sc[j][h][n], sc[j][h][2 + n]);
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1) mx[h][n] = fmaxf(mx[h][n], __shfl_xor_sync(0xffffffffu, mx[h][n], off));
+                    grow |= mx[h][n] > m[h][n] + kRescale || (m[h][n] == -INFINITY && mx[h][n] > -INFINITY);
+                }
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const float m_new = fmaxf(m[h], mx[h]);
-                    const float f = m_new == -INFINITY ? 1.f : ex2_approx(m[h] - m_new);
-                    m[h] = m_new;
-                    l[h] *= f;
+                for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-                    for (int n = 0; n < D / 8; ++n) {
-                        o[n][2 * h] *= f;
-                        o[n][2 * h + 1] *= f;
+                    for (int n = 0; n < 2; ++n) {
+                        const float m_new = fmaxf(m[h][n], mx[h][n]);
+                        const float f = m_new == -INFINITY ? 1.f : ex2_approx(m[h][n] - m_new);
+                        m[h][n] = m_new;
+                        l[h][n] *= f;
+#pragma unroll
+                        for (int d = 0; d < D / 16; ++d) {
+                            o[d][h][n] *= f;
+                            o[d][h][2 + n] *= f;
+                        }
                     }
-                }
             }
-            const float ref[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
 #pragma unroll
-            for (int kt2 = 0; kt2 < kKeys / 16; ++kt2) {
-                uint32_t pf[4];
+            for (int j = 0; j < kMt; ++j) {
+                uint32_t pf[kTiles][2];  // P as the right operand: keys 2t, 2t+1 (and + 8) x head g
 #pragma unroll
-                for (int jj = 0; jj < 2; ++jj) {
-                    const int j = 2 * kt2 + jj;
+                for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        sc[j][e] = ex2_approx(sc[j][e] - ref[e >> 1]);
-                        l[e >> 1] += kE4m3 ? sc[j][e] * rv[j][e & 1] : sc[j][e];
+                    for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            float& x = sc[j][h][2 * e + n];
+                            x = ex2_approx(x - (m[h][n] == -INFINITY ? 0.f : m[h][n]));
+                            l[h][n] += kE4m3 ? x * rv[j][e] : x;
+                        }
+                        pf[h][e] = transpose8(pack2<kMmaBf16>(sc[j][h][2 * e], sc[j][h][2 * e + 1]));
                     }
-                    pf[2 * jj] = pack2<kMmaBf16>(sc[j][0], sc[j][1]);
-                    pf[2 * jj + 1] = pack2<kMmaBf16>(sc[j][2], sc[j][3]);
-                }
-                // ---- O += P V
-                const int r = 16 * kt2 + (lane & 15);
+                // ---- O^T += V^T P^T
                 if constexpr (!kE4m3) {
+                    const int r = 16 * j + (lane & 7) + (lane & 16 ? 8 : 0);
 #pragma unroll
-                    for (int n = 0; n < D / 8; n += 2) {
-                        uint32_t v4[4];  // (keys 0-7, 8-15) of chunk n, of chunk n + 1
-                        ldsm4_t(vt + swizzle<C::kChunks>(r, n + (lane >> 4)) * 16, v4);
-                        mma16816<kMmaBf16>(o[n], pf, v4[0], v4[1]);
-                        mma16816<kMmaBf16>(o[n + 1], pf, v4[2], v4[3]);
+                    for (int d = 0; d < D / 16; ++d) {
+                        uint32_t v4[4];  // keys 0-7 of (d 0-7, 8-15 of this tile), then keys 8-15
+                        ldsm4_t(vt + swizzle<C::kChunks>(r, 2 * d + ((lane >> 3) & 1)) * 16, v4);
+#pragma unroll
+                        for (int h = 0; h < kTiles; ++h) mma16816<kMmaBf16>(o[d][h], v4, pf[h][0], pf[h][1]);
                     }
                 } else {
 #pragma unroll
-                    for (int n = 0; n < D / 16; n += 2) {
-                        uint32_t v4[4];  // 16-code chunks n, n + 1: keys 2t, 2t+1 (and + 8) x codes 2g, 2g+1
-                        ldsm4_t(vt + swizzle<C::kChunks>(r, n + (lane >> 4)) * 16, v4);
+                    for (int d = 0; d < D / 16; d += 2) {
+                        uint32_t v4[4];  // (keys 0-7, 8-15) of 16 codes, of the next 16: keys 2t, 2t+1 x codes 2g, 2g+1
+                        ldsm4_t(vt + swizzle<C::kChunks>(16 * j + (lane & 15), d + (lane >> 4)) * 16, v4);
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t b0, b1, b2, b3;  // keys 2t, 2t+1 of the even, of the odd code; keys + 8
-                            e4m3x4_to_f16x4(__byte_perm(v4[2 * h], 0, 0x3120), b0, b2);
-                            e4m3x4_to_f16x4(__byte_perm(v4[2 * h + 1], 0, 0x3120), b1, b3);
-                            mma16816<false>(o[2 * (n + h)], pf, b0, b1);
-                            mma16816<false>(o[2 * (n + h) + 1], pf, b2, b3);
+                        for (int e = 0; e < 2; ++e) {
+                            uint32_t a4[4];  // rows g: the even codes, rows g + 8: the odd ones
+                            e4m3x4_to_f16x4(__byte_perm(v4[2 * e], 0, 0x3120), a4[0], a4[1]);
+                            e4m3x4_to_f16x4(__byte_perm(v4[2 * e + 1], 0, 0x3120), a4[2], a4[3]);
+#pragma unroll
+                            for (int h = 0; h < kTiles; ++h) mma16816<false>(o[d + e][h], a4, pf[h][0], pf[h][1]);
                         }
                     }
                 }
@@ -597,62 +626,65 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_decode_kernel(const DecodePar
             __syncwarp();  // the stage may be filled again
         }
 
-        // ---- the warps' results together, kMergeRows rows at a time: a warp per row, a lane per D / 32 columns
+        // ---- the warps' results together, kMergeRows rows at a time: kWarps / kMergeRows warps per row
         const bool whole = seg.k0 == 0 && seg.k1 == seg.nb;
         const int which = first_item ? 0 : 1;
         const int64_t out_row = (int64_t)seg.b * p.heads + head0;
         if (seg.k0 == 0 && !whole) ends_later = {rows, (int)split.owner(seg.next - 1), which, (int)out_row};
-        float* part = partial<D>(p.workspace, blockIdx.x, which);
+        float* part = partial<D, kRows>(p.workspace, blockIdx.x, which);
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
-            l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
-        }
+        for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-        for (int round = 0; round < kRows / kMergeRows; ++round) {
-            if (round * kMergeRows >= rows) break;
-            const int h = round / 2;
-            if (g / kMergeRows == round % 2) {
-                float* row = merge + (warp * kMergeRows + g % kMergeRows) * C::kPitch;
+            for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int n = 0; n < D / 8; n += 2) {
-                    if constexpr (!kE4m3) {  // columns 8 n + 2 t, + 1
-                        *reinterpret_cast<float2*>(row + 8 * n + 2 * t) = make_float2(o[n][2 * h], o[n][2 * h + 1]);
-                        *reinterpret_cast<float2*>(row + 8 * n + 8 + 2 * t) = make_float2(o[n + 1][2 * h], o[n + 1][2 * h + 1]);
-                    } else {  // tiles n, n + 1 hold the even and odd codes of a chunk: columns 8 n + 4 t .. + 3
-                        *reinterpret_cast<float4*>(row + 8 * n + 4 * t) =
-                            make_float4(o[n][2 * h], o[n + 1][2 * h], o[n][2 * h + 1], o[n + 1][2 * h + 1]);
+                for (int off = 4; off < 32; off <<= 1) l[h][n] += __shfl_xor_sync(0xffffffffu, l[h][n], off);
+#pragma unroll
+        for (int round = 0; round < kRows / 2; ++round) {  // rows 2 round, 2 round + 1: the heads of the lanes t = round % 4
+            if (2 * round >= rows) break;
+            const int h = round / 4;
+            if (t == round % 4) {
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    float* row = merge + (warp * 2 + n) * C::kPitch;
+#pragma unroll
+                    for (int d = 0; d < D / 16; ++d) {
+                        if constexpr (!kE4m3) {
+                            row[16 * d + g] = o[d][h][n];
+                            row[16 * d + 8 + g] = o[d][h][2 + n];
+                        } else {
+                            *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[d][h][n], o[d][h][2 + n]);
+                        }
                     }
+                    if (g == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[h][n], l[h][n]);
                 }
-                if (t == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[h], l[h]);
             }
             __syncthreads();
-            const int r = round * kMergeRows + warp;
+            constexpr int kShare = kWarps / 2;  // warps per row
+            const int n = warp / kShare, r = 2 * round + n;
             if (r < rows) {
-                constexpr int kCols = D / 32;
                 float big = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) big = fmaxf(big, merge[(w * kMergeRows + warp) * C::kPitch + D]);
+                for (int w = 0; w < kWarps; ++w) big = fmaxf(big, merge[(w * 2 + n) * C::kPitch + D]);
                 const float from = big == -INFINITY ? 0.f : big;
-                float a[kCols] = {}, sum = 0.f;
+                float f[kWarps], sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float* row = merge + (w * kMergeRows + warp) * C::kPitch;
-                    const float f = ex2_approx(row[D] - from);
-                    sum += f * row[D + 1];
-#pragma unroll
-                    for (int i = 0; i < kCols; ++i) a[i] += f * row[lane + 32 * i];
+                    const float* row = merge + (w * 2 + n) * C::kPitch;
+                    f[w] = ex2_approx(row[D] - from);
+                    sum += f[w] * row[D + 1];
                 }
-                if (whole) {
-                    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+                const float inv = !whole ? 1.f : (sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum));
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i)
-                        if (lane + 32 * i < c.d) put<kBf16>(p.o, (out_row + r) * c.d + lane + 32 * i, a[i] * inv);
-                    if (lane == 0) p.lse[out_row + r] = sum == 0.f ? -INFINITY : (big + lg2_approx(sum)) * kLn2;
-                } else {
+                for (int d = lane + 32 * (warp % kShare); d < D; d += 32 * kShare) {
+                    float a = 0.f;
 #pragma unroll
-                    for (int i = 0; i < kCols; ++i) part[r * D + lane + 32 * i] = a[i];
-                    if (lane == 0) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(big, sum);
+                    for (int w = 0; w < kWarps; ++w) a += f[w] * merge[(w * 2 + n) * C::kPitch + d];
+                    if (!whole) part[r * D + d] = a;
+                    else if (d < c.d) put<kBf16>(p.o, (out_row + r) * c.d + d, a * inv);
+                }
+                if (lane == 0 && warp % kShare == 0) {
+                    if (!whole) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(big, sum);
+                    else p.lse[out_row + r] = sum == 0.f ? -INFINITY : (big + lg2_approx(sum)) * kLn2;
                 }
             }
             __syncthreads();
@@ -661,14 +693,15 @@ __global__ void __launch_bounds__(kThreads, 2) fa2_decode_kernel(const DecodePar
         live = seek(seg, seg.next);
     }
     cp_async_wait<0>();
-    if (threadIdx.x == 0) *torn<D>(p.workspace, blockIdx.x) = ends_later;
+    if (threadIdx.x == 0) *torn<C, D>(p.workspace, blockIdx.x) = ends_later;
 }
 
 // Joins the items that several CTAs worked on: CTA (x, y) rows kJoinRows y .. of the item that
 // began in CTA x, if it ended in a later one. A quarter of the warps for each row, a warp for
 // every fourth partial result, its lanes for the columns.
-template <int D, bool kBf16>
+template <int D, bool kBf16, typename C>
 __global__ void __launch_bounds__(kJoinWarps * 32) fa2_decode_join_kernel(const DecodeParams p) {
+    constexpr int kRows = C::kRows;
     constexpr int kShare = kJoinWarps / kJoinRows;  // warps per row
     constexpr int kCols = D / 32;                   // columns a lane
     __shared__ float parts[kJoinWarps][D + 1];
@@ -676,11 +709,11 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa2_decode_join_kernel(const 
     const int share = warp % kShare, r = blockIdx.y * kJoinRows + warp / kShare;
     // launched while the first kernel still runs: everything it wrote is here after this wait
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    const Torn item = *torn<D>(p.workspace, blockIdx.x);
+    const Torn item = *torn<C, D>(p.workspace, blockIdx.x);
     if ((int)blockIdx.y * kJoinRows >= item.rows) return;
     const int first = blockIdx.x, n = item.last_cta - first + 1;
     const bool on = r < item.rows;
-    auto part = [&](int k) { return partial<D>(p.workspace, first + k, k == 0 ? item.which : 0); };
+    auto part = [&](int k) { return partial<D, kRows>(p.workspace, first + k, k == 0 ? item.which : 0); };
     float big = -INFINITY, sum = 0.f, a[kCols] = {};
     if (on) {
         for (int k = lane; k < n; k += 32) big = fmaxf(big, part(k)[kRows * D + 2 * r]);
@@ -718,18 +751,18 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa2_decode_join_kernel(const 
     if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (big + lg2_approx(sum)) * kLn2;
 }
 
-template <int D, bool kBf16, bool kE4m3>
+template <int D, bool kBf16, bool kE4m3, int kTiles>
 cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
-    using C = Cfg<D, kE4m3>;
-    auto kern = fa2_decode_kernel<D, kBf16, kE4m3>;
+    using C = Cfg<D, kE4m3, kTiles>;
+    auto kern = fa2_decode_kernel<D, kBf16, kE4m3, kTiles>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, slot);
     if (e != cudaSuccess) return e;
-    kern<<<kMaxCtas, kThreads, C::kSmem, stream>>>(p);
+    kern<<<C::kMaxCtas, kThreads, C::kSmem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    const int rows = std::min(kRows, p.heads / p.c.hkv);
+    const int rows = std::min(C::kRows, p.heads / p.c.hkv);
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(kMaxCtas, (unsigned)((rows + kJoinRows - 1) / kJoinRows), 1);
+    cfg.gridDim = dim3(C::kMaxCtas, (unsigned)((rows + kJoinRows - 1) / kJoinRows), 1);
     cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
@@ -737,27 +770,44 @@ cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa2_decode_join_kernel<D, kBf16>, p);
+    return cudaLaunchKernelEx(&cfg, fa2_decode_join_kernel<D, kBf16, C>, p);
+}
+
+// Up to 8 query heads a key-value head: one column tile, else two.
+template <int D, bool kBf16, bool kE4m3>
+cudaError_t launch_tiles(const DecodeParams& p, cudaStream_t stream, int slot) {
+    return p.heads / p.c.hkv <= 8 ? launch_d<D, kBf16, kE4m3, 1>(p, stream, slot) : launch_d<D, kBf16, kE4m3, 2>(p, stream, slot + 1);
 }
 
 template <int D>
 cudaError_t launch_kind(const DecodeParams& p, cudaStream_t stream, int slot) {
     const bool bf = p.c.dtype == kBf16;
-    if (p.c.e4m3) return bf ? launch_d<D, true, true>(p, stream, slot) : launch_d<D, false, true>(p, stream, slot + 1);
-    return bf ? launch_d<D, true, false>(p, stream, slot + 2) : launch_d<D, false, false>(p, stream, slot + 3);
+    if (p.c.e4m3) return bf ? launch_tiles<D, true, true>(p, stream, slot) : launch_tiles<D, false, true>(p, stream, slot + 2);
+    return bf ? launch_tiles<D, true, false>(p, stream, slot + 4) : launch_tiles<D, false, false>(p, stream, slot + 6);
+}
+
+template <int D, int kTiles>
+size_t workspace_for() {
+    using C = Cfg<D, false, kTiles>;
+    return (size_t)C::kMaxCtas * (2 * C::kRows * (D + 2) * sizeof(float) + sizeof(Torn));
 }
 
 }  // namespace
 
-size_t decode_workspace_bytes(int, int, int d) {
-    return (size_t)kMaxCtas * (2 * kRows * (pad_head_dim(d) + 2) * sizeof(float) + sizeof(Torn));
+size_t decode_workspace_bytes(int heads, int hkv, int d) {
+    const bool one = heads / hkv <= 8;
+    switch (pad_head_dim(d)) {
+        case 32: return one ? workspace_for<32, 1>() : workspace_for<32, 2>();
+        case 64: return one ? workspace_for<64, 1>() : workspace_for<64, 2>();
+        default: return one ? workspace_for<128, 1>() : workspace_for<128, 2>();
+    }
 }
 
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
     switch (pad_head_dim(p.c.d)) {
         case 32: return launch_kind<32>(p, stream, 52);
-        case 64: return launch_kind<64>(p, stream, 56);
-        default: return launch_kind<128>(p, stream, 60);
+        case 64: return launch_kind<64>(p, stream, 60);
+        default: return launch_kind<128>(p, stream, 68);
     }
 }
 

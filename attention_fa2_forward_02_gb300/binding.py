@@ -5,13 +5,13 @@ on the GPU, checks shapes / dtypes / contiguity, and passes raw device pointers,
 sizes and the current CUDA stream to the library function of the same name.
 Every step of the computation runs in the library's CUDA kernels.  If the
 shared library has not been built, the first call raises :class:`Fa2Error`;
-there is no fallback.
+there is no fallback.  The calls of a decoding step marshal their arguments in
+a small CPython extension instead of ctypes (see the end of this file).
 """
 from __future__ import annotations
 
 import ctypes
 import os
-import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_NAME = "libfa2_gb300.so"
@@ -183,7 +183,7 @@ def _require_f32(where, **tensors):
             raise TypeError(f"{where}: {name} must be float32, got {t.dtype}")
 
 
-def _on_current_device(t, name):
+def _dev(t, name, ndim=None):
     if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     import torch
@@ -191,10 +191,6 @@ def _on_current_device(t, name):
     if t.device.index != current:
         # the library launches on the current device; another device's memory is not its to read
         raise ValueError(f"{name} is on {t.device}, but the current device is cuda:{current}")
-
-
-def _dev(t, name, ndim=None):
-    _on_current_device(t, name)
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     if ndim is not None and t.dim() != ndim:
@@ -419,66 +415,28 @@ def fa2_watchdog_selftest(stream=None) -> None:
 
 # ---------------------------------------------------------------------------- rotary positions and the paged cache
 #
-# A decoding step makes these calls on tensors so small that the host's work sets the pace, so the arguments are
-# marshalled with few Python operations: pointers as plain integers, structures and stride arrays packed into bytes.
+# A decoding step makes these calls on tensors so small that the host's work sets the pace: the extension _fa2_torch
+# (csrc/torch_args.cpp) checks the tensors' devices, shapes, types and strides and calls the library.
 
 CACHE_SAME, CACHE_E4M3 = 0, 1
 ROPE_SCALINGS = ("plain", "linear", "base", "turns", "ramp")  # fa2_rope_scaling's values in order
-_pack_cache = struct.Struct("@4Q4q3ii").pack  # fa2_kv_cache
-_pack2, _pack3 = struct.Struct("@2q").pack, struct.Struct("@3q").pack
-_torch_codes = {}
+_ext = None
 
 
-def _row_code(t):
-    """The library's code of a tensor's type."""
-    try:
-        return _torch_codes[t.dtype]
-    except KeyError:
-        _torch_codes[t.dtype] = _dtype_code(t)  # refuses others
-        return _torch_codes[t.dtype]
-
-
-def _refuse_device(name, t):
-    _on_current_device(t, name)
-    raise ValueError(f"{name} is not on the current device")
-
-
-def _at(t, name, device):
-    """Pointer of a contiguous tensor."""
-    if t.get_device() != device:
-        _refuse_device(name, t)
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
-
-
-def _rows_at(t, name, device, shape, strides):
-    """Pointer of a tensor whose last dimension is contiguous; the library takes its other strides."""
-    if t.get_device() != device:
-        _refuse_device(name, t)
-    if strides[-1] != 1 and shape[-1] > 1:
-        raise ValueError(f"{name}'s last dimension must be contiguous")
-    return t.data_ptr()
-
-
-def _same_strides(shape, a, b):
-    """Whether two stride tuples agree (the stride of a dimension of one element means nothing)."""
-    return a == b or all(x == y or n <= 1 for n, x, y in zip(shape, a, b))
-
-
-def _require_dtype(where, dtype, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.dtype != dtype:
-            raise TypeError(f"{where}: {name} must be {dtype}, got {t.dtype}")
-
-
-def _now(t, stream):
-    """(current device, raw stream) of a call on `t`: the given stream, or torch's current one."""
-    import torch
-    if not t.is_cuda:
-        _refuse_device("every tensor", t)
-    device = torch.cuda.current_device()
-    return device, torch._C._cuda_getCurrentRawStream(device) if stream is None else stream.cuda_stream
+def _extension():
+    """The built extension, given the library's entry points (once)."""
+    global _ext
+    if _ext is None:
+        import torch  # noqa: F401  (its libraries, which the extension uses)
+        lib = library()
+        try:
+            from . import _fa2_torch
+        except ImportError as e:
+            raise Fa2Error(-1, f"_fa2_torch: {e} (run __graft_entry__.build())") from e
+        _fa2_torch.set_entry_points(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
+            "fa2_rope", "fa2_rope_backward", "fa2_kv_append", "fa2_kv_read", "fa2_decode")))
+        _ext = _fa2_torch
+    return _ext
 
 
 def fa2_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "plain", factor: float = 1.0,
@@ -496,138 +454,35 @@ def fa2_rope_frequencies(rot_dim: int, base: float = 10000.0, scaling: str = "pl
     return inv_freq, float(magnitude.value)
 
 
-def _rope(where, x, y, inv_freq, positions, interleaved, magnitude, stream):
-    import torch
-    shape = x.shape
-    if len(shape) != 4 or y.shape != shape:
-        raise ValueError(f"{where}: the tensors are [B, H, N, d], both of one shape")
-    b, h, n, d = shape
-    if y.dtype != x.dtype:
-        _same_dtype(where, x, y=y)
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
-        raise TypeError(f"{where}: inv_freq must be float64 [rot_dim / 2], got {inv_freq.dtype} {tuple(inv_freq.shape)}")
-    position_stride, at = 0, None
-    if positions is not None:
-        if positions.dtype != torch.int32:
-            raise TypeError(f"{where}: positions must be int32, got {positions.dtype}")
-        given = positions.shape
-        if given != (b, n) and given != (n,) and given != (1, n):
-            raise ValueError(f"{where}: positions must be [N], [1, N] or [B, N], got {tuple(given)}")
-    device, raw = _now(x, stream)
-    if positions is not None:
-        steps = positions.stride()
-        at = _rows_at(positions, "positions", device, given, steps)
-        if len(given) == 2 and given[0] > 1:
-            position_stride = steps[0]
-    xs, ys = x.stride(), y.stride()
-    st = getattr(library(), where)(_rows_at(x, "x", device, shape, xs), _rows_at(y, "y", device, shape, ys), at, position_stride,
-                                   _at(inv_freq, "inv_freq", device), b, h, n, d, 2 * inv_freq.numel(), _pack3(*xs[:3]),
-                                   _pack3(*ys[:3]), 1 if interleaved else 0, magnitude, _row_code(x), raw)
-    if st:
-        _check(st, where)
-
-
 def fa2_rope(x, y, inv_freq, positions=None, interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
     """Rotary positions: x, y [B, H, N, d] (any strides, d contiguous; y may be x); inv_freq float64 [rot_dim / 2];
     positions int32 [B, N] or [N] (None: 0 .. N - 1)."""
-    _rope("fa2_rope", x, y, inv_freq, positions, interleaved, magnitude, stream)
+    st = (_ext or _extension()).rope(x, y, inv_freq, positions, interleaved, magnitude, stream, False)
+    if st:
+        _check(st, "fa2_rope")
 
 
 def fa2_rope_backward(dy, dx, inv_freq, positions=None, interleaved: bool = False, magnitude: float = 1.0, stream=None) -> None:
     """Gradient of fa2_rope: dx from dy, the other arguments as for the forward call."""
-    _rope("fa2_rope_backward", dy, dx, inv_freq, positions, interleaved, magnitude, stream)
-
-
-def _cache_of(where, k_pages, v_pages, k_exp, v_exp, row_dtype, block_table, seq_lens):
-    """Checks two page pools [num_pages, n_kv_heads, page_size, d] (any strides, d contiguous), their scale bytes, the
-    block table and the lengths; (batch, n_kv_heads, d, pointers), where pointers(device) gives the packed fa2_kv_cache,
-    the table's pointer, row stride and pages per sequence, and the lengths' pointer."""
-    import torch
-    shape = k_pages.shape
-    if len(shape) != 4 or v_pages.shape != shape:
-        raise ValueError(f"{where}: k_pages and v_pages are [num_pages, n_kv_heads, page_size, d], both of one shape")
-    pages, heads, page_size, d = shape
-    strides, vs = k_pages.stride(), v_pages.stride()
-    if not _same_strides(shape, strides, vs):
-        raise ValueError(f"{where}: k_pages and v_pages must have the same strides")
-    kind = k_pages.dtype
-    if v_pages.dtype != kind:
-        _same_dtype(where, k_pages, v_pages=v_pages)
-    e4m3 = kind == torch.float8_e4m3fn
-    if e4m3:
-        if k_exp is None or v_exp is None:
-            raise ValueError(f"{where}: an e4m3 cache has scale bytes, k_exp and v_exp")
-        if k_exp.dtype != torch.uint8 or v_exp.dtype != torch.uint8:
-            _require_dtype(where, torch.uint8, k_exp=k_exp, v_exp=v_exp)
-        if k_exp.shape != shape[:3] or v_exp.shape != shape[:3]:
-            raise ValueError(f"{where}: k_exp and v_exp must be [num_pages, n_kv_heads, page_size]")
-    elif k_exp is not None or v_exp is not None:
-        raise ValueError(f"{where}: k_exp and v_exp belong to an e4m3 cache")
-    elif kind != row_dtype:
-        raise TypeError(f"{where}: the pages are {kind}, expected {row_dtype} or float8_e4m3fn")
-    if block_table.dtype != torch.int32 or seq_lens.dtype != torch.int32:
-        _require_dtype(where, torch.int32, block_table=block_table, seq_lens=seq_lens)
-    table_shape = block_table.shape
-    if len(table_shape) != 2 or seq_lens.shape != table_shape[:1]:
-        raise ValueError(f"{where}: block_table is [batch, pages_per_seq] and seq_lens [batch]")
-    batch, per_seq = table_shape
-
-    def pointers(device):
-        steps = block_table.stride()
-        return (_pack_cache(_rows_at(k_pages, "k_pages", device, shape, strides), _rows_at(v_pages, "v_pages", device, shape, vs),
-                            _at(k_exp, "k_exp", device) if e4m3 else 0, _at(v_exp, "v_exp", device) if e4m3 else 0,
-                            pages, *strides[:3], heads, page_size, d, CACHE_E4M3 if e4m3 else CACHE_SAME),
-                (_rows_at(block_table, "block_table", device, table_shape, steps), steps[0] if batch > 1 else per_seq, per_seq),
-                _at(seq_lens, "seq_lens", device))
-
-    return batch, heads, d, pointers
+    st = (_ext or _extension()).rope(dy, dx, inv_freq, positions, interleaved, magnitude, stream, True)
+    if st:
+        _check(st, "fa2_rope_backward")
 
 
 def fa2_kv_append(k_pages, v_pages, k, v, block_table, seq_lens, cu_new=None, k_exp=None, v_exp=None, stream=None) -> None:
-    """Write new keys and values k, v [tokens, n_kv_heads, d] into the pages [num_pages, n_kv_heads, page_size, d] (the
-    rows' dtype, or float8_e4m3fn with scale bytes k_exp, v_exp).  seq_lens counts the new tokens in; cu_new int32
-    [batch + 1] says which rows are whose (None: one a sequence)."""
-    import torch
-    where = "fa2_kv_append"
-    batch, heads, d, pointers = _cache_of(where, k_pages, v_pages, k_exp, v_exp, k.dtype, block_table, seq_lens)
-    shape = k.shape
-    if len(shape) != 3 or v.shape != shape or shape[1] != heads or shape[2] != d:
-        raise ValueError(f"{where}: k and v are [tokens, n_kv_heads, d]")
-    if v.dtype != k.dtype:
-        _same_dtype(where, k, v=v)
-    if cu_new is not None:
-        if cu_new.dtype != torch.int32:
-            _require_dtype(where, torch.int32, cu_new=cu_new)
-        if cu_new.shape != (batch + 1,):
-            raise ValueError(f"{where}: cu_new must be [batch + 1]")
-    device, raw = _now(k, stream)
-    cache, table, lens = pointers(device)
-    ks, vs = k.stride(), v.stride()
-    st = library().fa2_kv_append(cache, _rows_at(k, "k", device, shape, ks), _rows_at(v, "v", device, shape, vs), _pack2(*ks[:2]),
-                                 _pack2(*vs[:2]), *table, None if cu_new is None else _at(cu_new, "cu_new", device), lens, batch,
-                                 shape[0], _row_code(k), raw)
+    """Write new keys and values k, v [tokens, n_kv_heads, d] into the pages [num_pages, n_kv_heads, page_size, d] (any
+    strides, d contiguous; the rows' dtype, or float8_e4m3fn with scale bytes k_exp, v_exp).  seq_lens counts the new tokens
+    in; cu_new int32 [batch + 1] says which rows are whose (None: one a sequence)."""
+    st = (_ext or _extension()).kv_append(k_pages, v_pages, k, v, block_table, seq_lens, cu_new, k_exp, v_exp, stream)
     if st:
-        _check(st, where)
+        _check(st, "fa2_kv_append")
 
 
 def fa2_kv_read(k_pages, v_pages, k_out, v_out, block_table, seq_lens, k_exp=None, v_exp=None, stream=None) -> None:
     """Copy the cached rows out: k_out, v_out [batch, n_kv_heads, max_len, d]; positions past a sequence's length stay."""
-    where = "fa2_kv_read"
-    batch, heads, d, pointers = _cache_of(where, k_pages, v_pages, k_exp, v_exp, k_out.dtype, block_table, seq_lens)
-    shape = k_out.shape
-    if len(shape) != 4 or v_out.shape != shape or shape[0] != batch or shape[1] != heads or shape[3] != d:
-        raise ValueError(f"{where}: k_out and v_out are [batch, n_kv_heads, max_len, d]")
-    strides, vs = k_out.stride(), v_out.stride()
-    if not _same_strides(shape, strides, vs):
-        raise ValueError(f"{where}: k_out and v_out must have the same strides")
-    if v_out.dtype != k_out.dtype:
-        _same_dtype(where, k_out, v_out=v_out)
-    device, raw = _now(k_out, stream)
-    cache, table, lens = pointers(device)
-    st = library().fa2_kv_read(cache, _rows_at(k_out, "k_out", device, shape, strides), _rows_at(v_out, "v_out", device, shape, vs),
-                               _pack3(*strides[:3]), *table, lens, batch, shape[2], _row_code(k_out), raw)
+    st = (_ext or _extension()).kv_read(k_pages, v_pages, k_out, v_out, block_table, seq_lens, k_exp, v_exp, stream)
     if st:
-        _check(st, where)
+        _check(st, "fa2_kv_read")
 
 
 def fa2_decode_workspace_size(batch: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
@@ -638,19 +493,7 @@ def fa2_decode(q, k_pages, v_pages, o, lse, block_table, seq_lens, workspace, so
                k_exp=None, v_exp=None, stream=None) -> None:
     """Attention of one new token a sequence over the paged cache: q, o [batch, n_heads, d], lse [batch, n_heads]
     float32; workspace a CUDA uint8 tensor of fa2_decode_workspace_size bytes; window > 0: the last keys only."""
-    where = "fa2_decode"
-    batch, heads, d, pointers = _cache_of(where, k_pages, v_pages, k_exp, v_exp, q.dtype, block_table, seq_lens)
-    shape = q.shape
-    if len(shape) != 3 or shape[0] != batch or shape[2] != d or o.shape != shape or lse.shape != shape[:2]:
-        raise ValueError(f"{where}: q and o are [batch, n_heads, d], lse [batch, n_heads]")
-    if o.dtype != q.dtype:
-        _same_dtype(where, q, o=o)
-    _require_f32(where, lse=lse)
-    device, raw = _now(q, stream)
-    cache, table, lens = pointers(device)
-    qs = q.stride()
-    st = library().fa2_decode(_rows_at(q, "q", device, shape, qs), _pack2(*qs[:2]), cache, _at(o, "o", device), _at(lse, "lse", device),
-                              *table, lens, batch, shape[1], window, _at(workspace, "workspace", device),
-                              workspace.numel() * workspace.element_size(), _row_code(q), softmax_scale, raw)
+    st = (_ext or _extension()).decode(q, k_pages, v_pages, o, lse, block_table, seq_lens, workspace, softmax_scale, window, k_exp,
+                                       v_exp, stream)
     if st:
-        _check(st, where)
+        _check(st, "fa2_decode")

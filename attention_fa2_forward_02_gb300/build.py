@@ -2,17 +2,21 @@
 
 Each translation unit compiles in its own nvcc process (in parallel); the
 objects are linked into one shared library with the CUDA runtime linked
-statically.  A rebuild happens only when a source or header is newer than the
-library (or when ``force=True``).
+statically.  Beside it ``_fa2_torch.so``, the CPython extension that reads the
+serving calls' torch tensors (``csrc/torch_args.cpp``), is compiled with g++
+against the installed torch.  A rebuild happens only when a source or header is
+newer than the libraries (or when ``force=True``).
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import glob
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -20,6 +24,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(HERE, "libfa2_gb300.so")
+TORCH_LIB = os.path.join(HERE, "_fa2_torch.so")
+TORCH_SRC = os.path.join(CSRC, "torch_args.cpp")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC,
@@ -37,11 +43,27 @@ def sources():
     return sorted(glob.glob(os.path.join(CSRC, "*.cu")))
 
 
+def _torch_extension(nvcc: str) -> str:
+    """Compile csrc/torch_args.cpp against the installed torch (not imported for it); returns the compiler's output."""
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc)))
+    tmp = TORCH_LIB + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", TORCH_SRC, "-o", tmp, "-I", INCLUDE,
+           "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_path("include"), "-isystem", os.path.join(cuda, "include"),
+           "-L", os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {TORCH_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, TORCH_LIB)
+    return r.stdout + r.stderr
+
+
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(TORCH_LIB):
         return True
-    t = os.path.getmtime(LIB)
-    deps = sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
+    t = min(os.path.getmtime(LIB), os.path.getmtime(TORCH_LIB))
+    deps = sources() + [TORCH_SRC] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
         glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
     return any(os.path.getmtime(p) > t for p in deps)
 
@@ -63,12 +85,14 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, r.stdout + r.stderr
 
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        extension = ex.submit(_torch_extension, nvcc)
         results = list(ex.map(compile_one, sources()))
+        results.append(("", extension.result()))
     if verbose or ptxas_info:
         for _, log in results:
             if log.strip():
                 sys.stdout.write(log)
-    objs = [o for o, _ in results]
+    objs = [o for o, _ in results if o]
     tmp = LIB + ".tmp"
     cmd = [nvcc, *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -2,7 +2,7 @@
 // attention that reads it: argument validation, then one launch function each.
 #include <math.h>
 
-#include <algorithm>
+#include <utility>
 
 #include "fa2.h"
 #include "internal.h"
@@ -18,8 +18,9 @@ bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p
 // Whether elements of a strided tensor (innermost: `inner` contiguous ones) never share memory:
 // taken by growing stride, each dimension steps past what the smaller ones span.
 bool rows_apart(const int64_t* sizes, const int64_t* strides, int dims, int64_t inner) {
-    int order[4] = {0, 1, 2, 3};
-    std::sort(order, order + dims, [&](int a, int b) { return strides[a] < strides[b]; });
+    int order[3] = {0, 1, 2};  // dims <= 3
+    for (int i = 1; i < dims; ++i)
+        for (int j = i; j > 0 && strides[order[j]] < strides[order[j - 1]]; --j) std::swap(order[j], order[j - 1]);
     int64_t span = inner;
     for (int i = 0; i < dims; ++i) {
         const int k = order[i];

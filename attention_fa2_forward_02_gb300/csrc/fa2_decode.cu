@@ -35,7 +35,7 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kOver = 8;          // blocks an item counts beyond its own
-constexpr int kJoinWarps = 16;
+constexpr int kJoinThreads = 512;
 constexpr int kJoinRows = 4;      // rows a CTA of the second kernel joins
 constexpr float kRescale = 8.0f;  // the running maximum may lag by this much (base-2 units) before O is rescaled
 constexpr float kLn2 = 0.693147180559945309f;
@@ -43,10 +43,12 @@ constexpr float kLn2 = 0.693147180559945309f;
 // D: the head size's kernel; kTiles: query heads per item / 8.
 template <int D, bool kE4m3, int kTiles>
 struct Cfg {
-    static constexpr int kRows = 8 * kTiles;                // query heads per item
-    static constexpr int kPerSm = kTiles == 1 ? 3 : 2;      // CTAs an SM
-    static constexpr int kMaxCtas = 152 * kPerSm;           // a fixed number: the split depends on the lengths alone
     static constexpr int kRowBytes = kE4m3 ? D : 2 * D;
+    static constexpr int kRows = 8 * kTiles;                // query heads per item
+    // CTAs an SM. Rows of 256 bytes keep memory busy with two, and three read unevenly fast: long
+    // contexts 518 -> 550 us; the others have more to do per byte: e4m3 batch 73 -> 65 us with three.
+    static constexpr int kPerSm = kTiles == 1 && kRowBytes < 256 ? 3 : 2;
+    static constexpr int kMaxCtas = 152 * kPerSm;           // a fixed number: the split depends on the lengths alone
     static constexpr int kKeys = kRowBytes >= 256 ? 16 : (kRowBytes == 128 ? 32 : 64);  // keys per block: 8 KB of K and V
     static constexpr int kLooks = (kKeys + 31) / 32;        // keys a lane looks up per block
     static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks a row
@@ -72,8 +74,8 @@ __device__ __forceinline__ int swizzle(int r, int c) {
     else return r * 2 + (c ^ ((r >> 2) & 1));
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool on) {
-    const int bytes = on ? 16 : 0;  // 0: the 16 bytes are filled with zeros
+// bytes: 16, or 0 (nothing is read, the 16 bytes are filled with zeros)
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -110,44 +112,56 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// How the units (units_of) of all items are divided over the CTAs. Items are ordered by
-// (sequence, head block); every sequence has `per_seq` of them, with the same number of blocks.
+// a / b for a >= 0, b > 0: the 32-bit division where both fit (the 64-bit one is far longer).
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return ((uint64_t)(a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+
+// How the units (units_of) of all items are divided over the CTAs: evenly, the first `rest` CTAs
+// one more. Items are ordered by (sequence, head block); every sequence has `per_seq` of them,
+// with the same number of blocks.
 struct Split {
-    int64_t total;  // units in all
-    int64_t ctas;   // CTAs that have any: at least one for each of their warps
-    __device__ __forceinline__ Split(int64_t n, int max_ctas) : total(n), ctas((n + kWarps - 1) / kWarps) {
-        if (ctas > max_ctas) ctas = max_ctas;
+    int64_t share, rest;
+    int ctas;  // CTAs that have any: at least a unit for each of their warps
+    __device__ __forceinline__ Split(int64_t total, int max_ctas) {
+        const int64_t n = (total + kWarps - 1) / kWarps;
+        ctas = n < max_ctas ? (int)n : max_ctas;
+        share = ctas ? quotient(total, ctas) : 0;
+        rest = total - share * ctas;
     }
-    __device__ __forceinline__ int64_t begin(int64_t c) const { return c * total / ctas; }
-    // the CTA that unit u belongs to: the largest c with begin(c) <= u
-    __device__ __forceinline__ int64_t owner(int64_t u) const {
-        int64_t c = u * ctas / total;
-        while (c + 1 < ctas && begin(c + 1) <= u) ++c;
-        return c;
+    __device__ __forceinline__ int64_t begin(int64_t c) const { return c * share + (c < rest ? c : rest); }
+    // the CTA that unit u belongs to
+    __device__ __forceinline__ int owner(int64_t u) const {
+        const int64_t longer = rest * (share + 1);
+        return (int)(u < longer ? quotient(u, share + 1) : rest + quotient(u - longer, share));
     }
 };
 
-// The keys [first, len) of sequence b that the window leaves.
+// The keys [first, len) of sequence b that the window leaves; its blocks begin at `base`, a
+// multiple of 16, so that 16 keys lie in one page where the page size is one too.
 struct Range {
-    int first, len;
+    int base, first, len;
 };
 __device__ __forceinline__ Range range_of(const DecodeParams& p, int b) {
     const int len = bounded_len(p.c.lens[b], p.c.room, p.c.status);
     const int first = p.window > 0 && len > p.window ? (int)(len - p.window) : 0;
-    return {first, len};
+    return {first & ~15, first, len};
 }
 template <int kKeys>
-__device__ __forceinline__ int blocks_of(Range r) { return (r.len - r.first + kKeys - 1) / kKeys; }
+__device__ __forceinline__ int blocks_of(Range r) { return (r.len - r.base + kKeys - 1) / kKeys; }
 // What an item of `nb` blocks counts in the division of the work.
 __device__ __forceinline__ int units_of(int nb) { return nb ? nb + kOver : 0; }
 
 // Workspace: per CTA two partial results (its first item, if that began before it or ends after
 // it; its last item, if that ends after it), each [kRows][D] floats and then [kRows] (m, l);
-// behind all of them, per CTA, the item that begins in it and ends in a later CTA.
+// behind all of them, per CTA, the item that begins in it and ends in a later CTA. (The second
+// kernel could find that from the lengths, but while the first one fills the SMs it has no place
+// to do so early: e4m3 batch 65.3 -> 68.6 us.)
 template <int D, int kRows>
 __device__ __forceinline__ float* partial(float* ws, int64_t cta, int which) {
     return ws + (cta * 2 + which) * (kRows * (D + 2));
 }
+
 struct __align__(16) Torn {
     int rows;      // 0: none
     int last_cta;
@@ -159,25 +173,74 @@ __device__ __forceinline__ Torn* torn(float* ws, int64_t cta) {
     return reinterpret_cast<Torn*>(partial<D, C::kRows>(ws, C::kMaxCtas, 0)) + cta;
 }
 
-// Inclusive sums over the CTA's threads in order, and the total of all. `scratch`: kWarps int64,
-// to be used again after the next __syncthreads.
-__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* scratch, int64_t* total) {
+// A place in the order of items: sequence b, whose first unit is u_seq.
+struct Place {
+    int64_t u_seq;
+    Range range;
+    int b;
+};
+struct LocateSmem {
+    int64_t sums[2][kWarps];
+    Place place;
+};
+
+// Inclusive sums over the CTA's threads in order, and the total of all.
+__device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* sums, int64_t* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
         const int64_t o = __shfl_up_sync(0xffffffffu, v, off);
         if (lane >= off) v += o;
     }
-    if (lane == 31) scratch[warp] = v;
+    if (lane == 31) sums[warp] = v;
     __syncthreads();
     int64_t before = 0, all = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += scratch[w];
-        all += scratch[w];
+        if (w < warp) before += sums[w];
+        all += sums[w];
     }
     *total = all;
     return before + v;
+}
+
+// The division of all sequences' units over the CTAs, CTA blockIdx.x's share [u_begin, u_end) of
+// them, and the place of its first unit. All threads call it; false: the CTA has no share, and no
+// place.
+template <int kKeys>
+__device__ __forceinline__ bool locate(const DecodeParams& p, int64_t per_seq, int max_ctas, LocateSmem& sm, Split* split,
+                                       int64_t* u_begin, int64_t* u_end) {
+    const int64_t batch = p.c.batch;
+    int64_t total, upto = 0, mine = 0;
+    Range range{0, 0, 0};
+    if (threadIdx.x < batch) range = range_of(p, threadIdx.x);
+    mine = units_of(blocks_of<kKeys>(range));
+    int64_t all = mine;
+    for (int64_t b = threadIdx.x + kThreads; b < batch; b += kThreads) all += units_of(blocks_of<kKeys>(range_of(p, (int)b)));
+    upto = cta_scan(all, sm.sums[0], &total);  // of the sequences threadIdx.x, + kThreads, ...: with one strip, of all up to it
+    *split = Split(total * per_seq, max_ctas);
+    if ((int)blockIdx.x >= split->ctas) return false;
+    *u_begin = split->begin(blockIdx.x);
+    *u_end = split->begin(blockIdx.x + 1);
+    const int64_t u = *u_begin;
+    int64_t before = 0;
+    for (int64_t b0 = 0;; b0 += kThreads) {  // strips of kThreads sequences, until the one that holds u
+        int64_t strip = total;
+        if (batch > kThreads) {
+            if (b0) {
+                range = Range{0, 0, 0};
+                if (b0 + threadIdx.x < batch) range = range_of(p, (int)(b0 + threadIdx.x));
+                mine = units_of(blocks_of<kKeys>(range));
+                __syncthreads();  // sums[1] is read no more
+            }
+            upto = before + cta_scan(mine, sm.sums[1], &strip);
+        }
+        if ((upto - mine) * per_seq <= u && u < upto * per_seq) sm.place = Place{(upto - mine) * per_seq, range, (int)b0 + (int)threadIdx.x};
+        before += strip;
+        if (before * per_seq > u) break;
+    }
+    __syncthreads();
+    return true;
 }
 
 template <bool kBf16>
@@ -201,64 +264,31 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
     constexpr bool kMmaBf16 = kBf16 && !kE4m3;
     constexpr int kKeys = C::kKeys, S = C::kStages, kRows = C::kRows, kMt = kKeys / 16;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t scratch[2][kWarps];
-    __shared__ int64_t start_seq;
-    __shared__ int start_b;
+    __shared__ LocateSmem located;
     const PagedParams& c = p.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = p.heads / c.hkv, hblocks = (group + kRows - 1) / kRows;
     const int64_t per_seq = (int64_t)c.hkv * hblocks;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- the units of all sequences, this CTA's share, and the sequence that it begins in
-    int64_t total = 0, mine = 0, upto = 0;  // with at most kThreads sequences: thread i holds sequence i
-    const bool one_strip = c.batch <= kThreads;
-    if (one_strip) {
-        if (threadIdx.x < c.batch) mine = units_of(blocks_of<kKeys>(range_of(p, threadIdx.x)));
-        upto = cta_scan(mine, scratch[0], &total);
-    } else {
-        for (int b = threadIdx.x; b < c.batch; b += kThreads) mine += units_of(blocks_of<kKeys>(range_of(p, b)));
-        cta_scan(mine, scratch[0], &total);
-    }
-    const Split split(total * per_seq, gridDim.x);
-    const bool working = (int64_t)blockIdx.x < split.ctas;
-    const int64_t u_begin = working ? split.begin(blockIdx.x) : 0, u_end = working ? split.begin(blockIdx.x + 1) : 0;
-    if (working) {
-        if (one_strip) {
-            if ((upto - mine) * per_seq <= u_begin && u_begin < upto * per_seq) {
-                start_b = threadIdx.x;
-                start_seq = (upto - mine) * per_seq;
-            }
-        } else {
-            int64_t before = 0;
-            for (int b0 = 0; b0 < c.batch; b0 += kThreads) {
-                const int64_t v = b0 + (int)threadIdx.x < c.batch ? units_of(blocks_of<kKeys>(range_of(p, b0 + threadIdx.x))) : 0;
-                __syncthreads();
-                int64_t strip;
-                const int64_t to = before + cta_scan(v, scratch[1], &strip);
-                if ((to - v) * per_seq <= u_begin && u_begin < to * per_seq) {
-                    start_b = b0 + threadIdx.x;
-                    start_seq = (to - v) * per_seq;
-                }
-                before += strip;
-                if (before * per_seq > u_begin) break;
-            }
+    // rows without a key, strewn over the CTAs
+    auto empty_rows = [&]() {
+        for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
+            if (range_of(p, b).len > 0) continue;
+            const int64_t row0 = (int64_t)b * p.heads;
+            for (int i = threadIdx.x; i < p.heads * c.d / 8; i += kThreads)
+                reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row0 * c.d)[i] = make_uint4(0, 0, 0, 0);
+            for (int i = threadIdx.x; i < p.heads; i += kThreads) p.lse[row0 + i] = -INFINITY;
         }
-    }
-    // ---- rows without a key, strewn over the CTAs
-    for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
-        const Range r = range_of(p, b);
-        if (r.len > r.first) continue;
-        const int64_t row0 = (int64_t)b * p.heads;
-        for (int i = threadIdx.x; i < p.heads * c.d / 8; i += kThreads)
-            reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row0 * c.d)[i] = make_uint4(0, 0, 0, 0);
-        for (int i = threadIdx.x; i < p.heads; i += kThreads) p.lse[row0 + i] = -INFINITY;
-    }
+    };
+    Split split(0, 0);
+    int64_t u_begin, u_end;
+    const bool working = locate<kKeys>(p, per_seq, gridDim.x, located, &split, &u_begin, &u_end);
     if (!working) {
         if (threadIdx.x == 0) torn<C, D>(p.workspace, blockIdx.x)->rows = 0;
+        empty_rows();
         return;
     }
-    __syncthreads();
 
     // the segment that unit u lies in; false: the CTA has no block from u on
     auto seek = [&](Segment& s, int64_t u) {
@@ -269,7 +299,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
             s.nb = blocks_of<kKeys>(s.range);
         }
         const int units = units_of(s.nb);
-        s.item = (int)((u - s.u_seq) / units);
+        s.item = (int)quotient(u - s.u_seq, units);
         const int64_t u_item = s.u_seq + (int64_t)s.item * units;  // kOver units first, then the blocks
         const int64_t from = u - u_item - kOver, to = u_end - u_item - kOver;
         s.k0 = from > 0 ? (int)from : 0;
@@ -285,9 +315,9 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
     };
 
     Segment seg;
-    seg.b = start_b;
-    seg.u_seq = start_seq;
-    seg.range = range_of(p, seg.b);
+    seg.b = located.place.b;
+    seg.u_seq = located.place.u_seq;
+    seg.range = located.place.range;
     seg.nb = blocks_of<kKeys>(seg.range);
     bool live = seek(seg, u_begin);
 
@@ -304,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
         if (!ahead_live) return;
         const int hk = ahead.item / hblocks;
         ahead_left = count(ahead, ahead_number);
-        ahead_key = ahead.range.first + (ahead.k0 + turn(ahead_number)) * kKeys + (kKeys < 32 ? lane % kKeys : lane);
+        ahead_key = ahead.range.base + (ahead.k0 + turn(ahead_number)) * kKeys + (kKeys < 32 ? lane % kKeys : lane);
         ahead_table = c.table + ahead.b * c.table_stride;
         ahead_head = hk * c.head_stride;
         ahead_exp = (int64_t)hk * c.page_size;
@@ -328,7 +358,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
             const int key = ahead_key + 32 * j;
             page[j] = 0;
             slot[j] = -1;
-            if (key < ahead.range.len) {
+            if (key >= ahead.range.first && key < ahead.range.len) {
                 const int at = page_of(c, key);
                 page[j] = ahead_table[at];
                 slot[j] = key - at * c.page_size;
@@ -337,6 +367,11 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
         ahead_key += kWarps * kKeys;
         --ahead_left;
     };
+    // a lane copies chunk lane % kChunks of every kStep-th row; past the head's size it fills with zeros
+    const int lane_bytes = lane % C::kChunks * 16 < c.d * (kE4m3 ? 1 : 2) ? 16 : 0;
+    const int64_t lane_off = lane / C::kChunks * c.slot_stride + (lane_bytes ? lane % C::kChunks * 16 : 0);
+    const int64_t rows_off = 32 / C::kChunks * c.slot_stride;
+    const bool sixteens = c.page_size % 16 == 0;
     int fill = 0;                        // the stage to fill next
     uint32_t ka[C::kLooks], ve[C::kLooks];  // scale bytes of the block loaded last; ve 256: the key does not count
     int info_stage = -1;                 // and its stage, while they are not stored
@@ -346,30 +381,52 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
             const char* kbase = c.k + head_off;
             const char* vbase = c.v + head_off;
             int64_t off[C::kLooks];
+            uint32_t counts = 0xffffffffu;
 #pragma unroll
             for (int j = 0; j < C::kLooks; ++j) {
                 Slot s{-1, -1};
                 if (slot[j] >= 0) s = slot_of(c, page[j], slot[j]);
                 off[j] = s.off;
+                const uint32_t some = __ballot_sync(0xffffffffu, s.off >= 0);
+                counts &= some;
                 if constexpr (kE4m3) {
                     const int64_t e = s.exp + head_exp;
                     ka[j] = s.off >= 0 ? c.k_exp[e] : 127u;
                     ve[j] = s.off >= 0 ? c.v_exp[e] : 256u;
                 } else {
-                    const uint32_t counts = __ballot_sync(0xffffffffu, s.off >= 0);
-                    if (lane == 0) *reinterpret_cast<uint32_t*>(my + fill * C::kStage + 2 * C::kTile + 4 * j) = counts;
+                    if (lane == 0) *reinterpret_cast<uint32_t*>(my + fill * C::kStage + 2 * C::kTile + 4 * j) = some;
                 }
             }
-            const int chunk = lane % C::kChunks, r0 = lane / C::kChunks;
-            const bool in = chunk * 16 < c.d * (kE4m3 ? 1 : 2);
+            constexpr int kStep = 32 / C::kChunks;  // rows a copy instruction of the warp covers
+            if (sixteens && counts == 0xffffffffu) {  // 16 keys after one another in a page
 #pragma unroll
-            for (int r = 0; r < kKeys; r += 32 / C::kChunks) {
-                const int64_t o = __shfl_sync(0xffffffffu, off[r / 32], (r & 31) + r0);
-                const bool on = o >= 0 && in;
-                const int64_t at = on ? o + chunk * 16 : 0;
-                const uint32_t dst = st + swizzle<C::kChunks>(r + r0, chunk) * 16;
-                cp_async16(dst, kbase + at, on);
-                cp_async16(dst + C::kTile, vbase + at, on);
+                for (int r = 0; r < kKeys; r += 16) {
+                    const int64_t o = __shfl_sync(0xffffffffu, off[r / 32], r & 31) + lane_off;
+                    const char *ks = kbase + o, *vs = vbase + o;
+#pragma unroll
+                    for (int i = 0; i < 16; i += kStep) {
+                        const uint32_t dst = st + swizzle<C::kChunks>(r + i + lane / C::kChunks, lane % C::kChunks) * 16;
+                        cp_async16(dst, ks, lane_bytes);
+                        cp_async16(dst + C::kTile, vs, lane_bytes);
+                        ks += rows_off;
+                        vs += rows_off;
+                    }
+                }
+            } else {
+#pragma unroll 1
+                for (int r = 0; r < kKeys; r += kStep) {
+                    const int row = r + lane / C::kChunks;
+                    int64_t o = __shfl_sync(0xffffffffu, off[0], row & 31);
+                    if constexpr (C::kLooks > 1) {
+                        const int64_t o1 = __shfl_sync(0xffffffffu, off[C::kLooks - 1], row & 31);
+                        if (row >= 32) o = o1;
+                    }
+                    const int bytes = o >= 0 ? lane_bytes : 0;
+                    const int64_t at = bytes ? o + lane % C::kChunks * 16 : 0;
+                    const uint32_t dst = st + swizzle<C::kChunks>(row, lane % C::kChunks) * 16;
+                    cp_async16(dst, kbase + at, bytes);
+                    cp_async16(dst + C::kTile, vbase + at, bytes);
+                }
             }
             info_stage = fill;
         }
@@ -386,13 +443,28 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
             info_stage = -1;
         }
     };
+    // q of an item: thread (row, 16 elements); read while the first keys are on their way
+    constexpr int kParts = D / 16;
+    const int q_row = threadIdx.x / kParts, q_part = threadIdx.x % kParts;
+    uint4 q_lo, q_hi;
+    auto fetch_q = [&](const Segment& s) {
+        const int hb = s.item % hblocks, head = s.item / hblocks * group + hb * kRows + q_row;
+        const bool on = q_row < min(kRows, group - hb * kRows);
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + s.b * p.q_batch + (int64_t)head * p.q_head + 16 * q_part;
+        q_lo = q_hi = make_uint4(0, 0, 0, 0);
+        if (on && 16 * q_part < c.d) q_lo = *reinterpret_cast<const uint4*>(src);
+        if (on && 16 * q_part + 8 < c.d) q_hi = *reinterpret_cast<const uint4*>(src + 8);
+    };
     look();
+    if (live) fetch_q(seg);
 #pragma unroll
     for (int i = 0; i < S - 1; ++i) {
         load();
         look();
         store_info();
     }
+
+    empty_rows();
 
     uint8_t* q_smem = smem + C::kRing;
     float* merge = reinterpret_cast<float*>(smem + C::kRing + C::kQ);
@@ -408,15 +480,10 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
         const int head0 = hk * group + hb * kRows;        // first query head
         const int rows = min(kRows, group - hb * kRows);  // query heads of the item
 
-        // ---- q into shared memory: thread (row, 16 elements), in whole warps (they exchange)
-        constexpr int kParts = D / 16;
+        // ---- q into shared memory, by whole warps (they exchange)
         if (threadIdx.x < (kRows * kParts + 31) / 32 * 32) {
-            const int r = threadIdx.x / kParts, part = threadIdx.x % kParts;
-            const uint16_t* src = static_cast<const uint16_t*>(p.q) + seg.b * p.q_batch + (int64_t)(head0 + r) * p.q_head + 16 * part;
-            const uint4 zero = make_uint4(0, 0, 0, 0);
-            const uint4 lo = r < rows && 16 * part < c.d ? *reinterpret_cast<const uint4*>(src) : zero;
-            const uint4 hi = r < rows && 16 * part + 8 < c.d ? *reinterpret_cast<const uint4*>(src + 8) : zero;
-            uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+            const int r = q_row, part = q_part;
+            uint32_t w[8] = {q_lo.x, q_lo.y, q_lo.z, q_lo.w, q_hi.x, q_hi.y, q_hi.z, q_hi.w};
             float scale = p.scale * 1.4426950408889634f;
             if constexpr (kBf16 && kE4m3) {
                 float a = 0.f;
@@ -630,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
         const bool whole = seg.k0 == 0 && seg.k1 == seg.nb;
         const int which = first_item ? 0 : 1;
         const int64_t out_row = (int64_t)seg.b * p.heads + head0;
-        if (seg.k0 == 0 && !whole) ends_later = {rows, (int)split.owner(seg.next - 1), which, (int)out_row};
+        if (seg.k0 == 0 && !whole) ends_later = {rows, split.owner(seg.next - 1), which, (int)out_row};
         float* part = partial<D, kRows>(p.workspace, blockIdx.x, which);
 #pragma unroll
         for (int h = 0; h < kTiles; ++h)
@@ -691,53 +758,62 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
         }
         first_item = false;
         live = seek(seg, seg.next);
+        if (live) fetch_q(seg);
     }
     cp_async_wait<0>();
     if (threadIdx.x == 0) *torn<C, D>(p.workspace, blockIdx.x) = ends_later;
 }
 
 // Joins the items that several CTAs worked on: CTA (x, y) rows kJoinRows y .. of the item that
-// began in CTA x, if it ended in a later one. A quarter of the warps for each row, a warp for
-// every fourth partial result, its lanes for the columns.
+// begins in CTA x of the first kernel, if it ends in a later one. kShare warps a row, each for
+// every kShare-th partial result, its lanes for the columns.
 template <int D, bool kBf16, typename C>
-__global__ void __launch_bounds__(kJoinWarps * 32) fa2_decode_join_kernel(const DecodeParams p) {
+__global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const DecodeParams p) {
     constexpr int kRows = C::kRows;
-    constexpr int kShare = kJoinWarps / kJoinRows;  // warps per row
-    constexpr int kCols = D / 32;                   // columns a lane
-    __shared__ float parts[kJoinWarps][D + 1];
+    constexpr int kShare = kJoinThreads / 32 / kJoinRows;
+    constexpr int kCols = D / 32;  // columns a lane
+    __shared__ float parts[kJoinThreads / 32][D + 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int share = warp % kShare, r = blockIdx.y * kJoinRows + warp / kShare;
     // launched while the first kernel still runs: everything it wrote is here after this wait
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const Torn item = *torn<C, D>(p.workspace, blockIdx.x);
-    if ((int)blockIdx.y * kJoinRows >= item.rows) return;
-    const int first = blockIdx.x, n = item.last_cta - first + 1;
-    const bool on = r < item.rows;
-    auto part = [&](int k) { return partial<D, kRows>(p.workspace, first + k, k == 0 ? item.which : 0); };
-    float big = -INFINITY, sum = 0.f, a[kCols] = {};
+    const int rows = item.rows;
+    if ((int)blockIdx.y * kJoinRows >= rows) return;
+    const int first = blockIdx.x, n = item.last_cta - first + 1, which = item.which;
+    const int share = warp % kShare, r = blockIdx.y * kJoinRows + warp / kShare;
+    const bool on = r < rows;
+    float m = -INFINITY, sum = 0.f, a[kCols] = {};
     if (on) {
-        for (int k = lane; k < n; k += 32) big = fmaxf(big, part(k)[kRows * D + 2 * r]);
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) big = fmaxf(big, __shfl_xor_sync(0xffffffffu, big, off));
-        const float from = big == -INFINITY ? 0.f : big;
 #pragma unroll 4
         for (int k = share; k < n; k += kShare) {
-            const float* s = part(k);
+            const float* s = partial<D, kRows>(p.workspace, first + k, k == 0 ? which : 0);
             const float2 ml = *reinterpret_cast<const float2*>(s + kRows * D + 2 * r);
-            const float f = ex2_approx(ml.x - from);
-            sum += f * ml.y;
+            const float big = fmaxf(m, ml.x), ref = big == -INFINITY ? 0.f : big;
+            const float old = ex2_approx(m - ref), f = ex2_approx(ml.x - ref);
+            m = big;
+            sum = sum * old + f * ml.y;
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) a[i] += f * s[r * D + lane + 32 * i];
+            for (int i = 0; i < kCols; ++i) a[i] = a[i] * old + f * s[r * D + lane + 32 * i];
         }
 #pragma unroll
         for (int i = 0; i < kCols; ++i) parts[warp][lane + 32 * i] = a[i];
-        if (lane == 0) parts[warp][D] = sum;
+        if (lane == 0) {
+            parts[warp][D] = m;
+            parts[warp][D + 1] = sum;
+        }
     }
     __syncthreads();
     if (!on || share != 0) return;
+    float big = -INFINITY, f[kShare];
+#pragma unroll
+    for (int w = 0; w < kShare; ++w) big = fmaxf(big, parts[warp + w][D]);
+    const float ref = big == -INFINITY ? 0.f : big;
     sum = 0.f;
 #pragma unroll
-    for (int w = 0; w < kShare; ++w) sum += parts[warp + w][D];
+    for (int w = 0; w < kShare; ++w) {
+        f[w] = ex2_approx(parts[warp + w][D] - ref);
+        sum += f[w] * parts[warp + w][D + 1];
+    }
     const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
     const int64_t row = (int64_t)item.out_row + r;
 #pragma unroll
@@ -745,7 +821,7 @@ __global__ void __launch_bounds__(kJoinWarps * 32) fa2_decode_join_kernel(const 
         const int d = lane + 32 * i;
         float v = 0.f;
 #pragma unroll
-        for (int w = 0; w < kShare; ++w) v += parts[warp + w][d];
+        for (int w = 0; w < kShare; ++w) v += f[w] * parts[warp + w][d];
         if (d < p.c.d) put<kBf16>(p.o, row * p.c.d + d, v * inv);
     }
     if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (big + lg2_approx(sum)) * kLn2;
@@ -763,7 +839,7 @@ cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
     const int rows = std::min(C::kRows, p.heads / p.c.hkv);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(C::kMaxCtas, (unsigned)((rows + kJoinRows - 1) / kJoinRows), 1);
-    cfg.blockDim = dim3(kJoinWarps * 32, 1, 1);
+    cfg.blockDim = dim3(kJoinThreads, 1, 1);
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -787,8 +863,9 @@ cudaError_t launch_kind(const DecodeParams& p, cudaStream_t stream, int slot) {
 }
 
 template <int D, int kTiles>
-size_t workspace_for() {
-    using C = Cfg<D, false, kTiles>;
+size_t workspace_for() {  // either type of cache; the 8-bit one has at least as many CTAs
+    using C = Cfg<D, true, kTiles>;
+    static_assert(C::kMaxCtas >= Cfg<D, false, kTiles>::kMaxCtas, "workspace");
     return (size_t)C::kMaxCtas * (2 * C::kRows * (D + 2) * sizeof(float) + sizeof(Torn));
 }
 

@@ -10,8 +10,9 @@
 // signed fraction of half a turn, go to sincospif.
 //
 // Each thread owns P pairs of one token (two 16-byte vectors where sizes and strides allow) and
-// walks over heads: the P sines and cosines, the only arithmetic of weight here, are made once
-// for all of them.
+// walks over heads, four of them in flight: the P sines and cosines, the only arithmetic of weight
+// here, are made once for all of them, while the first four heads are being read. Bound by memory:
+// 134 MB (B=2 H=16 N=8192 d=128, bf16) in 21.7 us, 6.2 TB/s.
 #include "common.cuh"
 #include "internal.h"
 
@@ -19,7 +20,8 @@ namespace fa2 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;  // heads in flight per thread
+constexpr int kUnroll = 4;    // heads in flight per thread
+constexpr int kMaxHeads = 16;  // heads a thread walks over
 
 // f / (2 pi) modulo 1 in units of 2^-64, for finite f.
 __device__ __forceinline__ uint64_t turns_of(double f) {
@@ -86,11 +88,23 @@ __global__ void __launch_bounds__(kThreads)
     const E* xr = x + b * xb + n * xn;
     E* yr = y + b * yb + n * yn;
     for (int u = threadIdx.x; u < units; u += blockDim.x) {
-        if (u < rot_units) {
-            const int i0 = kInterleaved ? 2 * P * u : P * u;
-            const int i1 = kInterleaved ? i0 + P : i0 + rot / 2;
+        const bool turns = u < rot_units;  // else elements that do not rotate: one or two packs, copied
+        const int i0 = turns ? (kInterleaved ? 2 * P * u : P * u) : rot + (u - rot_units) * 2 * P;
+        const int i1 = turns && !kInterleaved ? i0 + rot / 2 : i0 + P;
+        const bool both = i1 < d;
+        Pack<E, P> a[kUnroll], g[kUnroll];
+        auto fetch = [&](int h) {
+#pragma unroll
+            for (int k = 0; k < kUnroll; ++k)
+                if (h + k < h1) {
+                    a[k].w = *reinterpret_cast<const W*>(xr + (h + k) * xh + i0);
+                    if (both) g[k].w = *reinterpret_cast<const W*>(xr + (h + k) * xh + i1);
+                }
+        };
+        fetch(h0);  // on their way while the angles are made
+        float c[P], s[P];
+        if (turns) {
             const int64_t pos = positions ? positions[b * position_stride + n] : n;
-            float c[P], s[P];
 #pragma unroll
             for (int p = 0; p < P; ++p) {
                 const uint64_t phase = (uint64_t)pos * turns_of(inv_freq[P * u + p]);
@@ -99,18 +113,15 @@ __global__ void __launch_bounds__(kThreads)
                 c[p] *= magnitude;
                 s[p] *= backward ? -magnitude : magnitude;
             }
-            for (int h = h0; h < h1; h += kUnroll) {
-                Pack<E, P> a[kUnroll], g[kUnroll];
+        }
+        for (int h = h0;;) {
 #pragma unroll
-                for (int k = 0; k < kUnroll; ++k)
-                    if (h + k < h1) {
-                        a[k].w = *reinterpret_cast<const W*>(xr + (h + k) * xh + i0);
-                        g[k].w = *reinterpret_cast<const W*>(xr + (h + k) * xh + i1);
-                    }
-#pragma unroll
-                for (int k = 0; k < kUnroll; ++k)
-                    if (h + k < h1) {
-                        Pack<E, P> o0, o1;
+            for (int k = 0; k < kUnroll; ++k)
+                if (h + k < h1) {
+                    Pack<E, P> o0, o1;
+                    o0.w = a[k].w;
+                    o1.w = g[k].w;
+                    if (turns) {
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
                             // pair p: elements p of the two packs, or elements 2 p, 2 p + 1 of both in a row
@@ -127,16 +138,13 @@ __global__ void __launch_bounds__(kThreads)
                                 o1.e[p] = y2;
                             }
                         }
-                        *reinterpret_cast<W*>(yr + (h + k) * yh + i0) = o0.w;
-                        *reinterpret_cast<W*>(yr + (h + k) * yh + i1) = o1.w;
                     }
-            }
-        } else {  // elements that do not rotate: one or two packs
-            const int i0 = rot + (u - rot_units) * 2 * P, i1 = i0 + P;
-            for (int h = h0; h < h1; ++h) {
-                *reinterpret_cast<W*>(yr + h * yh + i0) = *reinterpret_cast<const W*>(xr + h * xh + i0);
-                if (i1 < d) *reinterpret_cast<W*>(yr + h * yh + i1) = *reinterpret_cast<const W*>(xr + h * xh + i1);
-            }
+                    *reinterpret_cast<W*>(yr + (h + k) * yh + i0) = o0.w;
+                    if (both) *reinterpret_cast<W*>(yr + (h + k) * yh + i1) = o1.w;
+                }
+            h += kUnroll;
+            if (h >= h1) break;
+            fetch(h);
         }
     }
 }
@@ -147,11 +155,13 @@ cudaError_t launch_p(const RopeParams& p, cudaStream_t stream) {
     const int ux = units < kThreads ? units : kThreads;
     const int ty = kThreads / ux;
     const int64_t blocks_x = (p.n + ty - 1) / ty;
-    // Heads per thread: all of them while that leaves every SM threads enough to hide the loads,
-    // else fewer (each part of the heads makes the angles again).
-    int hpt = (int)p.h;
-    while (hpt > 1 && blocks_x * p.b * ((p.h + hpt - 1) / hpt) < (int64_t)152 * 8) hpt = (hpt + 1) / 2;
-    int64_t chunks = (p.h + hpt - 1) / hpt;
+    // Heads per thread: up to kMaxHeads, in equal parts, while that leaves every SM threads enough to
+    // hide the loads, else fewer (each part of the heads makes the angles again). GB300, B=2 H=16
+    // N=8192 d=128: 16 or 8 heads a thread 21.7 us, 4 heads 24.0 us.
+    int64_t chunks = (p.h + kMaxHeads - 1) / kMaxHeads;
+    while (chunks < p.h && blocks_x * p.b * chunks < (int64_t)152 * 8) chunks *= 2;
+    int hpt = (int)((p.h + chunks - 1) / chunks);
+    chunks = (p.h + hpt - 1) / hpt;
     auto kern = p.interleaved ? rope_kernel<E, P, true> : rope_kernel<E, P, false>;
     for (int64_t b0 = 0; b0 < p.b;) {  // grid.y holds at most 65535 (batch entry, part of the heads)
         int64_t nb = 65535 / chunks;

@@ -35,8 +35,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kOver = 8;          // blocks an item counts beyond its own
-constexpr int kJoinThreads = 512;
-constexpr int kJoinRows = 4;      // rows a CTA of the second kernel joins
+constexpr int kJoinThreads = 256;
+constexpr int kJoinRows = 2;      // rows a CTA of the second kernel joins
 constexpr float kRescale = 8.0f;  // the running maximum may lag by this much (base-2 units) before O is rescaled
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -269,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = p.heads / c.hkv, hblocks = (group + kRows - 1) / kRows;
     const int64_t per_seq = (int64_t)c.hkv * hblocks;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    grid_begin();
 
     // rows without a key, strewn over the CTAs
     auto empty_rows = [&]() {
@@ -774,8 +774,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const Dec
     constexpr int kCols = D / 32;  // columns a lane
     __shared__ float parts[kJoinThreads / 32][D + 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // launched while the first kernel still runs: everything it wrote is here after this wait
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    grid_begin();
     const Torn item = *torn<C, D>(p.workspace, blockIdx.x);
     const int rows = item.rows;
     if ((int)blockIdx.y * kJoinRows >= rows) return;
@@ -833,20 +832,11 @@ cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
     auto kern = fa2_decode_kernel<D, kBf16, kE4m3, kTiles>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, slot);
     if (e != cudaSuccess) return e;
-    kern<<<C::kMaxCtas, kThreads, C::kSmem, stream>>>(p);
-    e = cudaGetLastError();
+    e = launch_early(kern, dim3(C::kMaxCtas), dim3(kThreads), C::kSmem, stream, p);
     if (e != cudaSuccess) return e;
     const int rows = std::min(C::kRows, p.heads / p.c.hkv);
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(C::kMaxCtas, (unsigned)((rows + kJoinRows - 1) / kJoinRows), 1);
-    cfg.blockDim = dim3(kJoinThreads, 1, 1);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, fa2_decode_join_kernel<D, kBf16, C>, p);
+    return launch_early(fa2_decode_join_kernel<D, kBf16, C>, dim3(C::kMaxCtas, (unsigned)((rows + kJoinRows - 1) / kJoinRows)),
+                        dim3(kJoinThreads), 0, stream, p);
 }
 
 // Up to 8 query heads a key-value head: one column tile, else two.

@@ -81,6 +81,7 @@ __global__ void __launch_bounds__(kThreads)
     using W = typename Word<P * sizeof(E)>::T;
     const int b = blockIdx.y / chunks, chunk = blockIdx.y % chunks;
     const int n = blockIdx.x * blockDim.y + threadIdx.y;
+    grid_begin();
     if (n >= n_tokens) return;
     const int h0 = chunk * heads_per_thread, h1 = min(heads, h0 + heads_per_thread);
     const bool in_place = x == y;
@@ -161,6 +162,7 @@ cudaError_t launch_p(const RopeParams& p, cudaStream_t stream) {
     int64_t chunks = (p.h + kMaxHeads - 1) / kMaxHeads;
     while (chunks < p.h && blocks_x * p.b * chunks < (int64_t)152 * 8) chunks *= 2;
     int hpt = (int)((p.h + chunks - 1) / chunks);
+    if (hpt > kUnroll) hpt = (hpt + kUnroll - 1) / kUnroll * kUnroll;  // whole rounds: 21.5 -> 20.7 us at 20 heads
     chunks = (p.h + hpt - 1) / hpt;
     auto kern = p.interleaved ? rope_kernel<E, P, true> : rope_kernel<E, P, false>;
     for (int64_t b0 = 0; b0 < p.b;) {  // grid.y holds at most 65535 (batch entry, part of the heads)
@@ -171,11 +173,11 @@ cudaError_t launch_p(const RopeParams& p, cudaStream_t stream) {
             nb = 1;
         }
         if (nb > p.b - b0) nb = p.b - b0;
-        kern<<<dim3((unsigned)blocks_x, (unsigned)(nb * chunks)), dim3(ux, ty), 0, stream>>>(
-            static_cast<const E*>(p.x) + b0 * p.xs[0], static_cast<E*>(p.y) + b0 * p.ys[0],
-            p.positions ? p.positions + b0 * p.position_stride : nullptr, p.position_stride, p.inv_freq, (int)p.n, (int)p.h,
-            hpt, (int)chunks, p.d, p.rot, p.xs[0], p.xs[1], p.xs[2], p.ys[0], p.ys[1], p.ys[2], p.magnitude, p.backward);
-        const cudaError_t e = cudaGetLastError();
+        const cudaError_t e = launch_early(
+            kern, dim3((unsigned)blocks_x, (unsigned)(nb * chunks)), dim3(ux, ty), 0, stream, static_cast<const E*>(p.x) + b0 * p.xs[0],
+            static_cast<E*>(p.y) + b0 * p.ys[0], p.positions ? p.positions + b0 * p.position_stride : nullptr, p.position_stride,
+            p.inv_freq, (int)p.n, (int)p.h, hpt, (int)chunks, p.d, p.rot, p.xs[0], p.xs[1], p.xs[2], p.ys[0], p.ys[1], p.ys[2],
+            p.magnitude, (int)p.backward);
         if (e != cudaSuccess) return e;
         b0 += nb;
     }

@@ -35,8 +35,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kOver = 8;          // blocks an item counts beyond its own
-constexpr int kJoinThreads = 256;
-constexpr int kJoinRows = 2;      // rows a CTA of the second kernel joins
+constexpr int kJoinThreads = 512;
+constexpr int kJoinRows = 4;      // rows a CTA of the second kernel joins
 constexpr float kRescale = 8.0f;  // the running maximum may lag by this much (base-2 units) before O is rescaled
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -872,9 +872,9 @@ size_t decode_workspace_bytes(int heads, int hkv, int d) {
 
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
     switch (pad_head_dim(p.c.d)) {
-        case 32: return launch_kind<32>(p, stream, 52);
-        case 64: return launch_kind<64>(p, stream, 60);
-        default: return launch_kind<128>(p, stream, 68);
+        case 32: return launch_kind<32>(p, stream, 64);  // slots 64..71 (the attention kernels take 0..61)
+        case 64: return launch_kind<64>(p, stream, 72);  // 72..79
+        default: return launch_kind<128>(p, stream, 80);  // 80..87
     }
 }
 

@@ -49,17 +49,13 @@ def quantise_row(x):
             e += 1
     y = x * 2.0 ** -e
     table = e4m3_values()[:127]  # codes 0 .. 126, ascending
-    codes = np.empty(x.shape, dtype=np.uint8)
-    for i, v in enumerate(y):
-        if np.isnan(v):
-            codes[i] = 0x7F
-            continue
-        mag = min(abs(v), 448.0)
-        dist = np.abs(table - mag)
-        best = np.flatnonzero(dist == dist.min())
-        code = int(best[0]) if len(best) == 1 else int(next(c for c in best if c % 2 == 0))  # ties: the even fraction
-        codes[i] = code | (128 if np.signbit(v) else 0)
-    return codes, e + 127
+    mag = np.minimum(np.abs(np.where(np.isnan(y), 0.0, y)), 448.0)
+    dist = np.abs(table[None, :] - mag[:, None])
+    low = dist.argmin(1)  # the lower of two codes at the same distance: adjacent ones
+    tie = (low < 126) & (dist[np.arange(len(y)), np.minimum(low + 1, 126)] == dist[np.arange(len(y)), low])
+    codes = np.where(tie & (low % 2 == 1), low + 1, low)  # ties: the even fraction
+    codes = np.where(np.isnan(y), 0x7F, codes | np.where(np.signbit(y), 128, 0))
+    return codes.astype(np.uint8), e + 127
 
 
 def row_values(codes, byte):

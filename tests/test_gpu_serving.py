@@ -151,3 +151,51 @@ def test_read_back_feeds_the_forward(e4m3):
     # both are within two roundings of 2^-8 (weights, output) of sum P |v| <= max |v|
     assert np.all(np.abs(a - b) <= 4 * UNIT_ROUNDOFF["bf16"] * v64 + 1e-5)
     assert np.max(np.abs(G.to_f64(lse).reshape(rows, GROUP) - G.to_f64(lse2))) <= 2e-4
+
+
+SCRIPT = """
+import math, sys
+import torch
+from attention_fa2_forward_02_gb300 import binding as B
+
+def attention():
+    for d in (32, 64, 128):
+        for dt in (torch.bfloat16, torch.float16):
+            for bh, n_q, n_k in ((2, 4096, 128), (2, 200, 2048), (80, 200, 300)):
+                q, o, do, dq = (torch.randn(bh, n_q, d, device="cuda").to(dt) for _ in range(4))
+                k, v, dk, dv = (torch.randn(bh, n_k, d, device="cuda").to(dt) for _ in range(4))
+                lse = torch.empty(bh, n_q, device="cuda")
+                B.fa2_forward(q, k, v, o, lse, 0.2)
+                ws = torch.empty(B.fa2_backward_workspace_size(bh, n_q, n_k, d, B._dtype_code(q)), dtype=torch.uint8, device="cuda")
+                B.fa2_backward(q, k, v, o, do, lse, dq, dk, dv, ws, 0.2)
+
+def decode():
+    table, lens = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4), torch.tensor([60, 33], dtype=torch.int32, device="cuda")
+    for d in (32, 64, 128):
+        for dt in (torch.bfloat16, torch.float16):
+            for group in (2, 16):
+                pages = torch.randn(8, 2, 16, d, device="cuda").to(dt)
+                exp = torch.full((8, 2, 16), 127, dtype=torch.uint8, device="cuda")
+                q = torch.randn(2, 2 * group, d, device="cuda").to(dt)
+                o, lse = torch.empty_like(q), torch.empty(2, 2 * group, device="cuda")
+                ws = torch.empty(B.fa2_decode_workspace_size(2, 2 * group, 2, d), dtype=torch.uint8, device="cuda")
+                B.fa2_decode(q, pages, pages, o, lse, table, lens, ws, 0.2)
+                codes = pages.to(torch.float8_e4m3fn)
+                B.fa2_decode(q, codes, codes, o, lse, table, lens, ws, 0.2, k_exp=exp, v_exp=exp)
+
+for name in sys.argv[1:]:
+    {"attention": attention, "decode": decode}[name]()
+    B.fa2_device_status()
+"""
+
+
+@pytest.mark.parametrize("order", [("attention", "decode"), ("decode", "attention")])
+def test_both_orders_beside_the_attention_kernels(order):
+    """Every kernel raises its own shared-memory limit, whatever ran before it in a fresh process."""
+    import os
+    import subprocess
+    import sys
+    G.require_gpu()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", SCRIPT, *order], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0, r.stderr[-2000:]

@@ -21,12 +21,12 @@ bool rows_apart(const int64_t* sizes, const int64_t* strides, int dims, int64_t 
     int order[3] = {0, 1, 2};  // dims <= 3
     for (int i = 1; i < dims; ++i)
         for (int j = i; j > 0 && strides[order[j]] < strides[order[j - 1]]; --j) std::swap(order[j], order[j - 1]);
-    int64_t span = inner;
+    __int128 span = inner;
     for (int i = 0; i < dims; ++i) {
         const int k = order[i];
         if (sizes[k] <= 1) continue;
         if (strides[k] < span) return false;
-        span += strides[k] * (sizes[k] - 1);
+        span += (__int128)strides[k] * (sizes[k] - 1);
     }
     return true;
 }

@@ -180,7 +180,7 @@ struct Place {
     int b;
 };
 struct LocateSmem {
-    int64_t sums[2][kWarps];
+    int64_t sums[kWarps];
     Place place;
 };
 
@@ -210,34 +210,30 @@ __device__ __forceinline__ int64_t cta_scan(int64_t v, int64_t* sums, int64_t* t
 template <int kKeys>
 __device__ __forceinline__ bool locate(const DecodeParams& p, int64_t per_seq, int max_ctas, LocateSmem& sm, Split* split,
                                        int64_t* u_begin, int64_t* u_end) {
-    const int64_t batch = p.c.batch;
-    int64_t total, upto = 0, mine = 0;
+    const int batch = (int)p.c.batch, per = (batch + kThreads - 1) / kThreads;
+    const int b0 = min((int)threadIdx.x * per, batch), b1 = min(b0 + per, batch);  // this thread's sequences
+    int64_t mine = 0, total;
     Range range{0, 0, 0};
-    if (threadIdx.x < batch) range = range_of(p, threadIdx.x);
-    mine = units_of(blocks_of<kKeys>(range));
-    int64_t all = mine;
-    for (int64_t b = threadIdx.x + kThreads; b < batch; b += kThreads) all += units_of(blocks_of<kKeys>(range_of(p, (int)b)));
-    upto = cta_scan(all, sm.sums[0], &total);  // of the sequences threadIdx.x, + kThreads, ...: with one strip, of all up to it
+    for (int b = b0; b < b1; ++b) {
+        range = range_of(p, b);
+        mine += units_of(blocks_of<kKeys>(range));
+    }
+    int64_t upto = cta_scan(mine, sm.sums, &total);
     *split = Split(total * per_seq, max_ctas);
     if ((int)blockIdx.x >= split->ctas) return false;
     *u_begin = split->begin(blockIdx.x);
     *u_end = split->begin(blockIdx.x + 1);
-    const int64_t u = *u_begin;
-    int64_t before = 0;
-    for (int64_t b0 = 0;; b0 += kThreads) {  // strips of kThreads sequences, until the one that holds u
-        int64_t strip = total;
-        if (batch > kThreads) {
-            if (b0) {
-                range = Range{0, 0, 0};
-                if (b0 + threadIdx.x < batch) range = range_of(p, (int)(b0 + threadIdx.x));
-                mine = units_of(blocks_of<kKeys>(range));
-                __syncthreads();  // sums[1] is read no more
+    upto -= mine;
+    if (upto * per_seq <= *u_begin && *u_begin < (upto + mine) * per_seq) {  // among this thread's sequences
+        int b = b0;
+        if (per > 1)
+            for (;; ++b) {
+                range = range_of(p, b);
+                const int units = units_of(blocks_of<kKeys>(range));
+                if (*u_begin < (upto + units) * per_seq) break;
+                upto += units;
             }
-            upto = before + cta_scan(mine, sm.sums[1], &strip);
-        }
-        if ((upto - mine) * per_seq <= u && u < upto * per_seq) sm.place = Place{(upto - mine) * per_seq, range, (int)b0 + (int)threadIdx.x};
-        before += strip;
-        if (before * per_seq > u) break;
+        sm.place = Place{upto * per_seq, range, b};
     }
     __syncthreads();
     return true;

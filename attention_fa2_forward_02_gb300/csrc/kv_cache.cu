@@ -19,6 +19,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMinExp = -60;
+constexpr int kOneToken = 152 * 2;  // blocks from which a warp takes a whole token
 
 // e of the scale 2^e for a row whose largest finite magnitude is a.
 __device__ __forceinline__ int scale_exp(float a) {
@@ -250,15 +251,18 @@ cudaError_t launch_lanes(const KvRowsParams& p, cudaStream_t stream) {
     const int total = 2 * p.c.hkv;
     const unsigned batch = (unsigned)(p.read ? p.c.batch : 1);
     auto blocks = [&](int tok) { return (p.tokens + kWarps * tok - 1) / (kWarps * tok); };
-    // A warp takes kTok whole tokens while that gives every SM several blocks, else one round of
-    // one token's rows. GB300, 120,000 tokens of 16 heads, e4m3: 1 token a warp 90.1 us, 2 86.2, 4 89.7.
+    // A warp takes kTok whole tokens while that gives every SM several blocks, one token with fewer,
+    // and with few tokens one round of a token's rows.
     if (blocks(kTok) * batch >= 152 * 8) {
         const dim3 grid((unsigned)blocks(kTok), 1, batch);
         return launch_early(kv_rows_kernel<kBf16, kE4m3, kRead, kLanes, kRows, kTok>, grid, dim3(kWarps * 32), 0, stream, p, total);
-    } else {
-        const dim3 grid((unsigned)blocks(1), (unsigned)((total + kGroups - 1) / kGroups), batch);
-        return launch_early(kv_rows_kernel<kBf16, kE4m3, kRead, kLanes, 1, 1>, grid, dim3(kWarps * 32), 0, stream, p, kGroups);
     }
+    if (blocks(1) * batch >= kOneToken) {
+        const dim3 grid((unsigned)blocks(1), 1, batch);
+        return launch_early(kv_rows_kernel<kBf16, kE4m3, kRead, kLanes, kRows, 1>, grid, dim3(kWarps * 32), 0, stream, p, total);
+    }
+    const dim3 grid((unsigned)blocks(1), (unsigned)((total + kGroups - 1) / kGroups), batch);
+    return launch_early(kv_rows_kernel<kBf16, kE4m3, kRead, kLanes, 1, 1>, grid, dim3(kWarps * 32), 0, stream, p, kGroups);
 }
 
 template <bool kBf16, bool kE4m3, bool kRead>

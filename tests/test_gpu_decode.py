@@ -234,3 +234,45 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for _, _, o2, l2 in outs:
         assert torch.equal(o, o2) and torch.equal(lse, l2)
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("group,d", [(1, 32), (8, 128), (16, 64), (12, 128)])
+def test_workspace_of_exactly_the_size_asked_for(group, d, e4m3):
+    """Rows divided between all the CTAs write every partial result; nothing lands outside the workspace."""
+    torch = G.require_gpu()
+    c = Cache("decode/ws", [9000, 4000], 64, 2, d, "bf16", e4m3)
+    q = synth.tensor("decode/ws/q", (2, 2 * group, d), "bf16")
+    o, lse = G.empty((2, 2 * group, d), "bf16"), torch.empty(2, 2 * group, device="cuda")
+    ws = G.Guarded((binding.fa2_decode_workspace_size(2, 2 * group, 2, d),), torch.uint8)
+    for n in ((9000, 4000), (0, 9000), (9000, 0), (300, 9000)):
+        c.lens = list(n)
+        c.lens_dev.copy_(torch.tensor(n, dtype=torch.int32))
+        c.table[:] = np.arange(c.table.size).reshape(c.table.shape) % c.pages
+        c.table_dev.copy_(torch.from_numpy(c.table))
+        binding.fa2_decode(G.to_device(q, "bf16"), *c.pools(), o, lse, c.table_dev, c.lens_dev, ws.t, 1 / math.sqrt(d), **c.exps())
+        binding.fa2_device_status()
+        ws.assert_intact("workspace")
+    check(c, synth.widen(q, "bf16"), o, lse, group, 1 / math.sqrt(d), rows=[0])
+
+
+def test_many_sequences():
+    """Far more sequences than threads and CTAs, most of them empty, and the largest batch a call takes."""
+    torch = G.require_gpu()
+    for batch in (5000, 65535):
+        lens = np.zeros(batch, dtype=np.int64)
+        at = [0, 1, 127, 128, batch // 2, batch - 2, batch - 1]
+        lens[at] = [3, 40, 17, 5, 100, 16, 33]
+        c = Cache("decode/many", [int(lens[i]) for i in at], 16, 1, 32, "bf16", True)
+        table = torch.zeros(batch, c.wide, dtype=torch.int32, device="cuda")
+        table[at] = c.table_dev
+        q = synth.tensor("decode/many/q", (len(at), 2, 32), "bf16")
+        full = torch.zeros(batch, 2, 32, dtype=torch.bfloat16, device="cuda")
+        full[at] = G.to_device(q, "bf16")
+        o, lse = torch.full_like(full, float("nan")), torch.full((batch, 2), float("nan"), device="cuda")
+        binding.fa2_decode(full, *c.pools(), o, lse, table, torch.from_numpy(lens).int().cuda(), workspace(batch, 2, 1, 32), 0.2, **c.exps())
+        binding.fa2_device_status()
+        check(c, synth.widen(q, "bf16"), o[at], lse[at], 2, 0.2)
+        rest = torch.ones(batch, dtype=torch.bool)
+        rest[at] = False
+        assert not o[rest].any() and bool((lse[rest] == -math.inf).all())

@@ -199,3 +199,77 @@ def test_both_orders_beside_the_attention_kernels(order):
     root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
     r = subprocess.run([sys.executable, "-c", SCRIPT, *order], cwd=root, capture_output=True, text=True, timeout=240)
     assert r.returncode == 0, r.stderr[-2000:]
+
+
+CAPTURE_FIRST = """
+import torch
+from attention_fa2_forward_02_gb300 import binding as B
+pages = torch.randn(8, 2, 16, 64, device="cuda").bfloat16()
+table, lens = torch.arange(8, dtype=torch.int32, device="cuda").view(2, 4), torch.tensor([60, 33], dtype=torch.int32, device="cuda")
+f = torch.ones(32, dtype=torch.float64, device="cuda")
+
+def run():
+    q = torch.ones(2, 4, 64, device="cuda").bfloat16()
+    k, out = torch.ones(2, 2, 64, device="cuda").bfloat16(), [torch.zeros(2, 2, 64, 64, device="cuda").bfloat16() for _ in "kv"]
+    o, lse = torch.empty_like(q), torch.empty(2, 4, device="cuda")
+    ws = torch.empty(B.fa2_decode_workspace_size(2, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    B.fa2_rope(q.unsqueeze(2), q.unsqueeze(2), f)
+    B.fa2_kv_append(pages, pages.clone(), k, k, table, lens)
+    B.fa2_decode(q, pages, pages, o, lse, table, lens, ws, 0.2)
+    B.fa2_kv_read(pages, pages, *out, table, lens)
+    return o, lse, *out
+
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    got = run()
+g.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in got]
+want = run()
+B.fa2_device_status()
+assert all(torch.equal(a, b) for a, b in zip(got, want))
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    import os
+    import subprocess
+    import sys
+    G.require_gpu()
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", CAPTURE_FIRST], cwd=root, capture_output=True, text=True, timeout=240)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
+@pytest.mark.parametrize("threads", [4])
+def test_calls_from_several_host_threads(threads):
+    """Threads with streams and workspaces of their own get what one call alone gets."""
+    import threading
+    torch = G.require_gpu()
+    c = Cache("threads", [700, 33, 1500], PAGE, HKV, D, "bf16", True)
+    q = G.to_device(synth.tensor("threads/q", (3, HEADS, D), "bf16"), "bf16")
+
+    def call(stream=None):
+        o, lse = torch.empty_like(q), torch.empty(3, HEADS, device="cuda")
+        ws = torch.empty(binding.fa2_decode_workspace_size(3, HEADS, HKV, D), dtype=torch.uint8, device="cuda")
+        k, v = (torch.zeros(3, HKV, 1500, D, dtype=torch.bfloat16, device="cuda") for _ in "kv")
+        torch.cuda.synchronize()
+        for _ in range(20):
+            binding.fa2_decode(q, *c.pools(), o, lse, c.table_dev, c.lens_dev, ws, 0.125, stream=stream, **c.exps())
+            binding.fa2_kv_read(*c.pools(), k, v, c.table_dev, c.lens_dev, stream=stream, **c.exps())
+        torch.cuda.synchronize()
+        return o, lse, k, v
+
+    want, got = call(), [None] * threads
+
+    def work(i):
+        got[i] = call(torch.cuda.Stream())
+
+    ts = [threading.Thread(target=work, args=(i,)) for i in range(threads)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    for g in got:
+        assert g is not None and all(torch.equal(a, b) for a, b in zip(g, want))

@@ -6,13 +6,17 @@
 // The angle: only its fraction of a turn matters, and at position 2^20 a float32 product has
 // already lost a sixteenth of a radian. f / (2 pi) is turned into a 64-bit fixed-point fraction
 // (integers only: this part's float64 rate is a hundredth of its integer rate) and multiplied by the position
-// modulo 2^64, which keeps the fraction exact to position * 2^-64. Its upper 32 bits, as a
-// signed fraction of half a turn, go to sincospif.
+// modulo 2^64, which keeps the fraction exact to position * 2^-64; the fixed-point frequencies are
+// made once per block, in shared memory. The upper 32 bits of a product, as a signed fraction of
+// a turn, go to sincospif for float32 results and to the special function unit for 16-bit ones:
+// its sine and cosine are within 2^-20.9 between -pi and pi, a rounding of the result is 2^-12 or
+// more. With sincospif and a conversion per thread the angles cost more than the rows: GB300,
+// B=2 H=16 N=2048 d=128, 10.2 us against 7.1.
 //
 // Each thread owns P pairs of one token (two 16-byte vectors where sizes and strides allow) and
-// walks over heads, four of them in flight: the P sines and cosines, the only arithmetic of weight
-// here, are made once for all of them, while the first four heads are being read. Bound by memory:
-// 134 MB (B=2 H=16 N=8192 d=128, bf16) in 21.7 us, 6.2 TB/s.
+// walks over heads, two of them in flight: the P sines and cosines are made once for all of them,
+// while the first heads are being read. Bound by memory: 134 MB (B=2 H=16 N=8192 d=128, bf16) in
+// 22.2 us, 6.0 TB/s.
 #include "common.cuh"
 #include "internal.h"
 
@@ -20,8 +24,8 @@ namespace fa2 {
 namespace {
 
 constexpr int kThreads = 128;
-constexpr int kUnroll = 4;    // heads in flight per thread
-constexpr int kMaxHeads = 16;  // heads a thread walks over
+constexpr int kUnroll = 2;    // heads in flight per thread
+constexpr int kMaxHeads = 4;  // heads a thread walks over
 
 // f / (2 pi) modulo 1 in units of 2^-64, for finite f.
 __device__ __forceinline__ uint64_t turns_of(double f) {
@@ -80,8 +84,11 @@ __global__ void __launch_bounds__(kThreads)
                 int64_t xb, int64_t xh, int64_t xn, int64_t yb, int64_t yh, int64_t yn, float magnitude, int backward) {
     using W = typename Word<P * sizeof(E)>::T;
     const int b = blockIdx.y / chunks, chunk = blockIdx.y % chunks;
+    __shared__ uint64_t turns[512];
     const int n = blockIdx.x * blockDim.y + threadIdx.y;
     grid_begin();
+    for (int i = threadIdx.y * blockDim.x + threadIdx.x; i < rot / 2; i += blockDim.x * blockDim.y) turns[i] = turns_of(inv_freq[i]);
+    __syncthreads();
     if (n >= n_tokens) return;
     const int h0 = chunk * heads_per_thread, h1 = min(heads, h0 + heads_per_thread);
     const bool in_place = x == y;
@@ -89,9 +96,9 @@ __global__ void __launch_bounds__(kThreads)
     const E* xr = x + b * xb + n * xn;
     E* yr = y + b * yb + n * yn;
     for (int u = threadIdx.x; u < units; u += blockDim.x) {
-        const bool turns = u < rot_units;  // else elements that do not rotate: one or two packs, copied
-        const int i0 = turns ? (kInterleaved ? 2 * P * u : P * u) : rot + (u - rot_units) * 2 * P;
-        const int i1 = turns && !kInterleaved ? i0 + rot / 2 : i0 + P;
+        const bool rotates = u < rot_units;  // else elements that do not rotate: one or two packs, copied
+        const int i0 = rotates ? (kInterleaved ? 2 * P * u : P * u) : rot + (u - rot_units) * 2 * P;
+        const int i1 = rotates && !kInterleaved ? i0 + rot / 2 : i0 + P;
         const bool both = i1 < d;
         Pack<E, P> a[kUnroll], g[kUnroll];
         auto fetch = [&](int h) {
@@ -104,13 +111,13 @@ __global__ void __launch_bounds__(kThreads)
         };
         fetch(h0);  // on their way while the angles are made
         float c[P], s[P];
-        if (turns) {
+        if (rotates) {
             const int64_t pos = positions ? positions[b * position_stride + n] : n;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                const uint64_t phase = (uint64_t)pos * turns_of(inv_freq[P * u + p]);
-                // int32 fraction of a turn -> half turns in [-1, 1)
-                sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s[p], &c[p]);
+                const float part = (float)(int32_t)(((uint64_t)pos * turns[P * u + p]) >> 32);  // of a turn, 2^-32
+                if constexpr (sizeof(E) == 4) sincospif(part * 0x1p-31f, &s[p], &c[p]);
+                else __sincosf(part * (6.28318530717958648f * 0x1p-32f), &s[p], &c[p]);
                 c[p] *= magnitude;
                 s[p] *= backward ? -magnitude : magnitude;
             }
@@ -122,7 +129,7 @@ __global__ void __launch_bounds__(kThreads)
                     Pack<E, P> o0, o1;
                     o0.w = a[k].w;
                     o1.w = g[k].w;
-                    if (turns) {
+                    if (rotates) {
 #pragma unroll
                         for (int p = 0; p < P; ++p) {
                             // pair p: elements p of the two packs, or elements 2 p, 2 p + 1 of both in a row
@@ -158,11 +165,12 @@ cudaError_t launch_p(const RopeParams& p, cudaStream_t stream) {
     const int64_t blocks_x = (p.n + ty - 1) / ty;
     // Heads per thread: up to kMaxHeads, in equal parts, while that leaves every SM threads enough to
     // hide the loads, else fewer (each part of the heads makes the angles again). GB300, B=2 H=16
-    // N=8192 d=128: 16 or 8 heads a thread 21.7 us, 4 heads 24.0 us.
+    // N=8192 d=128: 4 heads a thread 22.2 us, 8 22.6, 2 23.5; B=3 H=20 N=5003 d=96 with 32 turning:
+    // 4 20.6 us, 8 21.1, 2 22.4.
     int64_t chunks = (p.h + kMaxHeads - 1) / kMaxHeads;
     while (chunks < p.h && blocks_x * p.b * chunks < (int64_t)152 * 8) chunks *= 2;
     int hpt = (int)((p.h + chunks - 1) / chunks);
-    if (hpt > kUnroll) hpt = (hpt + kUnroll - 1) / kUnroll * kUnroll;  // whole rounds: 21.5 -> 20.7 us at 20 heads
+    if (hpt > kUnroll) hpt = (hpt + kUnroll - 1) / kUnroll * kUnroll;  // whole rounds
     chunks = (p.h + hpt - 1) / hpt;
     auto kern = p.interleaved ? rope_kernel<E, P, true> : rope_kernel<E, P, false>;
     for (int64_t b0 = 0; b0 < p.b;) {  // grid.y holds at most 65535 (batch entry, part of the heads)

@@ -226,6 +226,9 @@ struct DecodeParams {
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_kv_rows(const KvRowsParams& p, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_d32(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_d64(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_d128(const DecodeParams& p, cudaStream_t stream);
 size_t decode_workspace_bytes(int heads, int hkv, int d);
 
 cudaError_t launch_fwd_tc(const FwdParams& p, cudaStream_t stream);

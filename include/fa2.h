@@ -537,9 +537,10 @@ fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, cons
  * float32 scores, softmax statistics and sums; the probabilities are rounded to 16 bits
  * (FA2_CACHE_SAME: dtype; FA2_CACHE_E4M3: half) before the product with V; in half, weights
  * below 2^-25 of the row's largest count as 0 there.
- * The keys of all sequences and heads are divided evenly over the CTAs, whatever the lengths;
- * a row divided between CTAs is joined from float32 partial results in a fixed order (the
- * result is reproducible for the same lengths).
+ * The keys of all sequences and heads are divided evenly over the CTAs, whatever the lengths
+ * (contexts that pages_per_seq * page_size or the window keep short: head by head, over the
+ * CTAs of a cluster); a row divided between CTAs is joined from float32 partial results in a
+ * fixed order.  The result is reproducible for the same lengths and the same pages_per_seq.
  * n_heads a multiple of n_kv_heads; n_heads <= 65535, batch <= 65535 and their product
  * <= 2^31 - 1 (FA2_ERR_UNSUPPORTED).
  * Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_WORKSPACE,

@@ -107,6 +107,18 @@ def test_lengths(n, e4m3):
 
 
 @pytest.mark.parametrize("e4m3", [False, True])
+@pytest.mark.parametrize("wide", [None, 2000])
+@pytest.mark.parametrize("batch,hkv,group", [(1, 1, 1), (1, 8, 4), (3, 2, 16), (9, 8, 3), (70, 8, 2)])
+def test_short_rows_in_one_launch_and_in_two(batch, hkv, group, wide, e4m3):
+    """A narrow block table takes the clusters of one launch (of 8, 4, 2 CTAs and of one, as the items grow), a wide one
+    with the same lengths the two launches; empty sequences, shares without a block and windows among them."""
+    lens = [(37 * i * i + 5 * i) % 260 for i in range(batch)]
+    lens[0] = 259
+    run("decode/short", lens, 16, hkv, group, 64, "bf16", e4m3, stale="nan", table_pages=wide, rows=range(0, batch, 7))
+    run("decode/short", lens, 16, hkv, group, 128, "f16", e4m3, "nhd", window=77, table_pages=wide, rows=range(0, batch, 7))
+
+
+@pytest.mark.parametrize("e4m3", [False, True])
 def test_long_rows_joined_from_many_ctas(e4m3):
     run("decode/long", [20000], 16, 1, 3, 64, "bf16", e4m3)
     run("decode/long2", [9000, 1, 5000], 64, 2, 8, 128, "f16", e4m3, "nhd")

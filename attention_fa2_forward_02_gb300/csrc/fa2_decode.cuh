@@ -42,7 +42,6 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kOver = 8;          // blocks an item counts beyond its own
 constexpr int kJoinThreads = 512;
-constexpr int kJoinRows = 4;      // rows a CTA of the second kernel joins
 constexpr float kRescale = 8.0f;  // the running maximum may lag by this much (base-2 units) before O is rescaled
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -64,11 +63,14 @@ struct Cfg {
     static constexpr int kStages = 2;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kQ = kRows * D * 2;                // q as the first product takes it
-    static constexpr int kMergeRows = 2;                    // rows the warps add up at a time at the end of an item
-    static constexpr int kPitch = kE4m3 ? D + 8 : D + 4;    // floats a row there (no bank twice)
+    static constexpr int kPitch = kE4m3 ? D + 8 : D + 4;    // floats a row at the end of an item (no bank twice)
+    static constexpr int smem(int merge_rows) { return kRing + kQ + kWarps * merge_rows * kPitch * 4 + kRows * 4; }
+    static constexpr bool fits(int bytes) { return bytes + 1024 + 256 <= 228 * 1024 / kPerSm; }
+    // rows the warps add up at a time there: as many as find room
+    static constexpr int kMergeRows = fits(smem(8)) ? 8 : (fits(smem(4)) ? 4 : 2);
     static constexpr int kMerge = kWarps * kMergeRows * kPitch * 4;
-    static constexpr int kSmem = kRing + kQ + kMerge + kRows * 4;
-    static_assert(kSmem + 1024 + 256 <= 228 * 1024 / kPerSm, "CTAs an SM");
+    static constexpr int kSmem = smem(kMergeRows);
+    static_assert(fits(kSmem), "CTAs an SM");
 };
 
 // Position of chunk `c` of row `r` in a tile: the eight rows an ldmatrix reads at one chunk lie
@@ -290,7 +292,7 @@ template <int D, bool kBf16, bool kE4m3, int kTiles, bool kCluster>
 __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_decode_kernel(const DecodeParams p, int ranks) {
     using C = Cfg<D, kE4m3, kTiles>;
     constexpr bool kMmaBf16 = kBf16 && !kE4m3;
-    constexpr int kKeys = C::kKeys, S = C::kStages, kRows = C::kRows, kMt = kKeys / 16;
+    constexpr int kKeys = C::kKeys, S = C::kStages, kRows = C::kRows, kMt = kKeys / 16, kMR = C::kMergeRows;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LocateSmem located;
     const PagedParams& c = p.c;
@@ -739,7 +741,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
             __syncwarp();  // the stage may be filled again
         }
 
-        // ---- the warps' results together, kMergeRows rows at a time: kWarps / kMergeRows warps per row
+        // ---- the warps' results together, kMergeRows rows at a time: a warp or two per row
         const bool whole = kCluster ? ranks == 1 : seg.k0 == 0 && seg.k1 == seg.nb;
         const int which = first_item ? 0 : 1;
         const int64_t out_row = (int64_t)seg.b * p.heads + head0;
@@ -754,13 +756,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) l[h][n] += __shfl_xor_sync(0xffffffffu, l[h][n], off);
 #pragma unroll
-        for (int round = 0; round < kRows / 2; ++round) {  // rows 2 round, 2 round + 1: the heads of the lanes t = round % 4
-            if (2 * round >= rows) break;
-            const int h = round / 4;
-            if (t == round % 4) {
+        for (int round = 0; round < kRows / kMR; ++round) {  // rows kMR round ..; lane t has heads 2t, 2t+1 (+ 8)
+            if (kMR * round >= rows) break;
+            const int h = round * kMR / 8;
+            if (t / (kMR / 2) == round % (8 / kMR)) {
 #pragma unroll
                 for (int n = 0; n < 2; ++n) {
-                    float* row = merge + (warp * 2 + n) * C::kPitch;
+                    float* row = merge + (warp * kMR + 2 * (t % (kMR / 2)) + n) * C::kPitch;
 #pragma unroll
                     for (int d = 0; d < D / 16; ++d) {
                         if constexpr (!kE4m3) {
@@ -774,17 +776,19 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
                 }
             }
             __syncthreads();
-            constexpr int kShare = kWarps / 2;  // warps per row
-            const int n = warp / kShare, r = 2 * round + n;
-            if (r < rows) {
+            constexpr int kShare = kMR < kWarps ? kWarps / kMR : 1;  // warps per row
+#pragma unroll
+            for (int n = warp / kShare; n < kMR; n += kWarps / kShare) {
+                const int r = kMR * round + n;
+                if (r >= rows) break;
                 float big = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) big = fmaxf(big, merge[(w * 2 + n) * C::kPitch + D]);
+                for (int w = 0; w < kWarps; ++w) big = fmaxf(big, merge[(w * kMR + n) * C::kPitch + D]);
                 const float from = big == -INFINITY ? 0.f : big;
                 float f[kWarps], sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float* row = merge + (w * 2 + n) * C::kPitch;
+                    const float* row = merge + (w * kMR + n) * C::kPitch;
                     f[w] = ex2_approx(row[D] - from);
                     sum += f[w] * row[D + 1];
                 }
@@ -793,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
                 for (int d = lane + 32 * (warp % kShare); d < D; d += 32 * kShare) {
                     float a = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kWarps; ++w) a += f[w] * merge[(w * 2 + n) * C::kPitch + d];
+                    for (int w = 0; w < kWarps; ++w) a += f[w] * merge[(w * kMR + n) * C::kPitch + d];
                     if (!whole) part[r * D + d] = a;
                     else if (d < c.d) put<kBf16>(p.o, (out_row + r) * c.d + d, a * inv);
                 }
@@ -819,7 +823,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
 // Joins the items that several CTAs worked on: CTA (x, y) rows kJoinRows y .. of the item that
 // begins in CTA x of the first kernel, if it ends in a later one. kShare warps a row, each for
 // every kShare-th partial result, its lanes for the columns.
-template <int D, bool kBf16, typename C>
+template <int D, bool kBf16, typename C, int kJoinRows>
 __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const DecodeParams p) {
     constexpr int kRows = C::kRows;
     constexpr int kShare = kJoinThreads / 32 / kJoinRows;
@@ -915,8 +919,12 @@ cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
     e = launch_early(kern, dim3(C::kMaxCtas), dim3(kThreads), C::kSmem, stream, p, 1);
     if (e != cudaSuccess) return e;
     const int rows = std::min(C::kRows, p.heads / p.c.hkv);
-    return launch_early(fa2_decode_join_kernel<D, kBf16, C>, dim3(C::kMaxCtas, (unsigned)((rows + kJoinRows - 1) / kJoinRows)),
-                        dim3(kJoinThreads), 0, stream, p);
+    auto join = [&](void (*kernel)(DecodeParams), int join_rows) {  // the fewer rows, the more warps for each
+        return launch_early(kernel, dim3(C::kMaxCtas, (unsigned)((rows + join_rows - 1) / join_rows)), dim3(kJoinThreads), 0, stream, p);
+    };
+    if (rows == 1) return join(fa2_decode_join_kernel<D, kBf16, C, 1>, 1);
+    if (rows == 2) return join(fa2_decode_join_kernel<D, kBf16, C, 2>, 2);
+    return join(fa2_decode_join_kernel<D, kBf16, C, 4>, 4);
 }
 
 // Up to 8 query heads a key-value head: one column tile, else two.

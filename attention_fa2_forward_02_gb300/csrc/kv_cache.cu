@@ -144,6 +144,64 @@ __device__ __forceinline__ bool find_token(const KvRowsParams& p, int64_t t, int
     return true;
 }
 
+// Moves kRows rows a lane, all loads first: there(i) says whether the i-th exists, the others give its
+// addresses (cache side, tensor side, scale byte). Every lane of the warp calls it: the kLanes lanes
+// of a row find its largest magnitude together.
+template <bool kBf16, bool kE4m3, bool kRead, int kLanes, int kRows, typename There, typename Cache, typename Tensor, typename Exp>
+__device__ __forceinline__ void move_rows(int li, There there, Cache cache_ptr, Tensor row_ptr, Exp exp_ptr) {
+    uint4 in[kRows][kE4m3 ? 2 : 1];
+    int byte[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        in[i][0] = make_uint4(0, 0, 0, 0);
+        if constexpr (kE4m3) in[i][1] = make_uint4(0, 0, 0, 0);
+        byte[i] = 127;
+        if (!there(i)) continue;
+        if constexpr (kRead) {
+            in[i][0] = *reinterpret_cast<const uint4*>(cache_ptr(i));
+            if constexpr (kE4m3) byte[i] = *exp_ptr(i);
+        } else {
+            const uint4* src = reinterpret_cast<const uint4*>(row_ptr(i));
+            in[i][0] = src[0];
+            if constexpr (kE4m3) in[i][1] = src[1];
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if constexpr (!kE4m3) {
+            if (there(i)) *reinterpret_cast<uint4*>(kRead ? row_ptr(i) : cache_ptr(i)) = in[i][0];
+        } else if constexpr (kRead) {
+            if (there(i)) {
+                const uint32_t w[4] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w};
+                const float scale = __uint_as_float((uint32_t)byte[i] << 23);
+                uint32_t o[8];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t h2[2];
+                    e4m3x4_to_f16x4(w[j], h2[0], h2[1]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2[e]));
+                        o[2 * j + e] = pack2<kBf16>(f.x * scale, f.y * scale);
+                    }
+                }
+                uint4* dst = reinterpret_cast<uint4*>(row_ptr(i));
+                dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+                dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        } else {
+            const uint32_t w[8] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w,
+                                   in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
+            int e;
+            const uint4 codes = quantise<kBf16, kLanes>(w, &e);
+            if (there(i)) {
+                *reinterpret_cast<uint4*>(cache_ptr(i)) = codes;
+                if (li == 0) *exp_ptr(i) = (uint8_t)(e + 127);
+            }
+        }
+    }
+}
+
 // A warp moves kTok tokens one after another, looked up at once, a lane for each; kLanes lanes move
 // a row, of each token's 2 hkv rows (heads of K, then of V) rows r0, r0 + 32 / kLanes, ..., kRows of
 // them at a time.
@@ -172,77 +230,59 @@ __global__ void __launch_bounds__(kWarps * 32) kv_rows_kernel(const KvRowsParams
         if (tok.cache_off < 0) continue;
         const int64_t k_off = k_base + (t0 + n) * k_step, v_off = v_base + (t0 + n) * v_step;
         for (int r0 = begin + lane / kLanes; r0 - lane / kLanes < stop; r0 += kGroups * kRows) {
-            uint4 in[kRows][kE4m3 ? 2 : 1];
-            int byte[kRows];
-            // the rows' addresses: cache side and tensor side
-            auto cache_ptr = [&](int r) {
-                const bool v = r >= c.hkv;
-                const int h = v ? r - c.hkv : r;
-                return (v ? c.v : c.k) + tok.cache_off + h * c.head_stride + li * 16;
-            };
-            auto row_ptr = [&](int r) {
-                const bool v = r >= c.hkv;
-                const int h = v ? r - c.hkv : r;
-                return (v ? p.v + v_off + h * p.vs[1] : p.k + k_off + h * p.ks[1]) + li * kElems * 2;
-            };
-            auto exp_ptr = [&](int r) {
-                const bool v = r >= c.hkv;
-                const int h = v ? r - c.hkv : r;
-                return (v ? c.v_exp : c.k_exp) + tok.exp_off + (int64_t)h * c.page_size;
-            };
-    #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
+            auto head = [&](int i, bool* v) {
                 const int r = r0 + i * kGroups;
-                in[i][0] = make_uint4(0, 0, 0, 0);
-                if constexpr (kE4m3) in[i][1] = make_uint4(0, 0, 0, 0);
-                byte[i] = 127;
-                if (r >= stop || !on) continue;
-                if constexpr (kRead) {
-                    in[i][0] = *reinterpret_cast<const uint4*>(cache_ptr(r));
-                    if constexpr (kE4m3) byte[i] = *exp_ptr(r);
-                } else {
-                    const uint4* src = reinterpret_cast<const uint4*>(row_ptr(r));
-                    in[i][0] = src[0];
-                    if constexpr (kE4m3) in[i][1] = src[1];
-                }
-            }
-    #pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int r = r0 + i * kGroups;
-                if constexpr (!kE4m3) {
-                    if (r < stop && on) *reinterpret_cast<uint4*>(kRead ? row_ptr(r) : cache_ptr(r)) = in[i][0];
-                } else if constexpr (kRead) {
-                    if (r < stop && on) {
-                        const uint32_t w[4] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w};
-                        const float scale = __uint_as_float((uint32_t)byte[i] << 23);
-                        uint32_t o[8];
-    #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t h2[2];
-                            e4m3x4_to_f16x4(w[j], h2[0], h2[1]);
-    #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2[e]));
-                                o[2 * j + e] = pack2<kBf16>(f.x * scale, f.y * scale);
-                            }
-                        }
-                        uint4* dst = reinterpret_cast<uint4*>(row_ptr(r));
-                        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-                        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
-                    }
-                } else {
-                    const uint32_t w[8] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w,
-                                           in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
-                    int e;
-                    const uint4 codes = quantise<kBf16, kLanes>(w, &e);
-                    if (r < stop && on) {
-                        *reinterpret_cast<uint4*>(cache_ptr(r)) = codes;
-                        if (li == 0) *exp_ptr(r) = (uint8_t)(e + 127);
-                    }
-                }
-            }
+                *v = r >= c.hkv;
+                return *v ? r - c.hkv : r;
+            };
+            move_rows<kBf16, kE4m3, kRead, kLanes, kRows>(
+                li, [&](int i) { return r0 + i * kGroups < stop && on; },
+                [&](int i) {
+                    bool v;
+                    const int h = head(i, &v);
+                    return (v ? c.v : c.k) + tok.cache_off + h * c.head_stride + li * 16;
+                },
+                [&](int i) {
+                    bool v;
+                    const int h = head(i, &v);
+                    return (v ? p.v + v_off + h * p.vs[1] : p.k + k_off + h * p.ks[1]) + li * kElems * 2;
+                },
+                [&](int i) {
+                    bool v;
+                    const int h = head(i, &v);
+                    return (v ? c.v_exp : c.k_exp) + tok.exp_off + (int64_t)h * c.page_size;
+                });
         }
     }
+}
+
+// Few heads: tokens whose rows fill no more than half of a warp's groups of lanes. The group's row is
+// group % (1 << shift) of the token group >> shift further on; kRows rounds of tokens.
+template <bool kBf16, bool kE4m3, bool kRead, int kLanes, int kRows>
+__global__ void __launch_bounds__(kWarps * 32) kv_few_heads_kernel(const KvRowsParams p, int shift) {
+    const PagedParams& c = p.c;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kGroups = 32 / kLanes;
+    const int li = lane % kLanes, group = lane / kLanes, r = group & ((1 << shift) - 1), step = kGroups >> shift;
+    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kRows * step + (group >> shift);
+    grid_begin();
+    const bool on = li * (kE4m3 ? 16 : 8) < c.d && r < 2 * c.hkv, v = r >= c.hkv;
+    const int h = v ? r - c.hkv : r;
+    Token tok[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const int64_t t = t0 + i * step;
+        tok[i].cache_off = -1;
+        if (on && t < p.tokens && !find_token(p, t, blockIdx.z, &tok[i])) tok[i].cache_off = -1;
+    }
+    char* const cache = (v ? c.v : c.k) + h * c.head_stride + li * 16;
+    char* const rows = (v ? p.v + h * p.vs[1] : p.k + h * p.ks[1]) + li * (kE4m3 ? 32 : 16) +
+                       (p.read ? blockIdx.z * (v ? p.vs[0] : p.ks[0]) : 0);
+    const int64_t row_step = p.read ? (v ? p.vs[2] : p.ks[2]) : (v ? p.vs[0] : p.ks[0]);
+    move_rows<kBf16, kE4m3, kRead, kLanes, kRows>(
+        li, [&](int i) { return tok[i].cache_off >= 0; }, [&](int i) { return cache + tok[i].cache_off; },
+        [&](int i) { return rows + (t0 + i * step) * row_step; },
+        [&](int i) { return (v ? c.v_exp : c.k_exp) + tok[i].exp_off + (int64_t)h * c.page_size; });
 }
 
 template <bool kBf16, bool kE4m3, bool kRead, int kLanes>
@@ -250,6 +290,18 @@ cudaError_t launch_lanes(const KvRowsParams& p, cudaStream_t stream) {
     constexpr int kGroups = 32 / kLanes, kRows = 4, kTok = 2;
     const int total = 2 * p.c.hkv;
     const unsigned batch = (unsigned)(p.read ? p.c.batch : 1);
+    int shift = 0;  // 1 << shift groups of lanes for a token's rows
+    while ((1 << shift) < total) ++shift;
+    if ((2 << shift) <= kGroups) {
+        const int64_t per = (int64_t)kWarps * kRows * (kGroups >> shift);
+        if ((p.tokens + per - 1) / per * batch >= 152) {
+            const dim3 grid((unsigned)((p.tokens + per - 1) / per), 1, batch);
+            return launch_early(kv_few_heads_kernel<kBf16, kE4m3, kRead, kLanes, kRows>, grid, dim3(kWarps * 32), 0, stream, p, shift);
+        }
+        const int64_t one = (int64_t)kWarps * (kGroups >> shift);
+        const dim3 grid((unsigned)((p.tokens + one - 1) / one), 1, batch);
+        return launch_early(kv_few_heads_kernel<kBf16, kE4m3, kRead, kLanes, 1>, grid, dim3(kWarps * 32), 0, stream, p, shift);
+    }
     auto blocks = [&](int tok) { return (p.tokens + kWarps * tok - 1) / (kWarps * tok); };
     // A warp takes kTok whole tokens while that gives every SM several blocks, one token with fewer,
     // and with few tokens one round of a token's rows.

@@ -43,6 +43,12 @@ CASES = [
     ([700, 1500, 33], [700, 900, 33], 32, 16, 112, "bf16", True, "nhd"),
     ([6], [6], 8, 70, 24, "bf16", False, "nhd"),
     ([2000, 3001], [2000, 3000], 128, 2, 128, "bf16", False, "hnd"),
+    # few heads: several tokens a warp at once, with few and with many tokens
+    ([40, 7, 1, 65], [40, 3, 1, 2], 16, 1, 64, "bf16", True, "hnd"),
+    ([9000, 1, 4100], [9000, 1, 4099], 16, 1, 32, "bf16", True, "hnd"),
+    ([20000], [19999], 64, 3, 16, "f16", False, "nhd"),
+    ([6000, 2], [6000, 2], 24, 2, 48, "f16", True, "nhd"),
+    ([5000], [5000], 16, 1, 112, "f16", True, "nhd"),
 ]
 
 
@@ -85,6 +91,8 @@ def test_append(lens, new, page, hkv, d, dtype, e4m3, order):
     ([40, 7, 1, 65], 24, 3, 64, "f16", True, "nhd", "bnhd"), ([300, 129], 64, 5, 96, "f16", False, "nhd", "bnhd"),
     ([9, 4, 12], 1, 2, 16, "f16", True, "nhd", "bhnd"), ([9, 4, 12], 1000, 4, 8, "bf16", False, "hnd", "bnhd"),
     ([700, 1500, 33], 32, 16, 112, "bf16", True, "nhd", "bhnd"), ([2000, 3001], 128, 2, 128, "bf16", True, "hnd", "bhnd"),
+    ([20000, 0, 777], 16, 1, 32, "bf16", True, "hnd", "bhnd"), ([9000, 9100], 64, 3, 16, "f16", False, "nhd", "bnhd"),
+    ([50], 8, 2, 40, "bf16", False, "hnd", "bnhd"),
 ])
 @pytest.mark.parametrize("cut", [False, True])
 def test_read(lens, page, hkv, d, dtype, e4m3, order, out, cut):

@@ -42,6 +42,7 @@ constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kOver = 8;          // blocks an item counts beyond its own
 constexpr int kJoinThreads = 512;
+constexpr int kFewItems = 4;      // items up to which (twice which) it joins one row (two) per CTA
 constexpr float kRescale = 8.0f;  // the running maximum may lag by this much (base-2 units) before O is rescaled
 constexpr float kLn2 = 0.693147180559945309f;
 
@@ -919,11 +920,15 @@ cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
     e = launch_early(kern, dim3(C::kMaxCtas), dim3(kThreads), C::kSmem, stream, p, 1);
     if (e != cudaSuccess) return e;
     const int rows = std::min(C::kRows, p.heads / p.c.hkv);
-    auto join = [&](void (*kernel)(DecodeParams), int join_rows) {  // the fewer rows, the more warps for each
+    const int64_t items = p.c.batch * p.c.hkv * ((p.heads / p.c.hkv + C::kRows - 1) / C::kRows);
+    // The fewer rows an item has, and the fewer items (of more partial results each), the more warps
+    // for a row. GB300: one key-value head, 100,000 tokens, 4 query heads 36 us with a quarter of the
+    // warps for each row, 23 us with all; 8 heads 11.0 us with a quarter, 10.4 half, 11.8 all.
+    auto join = [&](void (*kernel)(DecodeParams), int join_rows) {
         return launch_early(kernel, dim3(C::kMaxCtas, (unsigned)((rows + join_rows - 1) / join_rows)), dim3(kJoinThreads), 0, stream, p);
     };
-    if (rows == 1) return join(fa2_decode_join_kernel<D, kBf16, C, 1>, 1);
-    if (rows == 2) return join(fa2_decode_join_kernel<D, kBf16, C, 2>, 2);
+    if (rows == 1 || items <= kFewItems) return join(fa2_decode_join_kernel<D, kBf16, C, 1>, 1);
+    if (rows == 2 || items <= 2 * kFewItems) return join(fa2_decode_join_kernel<D, kBf16, C, 2>, 2);
     return join(fa2_decode_join_kernel<D, kBf16, C, 4>, 4);
 }
 

@@ -28,7 +28,7 @@
 //
 // Contexts that can only be short (by the block table's width, or the window) take one launch: the
 // CTAs of a thread-block cluster share an item and join their results in distributed shared
-// memory. GB300, one sequence of 1000 tokens, 8 heads: 8.5 us in two launches, 7.1 in one.
+// memory. GB300, one sequence of 1000 tokens, 8 heads: 8.5 us in two launches, 6.8 in one.
 #pragma once
 
 #include <algorithm>
@@ -142,7 +142,8 @@ struct Split {
     // the CTA that unit u belongs to
     __device__ __forceinline__ int owner(int64_t u) const {
         const int64_t longer = rest * (share + 1);
-        return (int)(u < longer ? quotient(u, share + 1) : rest + quotient(u - longer, share));
+        const int64_t c = u < longer ? quotient(u, share + 1) : rest + quotient(u - longer, share);
+        return c < ctas ? (int)c : ctas - 1;
     }
 };
 
@@ -239,7 +240,7 @@ __device__ __forceinline__ bool locate(const DecodeParams& p, int64_t per_seq, i
             for (;; ++b) {
                 range = range_of(p, b);
                 const int units = units_of(blocks_of<kKeys>(range));
-                if (*u_begin < (upto + units) * per_seq) break;
+                if (*u_begin < (upto + units) * per_seq || b + 1 >= b1) break;  // (b1: lengths written meanwhile)
                 upto += units;
             }
         sm.place = Place{upto * per_seq, range, b};
@@ -329,11 +330,13 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
         } else {
             if (u >= u_end) return false;
             while (u >= s.u_seq + units_of(s.nb) * per_seq) {
+                if (s.b + 1 >= c.batch) return false;  // (only with lengths written meanwhile)
                 s.u_seq += units_of(s.nb) * per_seq;
                 s.range = range_of(p, ++s.b);
                 s.nb = blocks_of<kKeys>(s.range);
             }
             const int units = units_of(s.nb);
+            if (units == 0) return false;  // (the same)
             s.item = (int)quotient(u - s.u_seq, units);
             const int64_t u_item = s.u_seq + (int64_t)s.item * units;  // kOver units first, then the blocks
             const int64_t from = u - u_item - kOver, to = u_end - u_item - kOver;
@@ -887,7 +890,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const Dec
 // CTAs are resident at once. 0 where an item's blocks could be more than 4 for each of their warps
 // (8 with more items than resident CTAs, which then balance one another): such a call goes by the
 // lengths themselves, in two launches. GB300, 8 heads of d = 128, bf16, two launches against one:
-// 1 sequence of 1000 8.5 / 7.1 us, of 2000 9.2 / 8.5; 30 of up to 200 11.0 / 8.8; 64 of up to 500
+// 1 sequence of 1000 8.5 / 6.8 us, of 2000 9.2 / 8.5; 30 of up to 200 11.0 / 8.8; 64 of up to 500
 // (8 blocks a warp) 23.4 / 21.5; past the limit 8 of up to 2000 13.0 / 15.2 (8 blocks a warp).
 template <typename C>
 int cluster_ranks(const DecodeParams& p) {

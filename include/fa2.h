@@ -463,7 +463,8 @@ fa2_status fa2_rope_backward(const void* dy, void* dx, const int32_t* positions,
  *              n_kv_heads <= 1024, pages_per_seq * page_size <= 2^30 (FA2_ERR_UNSUPPORTED).
  *
  * The lengths (int32 [batch], device) and the block table are read on the device, so that a
- * captured graph replays with new ones.  What they say is checked there: a length that is
+ * captured graph replays with new ones; like every input they are not to be written while a
+ * call's work may be running.  What they say is checked there: a length that is
  * negative or passes pages_per_seq * page_size counts as 0 or as that product, a page number
  * outside [0, num_pages) is never followed (its tokens are not written, not read back, and
  * masked out of the attention), and either sets the status that fa2_device_status reports as

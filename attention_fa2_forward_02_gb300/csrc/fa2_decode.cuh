@@ -433,33 +433,36 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
             const char* kbase = c.k + head_off;
             const char* vbase = c.v + head_off;
             int64_t off[C::kLooks];
-            uint32_t counts = 0xffffffffu;
+            uint32_t some[C::kLooks];  // the keys that count, as bits
 #pragma unroll
             for (int j = 0; j < C::kLooks; ++j) {
                 Slot s{-1, -1};
                 if (slot[j] >= 0) s = slot_of(c, page[j], slot[j]);
                 off[j] = s.off;
-                const uint32_t some = __ballot_sync(0xffffffffu, s.off >= 0);
-                counts &= some;
+                some[j] = __ballot_sync(0xffffffffu, s.off >= 0);
                 if constexpr (kE4m3) {
                     const int64_t e = s.exp + head_exp;
                     ka[j] = s.off >= 0 ? c.k_exp[e] : 127u;
                     ve[j] = s.off >= 0 ? c.v_exp[e] : 256u;
                 } else {
-                    if (lane == 0) *reinterpret_cast<uint32_t*>(my + fill * C::kStage + 2 * C::kTile + 4 * j) = some;
+                    if (lane == 0) *reinterpret_cast<uint32_t*>(my + fill * C::kStage + 2 * C::kTile + 4 * j) = some[j];
                 }
             }
             constexpr int kStep = 32 / C::kChunks;  // rows a copy instruction of the warp covers
-            if (sixteens && counts == 0xffffffffu) {  // 16 keys after one another in a page
+            if (sixteens) {  // 16 keys lie after one another in a page: the address of one tells the others'
 #pragma unroll
                 for (int r = 0; r < kKeys; r += 16) {
-                    const int64_t o = __shfl_sync(0xffffffffu, off[r / 32], r & 31) + lane_off;
+                    const uint32_t there = (some[r / 32] >> (r & 31)) & 0xffffu;
+                    const int one = there ? __ffs(there) - 1 : 0;
+                    int64_t o = __shfl_sync(0xffffffffu, off[r / 32], (r & 31) + one) - one * c.slot_stride + lane_off;
+                    if (!there) o = 0;
                     const char *ks = kbase + o, *vs = vbase + o;
 #pragma unroll
                     for (int i = 0; i < 16; i += kStep) {
+                        const int bytes = (there >> (i + lane / C::kChunks)) & 1u ? lane_bytes : 0;
                         const uint32_t dst = st + swizzle<C::kChunks>(r + i + lane / C::kChunks, lane % C::kChunks) * 16;
-                        cp_async16(dst, ks, lane_bytes);
-                        cp_async16(dst + C::kTile, vs, lane_bytes);
+                        cp_async16(dst, ks, bytes);
+                        cp_async16(dst + C::kTile, vs, bytes);
                         ks += rows_off;
                         vs += rows_off;
                     }

@@ -234,9 +234,11 @@ PyObject* rope(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const int64_t rot = 2 * f.size(0);
         const int32_t d32 = (int32_t)(d > INT32_MAX ? INT32_MAX : d), r32 = (int32_t)(rot > INT32_MAX ? INT32_MAX : rot);
         fa2_status st;
-        Py_BEGIN_ALLOW_THREADS st = (backward ? g_rope_backward : g_rope)(xp, yp, pp, step, fp, b, h, n, d32, r32, xs, ys, interleaved,
-                                                                         magnitude, code, c.stream);
-        Py_END_ALLOW_THREADS return st;
+        Py_BEGIN_ALLOW_THREADS
+        st = (backward ? g_rope_backward : g_rope)(xp, yp, pp, step, fp, b, h, n, d32, r32, xs, ys, interleaved, magnitude, code,
+                                                   c.stream);
+        Py_END_ALLOW_THREADS
+        return st;
     });
 }
 
@@ -259,9 +261,10 @@ PyObject* kv_append(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const int32_t *table = p.table_at(), *lens = p.lens_at(), *cp = cu ? static_cast<const int32_t*>(c.whole(cu)) : nullptr;
         const int64_t tokens = k.size(0);
         fa2_status st;
-        Py_BEGIN_ALLOW_THREADS st = g_kv_append(cache, kp, vp, ks, vs, table, p.table_stride, p.per_seq, cp, lens, p.batch, tokens, code,
-                                                c.stream);
-        Py_END_ALLOW_THREADS return st;
+        Py_BEGIN_ALLOW_THREADS
+        st = g_kv_append(cache, kp, vp, ks, vs, table, p.table_stride, p.per_seq, cp, lens, p.batch, tokens, code, c.stream);
+        Py_END_ALLOW_THREADS
+        return st;
     });
 }
 
@@ -282,9 +285,10 @@ PyObject* kv_read(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const int64_t strides[3] = {k.stride(0), k.stride(1), k.stride(2)}, longest = k.size(2);
         const int32_t *table = p.table_at(), *lens = p.lens_at();
         fa2_status st;
-        Py_BEGIN_ALLOW_THREADS st = g_kv_read(cache, kp, vp, strides, table, p.table_stride, p.per_seq, lens, p.batch, longest, code,
-                                              c.stream);
-        Py_END_ALLOW_THREADS return st;
+        Py_BEGIN_ALLOW_THREADS
+        st = g_kv_read(cache, kp, vp, strides, table, p.table_stride, p.per_seq, lens, p.batch, longest, code, c.stream);
+        Py_END_ALLOW_THREADS
+        return st;
     });
 }
 
@@ -315,9 +319,10 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
         const int32_t *table = p.table_at(), *lens = p.lens_at();
         const int32_t heads = (int32_t)q.size(1);
         fa2_status st;
-        Py_BEGIN_ALLOW_THREADS st = g_decode(qp, qs, cache, op, lp, table, p.table_stride, p.per_seq, lens, p.batch, heads, window, wp,
-                                             bytes, code, scale, c.stream);
-        Py_END_ALLOW_THREADS return st;
+        Py_BEGIN_ALLOW_THREADS
+        st = g_decode(qp, qs, cache, op, lp, table, p.table_stride, p.per_seq, lens, p.batch, heads, window, wp, bytes, code, scale, c.stream);
+        Py_END_ALLOW_THREADS
+        return st;
     });
 }
 

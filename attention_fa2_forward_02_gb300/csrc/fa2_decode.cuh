@@ -59,6 +59,13 @@ struct Cfg {
     static constexpr int kLooks = (kKeys + 31) / 32;        // keys a lane looks up per block
     static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks a row
     static constexpr int kTile = kKeys * kRowBytes;         // K or V of a block
+    // Rows that are no whole lines of 128 bytes are fetched by halves of lines: left to itself L2
+    // fetches the other half of a row's last line too, which in a token-major cache is another
+    // head's row and gone again before that head's CTA comes to it. Token-major, 8 heads, 21
+    // sequences of up to 65536 tokens in 16 bits: d 96 531 -> 466 us, d 48 420 -> 359, d 32 256 ->
+    // 172; 32 of up to 8192 in e4m3: d 64 50 -> 40, d 96 82 -> 74. Whole lines of 16-bit rows were
+    // 1% slower by halves, so there d is asked; those of e4m3 rows were not.
+    static constexpr bool kHalfLines = kE4m3 || kRowBytes <= 64;
     static constexpr int kInfo = kE4m3 ? kKeys * 8 : 16;    // e4m3: a float2 per key; else the keys that count, as bits
     static constexpr int kStage = 2 * kTile + kInfo;
     static constexpr int kStages = 2;
@@ -84,8 +91,13 @@ __device__ __forceinline__ int swizzle(int r, int c) {
 }
 
 // bytes: 16, or 0 (nothing is read, the 16 bytes are filled with zeros)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+// Always or half: L2 fetches 64 bytes for this and no more
+template <bool kAlways>
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, int bytes, bool half) {
+    if (kAlways || half)
+        asm volatile("cp.async.cg.shared.global.L2::64B [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+    else
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N>
@@ -424,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
     const int64_t lane_off = lane / C::kChunks * c.slot_stride + (lane_bytes ? lane % C::kChunks * 16 : 0);
     const int64_t rows_off = 32 / C::kChunks * c.slot_stride;
     const bool sixteens = c.page_size % 16 == 0;
+    const bool half_lines = c.d * 2 % 128 != 0;
     int fill = 0;                        // the stage to fill next
     uint32_t ka[C::kLooks], ve[C::kLooks];  // scale bytes of the block loaded last; ve 256: the key does not count
     int info_stage = -1;                 // and its stage, while they are not stored
@@ -461,8 +474,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
                     for (int i = 0; i < 16; i += kStep) {
                         const int bytes = (there >> (i + lane / C::kChunks)) & 1u ? lane_bytes : 0;
                         const uint32_t dst = st + swizzle<C::kChunks>(r + i + lane / C::kChunks, lane % C::kChunks) * 16;
-                        cp_async16(dst, ks, bytes);
-                        cp_async16(dst + C::kTile, vs, bytes);
+                        cp_async16<C::kHalfLines>(dst, ks, bytes, half_lines);
+                        cp_async16<C::kHalfLines>(dst + C::kTile, vs, bytes, half_lines);
                         ks += rows_off;
                         vs += rows_off;
                     }
@@ -479,8 +492,8 @@ __global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_d
                     const int bytes = o >= 0 ? lane_bytes : 0;
                     const int64_t at = bytes ? o + lane % C::kChunks * 16 : 0;
                     const uint32_t dst = st + swizzle<C::kChunks>(row, lane % C::kChunks) * 16;
-                    cp_async16(dst, kbase + at, bytes);
-                    cp_async16(dst + C::kTile, vbase + at, bytes);
+                    cp_async16<C::kHalfLines>(dst, kbase + at, bytes, half_lines);
+                    cp_async16<C::kHalfLines>(dst + C::kTile, vbase + at, bytes, half_lines);
                 }
             }
             info_stage = fill;

@@ -51,10 +51,14 @@ template <int D, bool kE4m3, int kTiles>
 struct Cfg {
     static constexpr int kRowBytes = kE4m3 ? D : 2 * D;
     static constexpr int kRows = 8 * kTiles;                // query heads per item
-    // CTAs an SM. Rows of 256 bytes keep memory busy with two, and three read unevenly fast: long
-    // contexts 518 -> 550 us; the others have more to do per byte: e4m3 batch 73 -> 65 us with three.
-    static constexpr int kPerSm = kTiles == 1 && kRowBytes < 256 ? 3 : 2;
+    // CTAs an SM. 16-bit rows keep memory busy with two, and three read unevenly fast (long contexts,
+    // 8 heads: d 128 518 -> 550 us, d 64 266 -> 297); e4m3 has more to do per byte (batch 73 -> 65 us
+    // with three), but 16 heads of d 64 and more need more registers than three leave (d 64 50 -> 57
+    // us, d 128 83 -> 127; d 32 42 -> 36).
+    static constexpr int kPerSm = kE4m3 && (kTiles == 1 || D == 32) ? 3 : 2;
     static constexpr int kMaxCtas = 152 * kPerSm;           // a fixed number: the split depends on the lengths alone
+    // in one launch, where latency is more than memory: 7 windows of 1024 keys, d 64, 9.6 -> 8.8 us
+    static constexpr int kShortPerSm = kTiles == 1 && kRowBytes < 256 ? 3 : kPerSm;
     static constexpr int kKeys = kRowBytes >= 256 ? 16 : (kRowBytes == 128 ? 32 : 64);  // keys per block: 8 KB of K and V
     static constexpr int kLooks = (kKeys + 31) / 32;        // keys a lane looks up per block
     static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks a row
@@ -73,7 +77,7 @@ struct Cfg {
     static constexpr int kQ = kRows * D * 2;                // q as the first product takes it
     static constexpr int kPitch = kE4m3 ? D + 8 : D + 4;    // floats a row at the end of an item (no bank twice)
     static constexpr int smem(int merge_rows) { return kRing + kQ + kWarps * merge_rows * kPitch * 4 + kRows * 4; }
-    static constexpr bool fits(int bytes) { return bytes + 1024 + 256 <= 228 * 1024 / kPerSm; }
+    static constexpr bool fits(int bytes) { return bytes + 1024 + 256 <= 228 * 1024 / kShortPerSm; }
     // rows the warps add up at a time there: as many as find room
     static constexpr int kMergeRows = fits(smem(8)) ? 8 : (fits(smem(4)) ? 4 : 2);
     static constexpr int kMerge = kWarps * kMergeRows * kPitch * 4;
@@ -303,7 +307,8 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& p, uint32_t par
 // kCluster: the CTAs of a cluster of `ranks` share the item blockIdx.x / ranks; nothing is left to
 // the second kernel.
 template <int D, bool kBf16, bool kE4m3, int kTiles, bool kCluster>
-__global__ void __launch_bounds__(kThreads, Cfg<D, kE4m3, kTiles>::kPerSm) fa2_decode_kernel(const DecodeParams p, int ranks) {
+__global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kShortPerSm : Cfg<D, kE4m3, kTiles>::kPerSm)
+    fa2_decode_kernel(const DecodeParams p, int ranks) {
     using C = Cfg<D, kE4m3, kTiles>;
     constexpr bool kMmaBf16 = kBf16 && !kE4m3;
     constexpr int kKeys = C::kKeys, S = C::kStages, kRows = C::kRows, kMt = kKeys / 16, kMR = C::kMergeRows;
@@ -914,9 +919,10 @@ int cluster_ranks(const DecodeParams& p) {
     const int64_t blocks = (keys + C::kKeys - 1) / C::kKeys;
     const int group = p.heads / p.c.hkv;
     const int64_t items = p.c.batch * p.c.hkv * ((group + C::kRows - 1) / C::kRows);
+    const int64_t resident = 152 * C::kShortPerSm;
     int ranks = 1;
-    while (ranks < 8 && items * ranks * 2 <= C::kMaxCtas && blocks > ranks * kWarps) ranks *= 2;
-    const int64_t most = (int64_t)ranks * kWarps * (items > C::kMaxCtas ? 8 : 4);
+    while (ranks < 8 && items * ranks * 2 <= resident && blocks > ranks * kWarps) ranks *= 2;
+    const int64_t most = (int64_t)ranks * kWarps * (items > resident ? 8 : 4);
     return blocks <= most && items * ranks <= INT32_MAX ? ranks : 0;
 }
 
@@ -965,10 +971,10 @@ cudaError_t launch_kind(const DecodeParams& p, cudaStream_t stream, int slot) { 
 }
 
 template <int D, int kTiles>
-size_t workspace_for() {  // either type of cache; the 8-bit one has at least as many CTAs
+size_t workspace_for() {  // either type of cache
     using C = Cfg<D, true, kTiles>;
-    static_assert(C::kMaxCtas >= Cfg<D, false, kTiles>::kMaxCtas, "workspace");
-    return (size_t)C::kMaxCtas * (2 * C::kRows * (D + 2) * sizeof(float) + sizeof(Torn));
+    constexpr int kCtas = std::max(C::kMaxCtas, Cfg<D, false, kTiles>::kMaxCtas);
+    return (size_t)kCtas * (2 * C::kRows * (D + 2) * sizeof(float) + sizeof(Torn));
 }
 
 }  // namespace

@@ -21,10 +21,12 @@
 // many heads finishes last.
 //
 // The 8-bit cache: with key scale 2^a and value scale 2^e per row, the score of a key is
-// x = scale log2(e) 2^a (q . codes) + e, its weight P = 2^(x - m) with m a maximum of x: the
-// value's scale is inside the weight, the second product runs on bare codes, and
-// l = sum P 2^-e counts the softmax's own terms. Codes are exact in half; q (bfloat16) is
-// brought to half exactly by a power of two of its row's largest element.
+// s = scale log2(e) 2^a (q . codes), its weight P = 2^(x - m) with x = s + e and m a maximum of x:
+// the value's scale is inside the weight, and the second product runs on bare codes. The
+// denominator has a maximum ml of its own, l = sum 2^(s - ml): scales lie up to 2^180 apart, and
+// counted as P 2^-e a key of small values would be gone from the sum before 2^-e could bring it
+// back. O = sum P codes / l * 2^(m - ml). Codes are exact in half; q (bfloat16) is brought to half
+// exactly by a power of two of its row's largest element.
 //
 // Contexts that can only be short (by the block table's width, or the window) take one launch: the
 // CTAs of a thread-block cluster share an item and join their results in distributed shared
@@ -45,6 +47,7 @@ constexpr int kJoinThreads = 512;
 constexpr int kFewItems = 4;      // items up to which (twice which) it joins one row (two) per CTA
 constexpr float kRescale = 8.0f;  // the running maximum may lag by this much (base-2 units) before O is rescaled
 constexpr float kLn2 = 0.693147180559945309f;
+constexpr float kNoScore = -3.402823466e38f;  // a maximum of no scores, from which -infinity can be subtracted
 
 // D: the head size's kernel; kTiles: query heads per item / 8.
 template <int D, bool kE4m3, int kTiles>
@@ -178,14 +181,42 @@ __device__ __forceinline__ int blocks_of(Range r) { return (r.len - r.base + kKe
 // What an item of `nb` blocks counts in the division of the work.
 __device__ __forceinline__ int units_of(int nb) { return nb ? nb + kOver : 0; }
 
+// What a share of a row's keys leaves beside its O (relative to 2^m): l relative to 2^ml.
+// (16-bit caches: ml = m.)
+struct __align__(16) Stats {
+    float m, l, ml, unused;
+};
+
+// The factors that bring the O and l of a share to the larger references (m, ml).
+template <bool kE4m3>
+struct Factors {
+    float o, l;
+    __device__ __forceinline__ Factors(const Stats& s, float m, float ml) {
+        o = ex2_approx(s.m - (m == -INFINITY ? 0.f : m));
+        l = kE4m3 ? ex2_approx(s.ml - ml) : o;
+    }
+};
+
+// A row's last step: O = sum P V times scale(), LSE.
+template <bool kE4m3>
+struct Last {
+    float inv, half, lse;
+    __device__ __forceinline__ Last(float m, float ml, float l) {
+        inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
+        half = kE4m3 ? ex2_approx(0.5f * (m - ml)) : 1.f;  // twice: m - ml reaches 120 and more
+        lse = l == 0.f ? -INFINITY : ((kE4m3 ? ml : m) + lg2_approx(l)) * kLn2;
+    }
+    __device__ __forceinline__ float operator()(float a) const { return kE4m3 ? a * half * inv * half : a * inv; }
+};
+
 // Workspace: per CTA two partial results (its first item, if that began before it or ends after
-// it; its last item, if that ends after it), each [kRows][D] floats and then [kRows] (m, l);
+// it; its last item, if that ends after it), each [kRows][D] floats and then [kRows] Stats;
 // behind all of them, per CTA, the item that begins in it and ends in a later CTA. (The second
 // kernel could find that from the lengths, but while the first one fills the SMs it has no place
 // to do so early: e4m3 batch 65.3 -> 68.6 us.)
 template <int D, int kRows>
 __device__ __forceinline__ float* partial(float* ws, int64_t cta, int which) {
-    return ws + (cta * 2 + which) * (kRows * (D + 2));
+    return ws + (cta * 2 + which) * (kRows * (D + 4));
 }
 
 struct __align__(16) Torn {
@@ -280,26 +311,37 @@ struct Segment {
     int item, k0, k1;
 };
 
-// Joins the shares [kRows][D], [kRows] (m, l) that each CTA of the cluster has at `part` in its
+// Joins the shares [kRows][D], [kRows] Stats that each CTA of the cluster has at `part` in its
 // shared memory, in rank order: CTA r writes rows r, r + ranks, ... Every thread of the cluster calls it.
-template <int D, bool kBf16, int kRows>
+template <int D, bool kBf16, bool kE4m3, int kRows>
 __device__ __forceinline__ void join_cluster(const DecodeParams& p, uint32_t part, int ranks, int rank, int rows, int64_t out_row) {
     cluster_sync_all();
     const int d = threadIdx.x;  // D <= kThreads: a column a thread
     for (int r = rank; r < rows; r += ranks) {
         if (d >= D) continue;
-        float big = -INFINITY, a = 0.f, sum = 0.f;
-        for (int k = 0; k < ranks; ++k) big = fmaxf(big, ld_cluster(cluster_map(part + (kRows * D + 2 * r) * 4, k)));
-        const float from = big == -INFINITY ? 0.f : big;
+        auto stats = [&](int k) {
+            const uint32_t at = cluster_map(part + (kRows * D + 4 * r) * 4, k);
+            Stats s;
+            s.m = ld_cluster(at);
+            s.l = ld_cluster(at + 4);
+            s.ml = kE4m3 ? ld_cluster(at + 8) : s.m;
+            return s;
+        };
+        float m = -INFINITY, ml = -INFINITY, a = 0.f, l = 0.f;
         for (int k = 0; k < ranks; ++k) {
-            const uint32_t at = cluster_map(part, k);
-            const float f = ex2_approx(ld_cluster(at + (kRows * D + 2 * r) * 4) - from);
-            sum += f * ld_cluster(at + (kRows * D + 2 * r + 1) * 4);
-            a += f * ld_cluster(at + (r * D + d) * 4);
+            const Stats s = stats(k);
+            m = fmaxf(m, s.m);
+            ml = fmaxf(ml, s.ml);
         }
-        const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
-        if (d < p.c.d) put<kBf16>(p.o, (out_row + r) * p.c.d + d, a * inv);
-        if (d == 0) p.lse[out_row + r] = sum == 0.f ? -INFINITY : (big + lg2_approx(sum)) * kLn2;
+        for (int k = 0; k < ranks; ++k) {
+            const Stats s = stats(k);
+            const Factors<kE4m3> f(s, m, ml);
+            l += f.l * s.l;
+            a += f.o * ld_cluster(cluster_map(part + (r * D + d) * 4, k));
+        }
+        const Last<kE4m3> last(m, ml, l);
+        if (d < p.c.d) put<kBf16>(p.o, (out_row + r) * p.c.d + d, last(a));
+        if (d == 0) p.lse[out_row + r] = last.lse;
     }
     cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
@@ -607,11 +649,13 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
         for (int i = 0; i < D / 16; ++i)
 #pragma unroll
             for (int h = 0; h < kTiles; ++h) o[i][h][0] = o[i][h][1] = o[i][h][2] = o[i][h][3] = 0.f;
-        float m[kTiles][2], l[kTiles][2];  // of heads 2t, 2t+1 (+ 8); l over this lane's keys
+        // of heads 2t, 2t+1 (+ 8); l over this lane's keys, in e4m3 relative to a maximum of its own
+        float m[kTiles][2], l[kTiles][2], ml[kTiles][2];
 #pragma unroll
         for (int h = 0; h < kTiles; ++h) {
             m[h][0] = m[h][1] = -INFINITY;
             l[h][0] = l[h][1] = 0.f;
+            ml[h][0] = ml[h][1] = kNoScore;
         }
 
         for (int i = count(seg, number); i > 0; --i) {
@@ -656,20 +700,39 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         }
                     }
             }
-            // ---- x, the running maximum, P
-            float rv[kMt][2];  // of keys g, g + 8: 2^-(value scale's exponent)
+            // ---- in e4m3 s, and l; x, the running maximum, P
             if constexpr (kE4m3) {
+                float ev[kMt][2];  // of keys g, g + 8: the value scale's exponent, -infinity: masked
 #pragma unroll
                 for (int j = 0; j < kMt; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
                         const float2 f = reinterpret_cast<const float2*>(info)[16 * j + 8 * e + g];
-                        // 2^-f.y out of the low bits of 1.5 2^23 + 127 - f.y; masked: 0
-                        rv[j][e] = __uint_as_float(__float_as_uint(12583039.f - f.y) << 23);
+                        ev[j][e] = f.y;
+                        const float off = f.y == -INFINITY ? -INFINITY : 0.f;
 #pragma unroll
                         for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-                            for (int n = 0; n < 2; ++n) sc[j][h][2 * e + n] = fmaf(sc[j][h][2 * e + n] * f.x, qscale[h][n], f.y);
+                            for (int n = 0; n < 2; ++n) sc[j][h][2 * e + n] = fmaf(sc[j][h][2 * e + n] * f.x, qscale[h][n], off);
+                    }
+#pragma unroll
+                for (int h = 0; h < kTiles; ++h)
+#pragma unroll
+                    for (int n = 0; n < 2; ++n) {
+                        float mx = fmaxf(sc[0][h][n], sc[0][h][2 + n]);
+#pragma unroll
+                        for (int j = 1; j < kMt; ++j) mx = fmax3(mx, sc[j][h][n], sc[j][h][2 + n]);
+                        if (mx > ml[h][n] + kRescale) {  // not -infinity, nor NaN
+                            l[h][n] *= ex2_approx(ml[h][n] - mx);
+                            ml[h][n] = mx;
+                        }
+#pragma unroll
+                        for (int j = 0; j < kMt; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                l[h][n] += ex2_approx(sc[j][h][2 * e + n] - ml[h][n]);
+                                sc[j][h][2 * e + n] += ev[j][e];
+                            }
                     }
             } else {
 #pragma unroll
@@ -714,7 +777,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         const float m_new = fmaxf(m[h][n], mx[h][n]);
                         const float f = m_new == -INFINITY ? 1.f : ex2_approx(m[h][n] - m_new);
                         m[h][n] = m_new;
-                        l[h][n] *= f;
+                        if constexpr (!kE4m3) l[h][n] *= f;
 #pragma unroll
                         for (int d = 0; d < D / 16; ++d) {
                             o[d][h][n] *= f;
@@ -733,7 +796,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         for (int n = 0; n < 2; ++n) {
                             float& x = sc[j][h][2 * e + n];
                             x = ex2_approx(x - (m[h][n] == -INFINITY ? 0.f : m[h][n]));
-                            l[h][n] += kE4m3 ? x * rv[j][e] : x;
+                            if constexpr (!kE4m3) l[h][n] += x;
                         }
                         pf[h][e] = transpose8(pack2<kMmaBf16>(sc[j][h][2 * e], sc[j][h][2 * e + 1]));
                     }
@@ -779,7 +842,16 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
 #pragma unroll
             for (int n = 0; n < 2; ++n)
 #pragma unroll
-                for (int off = 4; off < 32; off <<= 1) l[h][n] += __shfl_xor_sync(0xffffffffu, l[h][n], off);
+                for (int off = 4; off < 32; off <<= 1) {
+                    float l2 = __shfl_xor_sync(0xffffffffu, l[h][n], off);
+                    if constexpr (kE4m3) {
+                        const float ml2 = __shfl_xor_sync(0xffffffffu, ml[h][n], off), big = fmaxf(ml[h][n], ml2);
+                        l[h][n] *= ex2_approx(ml[h][n] - big);
+                        l2 *= ex2_approx(ml2 - big);
+                        ml[h][n] = big;
+                    }
+                    l[h][n] += l2;
+                }
 #pragma unroll
         for (int round = 0; round < kRows / kMR; ++round) {  // rows kMR round ..; lane t has heads 2t, 2t+1 (+ 8)
             if (kMR * round >= rows) break;
@@ -797,7 +869,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                             *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[d][h][n], o[d][h][2 + n]);
                         }
                     }
-                    if (g == 0) *reinterpret_cast<float2*>(row + D) = make_float2(m[h][n], l[h][n]);
+                    if (g == 0) *reinterpret_cast<Stats*>(row + D) = Stats{m[h][n], l[h][n], kE4m3 ? ml[h][n] : m[h][n], 0.f};
                 }
             }
             __syncthreads();
@@ -806,35 +878,39 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
             for (int n = warp / kShare; n < kMR; n += kWarps / kShare) {
                 const int r = kMR * round + n;
                 if (r >= rows) break;
-                float big = -INFINITY;
+                float big = -INFINITY, big_l = -INFINITY;
 #pragma unroll
-                for (int w = 0; w < kWarps; ++w) big = fmaxf(big, merge[(w * kMR + n) * C::kPitch + D]);
-                const float from = big == -INFINITY ? 0.f : big;
+                for (int w = 0; w < kWarps; ++w) {
+                    const Stats s = *reinterpret_cast<const Stats*>(merge + (w * kMR + n) * C::kPitch + D);
+                    big = fmaxf(big, s.m);
+                    big_l = fmaxf(big_l, s.ml);
+                }
                 float f[kWarps], sum = 0.f;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
-                    const float* row = merge + (w * kMR + n) * C::kPitch;
-                    f[w] = ex2_approx(row[D] - from);
-                    sum += f[w] * row[D + 1];
+                    const Stats s = *reinterpret_cast<const Stats*>(merge + (w * kMR + n) * C::kPitch + D);
+                    const Factors<kE4m3> to(s, big, big_l);
+                    f[w] = to.o;
+                    sum += to.l * s.l;
                 }
-                const float inv = !whole ? 1.f : (sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum));
+                const Last<kE4m3> last(big, big_l, sum);
 #pragma unroll
                 for (int d = lane + 32 * (warp % kShare); d < D; d += 32 * kShare) {
                     float a = 0.f;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) a += f[w] * merge[(w * kMR + n) * C::kPitch + d];
                     if (!whole) part[r * D + d] = a;
-                    else if (d < c.d) put<kBf16>(p.o, (out_row + r) * c.d + d, a * inv);
+                    else if (d < c.d) put<kBf16>(p.o, (out_row + r) * c.d + d, last(a));
                 }
                 if (lane == 0 && warp % kShare == 0) {
-                    if (!whole) *reinterpret_cast<float2*>(part + kRows * D + 2 * r) = make_float2(big, sum);
-                    else p.lse[out_row + r] = sum == 0.f ? -INFINITY : (big + lg2_approx(sum)) * kLn2;
+                    if (!whole) reinterpret_cast<Stats*>(part + kRows * D)[r] = Stats{big, sum, big_l, 0.f};
+                    else p.lse[out_row + r] = last.lse;
                 }
             }
             __syncthreads();
         }
         if constexpr (kCluster) {
-            if (ranks > 1) join_cluster<D, kBf16, kRows>(p, smem_u32(part), ranks, rank, rows, out_row);
+            if (ranks > 1) join_cluster<D, kBf16, kE4m3, kRows>(p, smem_u32(part), ranks, rank, rows, out_row);
             return;
         }
         first_item = false;
@@ -848,12 +924,13 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
 // Joins the items that several CTAs worked on: CTA (x, y) rows kJoinRows y .. of the item that
 // begins in CTA x of the first kernel, if it ends in a later one. kShare warps a row, each for
 // every kShare-th partial result, its lanes for the columns.
-template <int D, bool kBf16, typename C, int kJoinRows>
+template <int D, bool kBf16, bool kE4m3, typename C, int kJoinRows>
 __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const DecodeParams p) {
     constexpr int kRows = C::kRows;
     constexpr int kShare = kJoinThreads / 32 / kJoinRows;
     constexpr int kCols = D / 32;  // columns a lane
-    __shared__ float parts[kJoinThreads / 32][D + 2];
+    __shared__ float parts[kJoinThreads / 32][D];
+    __shared__ Stats stats[kJoinThreads / 32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     grid_begin();
     const Torn item = *torn<C, D>(p.workspace, blockIdx.x);
@@ -862,39 +939,42 @@ __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const Dec
     const int first = blockIdx.x, n = item.last_cta - first + 1, which = item.which;
     const int share = warp % kShare, r = blockIdx.y * kJoinRows + warp / kShare;
     const bool on = r < rows;
-    float m = -INFINITY, sum = 0.f, a[kCols] = {};
+    float m = -INFINITY, ml = -INFINITY, l = 0.f, a[kCols] = {};
     if (on) {
 #pragma unroll 4
         for (int k = share; k < n; k += kShare) {
             const float* s = partial<D, kRows>(p.workspace, first + k, k == 0 ? which : 0);
-            const float2 ml = *reinterpret_cast<const float2*>(s + kRows * D + 2 * r);
-            const float big = fmaxf(m, ml.x), ref = big == -INFINITY ? 0.f : big;
-            const float old = ex2_approx(m - ref), f = ex2_approx(ml.x - ref);
-            m = big;
-            sum = sum * old + f * ml.y;
+            const Stats st = reinterpret_cast<const Stats*>(s + kRows * D)[r];
+            const Stats so_far{m, l, ml, 0.f};
+            m = fmaxf(m, st.m);
+            ml = fmaxf(ml, st.ml);
+            const Factors<kE4m3> old(so_far, m, ml), add(st, m, ml);
+            l = l * old.l + add.l * st.l;
 #pragma unroll
-            for (int i = 0; i < kCols; ++i) a[i] = a[i] * old + f * s[r * D + lane + 32 * i];
+            for (int i = 0; i < kCols; ++i) a[i] = a[i] * old.o + add.o * s[r * D + lane + 32 * i];
         }
 #pragma unroll
         for (int i = 0; i < kCols; ++i) parts[warp][lane + 32 * i] = a[i];
-        if (lane == 0) {
-            parts[warp][D] = m;
-            parts[warp][D + 1] = sum;
-        }
+        if (lane == 0) stats[warp] = Stats{m, l, ml, 0.f};
     }
     __syncthreads();
     if (!on || share != 0) return;
-    float big = -INFINITY, f[kShare];
-#pragma unroll
-    for (int w = 0; w < kShare; ++w) big = fmaxf(big, parts[warp + w][D]);
-    const float ref = big == -INFINITY ? 0.f : big;
-    sum = 0.f;
+    m = ml = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kShare; ++w) {
-        f[w] = ex2_approx(parts[warp + w][D] - ref);
-        sum += f[w] * parts[warp + w][D + 1];
+        m = fmaxf(m, stats[warp + w].m);
+        ml = fmaxf(ml, stats[warp + w].ml);
     }
-    const float inv = sum > 0.f ? 1.f / sum : (sum == 0.f ? 0.f : sum);
+    float f[kShare];
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kShare; ++w) {
+        const Stats st = stats[warp + w];
+        const Factors<kE4m3> to(st, m, ml);
+        f[w] = to.o;
+        l += to.l * st.l;
+    }
+    const Last<kE4m3> last(m, ml, l);
     const int64_t row = (int64_t)item.out_row + r;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) {
@@ -902,9 +982,9 @@ __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const Dec
         float v = 0.f;
 #pragma unroll
         for (int w = 0; w < kShare; ++w) v += f[w] * parts[warp + w][d];
-        if (d < p.c.d) put<kBf16>(p.o, row * p.c.d + d, v * inv);
+        if (d < p.c.d) put<kBf16>(p.o, row * p.c.d + d, last(v));
     }
-    if (lane == 0) p.lse[row] = sum == 0.f ? -INFINITY : (big + lg2_approx(sum)) * kLn2;
+    if (lane == 0) p.lse[row] = last.lse;
 }
 
 // The cluster size of a call in one launch: the most CTAs per item, up to 8, with which all items'
@@ -952,9 +1032,9 @@ cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
     auto join = [&](void (*kernel)(DecodeParams), int join_rows) {
         return launch_early(kernel, dim3(C::kMaxCtas, (unsigned)((rows + join_rows - 1) / join_rows)), dim3(kJoinThreads), 0, stream, p);
     };
-    if (rows == 1 || items <= kFewItems) return join(fa2_decode_join_kernel<D, kBf16, C, 1>, 1);
-    if (rows == 2 || items <= 2 * kFewItems) return join(fa2_decode_join_kernel<D, kBf16, C, 2>, 2);
-    return join(fa2_decode_join_kernel<D, kBf16, C, 4>, 4);
+    if (rows == 1 || items <= kFewItems) return join(fa2_decode_join_kernel<D, kBf16, kE4m3, C, 1>, 1);
+    if (rows == 2 || items <= 2 * kFewItems) return join(fa2_decode_join_kernel<D, kBf16, kE4m3, C, 2>, 2);
+    return join(fa2_decode_join_kernel<D, kBf16, kE4m3, C, 4>, 4);
 }
 
 // Up to 8 query heads a key-value head: one column tile, else two.
@@ -974,7 +1054,7 @@ template <int D, int kTiles>
 size_t workspace_for() {  // either type of cache
     using C = Cfg<D, true, kTiles>;
     constexpr int kCtas = std::max(C::kMaxCtas, Cfg<D, false, kTiles>::kMaxCtas);
-    return (size_t)kCtas * (2 * C::kRows * (D + 2) * sizeof(float) + sizeof(Torn));
+    return (size_t)kCtas * (2 * C::kRows * (D + 4) * sizeof(float) + sizeof(Torn));
 }
 
 }  // namespace

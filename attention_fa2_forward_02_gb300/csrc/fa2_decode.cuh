@@ -25,8 +25,9 @@
 // the value's scale is inside the weight, and the second product runs on bare codes. The
 // denominator has a maximum ml of its own, l = sum 2^(s - ml): scales lie up to 2^180 apart, and
 // counted as P 2^-e a key of small values would be gone from the sum before 2^-e could bring it
-// back. O = sum P codes / l * 2^(m - ml). Codes are exact in half; q (bfloat16) is brought to half
-// exactly by a power of two of its row's largest element.
+// back. O = sum P codes / l * 2^(m - ml). Rows of zeros are stored with e = 0, often far above the
+// others' and next to nothing in O: they do not raise m. Codes are exact in half; q (bfloat16) is
+// brought to half exactly by a power of two of its row's largest element.
 //
 // Contexts that can only be short (by the block table's width, or the window) take one launch: the
 // CTAs of a thread-block cluster share an item and join their results in distributed shared
@@ -757,19 +758,55 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                 }
             }
             float mx[kTiles][2];
-            bool grow = false;
+            auto grows = [&]() {  // the block's maxima; whether one is well above the running maximum
+                bool grow = false;
 #pragma unroll
-            for (int h = 0; h < kTiles; ++h)
+                for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-                for (int n = 0; n < 2; ++n) {
-                    mx[h][n] = fmaxf(sc[0][h][n], sc[0][h][2 + n]);
+                    for (int n = 0; n < 2; ++n) {
+                        mx[h][n] = fmaxf(sc[0][h][n], sc[0][h][2 + n]);
 #pragma unroll
-                    for (int j = 1; j < kMt; ++j) mx[h][n] = fmax3(mx[h][n], sc[j][h][n], sc[j][h][2 + n]);
+                        for (int j = 1; j < kMt; ++j) mx[h][n] = fmax3(mx[h][n], sc[j][h][n], sc[j][h][2 + n]);
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1) mx[h][n] = fmaxf(mx[h][n], __shfl_xor_sync(0xffffffffu, mx[h][n], off));
-                    grow |= mx[h][n] > m[h][n] + kRescale || (m[h][n] == -INFINITY && mx[h][n] > -INFINITY);
+                        for (int off = 4; off < 32; off <<= 1) mx[h][n] = fmaxf(mx[h][n], __shfl_xor_sync(0xffffffffu, mx[h][n], off));
+                        grow |= mx[h][n] > m[h][n] + kRescale || (m[h][n] == -INFINITY && mx[h][n] > -INFINITY);
+                    }
+                return __any_sync(0xffffffffu, grow);
+            };
+            bool grow = grows();
+            if constexpr (kE4m3) {
+                // Looked for only where a maximum would grow: the first blocks, and rows of zeros that
+                // stand out. (For every block it would be the stage's values read once more.)
+                if (grow) {
+                    uint32_t zeros[C::kLooks];  // as bits: keys that count, whose value codes are all 0
+                    uint32_t some = 0;
+#pragma unroll
+                    for (int j = 0; j < C::kLooks; ++j) {
+                        const int r = lane + 32 * j;
+                        uint32_t any = 0;
+#pragma unroll
+                        for (int i = 0; i < C::kChunks; ++i) {
+                            const uint4 w = *reinterpret_cast<const uint4*>(info - C::kTile + swizzle<C::kChunks>(r, i) * 16);
+                            any |= w.x | w.y | w.z | w.w;
+                        }
+                        const bool counts = reinterpret_cast<const float2*>(info)[r].y > -INFINITY;
+                        zeros[j] = __ballot_sync(0xffffffffu, counts && (any & 0x7f7f7f7fu) == 0);
+                        some |= zeros[j];
+                    }
+                    if (some) {
+#pragma unroll
+                        for (int j = 0; j < kMt; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e)
+                                if ((zeros[j / 2] >> (16 * (j % 2) + 8 * e + g)) & 1u) {
+#pragma unroll
+                                    for (int h = 0; h < kTiles; ++h) sc[j][h][2 * e] = sc[j][h][2 * e + 1] = -INFINITY;
+                                }
+                        grow = grows();
+                    }
                 }
-            if (__any_sync(0xffffffffu, grow)) {
+            }
+            if (grow) {
 #pragma unroll
                 for (int h = 0; h < kTiles; ++h)
 #pragma unroll

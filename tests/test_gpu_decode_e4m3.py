@@ -9,6 +9,7 @@ from oracle import serving as S
 from tests import gpu_util as G
 from tests.paged import Cache
 from tests.test_gpu_decode import check, workspace
+from tests.tolerance import UNIT_ROUNDOFF
 
 pytestmark = pytest.mark.gpu
 
@@ -67,3 +68,69 @@ def test_rows_of_small_values_count_in_the_denominator(n, at, wide, d, group):
     ones = synth.to_storage(np.ones((1, group, d)), "bf16")
     o, lse = attend(c, ones, 1 / d, group)
     check(c, np.ones((1, group, d)), o, lse, group, 1 / d)
+
+
+def appended(tag, k, v, page=16, table_pages=None):
+    """A cache of one sequence, its rows k, v [tokens, 1, d] (bf16 storage) written by fa2_kv_append."""
+    import torch
+    n, _, d = k.shape
+    c = Cache(tag, [n], page, 1, d, "bf16", True, table_pages=table_pages)
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    binding.fa2_kv_append(*c.pools(), G.to_device(k, "bf16"), G.to_device(v, "bf16"), c.table_dev, c.lens_dev, cu_new=cu, **c.exps())
+    for side in "kv":
+        codes = c.dev[side].contiguous().view(torch.uint8).cpu().numpy()
+        c.host[side] = S.e4m3_values()[codes] * 2.0 ** (c.exp[side].cpu().numpy()[..., None].astype(np.float64) - 127)
+    return c
+
+
+def check_closely(c, q64, o, lse, scale, step=2.0 ** -11, least=2.0 ** -25):
+    """As test_gpu_decode.check, but the weights that set the maximum are those of rows with a code that is not 0: a weight
+    W_j = 2^(s_j + e_j) is off by `step` of itself and by `least` of the largest such weight W_*, so O, whose denominator is
+    L = sum 2^s_j, by (least W_* / L) sum_j |v_j| 2^-e_j beside the errors that are in proportion to P_j |v_j|."""
+    k, v = c.rows("k", 0)[0][:, 0], c.rows("v", 0)[0][:, 0]
+    e_j, n = c.value_exps(0, 0), len(k)
+    for h in range(q64.shape[1]):
+        ref, rl, w, e = S.decode_row(q64[0, h], k, v, scale)
+        s = scale * (k @ q64[0, h]) / math.log(2)
+        top = s.max()
+        filled = np.abs(v).max(1) > 0
+        largest = np.exp2((s + e_j)[filled].max() - top) if filled.any() else 0.0
+        floor = least * largest / np.exp2(s - top).sum() * (np.exp2(-e_j) @ np.abs(v))
+        score = (c.d + 8) * 2.0 ** -24 * e + 2.0 ** -21
+        bound = (step + 2 * score + 2 * n * 2.0 ** -24) * w + floor + UNIT_ROUNDOFF["bf16"] * np.abs(ref)
+        diff = np.abs(G.to_f64(o)[0, h] - ref)
+        assert np.all(diff <= bound), f"head {h}: worst {np.max(diff / np.maximum(bound, 1e-300)):.3g} times its bound"
+        assert abs(G.to_f64(lse)[0, h] - rl) <= score + n * 2.0 ** -24 + 2.0 ** -23 * (abs(rl) + e)
+
+
+def rows_with_a_sink(tag, n, d, at, nats, v_scale):
+    """q, k, v of which key `at` scores about `nats` more than an average key and has zero values."""
+    q64 = synth.widen(synth.tensor(tag + "/q", (1, 1, d), "bf16"), "bf16")
+    k64 = synth.widen(synth.tensor(tag + "/k", (n, 1, d), "bf16"), "bf16")
+    v64 = synth.widen(synth.tensor(tag + "/v", (n, 1, d), "bf16"), "bf16") * v_scale
+    k64[at, 0] = q64[0, 0] * (nats * math.sqrt(d) / (q64[0, 0] @ q64[0, 0]))
+    v64[at] = 0
+    return q64, synth.to_storage(k64, "bf16"), synth.to_storage(v64, "bf16")
+
+
+@pytest.mark.parametrize("v_exp", [0, -6, -14, -16, -18, -40])
+@pytest.mark.parametrize("nats", [0, 8, 10, 12, 30])
+@pytest.mark.parametrize("n,at,d,wide", [(64, 0, 64, None), (64, 37, 32, None), (700, 699, 128, None), (5000, 0, 64, 1000)])
+def test_zero_value_rows_do_not_hide_the_others(n, at, d, wide, nats, v_exp):
+    """A key without values (an attention sink, padding) is stored with scale 2^0: whatever its score and the size of the other
+    values, the others keep their precision."""
+    G.require_gpu()
+    q64, k, v = rows_with_a_sink(f"sink/{n}/{d}", n, d, at, nats, 2.0 ** v_exp)
+    c = appended("sink", k, v, table_pages=wide)
+    o, lse = attend(c, synth.to_storage(q64, "bf16"), 1 / math.sqrt(d), 1)
+    check_closely(c, q64, o, lse, 1 / math.sqrt(d))
+
+
+@pytest.mark.parametrize("d", [16, 64, 128])
+def test_only_zero_values(d):
+    G.require_gpu()
+    q64, k, v = rows_with_a_sink("nothing", 300, d, 0, 3, 0.0)
+    c = appended("nothing", k, v)
+    o, lse = attend(c, synth.to_storage(q64, "bf16"), 1 / math.sqrt(d), 1)
+    assert not G.to_f64(o).any()
+    check_closely(c, q64, o, lse, 1 / math.sqrt(d))

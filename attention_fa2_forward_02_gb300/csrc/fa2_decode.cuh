@@ -723,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         float mx = fmaxf(sc[0][h][n], sc[0][h][2 + n]);
 #pragma unroll
                         for (int j = 1; j < kMt; ++j) mx = fmax3(mx, sc[j][h][n], sc[j][h][2 + n]);
-                        if (mx > ml[h][n] + kRescale) {  // not -infinity, nor NaN
+                        if (mx - ml[h][n] > kRescale) {  // mx -infinity: not
                             l[h][n] *= ex2_approx(ml[h][n] - mx);
                             ml[h][n] = mx;
                         }
@@ -769,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         for (int j = 1; j < kMt; ++j) mx[h][n] = fmax3(mx[h][n], sc[j][h][n], sc[j][h][2 + n]);
 #pragma unroll
                         for (int off = 4; off < 32; off <<= 1) mx[h][n] = fmaxf(mx[h][n], __shfl_xor_sync(0xffffffffu, mx[h][n], off));
-                        grow |= mx[h][n] > m[h][n] + kRescale || (m[h][n] == -INFINITY && mx[h][n] > -INFINITY);
+                        grow |= mx[h][n] - m[h][n] > kRescale;  // exact where it matters; m + kRescale is not, past 2^26
                     }
                 return __any_sync(0xffffffffu, grow);
             };

@@ -1,0 +1,37 @@
+"""Scores at the ends of their range, in the attention of one new token: against the float64 oracle."""
+import numpy as np
+import pytest
+
+from attention_fa2_forward_02_gb300 import binding, synth
+from tests import gpu_util as G
+from tests.paged import Cache
+from tests.test_gpu_decode import workspace
+
+pytestmark = pytest.mark.gpu
+
+
+def test_scores_a_step_apart_at_2_27():
+    """fp16 keys whose products with q are 2^27 + 16 j, float32's steps there, j = 1 .. 4 for a quarter of the keys each: in blocks
+    of 64 keys that four warps take in turn, each warp meets all four.  The last quarter takes all, and no weight may leave
+    half's range on the way."""
+    torch = G.require_gpu()
+    n, hkv, d = 1024, 304, 32
+    c = Cache("scores/steps", [n], 64, hkv, d, "f16")
+    q64, k64 = np.zeros((1, hkv, d)), np.zeros((c.pages, hkv, 64, d))
+    q64[..., :9] = 4096.0
+    q64[..., 9] = 1.0
+    for block in range(16):
+        row = np.zeros(d)
+        row[:8], row[9] = 4096.0, 16.0 * (1 + block // 4)  # 2^27 and the step
+        k64[c.table[0, block], :] = row
+    c.host["k"] = k64
+    c.dev["k"] = G.to_device(synth.to_storage(k64, "f16"), "f16")
+    o, lse = G.empty((1, hkv, d), "f16"), torch.empty(1, hkv, device="cuda")
+    q = G.to_device(synth.to_storage(q64, "f16"), "f16")
+    for scale in (0.6931472, 0.6931471, 1.3862944):
+        o.fill_(float("nan"))
+        binding.fa2_decode(q, *c.pools(), o, lse, c.table_dev, c.lens_dev, workspace(1, hkv, hkv, d), scale)
+        binding.fa2_device_status()
+        got, last = G.to_f64(o)[0], c.rows("v", 0)[0][768:]
+        assert np.isfinite(got).all() and torch.isfinite(lse).all()
+        assert np.all(np.abs(got - last.mean(0)) <= (2 * 2.0 ** -11 + 512 * 2.0 ** -24) * np.abs(last).max(0))  # weights, output; sums

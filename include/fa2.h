@@ -535,11 +535,11 @@ fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, cons
  *   window     >= 0
  *   workspace  fa2_decode_workspace_size bytes, 16-byte aligned, contents do not matter;
  *              calls whose GPU work may overlap need one each
- * float32 scores, softmax statistics and sums; the probabilities are rounded to 16 bits
- * (FA2_CACHE_SAME: dtype; FA2_CACHE_E4M3: half) before the product with V; in half, weights
- * below 2^-25 of the row's largest count as 0 there. In FA2_CACHE_E4M3 these weights have the
- * value row's scale in them (rows whose codes are all 0 are not among the largest); the
- * denominator and the LSE do not.
+ * float32 scores, softmax statistics and sums; the product with V takes each probability as two
+ * 16-bit numbers (FA2_CACHE_SAME: dtype; FA2_CACHE_E4M3: half), its rounding and what that left
+ * off: within 2^-16 (BF16) or 2^-22 of it. In half, weights below 2^-32 of the row's largest
+ * count as 0 there; in FA2_CACHE_E4M3 these weights have the value row's scale in them (rows
+ * whose codes are all 0 are not among the largest), the denominator and the LSE do not.
  * The keys of all sequences and heads are divided evenly over the CTAs, whatever the lengths
  * (contexts that pages_per_seq * page_size or the window keep short: head by head, over the
  * CTAs of a cluster); a row divided between CTAs is joined from float32 partial results in a

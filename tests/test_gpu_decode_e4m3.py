@@ -83,21 +83,27 @@ def appended(tag, k, v, page=16, table_pages=None):
     return c
 
 
-def check_closely(c, q64, o, lse, scale, step=2.0 ** -11, least=2.0 ** -25):
-    """As test_gpu_decode.check, but the weights that set the maximum are those of rows with a code that is not 0: a weight
-    W_j = 2^(s_j + e_j) is off by `step` of itself and by `least` of the largest such weight W_*, so O, whose denominator is
-    L = sum 2^s_j, by (least W_* / L) sum_j |v_j| 2^-e_j beside the errors that are in proportion to P_j |v_j|."""
-    k, v = c.rows("k", 0)[0][:, 0], c.rows("v", 0)[0][:, 0]
-    e_j, n = c.value_exps(0, 0), len(k)
+def check_closely(c, q64, o, lse, scale, group=1):
+    """As test_gpu_decode.check for sequence 0, but with the weights' rounding in two parts, and the weights that set the maximum
+    those of rows with an element that is not 0.  A weight W_j = 2^(s_j + e_j) goes into the product as two 16-bit numbers, the
+    second the rounded rest of the first: off by u^2 W_j, u the type's roundoff.  In half also by half a step of 2^-24 of a
+    reference that is 2^7 below the largest weight W_* or lower: 2^-32 W_*, so O, whose denominator is L = sum 2^s_j, by
+    (2^-32 W_* / L) sum_j |v_j| 2^-e_j."""
+    half = c.e4m3 or c.dtype == "f16"
+    step = UNIT_ROUNDOFF["f16" if half else "bf16"] ** 2
     for h in range(q64.shape[1]):
+        k, v = c.rows("k", 0)[0][:, h // group], c.rows("v", 0)[0][:, h // group]
+        e_j, n = c.value_exps(0, h // group), len(k)
         ref, rl, w, e = S.decode_row(q64[0, h], k, v, scale)
         s = scale * (k @ q64[0, h]) / math.log(2)
         top = s.max()
         filled = np.abs(v).max(1) > 0
-        largest = np.exp2((s + e_j)[filled].max() - top) if filled.any() else 0.0
-        floor = least * largest / np.exp2(s - top).sum() * (np.exp2(-e_j) @ np.abs(v))
+        largest = np.exp2((s + e_j)[filled].max() - top) if half and filled.any() else 0.0
+        floor = 2.0 ** -32 * largest / np.exp2(s - top).sum() * (np.exp2(-e_j) @ np.abs(v))
         score = (c.d + 8) * 2.0 ** -24 * e + 2.0 ** -21
-        bound = (step + 2 * score + 2 * n * 2.0 ** -24) * w + floor + UNIT_ROUNDOFF["bf16"] * np.abs(ref)
+        bound = (step + 2 * score + 2 * n * 2.0 ** -24) * w + floor + UNIT_ROUNDOFF[c.dtype] * np.abs(ref)
+        if c.dtype == "f16":
+            bound = bound + 2.0 ** -25  # half a step of the smallest halves
         diff = np.abs(G.to_f64(o)[0, h] - ref)
         assert np.all(diff <= bound), f"head {h}: worst {np.max(diff / np.maximum(bound, 1e-300)):.3g} times its bound"
         assert abs(G.to_f64(lse)[0, h] - rl) <= score + n * 2.0 ** -24 + 2.0 ** -23 * (abs(rl) + e)

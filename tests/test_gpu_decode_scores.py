@@ -1,4 +1,6 @@
 """Scores at the ends of their range, in the attention of one new token: against the float64 oracle."""
+import math
+
 import numpy as np
 import pytest
 
@@ -6,6 +8,7 @@ from attention_fa2_forward_02_gb300 import binding, synth
 from tests import gpu_util as G
 from tests.paged import Cache
 from tests.test_gpu_decode import workspace
+from tests.test_gpu_decode_e4m3 import attend, check_closely
 
 pytestmark = pytest.mark.gpu
 
@@ -35,3 +38,15 @@ def test_scores_a_step_apart_at_2_27():
         got, last = G.to_f64(o)[0], c.rows("v", 0)[0][768:]
         assert np.isfinite(got).all() and torch.isfinite(lse).all()
         assert np.all(np.abs(got - last.mean(0)) <= (2 * 2.0 ** -11 + 512 * 2.0 ** -24) * np.abs(last).max(0))  # weights, output; sums
+
+
+@pytest.mark.parametrize("dtype,e4m3", [("bf16", False), ("f16", False), ("bf16", True), ("f16", True)])
+@pytest.mark.parametrize("d,group", [(32, 1), (64, 16), (128, 4), (128, 12), (80, 8)])
+@pytest.mark.parametrize("n,wide", [(16, None), (40, None), (200, None), (3000, 1000)])
+def test_weights_keep_more_than_16_bits(n, wide, d, group, dtype, e4m3):
+    """Scores so small that a weight rounded to 16 bits alone would be the largest error by far."""
+    G.require_gpu()
+    c = Cache(f"scores/weights/{n}", [n], 16, 1, d, dtype, e4m3, table_pages=wide)
+    q = synth.tensor("scores/weights/q", (1, group, d), dtype, scale=2.0 ** -6)
+    o, lse = attend(c, q, 1 / math.sqrt(d), group)
+    check_closely(c, synth.widen(q, dtype), o, lse, 1 / math.sqrt(d), group)

@@ -653,6 +653,19 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
             qscale[h][0] = q_scale[8 * h + 2 * t];
             qscale[h][1] = q_scale[8 * h + 2 * t + 1];
         }
+        // e4m3: a product with q in half, 2^31 at most, times the key's scale (to 2^126) and the row's
+        // (2^-126 to 2^113 and the softmax's) must not overflow on the way to a score that does not.
+        // The scales are multiplied first, a row's of more than 1 last.
+        bool large_q = false;
+        if constexpr (kE4m3) {
+#pragma unroll
+            for (int h = 0; h < kTiles; ++h)
+#pragma unroll
+                for (int n = 0; n < 2; ++n) {
+                    large_q |= qscale[h][n] > 1.f;
+                    qscale[h][n] = fminf(qscale[h][n], 1.f);
+                }
+        }
 
         float o[D / 16][kTiles][4];
 #pragma unroll
@@ -723,8 +736,21 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
 #pragma unroll
                         for (int h = 0; h < kTiles; ++h)
 #pragma unroll
-                            for (int n = 0; n < 2; ++n) sc[j][h][2 * e + n] = fmaf(sc[j][h][2 * e + n] * f.x, qscale[h][n], off);
+                            for (int n = 0; n < 2; ++n) sc[j][h][2 * e + n] = fmaf(sc[j][h][2 * e + n], f.x * qscale[h][n], off);
                     }
+                if (large_q) {
+#pragma unroll
+                    for (int h = 0; h < kTiles; ++h)
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const float rest = fmaxf(q_scale[8 * h + 2 * t + n], 1.f);
+#pragma unroll
+                            for (int j = 0; j < kMt; ++j) {
+                                sc[j][h][n] *= rest;
+                                sc[j][h][2 + n] *= rest;
+                            }
+                        }
+                }
 #pragma unroll
                 for (int h = 0; h < kTiles; ++h)
 #pragma unroll

@@ -8,7 +8,7 @@ from attention_fa2_forward_02_gb300 import binding, synth
 from tests import gpu_util as G
 from tests.paged import Cache
 from tests.test_gpu_decode import workspace
-from tests.test_gpu_decode_e4m3 import attend, check_closely
+from tests.test_gpu_decode_e4m3 import appended, attend, check_closely
 
 pytestmark = pytest.mark.gpu
 
@@ -50,3 +50,30 @@ def test_weights_keep_more_than_16_bits(n, wide, d, group, dtype, e4m3):
     q = synth.tensor("scores/weights/q", (1, group, d), dtype, scale=2.0 ** -6)
     o, lse = attend(c, q, 1 / math.sqrt(d), group)
     check_closely(c, synth.widen(q, dtype), o, lse, 1 / math.sqrt(d), group)
+
+
+@pytest.mark.parametrize("q_exp,k_exp", [(-118, 118), (-60, 60), (-100, 105), (60, -60), (90, -60), (20, 0), (-130, 100)])
+@pytest.mark.parametrize("d,wide", [(64, None), (128, 500)])
+def test_small_queries_and_large_keys(q_exp, k_exp, d, wide):
+    """bf16 rows whose sizes make up for one another in an 8-bit cache: neither half of a score's scale may overflow alone."""
+    G.require_gpu()
+    n = 300
+    q64 = synth.widen(synth.tensor("scores/small/q", (1, 1, d), "bf16"), "bf16") * 2.0 ** q_exp
+    k64 = synth.widen(synth.tensor("scores/small/k", (n, 1, d), "bf16"), "bf16") * 2.0 ** k_exp
+    v = synth.tensor("scores/small/v", (n, 1, d), "bf16")
+    q = synth.to_storage(q64, "bf16")
+    c = appended("scores/small", synth.to_storage(k64, "bf16"), v, table_pages=wide)
+    o, lse = attend(c, q, 1 / math.sqrt(d), 1)
+    check_closely(c, synth.widen(q, "bf16"), o, lse, 1 / math.sqrt(d))
+
+
+def test_large_queries_beside_large_keys_at_right_angles():
+    """Products of exactly 0 stay 0 whatever the scales."""
+    G.require_gpu()
+    n, d = 100, 32
+    q64, k64 = np.zeros((1, 1, d)), np.zeros((n, 1, d))
+    q64[..., : d // 2], k64[..., d // 2:] = 2.0 ** 100, 2.0 ** 110
+    q = synth.to_storage(q64, "bf16")
+    c = appended("scores/angles", synth.to_storage(k64, "bf16"), synth.tensor("scores/angles/v", (n, 1, d), "bf16"))
+    o, lse = attend(c, q, 1 / math.sqrt(d), 1)
+    check_closely(c, q64, o, lse, 1 / math.sqrt(d))

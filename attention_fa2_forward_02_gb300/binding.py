@@ -49,6 +49,7 @@ EXPORTS = (
     "fa2_kv_read",
     "fa2_decode_workspace_size",
     "fa2_decode",
+    "fa2_last_decode_info",
 )
 
 
@@ -117,6 +118,7 @@ def _declare(lib):
         "fa2_decode_workspace_size": (ctypes.c_size_t, [_i64, _i32, _i32, _i32]),
         "fa2_decode": (ctypes.c_int, [_c_ptr] * 5 + [_c_ptr, _i64, _i64, _c_ptr, _i64, _i32, _i64, _c_ptr, ctypes.c_size_t,
                                                      _i32, _f32, _c_ptr]),
+        "fa2_last_decode_info": (ctypes.c_int, [ctypes.POINTER(_i32)]),
     }
     sig["fa2_rope_backward"] = sig["fa2_rope"]
     for name, (res, args) in sig.items():
@@ -487,6 +489,13 @@ def fa2_kv_read(k_pages, v_pages, k_out, v_out, block_table, seq_lens, k_exp=Non
 
 def fa2_decode_workspace_size(batch: int, n_heads: int, n_kv_heads: int, head_dim: int) -> int:
     return int(library().fa2_decode_workspace_size(batch, n_heads, n_kv_heads, head_dim))
+
+
+def fa2_last_decode_info() -> int:
+    """CTAs that shared an item in this host thread's most recent fa2_decode; 0: two launches; -1: none yet (fa2.h)."""
+    ctas = _i32()
+    _check(library().fa2_last_decode_info(ctypes.byref(ctas)), "fa2_last_decode_info")
+    return int(ctas.value)
 
 
 def fa2_decode(q, k_pages, v_pages, o, lse, block_table, seq_lens, workspace, softmax_scale: float, window: int = 0,

@@ -110,6 +110,12 @@ fa2_status run(Params& p, cudaError_t (*launch)(const Params&, cudaStream_t), vo
 }
 
 }  // namespace
+
+int32_t& decode_record() {
+    thread_local int32_t record = -1;
+    return record;
+}
+
 }  // namespace fa2
 
 using namespace fa2;
@@ -241,6 +247,12 @@ fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_ca
     p.workspace = static_cast<float*>(workspace);
     p.scale = softmax_scale;
     return run(p, launch_decode, stream);
+}
+
+fa2_status fa2_last_decode_info(int32_t* ctas_per_item) {
+    if (!ctas_per_item) return FA2_ERR_INVALID_ARG;
+    *ctas_per_item = decode_record();
+    return FA2_OK;
 }
 
 }  // extern "C"

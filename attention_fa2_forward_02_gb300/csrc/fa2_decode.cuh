@@ -1100,9 +1100,11 @@ cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
         if (e != cudaSuccess) return e;
         if (ranks == 1 || cluster_fits(reinterpret_cast<const void*>(kern), kThreads, C::kSmem, ranks, slot + 1)) {
             const int64_t items = p.c.batch * p.c.hkv * ((p.heads / p.c.hkv + C::kRows - 1) / C::kRows);
+            decode_record() = ranks;
             return launch_early_cluster(kern, dim3((unsigned)(items * ranks)), dim3(kThreads), C::kSmem, stream, (unsigned)ranks, p, ranks);
         }
     }
+    decode_record() = 0;
     auto kern = fa2_decode_kernel<D, kBf16, kE4m3, kTiles, false>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, slot);
     if (e != cudaSuccess) return e;

@@ -274,6 +274,9 @@ bool cluster_fits(const void* func, int threads, int smem, int size, int slot);
 // fa2_last_launch_info); the launch code writes the choices it made.
 fa2_launch_info& launch_record();
 
+// The same for fa2_last_decode_info.
+int32_t& decode_record();
+
 // Raises the dynamic shared-memory limit of `func` on the current device once.
 cudaError_t ensure_smem_limit(const void* func, int bytes, int slot);
 

@@ -626,6 +626,15 @@ typedef struct fa2_launch_info {
 } fa2_launch_info;
 fa2_status fa2_last_launch_info(fa2_launch_info* info);
 
+/*
+ * fa2_last_decode_info - how the calling host thread's most recent fa2_decode divided its work:
+ *   *ctas_per_item   CTAs of a thread-block cluster that shared each sequence's key-value head
+ *                    (and 8 or 16 of its query heads), 1 to 8, in one launch; 0: all keys divided
+ *                    evenly over the CTAs, whatever the lengths, in two launches; -1 before any
+ * Errors: FA2_ERR_INVALID_ARG (ctas_per_item is NULL).
+ */
+fa2_status fa2_last_decode_info(int32_t* ctas_per_item);
+
 /* fa2_status_string - a static, human-readable message for a status code. */
 const char* fa2_status_string(fa2_status s);
 

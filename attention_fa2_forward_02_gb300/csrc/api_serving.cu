@@ -243,7 +243,8 @@ fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_ca
         workspace_bytes < decode_workspace_bytes(n_heads, cache->n_kv_heads, cache->head_dim))
         return FA2_ERR_WORKSPACE;
     p.q = q; p.q_batch = q_strides[0]; p.q_head = q_strides[1];
-    p.o = o; p.lse = lse; p.heads = n_heads; p.window = window;
+    p.o = o; p.lse = lse; p.heads = n_heads;
+    p.window = window < p.c.room ? window : 0;  // as wide as the table: all keys
     p.workspace = static_cast<float*>(workspace);
     p.scale = softmax_scale;
     return run(p, launch_decode, stream);

@@ -1,8 +1,10 @@
 """Which division of the work fa2_decode takes: the rule of its sizes, written out, against what the library records."""
+import math
+
 import pytest
 
 from attention_fa2_forward_02_gb300 import binding
-from tests.test_gpu_decode import run
+from tests.test_gpu_decode import run, workspace
 
 pytestmark = pytest.mark.gpu
 
@@ -42,3 +44,15 @@ def test_short_contexts_take_clusters(batch, hkv, group, wide, d, e4m3):
 def test_every_division_is_among_the_cases():
     got = {ctas_per_item(*c[:3], d, e, 16 * c[3], w) for c in CASES for d in (32, 64, 80, 128) for e in (False, True) for w in (0, 77)}
     assert got == {0, 1, 2, 4, 8}
+
+
+@pytest.mark.parametrize("window", [3000, 4000, 1 << 40, 2 ** 63 - 16, 2 ** 63 - 15, 2 ** 63 - 1])
+def test_windows_as_wide_as_the_table_and_wider(window):
+    """They leave all keys: the division and the bits of a call without one."""
+    import torch
+    c, q, o, lse = run("paths/wide", [2900, 700], 16, 2, 4, 128, table_pages=188)
+    assert binding.fa2_last_decode_info() == 0
+    o2, l2 = torch.empty_like(o), torch.empty_like(lse)
+    binding.fa2_decode(q, *c.pools(), o2, l2, c.table_dev, c.lens_dev, workspace(2, 8, 2, 128), 1 / math.sqrt(128), window=window)
+    assert binding.fa2_last_decode_info() == 0
+    assert torch.equal(o, o2) and torch.equal(lse, l2)

@@ -75,12 +75,15 @@ union Pack {
     __device__ Pack() {}
 };
 
+// None of the inputs is declared __restrict__: the kernel before may still be writing them while this
+// one is set up, and such loads need not stay behind the wait.
+//
 // A thread's two packs of P elements: for the half layout the packs at i and i + rot / 2, for
 // the interleaved one the 2 P elements from 2 i.
 template <typename E, int P, bool kInterleaved>
 __global__ void __launch_bounds__(kThreads)
-    rope_kernel(const E* x, E* y, const int32_t* __restrict__ positions, int64_t position_stride,
-                const double* __restrict__ inv_freq, int n_tokens, int heads, int heads_per_thread, int chunks, int d, int rot,
+    rope_kernel(const E* x, E* y, const int32_t* positions, int64_t position_stride,
+                const double* inv_freq, int n_tokens, int heads, int heads_per_thread, int chunks, int d, int rot,
                 int64_t xb, int64_t xh, int64_t xn, int64_t yb, int64_t yh, int64_t yn, float magnitude, int backward) {
     using W = typename Word<P * sizeof(E)>::T;
     const int b = blockIdx.y / chunks, chunk = blockIdx.y % chunks;

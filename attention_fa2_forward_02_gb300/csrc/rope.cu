@@ -8,15 +8,15 @@
 // (integers only: this part's float64 rate is a hundredth of its integer rate) and multiplied by the position
 // modulo 2^64, which keeps the fraction exact to position * 2^-64; the fixed-point frequencies are
 // made once per block, in shared memory. The upper 32 bits of a product, as a signed fraction of
-// a turn, go to sincospif for float32 results and to the special function unit for 16-bit ones:
-// its sine and cosine are within 2^-20.9 between -pi and pi, a rounding of the result is 2^-12 or
-// more. With sincospif and a conversion per thread the angles cost more than the rows: GB300,
-// B=2 H=16 N=2048 d=128, 10.2 us against 7.1.
+// a turn, lose their nearest quarter turn as an integer, exactly, and what is left, at most an
+// eighth, goes into the Taylor sums of sine and cosine in float32 (turn_sincos). GB300, bf16,
+// d = 128: B=2 H=16 N=2048 7.7 us, and 8.0 with sincospif; B=64 H=1 N=4096, where every sine is used
+// once, 35.7 and 39.2; the special function unit's sine and cosine, within 2^-20.9 only, 7.4 and 30.5.
 //
 // Each thread owns P pairs of one token (two 16-byte vectors where sizes and strides allow) and
 // walks over heads, two of them in flight: the P sines and cosines are made once for all of them,
 // while the first heads are being read. Bound by memory: 134 MB (B=2 H=16 N=8192 d=128, bf16) in
-// 22.2 us, 6.0 TB/s.
+// 22.3 us, 6.0 TB/s.
 #include "common.cuh"
 #include "internal.h"
 
@@ -38,6 +38,19 @@ __device__ __forceinline__ uint64_t turns_of(double f) {
     if (e <= 1) t = 1 - e < 64 ? hi >> (1 - e) : 0;  // (zero and subnormal f land here: 0)
     else t = e - 1 < 64 ? hi << (e - 1) : 0;
     return (bits >> 63) ? 0 - t : t;
+}
+
+// sin and cos of t 2^-32 turns. a = 2 pi 2^-32 (t - q 2^30) lies within pi / 4; the sums' next terms
+// are a^11 / 11! < 2^-29 and a^10 / 10! < 2^-25. With u = 2^-24 a's own error is 3 u |a|, the sine's
+// 2.8 u in all, the cosine's 3.4 u.
+__device__ __forceinline__ void turn_sincos(uint32_t t, float* s, float* c) {
+    const uint32_t q = (t + (1u << 29)) >> 30;
+    const float a = (float)(int32_t)(t - (q << 30)) * (6.28318530717958648f * 0x1p-32f), z = a * a;
+    const float sn = fmaf(a * z, fmaf(z, fmaf(z, fmaf(z, 1.f / 362880, -1.f / 5040), 1.f / 120), -1.f / 6), a);
+    const float cs = fmaf(z, fmaf(z, fmaf(z, fmaf(z, 1.f / 40320, -1.f / 720), 1.f / 24), -0.5f), 1.f);
+    const float s1 = q & 1 ? cs : sn, c1 = q & 1 ? sn : cs;
+    *s = __uint_as_float(__float_as_uint(s1) ^ (q & 2) << 30);
+    *c = __uint_as_float(__float_as_uint(c1) ^ ((q + 1) & 2) << 30);
 }
 
 template <int kBytes>
@@ -118,9 +131,7 @@ __global__ void __launch_bounds__(kThreads)
             const int64_t pos = positions ? positions[b * position_stride + n] : n;
 #pragma unroll
             for (int p = 0; p < P; ++p) {
-                const float part = (float)(int32_t)(((uint64_t)pos * turns[P * u + p]) >> 32);  // of a turn, 2^-32
-                if constexpr (sizeof(E) == 4) sincospif(part * 0x1p-31f, &s[p], &c[p]);
-                else __sincosf(part * (6.28318530717958648f * 0x1p-32f), &s[p], &c[p]);
+                turn_sincos((uint32_t)(((uint64_t)pos * turns[P * u + p]) >> 32), &s[p], &c[p]);
                 c[p] *= magnitude;
                 s[p] *= backward ? -magnitude : magnitude;
             }

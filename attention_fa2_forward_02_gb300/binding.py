@@ -420,7 +420,6 @@ def fa2_watchdog_selftest(stream=None) -> None:
 # A decoding step makes these calls on tensors so small that the host's work sets the pace: the extension _fa2_torch
 # (csrc/torch_args.cpp) checks the tensors' devices, shapes, types and strides and calls the library.
 
-CACHE_SAME, CACHE_E4M3 = 0, 1
 ROPE_SCALINGS = ("plain", "linear", "base", "turns", "ramp")  # fa2_rope_scaling's values in order
 _ext = None
 

@@ -363,6 +363,11 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
     // m lies this much below the maximum it was taken from: weights 2^-(14 + kLift) of the largest
     // still have all of half's bits (bfloat16 has float32's exponents)
     constexpr float kLift = kMmaBf16 ? 0.f : 7.f;
+    // Whether the product with V takes what a weight's rounding to 16 bits left off as well: it is the
+    // largest error of O but where a half weight's 2^-11 stands beside a bfloat16 result's 2^-8. (e4m3
+    // with bfloat16, batch of 32: 8 heads 66.0 us in one product and 67.7 in two, 16 heads 79.8 and
+    // 85.5; 16-bit long contexts, bound by memory, the same.)
+    constexpr bool kRest = !(kE4m3 && kBf16);
     constexpr int kKeys = C::kKeys, S = C::kStages, kRows = C::kRows, kMt = kKeys / 16, kMR = C::kMergeRows;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LocateSmem located;
@@ -859,9 +864,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
             }
 #pragma unroll
             for (int j = 0; j < kMt; ++j) {
-                // P as the right operand: keys 2t, 2t+1 (and + 8) x head g; and what its rounding to 16
-                // bits left off, for a second product: together within 2^-16 (bfloat16) or 2^-22 (half)
-                // of a weight. (One product: bf16 long contexts 508 us, two 518; e4m3 batch 64.9, 66.9.)
+                // P as the right operand: keys 2t, 2t+1 (and + 8) x head g; and the rest of its rounding,
+                // together within 2^-16 (bfloat16) or 2^-22 (half) of a weight
                 uint32_t pf[kTiles][2], pl[kTiles][2];
 #pragma unroll
                 for (int h = 0; h < kTiles; ++h)
@@ -874,8 +878,9 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                             if constexpr (!kE4m3) l[h][n] += x;
                         }
                         const uint32_t w = pack2<kMmaBf16>(sc[j][h][2 * e], sc[j][h][2 * e + 1]);
-                        const float2 f = unpack2<kMmaBf16>(w);
                         pf[h][e] = transpose8(w);
+                        if constexpr (!kRest) continue;
+                        const float2 f = unpack2<kMmaBf16>(w);
                         pl[h][e] = transpose8(pack2<kMmaBf16>(sc[j][h][2 * e] - f.x, sc[j][h][2 * e + 1] - f.y));
                     }
                 // ---- O^T += V^T P^T
@@ -888,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
 #pragma unroll
                         for (int h = 0; h < kTiles; ++h) {
                             mma16816<kMmaBf16>(o[d][h], v4, pf[h][0], pf[h][1]);
-                            mma16816<kMmaBf16>(o[d][h], v4, pl[h][0], pl[h][1]);
+                            if constexpr (kRest) mma16816<kMmaBf16>(o[d][h], v4, pl[h][0], pl[h][1]);
                         }
                     }
                 } else {
@@ -904,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
 #pragma unroll
                             for (int h = 0; h < kTiles; ++h) {
                                 mma16816<false>(o[d + e][h], a4, pf[h][0], pf[h][1]);
-                                mma16816<false>(o[d + e][h], a4, pl[h][0], pl[h][1]);
+                                if constexpr (kRest) mma16816<false>(o[d + e][h], a4, pl[h][0], pl[h][1]);
                             }
                         }
                     }

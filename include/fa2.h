@@ -537,7 +537,8 @@ fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, cons
  *              calls whose GPU work may overlap need one each
  * float32 scores, softmax statistics and sums; the product with V takes each probability as two
  * 16-bit numbers (FA2_CACHE_SAME: dtype; FA2_CACHE_E4M3: half), its rounding and what that left
- * off: within 2^-16 (BF16) or 2^-22 of it. In half, weights below 2^-32 of the row's largest
+ * off: within 2^-16 (BF16) or 2^-22 of it; in FA2_CACHE_E4M3 with BF16, whose results have steps
+ * of 2^-8, one half, within 2^-11. In half, weights below 2^-32 of the row's largest
  * count as 0 there; in FA2_CACHE_E4M3 these weights have the value row's scale in them (rows
  * whose codes are all 0 are not among the largest), the denominator and the LSE do not.
  * The keys of all sequences and heads are divided evenly over the CTAs, whatever the lengths

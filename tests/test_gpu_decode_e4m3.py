@@ -86,11 +86,13 @@ def appended(tag, k, v, page=16, table_pages=None):
 def check_closely(c, q64, o, lse, scale, group=1):
     """As test_gpu_decode.check for sequence 0, but with the weights' rounding in two parts, and the weights that set the maximum
     those of rows with an element that is not 0.  A weight W_j = 2^(s_j + e_j) goes into the product as two 16-bit numbers, the
-    second the rounded rest of the first: off by u^2 W_j, u the type's roundoff.  In half also by half a step of 2^-24 of a
+    second the rounded rest of the first: off by u^2 W_j, u the type's roundoff (from an 8-bit cache to bfloat16 results only
+    the first: u W_j, u half's).  In half also by half a step of 2^-24 of a
     reference that is 2^7 below the largest weight W_* or lower: 2^-32 W_*, so O, whose denominator is L = sum 2^s_j, by
     (2^-32 W_* / L) sum_j |v_j| 2^-e_j."""
     half = c.e4m3 or c.dtype == "f16"
-    step = UNIT_ROUNDOFF["f16" if half else "bf16"] ** 2
+    u = UNIT_ROUNDOFF["f16" if half else "bf16"]
+    step = u if c.e4m3 and c.dtype == "bf16" else u ** 2
     for h in range(q64.shape[1]):
         k, v = c.rows("k", 0)[0][:, h // group], c.rows("v", 0)[0][:, h // group]
         e_j, n = c.value_exps(0, h // group), len(k)

@@ -55,15 +55,17 @@ template <int D, bool kE4m3, int kTiles>
 struct Cfg {
     static constexpr int kRowBytes = kE4m3 ? D : 2 * D;
     static constexpr int kRows = 8 * kTiles;                // query heads per item
-    // CTAs an SM. 16-bit rows keep memory busy with two, and three read unevenly fast (long contexts,
-    // 8 heads: d 128 518 -> 550 us, d 64 266 -> 297); e4m3 has more to do per byte (batch 73 -> 65 us
-    // with three), but 16 heads of d 64 and more need more registers than three leave (d 64 50 -> 57
-    // us, d 128 83 -> 127; d 32 42 -> 36).
-    static constexpr int kPerSm = kE4m3 && (kTiles == 1 || D == 32) ? 3 : 2;
+    // CTAs an SM. 16-bit rows keep memory busy with two, and three read unevenly fast (21 sequences of
+    // up to 65536, 8 heads: d 128 567 -> 634 us, d 64 317 -> 341). e4m3 has more to do per byte: 32
+    // sequences of up to 8192, a one-token one among them, d 128 76 us with two and 65 with three (long
+    // contexts 304 and 322), d 32 34 and 33. But three leave 168 registers: too few at d 64, 8 heads
+    // (41 us with two, 50 with three; long 163 and 198), and for 16 heads (d 64 57 and 70, d 128 86
+    // and 155; d 32 42 and 40).
+    static constexpr int kPerSm = kE4m3 && (D == 32 || (D == 128 && kTiles == 1)) ? 3 : 2;
     static constexpr int kMaxCtas = 152 * kPerSm;           // a fixed number: the split depends on the lengths alone
     // in one launch, where latency is more than memory: 7 windows of 1024 keys, d 64, 9.6 -> 8.8 us
     static constexpr int kShortPerSm = kTiles == 1 && kRowBytes < 256 ? 3 : kPerSm;
-    static constexpr int kKeys = kRowBytes >= 256 ? 16 : (kRowBytes == 128 ? 32 : 64);  // keys per block: 8 KB of K and V
+    static constexpr int kKeys = kRowBytes >= 256 ? 16 : (kRowBytes == 128 ? 32 : 64);  // keys per block: 8 KB of K and V (4 of 32-byte rows)
     static constexpr int kLooks = (kKeys + 31) / 32;        // keys a lane looks up per block
     static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks a row
     static constexpr int kTile = kKeys * kRowBytes;         // K or V of a block

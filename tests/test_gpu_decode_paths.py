@@ -15,7 +15,7 @@ def ctas_per_item(batch, hkv, group, d, e4m3, room, window=0):
     kernel_d = 32 if d <= 32 else 64 if d <= 64 else 128
     row_bytes = kernel_d if e4m3 else 2 * kernel_d
     block = 16 if row_bytes >= 256 else 32 if row_bytes == 128 else 64
-    per_sm = 3 if (group <= 8 and row_bytes < 256) or (e4m3 and (group <= 8 or kernel_d == 32)) else 2
+    per_sm = 3 if (group <= 8 and row_bytes < 256) or (e4m3 and kernel_d == 32) else 2
     items, resident = batch * hkv * -(-group // (8 if group <= 8 else 16)), 152 * per_sm
     keys = min(room, window + 15) if window else room
     blocks, ctas = -(-keys // block), 1

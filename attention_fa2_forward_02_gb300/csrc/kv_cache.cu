@@ -19,7 +19,16 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kMinExp = -60;
-constexpr int kOneToken = 152 * 2;  // blocks from which a warp takes a whole token
+// Blocks from which a warp takes a whole token (with fewer, one round of its rows). GB300, 8 heads of
+// d = 128, whole tokens against rounds: append e4m3 of 1200 tokens (300 blocks) 3.5 / 3.1 us, of 1800
+// 3.8 / 4.6; 16 bits 3.2 / 3.7 and 3.5 / 5.1; 120,000 e4m3 111 / 178. (Reading e4m3 back, rounds stay
+// ahead longer: 9600 tokens 16.1 / 13.2, 120,000 116 / 129.)
+constexpr int kOneToken = 152 * 2;
+// Blocks from which a warp takes kRows rounds of tokens of few heads, in 16 bits and in e4m3. One head,
+// four rounds against one: e4m3 append d = 128 40,000 tokens (1250 blocks) 11.6 / 9.6 us, 160,000 29.4 /
+// 29.9, 640,000 102 / 111; read 9.3 / 8.4, 23.4 / 24.7, 77 / 90. 16 bits d = 64 append 40,000 (1250)
+// 7.4 / 6.7, 80,000 11.7 / 13.1, 640,000 61 / 84; read 20,000 3.2 / 3.2, 40,000 4.8 / 5.6, 640,000 50 / 82.
+constexpr int kFewRounds16 = 152 * 8, kFewRoundsE4m3 = 152 * 32;
 
 // e of the scale 2^e for a row whose largest finite magnitude is a.
 __device__ __forceinline__ int scale_exp(float a) {
@@ -294,7 +303,7 @@ cudaError_t launch_lanes(const KvRowsParams& p, cudaStream_t stream) {
     while ((1 << shift) < total) ++shift;
     if ((2 << shift) <= kGroups) {
         const int64_t per = (int64_t)kWarps * kRows * (kGroups >> shift);
-        if ((p.tokens + per - 1) / per * batch >= 152) {
+        if ((p.tokens + per - 1) / per * batch >= (kE4m3 ? kFewRoundsE4m3 : kFewRounds16)) {
             const dim3 grid((unsigned)((p.tokens + per - 1) / per), 1, batch);
             return launch_early(kv_few_heads_kernel<kBf16, kE4m3, kRead, kLanes, kRows>, grid, dim3(kWarps * 32), 0, stream, p, shift);
         }
@@ -304,7 +313,9 @@ cudaError_t launch_lanes(const KvRowsParams& p, cudaStream_t stream) {
     }
     auto blocks = [&](int tok) { return (p.tokens + kWarps * tok - 1) / (kWarps * tok); };
     // A warp takes kTok whole tokens while that gives every SM several blocks, one token with fewer,
-    // and with few tokens one round of a token's rows.
+    // and with few tokens one round of a token's rows. 120,000 tokens, 8 heads, d = 128, append e4m3 /
+    // 16 bits / read e4m3: kTok 1 118.6 / 144.6 / 126.4 us, 2 111.1 / 145.5 / 116.3, 4 113.2 / 148.7 /
+    // 118.6; kRows 2 113.0 / 146.8 / 115.0, 8 171.5 / 144.6 / 130.8.
     if (blocks(kTok) * batch >= 152 * 8) {
         const dim3 grid((unsigned)blocks(kTok), 1, batch);
         return launch_early(kv_rows_kernel<kBf16, kE4m3, kRead, kLanes, kRows, kTok>, grid, dim3(kWarps * 32), 0, stream, p, total);

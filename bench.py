@@ -22,6 +22,8 @@ dV: 512 MiB) is larger than the 129 MB L2, so no flush is inserted.
 ``--impl reference`` times the float64 CPU oracle instead (on a bounded sample
 of the same workload per step); it is a deliberately slow baseline.
 
+``--serving`` times the rotary, cache and decode calls one by one instead.
+
 Multi-GPU (torchrun, one process per GPU): each rank runs its own batch (weak
 scaling, no collective on the data path); the step time is the maximum over
 ranks and ``value`` counts the work of all ranks.
@@ -799,6 +801,67 @@ def psa_bandwidth(torch, B, dev, pk):
     return out
 
 
+def serving_cases(ops):
+    """The cases of perf/operators.py, and more of the decode's: what its listed ones leave out."""
+    listed = ops.listed()
+    one, batch, long = ({c["name"]: c for c in listed}[n] for n in ("decode one", "decode batch e4m3", "decode long"))
+    return listed + [
+        dict(one, name="decode one, table of 131072 tokens", table_pages=131072 // one["page"]),
+        dict(batch, name="decode batch e4m3, 16 heads", group=16),
+        dict(batch, name="decode batch e4m3, 20 heads", group=20),
+        dict(batch, name="decode batch e4m3, pages of 1", page=1),
+        dict(batch, name="decode batch e4m3, pages of 8", page=8),
+        dict(batch, name="decode batch e4m3, pages of 24", page=24),
+        dict(batch, name="decode batch e4m3, d 64", d=64),
+        dict(batch, name="decode batch e4m3, d 80", d=80),
+        dict(batch, name="decode batch e4m3, fp16", dtype="f16"),
+        dict(long, name="decode long, d 80", d=80),
+        dict(long, name="decode long e4m3", cache="e4m3"),
+    ]
+
+
+def run_serving(args):
+    """The rotary, cache and decode calls: device time of a call among others of its kind (three sets of tensors in turn,
+    the median of 9 timings between two events), one JSON line."""
+    import torch
+
+    from attention_fa2_forward_02_gb300 import binding as B
+    from perf import operators as ops
+    pk, out = peaks(), {}
+    sampler = ClockSampler(str(torch.cuda.current_device()))
+    sampler.begin()
+    for case in serving_cases(ops):
+        ops.own = True
+        states = [ops.prepare(case, seed) for seed in range(3)]
+        if "table_pages" in case:
+            for s in states:
+                wide = torch.zeros(s["table"].shape[0], case["table_pages"], dtype=torch.int32, device="cuda")
+                wide[:, :s["table"].shape[1]] = s["table"]
+                s["table"] = wide
+        for _ in range(3):
+            for s in states:
+                ops.run(s)
+        work = ops.work(case)
+        calls = 3 * max(2, min(30, int(4e9 / work["bytes"])))
+        ms = []
+        for _ in range(9):
+            e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            e0.record()
+            for i in range(calls):
+                ops.run(states[i % 3])
+            e1.record()
+            torch.cuda.synchronize()
+            ms.append(e0.elapsed_time(e1) / calls)
+        us = statistics.median(ms) * 1e3
+        out[case["name"]] = {"us": round(us, 2), "gbs": round(work["bytes"] / us * 1e-3, 1),
+                             "floor_us": round(work["bytes"] / pk["hbm_gbs"] * 1e-3, 2)}
+        del states
+    B.fa2_device_status()
+    sampler.end()
+    print(json.dumps({"serving": out, "clocks": sampler.stop(), "hbm_gbs": pk["hbm_gbs"], "data": "synthetic"}))
+    return 0
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__.split("\n")[0])
     ap.add_argument("--gpus", type=int, default=1)
@@ -808,9 +871,12 @@ def main():
     ap.add_argument("--bh", type=int, default=32, help="attention batch*heads (32 = B=2 H=16, the headline workload)")
     ap.add_argument("--cpu-budget", type=float, default=12.0, help="seconds of oracle work for cpu_baseline")
     ap.add_argument("--no-cpu-baseline", action="store_true")
+    ap.add_argument("--serving", action="store_true", help="time the rotary, cache and decode calls instead")
     args = ap.parse_args()
     args.warmup = max(3, args.warmup)  # at least three untimed warm-up steps
     set_heads(args.bh)
+    if args.serving:
+        return run_serving(args)
     return run_reference(args) if args.impl == "reference" else run_ours(args)
 
 

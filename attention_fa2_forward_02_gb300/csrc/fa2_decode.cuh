@@ -222,7 +222,7 @@ struct Last {
 // it; its last item, if that ends after it), each [kRows][D] floats and then [kRows] Stats;
 // behind all of them, per CTA, the item that begins in it and ends in a later CTA. (The second
 // kernel could find that from the lengths, but while the first one fills the SMs it has no place
-// to do so early: e4m3 batch 65.3 -> 68.6 us.)
+// to do so early: 3 us of the e4m3 batch.)
 template <int D, int kRows>
 __device__ __forceinline__ float* partial(float* ws, int64_t cta, int which) {
     return ws + (cta * 2 + which) * (kRows * (D + 4));

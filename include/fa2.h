@@ -540,7 +540,9 @@ fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, cons
  * off: within 2^-16 (BF16) or 2^-22 of it; in FA2_CACHE_E4M3 with BF16, whose results have steps
  * of 2^-8, one half, within 2^-11. In half, weights below 2^-32 of the row's largest
  * count as 0 there; in FA2_CACHE_E4M3 these weights have the value row's scale in them (rows
- * whose codes are all 0 are not among the largest), the denominator and the LSE do not.
+ * whose codes are all 0 are not among the largest), the denominator and the LSE do not. There
+ * BF16 queries are brought to half by a power of two a row: elements below 2^-29 of the row's
+ * largest lose bits, below 2^-39 all of them.
  * The keys of all sequences and heads are divided evenly over the CTAs, whatever the lengths
  * (contexts that pages_per_seq * page_size or the window keep short: head by head, over the
  * CTAs of a cluster); a row divided between CTAs is joined from float32 partial results in a

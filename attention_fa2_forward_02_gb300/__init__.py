@@ -14,14 +14,19 @@ from .binding import (  # noqa: F401
     fa2_backward_preprocess,
     fa2_backward_workspace_size,
     fa2_decode,
+    fa2_decode_selected,
     fa2_decode_workspace_size,
     fa2_device_status,
     fa2_forward,
     fa2_kv_append,
+    fa2_kv_bounds,
     fa2_kv_read,
     fa2_rope,
+    fa2_rope_append,
     fa2_rope_backward,
     fa2_rope_frequencies,
+    fa2_select_pages,
+    fa2_select_workspace_size,
     fa2_status_string,
     library,
     psa_merge_attn_nchw,

@@ -50,6 +50,11 @@ EXPORTS = (
     "fa2_decode_workspace_size",
     "fa2_decode",
     "fa2_last_decode_info",
+    "fa2_rope_append",
+    "fa2_kv_bounds",
+    "fa2_select_workspace_size",
+    "fa2_select_pages",
+    "fa2_decode_selected",
 )
 
 
@@ -82,7 +87,7 @@ class KvCache(ctypes.Structure):
     _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_exp", ctypes.c_void_p), ("v_exp", ctypes.c_void_p),
                 ("num_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
                 ("slot_stride", ctypes.c_int64), ("n_kv_heads", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("head_dim", ctypes.c_int32), ("type", ctypes.c_int)]
+                ("head_dim", ctypes.c_int32), ("type", ctypes.c_int), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p)]
 
 
 def _declare(lib):
@@ -119,6 +124,13 @@ def _declare(lib):
         "fa2_decode": (ctypes.c_int, [_c_ptr] * 5 + [_c_ptr, _i64, _i64, _c_ptr, _i64, _i32, _i64, _c_ptr, ctypes.c_size_t,
                                                      _i32, _f32, _c_ptr]),
         "fa2_last_decode_info": (ctypes.c_int, [ctypes.POINTER(_i32)]),
+        "fa2_rope_append": (ctypes.c_int, [_c_ptr] * 10 + [_i32, _i32, _f32, _c_ptr, _c_ptr, _i64, _i64, _c_ptr, _c_ptr, _i64, _i64,
+                                                           _i32, _i32, _c_ptr]),
+        "fa2_kv_bounds": (ctypes.c_int, [_c_ptr] * 4 + [_i64, _i64, _c_ptr, _c_ptr, _i64, _i64, _i32, _c_ptr]),
+        "fa2_select_workspace_size": (ctypes.c_size_t, [_i64, _i32, _i64]),
+        "fa2_select_pages": (ctypes.c_int, [_c_ptr] * 4 + [_i64, _i32, _i32, _i32, _i32, _c_ptr, _i64, _i64, _c_ptr, _i64, _c_ptr, _c_ptr,
+                                                           _i64, _i64, _i64, _c_ptr, ctypes.c_size_t, _i32, _c_ptr]),
+        "fa2_decode_selected": (ctypes.c_int, [_c_ptr] * 6 + [_i64, _c_ptr, _i64, _i32, _c_ptr, ctypes.c_size_t, _i32, _f32, _c_ptr]),
     }
     sig["fa2_rope_backward"] = sig["fa2_rope"]
     for name, (res, args) in sig.items():
@@ -435,7 +447,8 @@ def _extension():
         except ImportError as e:
             raise Fa2Error(-1, f"_fa2_torch: {e} (run __graft_entry__.build())") from e
         _fa2_torch.set_entry_points(*(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in (
-            "fa2_rope", "fa2_rope_backward", "fa2_kv_append", "fa2_kv_read", "fa2_decode")))
+            "fa2_rope", "fa2_rope_backward", "fa2_kv_append", "fa2_kv_read", "fa2_decode", "fa2_rope_append", "fa2_kv_bounds",
+            "fa2_select_pages", "fa2_decode_selected")))
         _ext = _fa2_torch
     return _ext
 
@@ -470,18 +483,32 @@ def fa2_rope_backward(dy, dx, inv_freq, positions=None, interleaved: bool = Fals
         _check(st, "fa2_rope_backward")
 
 
-def fa2_kv_append(k_pages, v_pages, k, v, block_table, seq_lens, cu_new=None, k_exp=None, v_exp=None, stream=None) -> None:
+def fa2_kv_append(k_pages, v_pages, k, v, block_table, seq_lens, cu_new=None, k_exp=None, v_exp=None, stream=None, k_scale=None,
+                  v_scale=None) -> None:
     """Write new keys and values k, v [tokens, n_kv_heads, d] into the pages [num_pages, n_kv_heads, page_size, d] (any
-    strides, d contiguous; the rows' dtype, or float8_e4m3fn with scale bytes k_exp, v_exp).  seq_lens counts the new tokens
+    strides, d contiguous; the rows' dtype, or float8_e4m3fn with scale bytes k_exp, v_exp, or uint8 [.., d / 2] of two
+    4-bit floats a byte with these and float8_e4m3fn scales k_scale, v_scale [.., d / 16]).  seq_lens counts the new tokens
     in; cu_new int32 [batch + 1] says which rows are whose (None: one a sequence)."""
-    st = (_ext or _extension()).kv_append(k_pages, v_pages, k, v, block_table, seq_lens, cu_new, k_exp, v_exp, stream)
+    st = (_ext or _extension()).kv_append(k_pages, v_pages, k, v, block_table, seq_lens, cu_new, k_exp, v_exp, stream, k_scale, v_scale)
     if st:
         _check(st, "fa2_kv_append")
 
 
-def fa2_kv_read(k_pages, v_pages, k_out, v_out, block_table, seq_lens, k_exp=None, v_exp=None, stream=None) -> None:
+def fa2_rope_append(k_pages, v_pages, k, v, inv_freq, block_table, seq_lens, q=None, q_out=None, cu_new=None, positions=None,
+                    interleaved: bool = False, magnitude: float = 1.0, k_exp=None, v_exp=None, k_scale=None, v_scale=None,
+                    stream=None) -> None:
+    """fa2_rope on new tokens' q (into q_out, which may be q; [tokens, n_heads, d]) and k, and fa2_kv_append of k and v, in one
+    pass; positions int32 [tokens] (None: the tokens' places in their sequences)."""
+    st = (_ext or _extension()).rope_append(k_pages, v_pages, k, v, inv_freq, block_table, seq_lens, q, q_out, cu_new, positions,
+                                            interleaved, magnitude, k_exp, v_exp, k_scale, v_scale, stream)
+    if st:
+        _check(st, "fa2_rope_append")
+
+
+def fa2_kv_read(k_pages, v_pages, k_out, v_out, block_table, seq_lens, k_exp=None, v_exp=None, stream=None, k_scale=None,
+                v_scale=None) -> None:
     """Copy the cached rows out: k_out, v_out [batch, n_kv_heads, max_len, d]; positions past a sequence's length stay."""
-    st = (_ext or _extension()).kv_read(k_pages, v_pages, k_out, v_out, block_table, seq_lens, k_exp, v_exp, stream)
+    st = (_ext or _extension()).kv_read(k_pages, v_pages, k_out, v_out, block_table, seq_lens, k_exp, v_exp, stream, k_scale, v_scale)
     if st:
         _check(st, "fa2_kv_read")
 
@@ -498,10 +525,43 @@ def fa2_last_decode_info() -> int:
 
 
 def fa2_decode(q, k_pages, v_pages, o, lse, block_table, seq_lens, workspace, softmax_scale: float, window: int = 0,
-               k_exp=None, v_exp=None, stream=None) -> None:
+               k_exp=None, v_exp=None, stream=None, k_scale=None, v_scale=None) -> None:
     """Attention of one new token a sequence over the paged cache: q, o [batch, n_heads, d], lse [batch, n_heads]
     float32; workspace a CUDA uint8 tensor of fa2_decode_workspace_size bytes; window > 0: the last keys only."""
     st = (_ext or _extension()).decode(q, k_pages, v_pages, o, lse, block_table, seq_lens, workspace, softmax_scale, window, k_exp,
-                                       v_exp, stream)
+                                       v_exp, stream, k_scale, v_scale, False)
     if st:
         _check(st, "fa2_decode")
+
+
+def fa2_kv_bounds(k_pages, bounds, bounds_exp, block_table, seq_lens, tokens: int, cu_new=None, k_exp=None, k_scale=None,
+                  stream=None) -> None:
+    """The lowest and highest key of every channel in the pages that new tokens lie in: bounds int8 [num_pages, n_kv_heads, 2,
+    d], bounds_exp uint8 [num_pages, n_kv_heads]; after an append of `tokens` rows, with its cu_new."""
+    st = (_ext or _extension()).kv_bounds(k_pages, bounds, bounds_exp, block_table, seq_lens, tokens, cu_new, k_exp, k_scale, stream)
+    if st:
+        _check(st, "fa2_kv_bounds")
+
+
+def fa2_select_workspace_size(batch: int, n_kv_heads: int, pages_per_seq: int) -> int:
+    return int(library().fa2_select_workspace_size(batch, n_kv_heads, pages_per_seq))
+
+
+def fa2_select_pages(q, bounds, bounds_exp, block_table, seq_lens, sel_table, sel_lens, workspace, page_size: int, first: int = 1,
+                     recent: int = 1, stream=None) -> None:
+    """The `first` first, the `recent` last and then the pages whose keys can score highest by their bounds, for each sequence
+    and key-value head: sel_table int32 [batch, n_kv_heads, budget], sel_lens int32 [batch, n_kv_heads] (the keys in them);
+    workspace a CUDA uint8 tensor of fa2_select_workspace_size bytes."""
+    st = (_ext or _extension()).select_pages(q, bounds, bounds_exp, block_table, seq_lens, sel_table, sel_lens, workspace, page_size,
+                                             first, recent, stream)
+    if st:
+        _check(st, "fa2_select_pages")
+
+
+def fa2_decode_selected(q, k_pages, v_pages, o, lse, sel_table, sel_lens, workspace, softmax_scale: float, k_exp=None, v_exp=None,
+                        stream=None, k_scale=None, v_scale=None) -> None:
+    """fa2_decode over a block table and a length for each sequence and key-value head, as fa2_select_pages writes them."""
+    st = (_ext or _extension()).decode(q, k_pages, v_pages, o, lse, sel_table, sel_lens, workspace, softmax_scale, 0, k_exp, v_exp,
+                                       stream, k_scale, v_scale, True)
+    if st:
+        _check(st, "fa2_decode_selected")

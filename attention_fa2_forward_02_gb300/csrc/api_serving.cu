@@ -67,12 +67,13 @@ fa2_status rope_call(const void* x, void* y, const int32_t* positions, int64_t p
 
 // Checks shared by the cache's calls, and the kernels' view of the cache.
 fa2_status paged(const fa2_kv_cache* c, const int32_t* table, int64_t table_stride, int64_t pages_per_seq,
-                 const int32_t* lens, int64_t batch, fa2_dtype dtype, PagedParams* out) {
-    if (!c || !c->k || !c->v || !table || !lens) return FA2_ERR_INVALID_ARG;
-    if (c->type != FA2_CACHE_SAME && c->type != FA2_CACHE_E4M3) return FA2_ERR_INVALID_ARG;
+                 const int32_t* lens, int64_t batch, fa2_dtype dtype, PagedParams* out, bool k_only = false) {
+    if (!c || !c->k || (!c->v && !k_only) || !table || !lens) return FA2_ERR_INVALID_ARG;
+    if (c->type != FA2_CACHE_SAME && c->type != FA2_CACHE_E4M3 && c->type != FA2_CACHE_E2M1) return FA2_ERR_INVALID_ARG;
     if (dtype != FA2_DTYPE_F32 && dtype != FA2_DTYPE_F16 && dtype != FA2_DTYPE_BF16) return FA2_ERR_INVALID_ARG;
-    const bool e4m3 = c->type == FA2_CACHE_E4M3;
-    if (e4m3 && (!c->k_exp || !c->v_exp)) return FA2_ERR_INVALID_ARG;
+    const bool e4m3 = c->type == FA2_CACHE_E4M3, e2m1 = c->type == FA2_CACHE_E2M1;
+    if ((e4m3 || e2m1) && (!c->k_exp || (!c->v_exp && !k_only))) return FA2_ERR_INVALID_ARG;
+    if (e2m1 && (!c->k_scale || (!c->v_scale && !k_only))) return FA2_ERR_INVALID_ARG;
     if (c->num_pages <= 0 || c->n_kv_heads <= 0 || c->page_size <= 0 || c->head_dim <= 0 || batch <= 0 || pages_per_seq <= 0 ||
         table_stride < 0)
         return FA2_ERR_INVALID_ARG;
@@ -81,32 +82,98 @@ fa2_status paged(const fa2_kv_cache* c, const int32_t* table, int64_t table_stri
     const int64_t sizes[3] = {c->num_pages, c->n_kv_heads, c->page_size};
     if (!strides_ok(strides, 3) || !rows_apart(sizes, strides, 3, c->head_dim)) return FA2_ERR_INVALID_ARG;
     if (dtype == FA2_DTYPE_F32) return FA2_ERR_UNSUPPORTED;
-    if (c->head_dim > 128 || c->head_dim % (e4m3 ? 16 : 8) != 0) return FA2_ERR_UNSUPPORTED;
+    if (c->head_dim > 128 || c->head_dim % (e2m1 ? 32 : (e4m3 ? 16 : 8)) != 0) return FA2_ERR_UNSUPPORTED;
     if (c->n_kv_heads > 1024 || c->num_pages > INT32_MAX || batch > kMaxGrid || c->page_size > kMaxLen ||
         pages_per_seq > kMaxLen || pages_per_seq * c->page_size > kMaxLen)
         return FA2_ERR_UNSUPPORTED;
-    const int64_t eb = e4m3 ? 1 : 2;
+    const int64_t bits = e2m1 ? 4 : (e4m3 ? 8 : 16);
+    if (e2m1 && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))) return FA2_ERR_MISALIGNED;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(table, 4) || !aligned(lens, 4)) return FA2_ERR_MISALIGNED;
     for (int i = 0; i < 3; ++i)
-        if (sizes[i] > 1 && strides[i] * eb % 16 != 0) return FA2_ERR_MISALIGNED;
+        if (sizes[i] > 1 && strides[i] * bits % 128 != 0) return FA2_ERR_MISALIGNED;
     PagedParams& p = *out;
     p.k = static_cast<char*>(c->k); p.v = static_cast<char*>(c->v);
     p.k_exp = c->k_exp; p.v_exp = c->v_exp;
     p.num_pages = c->num_pages;
-    p.page_stride = c->page_stride * eb; p.head_stride = c->head_stride * eb; p.slot_stride = c->slot_stride * eb;
+    if (e2m1) { p.k_scale = c->k_scale; p.v_scale = c->v_scale; }
+    p.page_stride = c->page_stride * bits / 8; p.head_stride = c->head_stride * bits / 8; p.slot_stride = c->slot_stride * bits / 8;
     p.hkv = c->n_kv_heads; p.page_size = c->page_size; p.d = c->head_dim;
     page_divisor(p.page_size, &p.page_mul, &p.page_shift);
-    p.e4m3 = e4m3;
+    p.form = (int)c->type;
     p.table = table; p.table_stride = table_stride; p.room = pages_per_seq * c->page_size;
     p.lens = lens; p.batch = batch; p.dtype = (int)dtype;
     return FA2_OK;
 }
 
+// Checks of an append's rows, and the kernels' view of them.
+fa2_status append_rows(const fa2_kv_cache* cache, const void* k, const void* v, const int64_t* k_strides, const int64_t* v_strides,
+                       const int32_t* block_table, int64_t table_stride, int64_t pages_per_seq, const int32_t* cu_new,
+                       const int32_t* seq_lens, int64_t batch, int64_t tokens, fa2_dtype dtype, KvRowsParams* out) {
+    if (!k || !v || !k_strides || !v_strides || tokens <= 0) return FA2_ERR_INVALID_ARG;
+    if (!strides_ok(k_strides, 2) || !strides_ok(v_strides, 2)) return FA2_ERR_INVALID_ARG;
+    if (!cu_new && tokens != batch) return FA2_ERR_INVALID_ARG;
+    KvRowsParams& p = *out;
+    const fa2_status st = paged(cache, block_table, table_stride, pages_per_seq, seq_lens, batch, dtype, &p.c);
+    if (st != FA2_OK) return st;
+    if (tokens > INT32_MAX) return FA2_ERR_UNSUPPORTED;
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_new, 4)) return FA2_ERR_MISALIGNED;
+    const int64_t sizes[2] = {tokens, cache->n_kv_heads};
+    for (int i = 0; i < 2; ++i)
+        if (sizes[i] > 1 && (k_strides[i] % 8 != 0 || v_strides[i] % 8 != 0)) return FA2_ERR_MISALIGNED;
+    p.k = static_cast<char*>(const_cast<void*>(k));
+    p.v = static_cast<char*>(const_cast<void*>(v));
+    for (int i = 0; i < 2; ++i) {
+        p.ks[i] = k_strides[i] * 2;
+        p.vs[i] = v_strides[i] * 2;
+    }
+    p.cu_new = cu_new;
+    p.tokens = tokens;
+    return FA2_OK;
+}
+
+unsigned int*& status_of(KvRowsParams& p) { return p.c.status; }
+unsigned int*& status_of(RopeAppendParams& p) { return p.rows.c.status; }
+unsigned int*& status_of(DecodeParams& p) { return p.c.status; }
+unsigned int*& status_of(KvBoundsParams& p) { return p.c.status; }
+unsigned int*& status_of(SelectParams& p) { return p.status; }
+
 // The last step of every cache call: the watchdog word, then the launch.
 template <typename Params>
 fa2_status run(Params& p, cudaError_t (*launch)(const Params&, cudaStream_t), void* stream) {
-    if (!watchdog_word(&p.c.status)) return FA2_ERR_CUDA;
+    if (!watchdog_word(&status_of(p))) return FA2_ERR_CUDA;
     return launch(p, static_cast<cudaStream_t>(stream)) == cudaSuccess ? FA2_OK : FA2_ERR_CUDA;
+}
+
+// per_head: block_table and seq_lens have a row for each sequence and key-value head.
+fa2_status decode_call(const void* q, const int64_t* q_strides, const fa2_kv_cache* cache, void* o, float* lse,
+                       const int32_t* block_table, int64_t table_stride, int64_t pages_per_seq, const int32_t* seq_lens,
+                       int64_t batch, int32_t n_heads, int64_t window, void* workspace, size_t workspace_bytes, fa2_dtype dtype,
+                       float softmax_scale, void* stream, bool per_head) {
+    if (!q || !q_strides || !o || !lse || n_heads <= 0 || window < 0) return FA2_ERR_INVALID_ARG;
+    if (!(softmax_scale > 0.f) || !isfinite(softmax_scale) || !strides_ok(q_strides, 2)) return FA2_ERR_INVALID_ARG;
+    DecodeParams p{};
+    const fa2_status st = paged(cache, block_table, table_stride, pages_per_seq, seq_lens, batch, dtype, &p.c);
+    if (st != FA2_OK) return st;
+    if (n_heads % cache->n_kv_heads != 0) return FA2_ERR_INVALID_ARG;
+    if (n_heads > kMaxGrid || batch * n_heads > INT32_MAX) return FA2_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16)) return FA2_ERR_MISALIGNED;
+    const int64_t sizes[2] = {batch, n_heads};
+    for (int i = 0; i < 2; ++i)
+        if (sizes[i] > 1 && q_strides[i] % 8 != 0) return FA2_ERR_MISALIGNED;
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < decode_workspace_bytes(n_heads, cache->n_kv_heads, cache->head_dim))
+        return FA2_ERR_WORKSPACE;
+    p.q = q; p.q_batch = q_strides[0]; p.q_head = q_strides[1];
+    p.o = o; p.lse = lse; p.heads = n_heads;
+    p.window = window < p.c.room ? window : 0;  // as wide as the table: all keys
+    p.workspace = static_cast<float*>(workspace);
+    p.scale = softmax_scale;
+    if (per_head) {
+        if (batch * cache->n_kv_heads > (1 << 20)) return FA2_ERR_UNSUPPORTED;
+        p.per_head = true;
+        p.c.batch = batch * cache->n_kv_heads;
+    }
+    return run(p, launch_decode, stream);
 }
 
 }  // namespace
@@ -174,26 +241,58 @@ fa2_status fa2_kv_append(const fa2_kv_cache* cache, const void* k, const void* v
                          const int64_t v_strides[2], const int32_t* block_table, int64_t table_stride,
                          int64_t pages_per_seq, const int32_t* cu_new, const int32_t* seq_lens, int64_t batch,
                          int64_t tokens, fa2_dtype dtype, void* stream) {
-    if (!k || !v || !k_strides || !v_strides || tokens <= 0) return FA2_ERR_INVALID_ARG;
-    if (!strides_ok(k_strides, 2) || !strides_ok(v_strides, 2)) return FA2_ERR_INVALID_ARG;
-    if (!cu_new && tokens != batch) return FA2_ERR_INVALID_ARG;
     KvRowsParams p{};
-    const fa2_status st = paged(cache, block_table, table_stride, pages_per_seq, seq_lens, batch, dtype, &p.c);
+    const fa2_status st = append_rows(cache, k, v, k_strides, v_strides, block_table, table_stride, pages_per_seq, cu_new, seq_lens,
+                                      batch, tokens, dtype, &p);
     if (st != FA2_OK) return st;
-    if (tokens > INT32_MAX) return FA2_ERR_UNSUPPORTED;
-    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(cu_new, 4)) return FA2_ERR_MISALIGNED;
-    const int64_t sizes[2] = {tokens, cache->n_kv_heads};
-    for (int i = 0; i < 2; ++i)
-        if (sizes[i] > 1 && (k_strides[i] % 8 != 0 || v_strides[i] % 8 != 0)) return FA2_ERR_MISALIGNED;
-    p.k = static_cast<char*>(const_cast<void*>(k));
-    p.v = static_cast<char*>(const_cast<void*>(v));
-    for (int i = 0; i < 2; ++i) {
-        p.ks[i] = k_strides[i] * 2;
-        p.vs[i] = v_strides[i] * 2;
+    if (p.c.form != kRowsE2m1) return run(p, launch_kv_rows, stream);
+    RopeAppendParams r{};
+    r.rows = p;
+    return run(r, launch_rope_append, stream);
+}
+
+fa2_status fa2_rope_append(const fa2_kv_cache* cache, const void* q, void* q_out, const void* k, const void* v,
+                           const int64_t q_strides[2], const int64_t q_out_strides[2], const int64_t k_strides[2],
+                           const int64_t v_strides[2], const double* inv_freq, int32_t rot_dim, int32_t interleaved,
+                           float magnitude, const int32_t* positions, const int32_t* block_table, int64_t table_stride,
+                           int64_t pages_per_seq, const int32_t* cu_new, const int32_t* seq_lens, int64_t batch,
+                           int64_t tokens, int32_t n_heads, fa2_dtype dtype, void* stream) {
+    if (!inv_freq || rot_dim <= 0 || rot_dim % 2 != 0 || !isfinite(magnitude) || n_heads < 0) return FA2_ERR_INVALID_ARG;
+    if (n_heads > 0 ? !q || !q_out || !q_strides || !q_out_strides : q || q_out) return FA2_ERR_INVALID_ARG;
+    RopeAppendParams p{};
+    const fa2_status st = append_rows(cache, k, v, k_strides, v_strides, block_table, table_stride, pages_per_seq, cu_new,
+                                      seq_lens, batch, tokens, dtype, &p.rows);
+    if (st != FA2_OK) return st;
+    if (rot_dim > cache->head_dim) return FA2_ERR_INVALID_ARG;
+    if (rot_dim % 16 != 0 || n_heads > kMaxGrid) return FA2_ERR_UNSUPPORTED;
+    if (!aligned(inv_freq, 8) || !aligned(positions, 4)) return FA2_ERR_MISALIGNED;
+    if (n_heads > 0) {
+        const int64_t sizes[2] = {tokens, n_heads};
+        if (!strides_ok(q_strides, 2) || !strides_ok(q_out_strides, 2) || !rows_apart(sizes, q_out_strides, 2, cache->head_dim))
+            return FA2_ERR_INVALID_ARG;
+        if (q == q_out)
+            for (int i = 0; i < 2; ++i)
+                if (sizes[i] > 1 && q_strides[i] != q_out_strides[i]) return FA2_ERR_INVALID_ARG;
+        if (!aligned(q, 16) || !aligned(q_out, 16)) return FA2_ERR_MISALIGNED;
+        for (int i = 0; i < 2; ++i) {
+            if (sizes[i] > 1 && (q_strides[i] % 8 != 0 || q_out_strides[i] % 8 != 0)) return FA2_ERR_MISALIGNED;
+            p.qs[i] = sizes[i] > 1 ? q_strides[i] * 2 : 0;
+            p.qos[i] = sizes[i] > 1 ? q_out_strides[i] * 2 : 0;
+        }
+        p.q = static_cast<const char*>(q);
+        p.q_out = static_cast<char*>(q_out);
+        p.heads = n_heads;
     }
-    p.cu_new = cu_new;
-    p.tokens = tokens;
-    return run(p, launch_kv_rows, stream);
+    p.inv_freq = inv_freq;
+    p.positions = positions;
+    p.rot = rot_dim;
+    p.interleaved = interleaved != 0;
+    p.magnitude = magnitude;
+    int exponent;
+    const float fraction = frexpf(fabsf(magnitude), &exponent);  // |magnitude| = fraction 2^exponent, fraction in [1/2, 1)
+    if (fraction == 0.5f) --exponent;
+    p.grow = magnitude != 0.f && exponent > 0 ? exponent : 0;
+    return run(p, launch_rope_append, stream);
 }
 
 fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, const int64_t out_strides[3],
@@ -214,7 +313,7 @@ fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, cons
     for (int i = 0; i < 3; ++i) p.ks[i] = p.vs[i] = out_strides[i] * 2;
     p.tokens = max_len;
     p.read = true;
-    return run(p, launch_kv_rows, stream);
+    return run(p, p.c.form == kRowsE2m1 ? launch_kv_read_e2m1 : launch_kv_rows, stream);
 }
 
 size_t fa2_decode_workspace_size(int64_t batch, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim) {
@@ -228,26 +327,73 @@ fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_ca
                       const int32_t* block_table, int64_t table_stride, int64_t pages_per_seq,
                       const int32_t* seq_lens, int64_t batch, int32_t n_heads, int64_t window, void* workspace,
                       size_t workspace_bytes, fa2_dtype dtype, float softmax_scale, void* stream) {
-    if (!q || !q_strides || !o || !lse || n_heads <= 0 || window < 0) return FA2_ERR_INVALID_ARG;
-    if (!(softmax_scale > 0.f) || !isfinite(softmax_scale) || !strides_ok(q_strides, 2)) return FA2_ERR_INVALID_ARG;
-    DecodeParams p{};
-    const fa2_status st = paged(cache, block_table, table_stride, pages_per_seq, seq_lens, batch, dtype, &p.c);
+    return decode_call(q, q_strides, cache, o, lse, block_table, table_stride, pages_per_seq, seq_lens, batch, n_heads, window,
+                       workspace, workspace_bytes, dtype, softmax_scale, stream, false);
+}
+
+fa2_status fa2_decode_selected(const void* q, const int64_t q_strides[2], const fa2_kv_cache* cache, void* o, float* lse,
+                               const int32_t* block_table, int64_t pages_per_seq, const int32_t* seq_lens, int64_t batch,
+                               int32_t n_heads, void* workspace, size_t workspace_bytes, fa2_dtype dtype,
+                               float softmax_scale, void* stream) {
+    return decode_call(q, q_strides, cache, o, lse, block_table, pages_per_seq, pages_per_seq, seq_lens, batch, n_heads, 0,
+                       workspace, workspace_bytes, dtype, softmax_scale, stream, true);
+}
+
+fa2_status fa2_kv_bounds(const fa2_kv_cache* cache, int8_t* bounds, uint8_t* bounds_exp, const int32_t* block_table,
+                         int64_t table_stride, int64_t pages_per_seq, const int32_t* cu_new, const int32_t* seq_lens,
+                         int64_t batch, int64_t tokens, fa2_dtype dtype, void* stream) {
+    if (!bounds || !bounds_exp || tokens <= 0 || (!cu_new && tokens != batch)) return FA2_ERR_INVALID_ARG;
+    KvBoundsParams p{};
+    const fa2_status st = paged(cache, block_table, table_stride, pages_per_seq, seq_lens, batch, dtype, &p.c, true);
     if (st != FA2_OK) return st;
-    if (n_heads % cache->n_kv_heads != 0) return FA2_ERR_INVALID_ARG;
-    if (n_heads > kMaxGrid || batch * n_heads > INT32_MAX) return FA2_ERR_UNSUPPORTED;
-    if (!aligned(q, 16) || !aligned(o, 16) || !aligned(lse, 16)) return FA2_ERR_MISALIGNED;
+    if (tokens > INT32_MAX) return FA2_ERR_UNSUPPORTED;
+    if (!aligned(bounds, 16) || !aligned(cu_new, 4)) return FA2_ERR_MISALIGNED;
+    p.bounds = bounds; p.bounds_exp = bounds_exp; p.cu_new = cu_new; p.tokens = tokens;
+    return run(p, launch_kv_bounds, stream);
+}
+
+size_t fa2_select_workspace_size(int64_t batch, int32_t n_kv_heads, int64_t pages_per_seq) {
+    if (batch <= 0 || n_kv_heads <= 0 || pages_per_seq <= 0 || batch > kMaxGrid || n_kv_heads > 1024 || pages_per_seq > kMaxLen) return 0;
+    return (size_t)batch * n_kv_heads * pages_per_seq * sizeof(uint32_t);
+}
+
+fa2_status fa2_select_pages(const void* q, const int64_t q_strides[2], const int8_t* bounds, const uint8_t* bounds_exp,
+                            int64_t num_pages, int32_t page_size, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                            const int32_t* block_table, int64_t table_stride, int64_t pages_per_seq,
+                            const int32_t* seq_lens, int64_t batch, int32_t* sel_table, int32_t* sel_lens, int64_t budget,
+                            int64_t first, int64_t recent, void* workspace, size_t workspace_bytes, fa2_dtype dtype,
+                            void* stream) {
+    if (!q || !q_strides || !bounds || !bounds_exp || !block_table || !seq_lens || !sel_table || !sel_lens) return FA2_ERR_INVALID_ARG;
+    if (dtype != FA2_DTYPE_F32 && dtype != FA2_DTYPE_F16 && dtype != FA2_DTYPE_BF16) return FA2_ERR_INVALID_ARG;
+    if (num_pages <= 0 || page_size <= 0 || n_heads <= 0 || n_kv_heads <= 0 || head_dim <= 0 || batch <= 0 || pages_per_seq <= 0 ||
+        budget <= 0 || first < 0 || recent < 0 || first > budget || recent > budget - first || n_heads % n_kv_heads != 0)
+        return FA2_ERR_INVALID_ARG;
+    if (table_stride < 0 || (batch > 1 && table_stride < pages_per_seq) || !strides_ok(q_strides, 2)) return FA2_ERR_INVALID_ARG;
+    if (dtype == FA2_DTYPE_F32 || head_dim > 128 || head_dim % 8 != 0) return FA2_ERR_UNSUPPORTED;
+    if (n_heads / n_kv_heads > 128 || n_kv_heads > 1024 || n_heads > kMaxGrid || num_pages > INT32_MAX || batch > kMaxGrid || batch * n_kv_heads > (1 << 20) ||
+        page_size > kMaxLen || pages_per_seq > kMaxLen || pages_per_seq * page_size > kMaxLen || budget > kMaxLen ||
+        budget * page_size > kMaxLen)
+        return FA2_ERR_UNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(sel_table, 4) ||
+        !aligned(sel_lens, 4))
+        return FA2_ERR_MISALIGNED;
     const int64_t sizes[2] = {batch, n_heads};
     for (int i = 0; i < 2; ++i)
         if (sizes[i] > 1 && q_strides[i] % 8 != 0) return FA2_ERR_MISALIGNED;
-    if (!workspace || !aligned(workspace, 16) ||
-        workspace_bytes < decode_workspace_bytes(n_heads, cache->n_kv_heads, cache->head_dim))
+    if (!workspace || !aligned(workspace, 16) || workspace_bytes < fa2_select_workspace_size(batch, n_kv_heads, pages_per_seq))
         return FA2_ERR_WORKSPACE;
+    SelectParams p{};
     p.q = q; p.q_batch = q_strides[0]; p.q_head = q_strides[1];
-    p.o = o; p.lse = lse; p.heads = n_heads;
-    p.window = window < p.c.room ? window : 0;  // as wide as the table: all keys
-    p.workspace = static_cast<float*>(workspace);
-    p.scale = softmax_scale;
-    return run(p, launch_decode, stream);
+    p.bounds = bounds; p.bounds_exp = bounds_exp; p.num_pages = num_pages;
+    p.page_size = page_size; p.group = n_heads / n_kv_heads; p.hkv = n_kv_heads; p.d = head_dim;
+    page_divisor(page_size, &p.page_mul, &p.page_shift);
+    p.table = block_table; p.table_stride = table_stride; p.per_seq = pages_per_seq;
+    p.lens = seq_lens; p.batch = batch;
+    p.sel_table = sel_table; p.sel_lens = sel_lens;
+    p.budget = (int)budget; p.first = (int)first; p.recent = (int)recent;
+    p.scores = static_cast<uint32_t*>(workspace);
+    p.dtype = (int)dtype;
+    return run(p, launch_select_pages, stream);
 }
 
 fa2_status fa2_last_decode_info(int32_t* ctas_per_item) {

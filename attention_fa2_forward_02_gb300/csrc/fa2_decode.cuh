@@ -50,10 +50,11 @@ constexpr float kRescale = 8.0f;  // the running maximum may lag by this much (b
 constexpr float kLn2 = 0.693147180559945309f;
 constexpr float kNoScore = -3.402823466e38f;  // a maximum of no scores, from which -infinity can be subtracted
 
-// D: the head size's kernel; kTiles: query heads per item / 8.
-template <int D, bool kE4m3, int kTiles>
+// D: the head size's kernel; kForm: the cache's type (CacheForm); kTiles: query heads per item / 8.
+template <int D, int kForm, int kTiles>
 struct Cfg {
-    static constexpr int kRowBytes = kE4m3 ? D : 2 * D;
+    static constexpr bool kCodes = kForm != kRows16, kE4m3 = kForm == kRowsE4m3, kE2m1 = kForm == kRowsE2m1;
+    static constexpr int kRowBytes = kE2m1 ? D / 2 : (kE4m3 ? D : 2 * D);
     static constexpr int kRows = 8 * kTiles;                // query heads per item
     // CTAs an SM. 16-bit rows keep memory busy with two, and three read unevenly fast (21 sequences of
     // up to 65536, 8 heads: d 128 567 -> 634 us, d 64 317 -> 341). e4m3 has more to do per byte: 32
@@ -65,7 +66,8 @@ struct Cfg {
     static constexpr int kMaxCtas = 152 * kPerSm;           // a fixed number: the split depends on the lengths alone
     // in one launch, where latency is more than memory: 7 windows of 1024 keys, d 64, 9.6 -> 8.8 us
     static constexpr int kShortPerSm = kTiles == 1 && kRowBytes < 256 ? 3 : kPerSm;
-    static constexpr int kKeys = kRowBytes >= 256 ? 16 : (kRowBytes == 128 ? 32 : 64);  // keys per block: 8 KB of K and V (4 of 32-byte rows)
+    // keys per block: 8 KB of K and V (4 of 32-byte rows, and of 4-bit rows at d 128)
+    static constexpr int kKeys = kRowBytes >= 256 ? 16 : (kRowBytes == 128 || (kE2m1 && D == 128) ? 32 : 64);
     static constexpr int kLooks = (kKeys + 31) / 32;        // keys a lane looks up per block
     static constexpr int kChunks = kRowBytes / 16;          // 16-byte chunks a row
     static constexpr int kTile = kKeys * kRowBytes;         // K or V of a block
@@ -75,13 +77,15 @@ struct Cfg {
     // sequences of up to 65536 tokens in 16 bits: d 96 531 -> 466 us, d 48 420 -> 359, d 32 256 ->
     // 172; 32 of up to 8192 in e4m3: d 64 50 -> 40, d 96 82 -> 74. Whole lines of 16-bit rows were
     // 1% slower by halves, so there d is asked; those of e4m3 rows were not.
-    static constexpr bool kHalfLines = kE4m3 || kRowBytes <= 64;
-    static constexpr int kInfo = kE4m3 ? kKeys * 8 : 16;    // e4m3: a float2 per key; else the keys that count, as bits
-    static constexpr int kStage = 2 * kTile + kInfo;
+    static constexpr bool kHalfLines = kCodes || kRowBytes <= 64;
+    static constexpr int kInfo = kCodes ? kKeys * 8 : 16;   // codes: a float2 per key; else the keys that count, as bits
+    static constexpr int kScaleRow = D / 16;                // e2m1: scale bytes of a key
+    static constexpr int kScales = kE2m1 ? kKeys * kScaleRow : 0;  // and of a block's keys, or values
+    static constexpr int kStage = 2 * kTile + kInfo + 2 * kScales;
     static constexpr int kStages = 2;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kQ = kRows * D * 2;                // q as the first product takes it
-    static constexpr int kPitch = kE4m3 ? D + 8 : D + 4;    // floats a row at the end of an item (no bank twice)
+    static constexpr int kPitch = kCodes ? D + 8 : D + 4;    // floats a row at the end of an item (no bank twice)
     static constexpr int smem(int merge_rows) { return kRing + kQ + kWarps * merge_rows * kPitch * 4 + kRows * 4; }
     static constexpr bool fits(int bytes) { return bytes + 1024 + 256 <= 228 * 1024 / kShortPerSm; }
     // rows the warps add up at a time there: as many as find room
@@ -97,7 +101,8 @@ template <int kChunks>
 __device__ __forceinline__ int swizzle(int r, int c) {
     if constexpr (kChunks >= 8) return r * kChunks + (c ^ (r & 7));
     else if constexpr (kChunks == 4) return r * 4 + (c ^ ((r >> 1) & 3));
-    else return r * 2 + (c ^ ((r >> 2) & 1));
+    else if constexpr (kChunks == 2) return r * 2 + (c ^ ((r >> 2) & 1));
+    else return r;
 }
 
 // bytes: 16, or 0 (nothing is read, the 16 bytes are filled with zeros)
@@ -120,6 +125,84 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
 __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+
+__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t (&r)[4]) {  // lanes 0 .. 15 give addresses
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm2_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
+}
+
+// kBytes: 4 or 8, read where `on`, else zeros
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool on) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(kBytes), "r"(on ? kBytes : 0) : "memory");
+}
+__device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
+    asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"((uint16_t)v) : "memory");
+}
+__device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
+__device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_shared_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// A key's scales of groups `half`, half + 2, ... as pairs of the same half number; `row`: its D / 16 bytes.
+template <int D>
+__device__ __forceinline__ void key_scales(uint32_t row, int half, uint32_t (&s)[D / 32]) {
+    if constexpr (D == 32) {
+        const uint32_t f = e4m3x2_to_f16x2(ld_shared_u16(row));
+        s[0] = __byte_perm(f, 0, half ? 0x3232 : 0x1010);
+    } else {
+        uint32_t w;
+        if constexpr (D == 128) {
+            const uint2 b = ld_shared_v2(row);
+            w = __byte_perm(b.x, b.y, half ? 0x7531 : 0x6420);
+        } else {
+            w = __byte_perm(ld_shared_u32(row), 0, half ? 0x4431 : 0x4420);
+        }
+        uint32_t f[2];
+        e4m3x4_to_f16x4(w, f[0], f[1]);
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) s[i] = __byte_perm(f[i / 2], 0, i % 2 ? 0x3232 : 0x1010);
+    }
+}
+
+// Two keys' scales of groups `half`, half + 2, ..., the first key's in the lower half; `rows`: their 2 D / 16 bytes.
+template <int D>
+__device__ __forceinline__ void value_scales(uint32_t rows, int half, uint32_t (&s)[D / 32]) {
+    if constexpr (D == 32) {
+        const uint32_t w = ld_shared_u32(rows);
+        s[0] = e4m3x2_to_f16x2(__byte_perm(w, 0, half ? 0x4431 : 0x4420));
+    } else if constexpr (D == 64) {
+        const uint2 w = ld_shared_v2(rows);
+        e4m3x4_to_f16x4(__byte_perm(w.x, w.y, half ? 0x7351 : 0x6240), s[0], s[1]);
+    } else {
+        const uint4 w = ld_shared_v4(rows);
+        const uint32_t a = __byte_perm(w.x, w.y, half ? 0x7531 : 0x6420), b = __byte_perm(w.z, w.w, half ? 0x7531 : 0x6420);
+        e4m3x4_to_f16x4(__byte_perm(a, b, 0x5140), s[0], s[1]);
+        e4m3x4_to_f16x4(__byte_perm(a, b, 0x7362), s[2], s[3]);
+    }
 }
 
 // The transpose of an 8 x 8 matrix of 16-bit elements, row g, columns 2t, 2t+1 in lane 4 g + t.
@@ -197,25 +280,25 @@ struct __align__(16) Stats {
 };
 
 // The factors that bring the O and l of a share to the larger references (m, ml).
-template <bool kE4m3>
+template <bool kCodes>
 struct Factors {
     float o, l;
     __device__ __forceinline__ Factors(const Stats& s, float m, float ml) {
         o = ex2_approx(s.m - (m == -INFINITY ? 0.f : m));
-        l = kE4m3 ? ex2_approx(s.ml - ml) : o;
+        l = kCodes ? ex2_approx(s.ml - ml) : o;
     }
 };
 
 // A row's last step: O = sum P V times scale(), LSE.
-template <bool kE4m3>
+template <bool kCodes>
 struct Last {
     float inv, half, lse;
     __device__ __forceinline__ Last(float m, float ml, float l) {
         inv = l > 0.f ? 1.f / l : (l == 0.f ? 0.f : l);
-        half = kE4m3 ? ex2_approx(0.5f * (m - ml)) : 1.f;  // twice: m - ml reaches 120 and more
-        lse = l == 0.f ? -INFINITY : ((kE4m3 ? ml : m) + lg2_approx(l)) * kLn2;
+        half = kCodes ? ex2_approx(0.5f * (m - ml)) : 1.f;  // twice: m - ml reaches 120 and more
+        lse = l == 0.f ? -INFINITY : ((kCodes ? ml : m) + lg2_approx(l)) * kLn2;
     }
-    __device__ __forceinline__ float operator()(float a) const { return kE4m3 ? a * half * inv * half : a * inv; }
+    __device__ __forceinline__ float operator()(float a) const { return kCodes ? a * half * inv * half : a * inv; }
 };
 
 // Workspace: per CTA two partial results (its first item, if that began before it or ends after
@@ -322,7 +405,7 @@ struct Segment {
 
 // Joins the shares [kRows][D], [kRows] Stats that each CTA of the cluster has at `part` in its
 // shared memory, in rank order: CTA r writes rows r, r + ranks, ... Every thread of the cluster calls it.
-template <int D, bool kBf16, bool kE4m3, int kRows>
+template <int D, bool kBf16, bool kCodes, int kRows>
 __device__ __forceinline__ void join_cluster(const DecodeParams& p, uint32_t part, int ranks, int rank, int rows, int64_t out_row) {
     cluster_sync_all();
     const int d = threadIdx.x;  // D <= kThreads: a column a thread
@@ -333,7 +416,7 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& p, uint32_t par
             Stats s;
             s.m = ld_cluster(at);
             s.l = ld_cluster(at + 4);
-            s.ml = kE4m3 ? ld_cluster(at + 8) : s.m;
+            s.ml = kCodes ? ld_cluster(at + 8) : s.m;
             return s;
         };
         float m = -INFINITY, ml = -INFINITY, a = 0.f, l = 0.f;
@@ -344,11 +427,11 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& p, uint32_t par
         }
         for (int k = 0; k < ranks; ++k) {
             const Stats s = stats(k);
-            const Factors<kE4m3> f(s, m, ml);
+            const Factors<kCodes> f(s, m, ml);
             l += f.l * s.l;
             a += f.o * ld_cluster(cluster_map(part + (r * D + d) * 4, k));
         }
-        const Last<kE4m3> last(m, ml, l);
+        const Last<kCodes> last(m, ml, l);
         if (d < p.c.d) put<kBf16>(p.o, (out_row + r) * p.c.d + d, last(a));
         if (d == 0) p.lse[out_row + r] = last.lse;
     }
@@ -357,11 +440,12 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& p, uint32_t par
 
 // kCluster: the CTAs of a cluster of `ranks` share the item blockIdx.x / ranks; nothing is left to
 // the second kernel.
-template <int D, bool kBf16, bool kE4m3, int kTiles, bool kCluster>
-__global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kShortPerSm : Cfg<D, kE4m3, kTiles>::kPerSm)
+template <int D, bool kBf16, int kForm, int kTiles, bool kCluster>
+__global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kShortPerSm : Cfg<D, kForm, kTiles>::kPerSm)
     fa2_decode_kernel(const DecodeParams p, int ranks) {
-    using C = Cfg<D, kE4m3, kTiles>;
-    constexpr bool kMmaBf16 = kBf16 && !kE4m3;
+    using C = Cfg<D, kForm, kTiles>;
+    constexpr bool kCodes = C::kCodes, kE4m3 = C::kE4m3, kE2m1 = C::kE2m1;
+    constexpr bool kMmaBf16 = kBf16 && !kCodes;
     // m lies this much below the maximum it was taken from: weights 2^-(14 + kLift) of the largest
     // still have all of half's bits (bfloat16 has float32's exponents)
     constexpr float kLift = kMmaBf16 ? 0.f : 7.f;
@@ -369,14 +453,14 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
     // largest error of O but where a half weight's 2^-11 stands beside a bfloat16 result's 2^-8. (e4m3
     // with bfloat16, batch of 32: 8 heads 66.0 us in one product and 67.7 in two, 16 heads 79.8 and
     // 85.5; 16-bit long contexts, bound by memory, the same.)
-    constexpr bool kRest = !(kE4m3 && kBf16);
+    constexpr bool kRest = !(kCodes && kBf16);
     constexpr int kKeys = C::kKeys, S = C::kStages, kRows = C::kRows, kMt = kKeys / 16, kMR = C::kMergeRows;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ LocateSmem located;
     const PagedParams& c = p.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = p.heads / c.hkv, hblocks = (group + kRows - 1) / kRows;
-    const int64_t per_seq = (int64_t)c.hkv * hblocks;
+    const int64_t per_seq = (int64_t)p.seq_heads() * hblocks;
     grid_begin();
 
     Split split(0, 0);
@@ -385,10 +469,11 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
     auto empty_rows = [&]() {
         for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
             if (range_of(p, b).len > 0) continue;
-            const int64_t row0 = (int64_t)b * p.heads;
-            for (int i = threadIdx.x; i < p.heads * c.d / 8; i += kThreads)
+            const int rows = group * p.seq_heads();
+            const int64_t row0 = (int64_t)b * rows;
+            for (int i = threadIdx.x; i < rows * c.d / 8; i += kThreads)
                 reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row0 * c.d)[i] = make_uint4(0, 0, 0, 0);
-            for (int i = threadIdx.x; i < p.heads; i += kThreads) p.lse[row0 + i] = -INFINITY;
+            for (int i = threadIdx.x; i < rows; i += kThreads) p.lse[row0 + i] = -INFINITY;
         }
     };
     if constexpr (!kCluster) {
@@ -422,6 +507,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
             return s.k1 > s.k0;
         }
     };
+    // the key-value head of a segment's item
+    auto kv_head = [&](const Segment& s) { return p.per_head ? s.b % c.hkv : s.item / hblocks; };
     // this warp's blocks of segment number `number`: k0 + turn(number), + kWarps, ...
     auto turn = [&](int number) { return (warp + number) % kWarps; };
     auto count = [&](const Segment& s, int number) {
@@ -460,7 +547,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
     int64_t ahead_head = 0, ahead_exp = 0;                // the head's offset in a page, in its scale bytes
     auto enter = [&]() {
         if (!ahead_live) return;
-        const int hk = ahead.item / hblocks;
+        const int hk = kv_head(ahead);
         ahead_left = count(ahead, ahead_number);
         ahead_key = ahead.range.base + (ahead.k0 + turn(ahead_number)) * kKeys + (kKeys < 32 ? lane % kKeys : lane);
         ahead_table = c.table + ahead.b * c.table_stride;
@@ -496,7 +583,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
         --ahead_left;
     };
     // a lane copies chunk lane % kChunks of every kStep-th row; past the head's size it fills with zeros
-    const int lane_bytes = lane % C::kChunks * 16 < c.d * (kE4m3 ? 1 : 2) ? 16 : 0;
+    const int lane_bytes = lane % C::kChunks * 16 < (kE2m1 ? c.d / 2 : (kE4m3 ? c.d : 2 * c.d)) ? 16 : 0;
     const int64_t lane_off = lane / C::kChunks * c.slot_stride + (lane_bytes ? lane % C::kChunks * 16 : 0);
     const int64_t rows_off = 32 / C::kChunks * c.slot_stride;
     const bool sixteens = c.page_size % 16 == 0;
@@ -504,6 +591,51 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
     int fill = 0;                        // the stage to fill next
     uint32_t ka[C::kLooks], ve[C::kLooks];  // scale bytes of the block loaded last; ve 256: the key does not count
     int info_stage = -1;                 // and its stage, while they are not stored
+    // e2m1: the scale bytes of the keys `some` at `at` into K's and V's scales at `dst`, rows of kScaleRow bytes.
+    // The scale bytes of keys that follow one another in a page do so too: 16 keys of whole rows are D
+    // contiguous bytes. Those of keys among them that do not count come along, and store_info clears them.
+    auto load_scales = [&](uint32_t dst, const uint32_t (&some)[C::kLooks], const int64_t (&at)[C::kLooks]) {
+        if constexpr (kE2m1) {
+            constexpr int kPer = D / 16;  // 16-byte pieces of 16 keys' scale bytes
+            const int row = c.d / 16;     // bytes a key has in memory
+            if (sixteens) {
+                // pieces 0 .. kKeys / 16 * kPer - 1 of K, then those of V; with d < D rows of d / 16 bytes, widened by store_info
+#pragma unroll
+                for (int i0 = 0; i0 < 2 * kKeys / 16 * kPer; i0 += 32) {  // (of D = 32 only half a warp's worth)
+                    const int i = i0 + lane, n = i % (kKeys / 16 * kPer), r = n / kPer * 16, piece = n % kPer;
+                    const uint32_t there = (some[0] >> (r & 31)) & 0xffffu, there1 = (some[C::kLooks - 1] >> (r & 31)) & 0xffffu;
+                    const uint32_t set = r < 32 ? there : there1;
+                    const int one = set ? __ffs(set) - 1 : 0;
+                    const int64_t a0 = __shfl_sync(0xffffffffu, at[0], (r & 31) + one);
+                    const int64_t a1 = __shfl_sync(0xffffffffu, at[C::kLooks - 1], (r & 31) + one);
+                    const bool on = set && piece < row, used = i < 2 * kKeys / 16 * kPer;
+                    const uint8_t* src = (i < kKeys / 16 * kPer ? c.k_scale : c.v_scale) + (on ? ((r < 32 ? a0 : a1) - one) * row + piece * 16 : 0);
+                    const uint32_t to = dst + (i < kKeys / 16 * kPer ? 0 : C::kScales) + n / kPer * (16 * C::kScaleRow) + piece * 16;
+                    if (used) cp_async16<true>(to, src, on ? 16 : 0, true);
+                }
+            } else {
+#pragma unroll
+                for (int j = 0; j < C::kLooks; ++j) {
+                    const bool on = (some[j] >> lane) & 1u;
+                    const uint8_t *ks = c.k_scale + (on ? at[j] * row : 0), *vs = c.v_scale + (on ? at[j] * row : 0);
+                    const uint32_t to = dst + (lane + 32 * j) * C::kScaleRow;
+                    if (D >= 64 && row == kPer) {
+                        cp_async_small<kPer>(to, ks, on);
+                        cp_async_small<kPer>(to + C::kScales, vs, on);
+                    } else {  // rows of 2 or 6 bytes have no asynchronous copy
+                        for (int e = 0; e < row; e += 2) {
+                            st_shared_u16(to + e, on ? *reinterpret_cast<const uint16_t*>(ks + e) : 0);
+                            st_shared_u16(to + C::kScales + e, on ? *reinterpret_cast<const uint16_t*>(vs + e) : 0);
+                        }
+                        for (int e = row; e < kPer; e += 2) {
+                            st_shared_u16(to + e, 0);
+                            st_shared_u16(to + C::kScales + e, 0);
+                        }
+                    }
+                }
+            }
+        }
+    };
     auto load = [&]() {  // copies the block looked up last into the next stage; commits one group
         if (found) {
             const uint32_t st = my_addr + fill * C::kStage;
@@ -511,14 +643,16 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
             const char* vbase = c.v + head_off;
             int64_t off[C::kLooks];
             uint32_t some[C::kLooks];  // the keys that count, as bits
+            int64_t scale_at[C::kLooks];  // e2m1: the key's place among the scale bytes
 #pragma unroll
             for (int j = 0; j < C::kLooks; ++j) {
                 Slot s{-1, -1};
                 if (slot[j] >= 0) s = slot_of(c, page[j], slot[j]);
                 off[j] = s.off;
                 some[j] = __ballot_sync(0xffffffffu, s.off >= 0);
-                if constexpr (kE4m3) {
+                if constexpr (kCodes) {
                     const int64_t e = s.exp + head_exp;
+                    scale_at[j] = e;
                     ka[j] = s.off >= 0 ? c.k_exp[e] : 127u;
                     ve[j] = s.off >= 0 ? c.v_exp[e] : 256u;
                 } else {
@@ -536,6 +670,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                     const char *ks = kbase + o, *vs = vbase + o;
 #pragma unroll
                     for (int i = 0; i < 16; i += kStep) {
+                        if (kStep > 16 && lane >= 16) break;  // 16 rows are all there is
                         const int bytes = (there >> (i + lane / C::kChunks)) & 1u ? lane_bytes : 0;
                         const uint32_t dst = st + swizzle<C::kChunks>(r + i + lane / C::kChunks, lane % C::kChunks) * 16;
                         cp_async16<C::kHalfLines>(dst, ks, bytes, half_lines);
@@ -560,14 +695,54 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                     cp_async16<C::kHalfLines>(dst + C::kTile, vbase + at, bytes, half_lines);
                 }
             }
+            if constexpr (kE2m1) load_scales(st + 2 * C::kTile + C::kInfo, some, scale_at);
             info_stage = fill;
         }
         cp_async_commit();
         fill = fill + 1 == S ? 0 : fill + 1;
     };
-    auto store_info = [&]() {  // e4m3: the key's scale, and the value scale's exponent (-infinity: masked)
-        if constexpr (kE4m3) {
+    // e2m1, once a block's copies are done: rows of d / 16 scale bytes to kScaleRow, and zeros for keys that do
+    // not count, so that whatever lies there (a NaN) times a code of zero is zero.
+    auto tidy_scales = [&](uint32_t scales) {
+        if constexpr (kE2m1) {
+            const bool widen = D == 128 && sixteens && c.d < D;
+            bool clear = false;
+#pragma unroll
+            for (int j = 0; j < C::kLooks; ++j) clear |= ve[j] >= 256;
+            if (!widen && !__any_sync(0xffffffffu, clear)) return;
+            __syncwarp();  // other lanes' copies
+            uint32_t w[C::kLooks][2][2];
+            if (widen) {
+#pragma unroll
+                for (int j = 0; j < C::kLooks; ++j)
+#pragma unroll
+                    for (int side = 0; side < 2; ++side) {
+                        // 16 keys' rows of d / 16 bytes lie together at the beginning of their 16 kScaleRow bytes
+                        const int key = lane + 32 * j;
+                        const uint32_t from = scales + side * C::kScales + key / 16 * (16 * C::kScaleRow) + key % 16 * (c.d / 16);
+                        w[j][side][0] = ld_shared_u16(from) | ld_shared_u16(from + 2) << 16;
+                        w[j][side][1] = ld_shared_u16(from + 4);
+                    }
+                __syncwarp();
+            }
+#pragma unroll
+            for (int j = 0; j < C::kLooks; ++j) {
+                if (!widen && ve[j] < 256) continue;
+#pragma unroll
+                for (int side = 0; side < 2; ++side) {
+                    const uint32_t to = scales + side * C::kScales + (lane + 32 * j) * C::kScaleRow;
+                    const bool keep = widen && ve[j] < 256;
+                    if constexpr (D == 128) st_shared_v2(to, keep ? w[j][side][0] : 0, keep ? w[j][side][1] : 0);
+                    else if constexpr (D == 64) st_shared_u32(to, 0);
+                    else st_shared_u16(to, 0);
+                }
+            }
+        }
+    };
+    auto store_info = [&]() {  // codes: the key's scale, and the value scale's exponent (-infinity: masked)
+        if constexpr (kCodes) {
             if (info_stage < 0) return;
+            if constexpr (kE2m1) tidy_scales(smem_u32(my + info_stage * C::kStage + 2 * C::kTile + C::kInfo));
 #pragma unroll
             for (int j = 0; j < C::kLooks; ++j)
                 reinterpret_cast<float2*>(my + info_stage * C::kStage + 2 * C::kTile)[lane + 32 * j] =
@@ -580,9 +755,10 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
     const int q_row = threadIdx.x / kParts, q_part = threadIdx.x % kParts;
     uint4 q_lo, q_hi;
     auto fetch_q = [&](const Segment& s) {
-        const int hb = s.item % hblocks, head = s.item / hblocks * group + hb * kRows + q_row;
+        const int hb = s.item % hblocks, head = kv_head(s) * group + hb * kRows + q_row;
+        const int b = p.per_head ? s.b / c.hkv : s.b;
         const bool on = q_row < min(kRows, group - hb * kRows);
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + s.b * p.q_batch + (int64_t)head * p.q_head + 16 * q_part;
+        const uint16_t* src = static_cast<const uint16_t*>(p.q) + b * p.q_batch + (int64_t)head * p.q_head + 16 * q_part;
         q_lo = q_hi = make_uint4(0, 0, 0, 0);
         if (on && 16 * q_part < c.d) q_lo = *reinterpret_cast<const uint4*>(src);
         if (on && 16 * q_part + 8 < c.d) q_hi = *reinterpret_cast<const uint4*>(src + 8);
@@ -593,7 +769,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
     for (int i = 0; i < S - 1; ++i) {
         load();
         look();
-        store_info();
+        if constexpr (!kE2m1) store_info();  // (it clears scales behind their copies: in the loop, once those are done)
     }
 
     if constexpr (!kCluster) empty_rows();
@@ -608,8 +784,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
     Torn ends_later{0, 0, 0, 0};
 
     for (; live; ++number) {
-        const int hk = seg.item / hblocks, hb = seg.item % hblocks;
-        const int head0 = hk * group + hb * kRows;        // first query head
+        const int hb = seg.item % hblocks;
         const int rows = min(kRows, group - hb * kRows);  // query heads of the item
 
         // ---- q into shared memory, by whole warps (they exchange)
@@ -617,7 +792,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
             const int r = q_row, part = q_part;
             uint32_t w[8] = {q_lo.x, q_lo.y, q_lo.z, q_lo.w, q_hi.x, q_hi.y, q_hi.z, q_hi.w};
             float scale = p.scale * 1.4426950408889634f;
-            if constexpr (kBf16 && kE4m3) {
+            if constexpr (kBf16 && kCodes) {
                 float a = 0.f;
 #pragma unroll
                 for (int i = 0; i < 8; ++i)
@@ -634,11 +809,21 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                 for (int i = 0; i < 8; ++i)
                     w[i] = pack2<false>(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
             }
-            // 8-bit cache: elements 4t .. 4t+3 of 16 as columns 2t, 2t+1, 2t+8, 2t+9, the order its codes come in
+            // 8-bit cache: elements 4t .. 4t+3 of 16 as columns 2t, 2t+1, 2t+8, 2t+9, the order its codes come in;
+            // 4-bit cache: the same of elements 8t .. 8t+3, and 8t+4 .. 8t+7, of 32 for its two steps of 16
             if (r < kRows) {
                 uint4* row = reinterpret_cast<uint4*>(q_smem);
+                if constexpr (kE2m1) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            reinterpret_cast<uint2*>(row + swizzle<D / 8>(r, 4 * (part / 2) + 2 * m + e))[part % 2] =
+                                make_uint2(w[2 * m + e], w[4 + 2 * m + e]);
+                } else {
                 row[swizzle<D / 8>(r, 2 * part)] = kE4m3 ? make_uint4(w[0], w[2], w[4], w[6]) : make_uint4(w[0], w[1], w[2], w[3]);
                 row[swizzle<D / 8>(r, 2 * part + 1)] = kE4m3 ? make_uint4(w[1], w[3], w[5], w[7]) : make_uint4(w[4], w[5], w[6], w[7]);
+                }
                 if (part == 0) q_scale[r] = scale;
             }
         }
@@ -660,11 +845,11 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
             qscale[h][0] = q_scale[8 * h + 2 * t];
             qscale[h][1] = q_scale[8 * h + 2 * t + 1];
         }
-        // e4m3: a product with q in half, 2^31 at most, times the key's scale (to 2^126) and the row's
+        // codes: a product with q in half, 2^31 (e4m3) or 2^34 (e2m1) at most, times the key's scale (to 2^126) and the row's
         // (2^-126 to 2^113 and the softmax's) must not overflow on the way to a score that does not.
         // The scales are multiplied first, a row's of more than 1 last.
         bool large_q = false;
-        if constexpr (kE4m3) {
+        if constexpr (kCodes) {
 #pragma unroll
             for (int h = 0; h < kTiles; ++h)
 #pragma unroll
@@ -703,7 +888,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
             for (int j = 0; j < kMt; ++j)
 #pragma unroll
                 for (int h = 0; h < kTiles; ++h) sc[j][h][0] = sc[j][h][1] = sc[j][h][2] = sc[j][h][3] = 0.f;
-            if constexpr (!kE4m3) {
+            if constexpr (!kCodes) {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
@@ -713,6 +898,36 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
 #pragma unroll
                         for (int h = 0; h < kTiles; ++h) mma16816<kMmaBf16>(sc[j][h], k4, qf[h][kk][0], qf[h][kk][1]);
                     }
+            } else if constexpr (kE2m1) {
+#pragma unroll
+                for (int j = 0; j < kMt; ++j) {
+                    // the scales of keys g, g + 8 (in half, twice) for this lane's half t / 2 of each 32 codes
+                    uint32_t ks[2][D / 32];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        key_scales<D>(vt + C::kTile + C::kInfo + (16 * j + 8 * e + g) * C::kScaleRow, t >> 1, ks[e]);
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; cc += 2) {
+                        uint32_t k4[4];  // (keys 0-7, 8-15) of 32 codes, of the next 32: codes 8t .. 8t+7
+                        const uint32_t at = kt + swizzle<C::kChunks>(16 * j + (lane & 15), C::kChunks > 1 ? cc + (lane >> 4) : 0) * 16;
+                        if constexpr (C::kChunks > 1) ldsm4(at, k4);
+                        else ldsm2(at, k4);
+#pragma unroll
+                        for (int e = 0; e < 2 && cc + e < D / 32; ++e) {
+                            uint32_t a[4], b[4];  // pairs of codes of key g, of key g + 8
+                            e2m1x8_to_f16x8(k4[2 * e], a);
+                            e2m1x8_to_f16x8(k4[2 * e + 1], b);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                const uint32_t a4[4] = {hmul2(a[2 * m], ks[0][cc + e]), hmul2(b[2 * m], ks[1][cc + e]),
+                                                        hmul2(a[2 * m + 1], ks[0][cc + e]), hmul2(b[2 * m + 1], ks[1][cc + e])};
+#pragma unroll
+                                for (int h = 0; h < kTiles; ++h)
+                                    mma16816<false>(sc[j][h], a4, qf[h][2 * (cc + e) + m][0], qf[h][2 * (cc + e) + m][1]);
+                            }
+                        }
+                    }
+                }
             } else {
 #pragma unroll
                 for (int kk = 0; kk < D / 16; kk += 2)
@@ -730,8 +945,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         }
                     }
             }
-            // ---- in e4m3 s, and l; x, the running maximum, P
-            if constexpr (kE4m3) {
+            // ---- with codes s, and l; x, the running maximum, P
+            if constexpr (kCodes) {
                 float ev[kMt][2];  // of keys g, g + 8: the value scale's exponent, -infinity: masked
 #pragma unroll
                 for (int j = 0; j < kMt; ++j)
@@ -816,7 +1031,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                 return __any_sync(0xffffffffu, grow);
             };
             bool grow = grows();
-            if constexpr (kE4m3) {
+            if constexpr (kCodes) {
                 // Looked for only where a maximum would grow: the first blocks, and rows of zeros that
                 // stand out. (For every block it would be the stage's values read once more.)
                 if (grow) {
@@ -832,7 +1047,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                             any |= w.x | w.y | w.z | w.w;
                         }
                         const bool counts = reinterpret_cast<const float2*>(info)[r].y > -INFINITY;
-                        zeros[j] = __ballot_sync(0xffffffffu, counts && (any & 0x7f7f7f7fu) == 0);
+                        zeros[j] = __ballot_sync(0xffffffffu, counts && (any & (kE2m1 ? 0x77777777u : 0x7f7f7f7fu)) == 0);
                         some |= zeros[j];
                     }
                     if (some) {
@@ -856,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         const float m_new = fmaxf(m[h][n], mx[h][n] - kLift);
                         const float f = m_new == -INFINITY ? 1.f : ex2_approx(m[h][n] - m_new);
                         m[h][n] = m_new;
-                        if constexpr (!kE4m3) l[h][n] *= f;
+                        if constexpr (!kCodes) l[h][n] *= f;
 #pragma unroll
                         for (int d = 0; d < D / 16; ++d) {
                             o[d][h][n] *= f;
@@ -877,7 +1092,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         for (int n = 0; n < 2; ++n) {
                             float& x = sc[j][h][2 * e + n];
                             x = ex2_approx(x - (m[h][n] == -INFINITY ? 0.f : m[h][n]));
-                            if constexpr (!kE4m3) l[h][n] += x;
+                            if constexpr (!kCodes) l[h][n] += x;
                         }
                         const uint32_t w = pack2<kMmaBf16>(sc[j][h][2 * e], sc[j][h][2 * e + 1]);
                         pf[h][e] = transpose8(w);
@@ -886,7 +1101,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         pl[h][e] = transpose8(pack2<kMmaBf16>(sc[j][h][2 * e] - f.x, sc[j][h][2 * e + 1] - f.y));
                     }
                 // ---- O^T += V^T P^T
-                if constexpr (!kE4m3) {
+                if constexpr (!kCodes) {
                     const int r = 16 * j + (lane & 7) + (lane & 16 ? 8 : 0);
 #pragma unroll
                     for (int d = 0; d < D / 16; ++d) {
@@ -896,6 +1111,35 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                         for (int h = 0; h < kTiles; ++h) {
                             mma16816<kMmaBf16>(o[d][h], v4, pf[h][0], pf[h][1]);
                             if constexpr (kRest) mma16816<kMmaBf16>(o[d][h], v4, pl[h][0], pl[h][1]);
+                        }
+                    }
+                } else if constexpr (kE2m1) {
+                    // the scales of keys 2t, 2t+1 (and + 8) for this lane's half g / 4 of each 32 codes
+                    uint32_t vs[2][D / 32];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        value_scales<D>(vt + C::kTile + C::kInfo + C::kScales + (16 * j + 8 * e + 2 * t) * C::kScaleRow, g >> 2, vs[e]);
+#pragma unroll
+                    for (int cc = 0; cc < D / 32; cc += 2) {
+                        uint32_t v4[4];  // (keys 0-7, 8-15) of 32 codes, of the next 32: keys 2t, 2t+1 x codes 4g .. 4g+3
+                        const uint32_t at = vt + swizzle<C::kChunks>(16 * j + (lane & 15), C::kChunks > 1 ? cc + (lane >> 4) : 0) * 16;
+                        if constexpr (C::kChunks > 1) ldsm4_t(at, v4);
+                        else ldsm2_t(at, v4);
+#pragma unroll
+                        for (int e = 0; e < 2 && cc + e < D / 32; ++e) {
+                            uint32_t lo[4], hi[4];  // code 4g + i of keys 2t, 2t+1; of keys 2t+8, 2t+9
+                            e2m1_2x4_to_f16(v4[2 * e], lo);
+                            e2m1_2x4_to_f16(v4[2 * e + 1], hi);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {  // rows g: codes 4g + 2m, rows g + 8: 4g + 2m + 1
+                                const uint32_t a4[4] = {hmul2(lo[2 * m], vs[0][cc + e]), hmul2(lo[2 * m + 1], vs[0][cc + e]),
+                                                        hmul2(hi[2 * m], vs[1][cc + e]), hmul2(hi[2 * m + 1], vs[1][cc + e])};
+#pragma unroll
+                                for (int h = 0; h < kTiles; ++h) {
+                                    mma16816<false>(o[2 * (cc + e) + m][h], a4, pf[h][0], pf[h][1]);
+                                    if constexpr (kRest) mma16816<false>(o[2 * (cc + e) + m][h], a4, pl[h][0], pl[h][1]);
+                                }
+                            }
                         }
                     }
                 } else {
@@ -923,7 +1167,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
         // ---- the warps' results together, kMergeRows rows at a time: a warp or two per row
         const bool whole = kCluster ? ranks == 1 : seg.k0 == 0 && seg.k1 == seg.nb;
         const int which = first_item ? 0 : 1;
-        const int64_t out_row = (int64_t)seg.b * p.heads + head0;
+        const int64_t out_row = ((int64_t)seg.b * p.seq_heads() + seg.item / hblocks) * group + hb * kRows;  // of the first query head
         // where the CTA's share of an item goes: for a cluster the ring, which is done with
         float* part = kCluster ? reinterpret_cast<float*>(smem) : partial<D, kRows>(p.workspace, blockIdx.x, which);
         if constexpr (kCluster) cp_async_wait<0>();
@@ -935,7 +1179,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
 #pragma unroll
                 for (int off = 4; off < 32; off <<= 1) {
                     float l2 = __shfl_xor_sync(0xffffffffu, l[h][n], off);
-                    if constexpr (kE4m3) {
+                    if constexpr (kCodes) {
                         const float ml2 = __shfl_xor_sync(0xffffffffu, ml[h][n], off), big = fmaxf(ml[h][n], ml2);
                         l[h][n] *= ex2_approx(ml[h][n] - big);
                         l2 *= ex2_approx(ml2 - big);
@@ -953,14 +1197,16 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
                     float* row = merge + (warp * kMR + 2 * (t % (kMR / 2)) + n) * C::kPitch;
 #pragma unroll
                     for (int d = 0; d < D / 16; ++d) {
-                        if constexpr (!kE4m3) {
+                        if constexpr (!kCodes) {
                             row[16 * d + g] = o[d][h][n];
                             row[16 * d + 8 + g] = o[d][h][2 + n];
+                        } else if constexpr (kE2m1) {
+                            *reinterpret_cast<float2*>(row + 32 * (d / 2) + 4 * g + 2 * (d % 2)) = make_float2(o[d][h][n], o[d][h][2 + n]);
                         } else {
                             *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[d][h][n], o[d][h][2 + n]);
                         }
                     }
-                    if (g == 0) *reinterpret_cast<Stats*>(row + D) = Stats{m[h][n], l[h][n], kE4m3 ? ml[h][n] : m[h][n], 0.f};
+                    if (g == 0) *reinterpret_cast<Stats*>(row + D) = Stats{m[h][n], l[h][n], kCodes ? ml[h][n] : m[h][n], 0.f};
                 }
             }
             __syncthreads();
@@ -980,11 +1226,11 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) {
                     const Stats s = *reinterpret_cast<const Stats*>(merge + (w * kMR + n) * C::kPitch + D);
-                    const Factors<kE4m3> to(s, big, big_l);
+                    const Factors<kCodes> to(s, big, big_l);
                     f[w] = to.o;
                     sum += to.l * s.l;
                 }
-                const Last<kE4m3> last(big, big_l, sum);
+                const Last<kCodes> last(big, big_l, sum);
 #pragma unroll
                 for (int d = lane + 32 * (warp % kShare); d < D; d += 32 * kShare) {
                     float a = 0.f;
@@ -1001,7 +1247,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
             __syncthreads();
         }
         if constexpr (kCluster) {
-            if (ranks > 1) join_cluster<D, kBf16, kE4m3, kRows>(p, smem_u32(part), ranks, rank, rows, out_row);
+            if (ranks > 1) join_cluster<D, kBf16, kCodes, kRows>(p, smem_u32(part), ranks, rank, rows, out_row);
             return;
         }
         first_item = false;
@@ -1015,8 +1261,9 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kE4m3, kTiles>::kS
 // Joins the items that several CTAs worked on: CTA (x, y) rows kJoinRows y .. of the item that
 // begins in CTA x of the first kernel, if it ends in a later one. kShare warps a row, each for
 // every kShare-th partial result, its lanes for the columns.
-template <int D, bool kBf16, bool kE4m3, typename C, int kJoinRows>
+template <int D, bool kBf16, typename C, int kJoinRows>
 __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const DecodeParams p) {
+    constexpr bool kCodes = C::kCodes;
     constexpr int kRows = C::kRows;
     constexpr int kShare = kJoinThreads / 32 / kJoinRows;
     constexpr int kCols = D / 32;  // columns a lane
@@ -1039,7 +1286,7 @@ __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const Dec
             const Stats so_far{m, l, ml, 0.f};
             m = fmaxf(m, st.m);
             ml = fmaxf(ml, st.ml);
-            const Factors<kE4m3> old(so_far, m, ml), add(st, m, ml);
+            const Factors<kCodes> old(so_far, m, ml), add(st, m, ml);
             l = l * old.l + add.l * st.l;
 #pragma unroll
             for (int i = 0; i < kCols; ++i) a[i] = a[i] * old.o + add.o * s[r * D + lane + 32 * i];
@@ -1061,11 +1308,11 @@ __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const Dec
 #pragma unroll
     for (int w = 0; w < kShare; ++w) {
         const Stats st = stats[warp + w];
-        const Factors<kE4m3> to(st, m, ml);
+        const Factors<kCodes> to(st, m, ml);
         f[w] = to.o;
         l += to.l * st.l;
     }
-    const Last<kE4m3> last(m, ml, l);
+    const Last<kCodes> last(m, ml, l);
     const int64_t row = (int64_t)item.out_row + r;
 #pragma unroll
     for (int i = 0; i < kCols; ++i) {
@@ -1089,7 +1336,7 @@ int cluster_ranks(const DecodeParams& p) {
     const int64_t keys = p.window > 0 && p.window + 15 < p.c.room ? p.window + 15 : p.c.room;
     const int64_t blocks = (keys + C::kKeys - 1) / C::kKeys;
     const int group = p.heads / p.c.hkv;
-    const int64_t items = p.c.batch * p.c.hkv * ((group + C::kRows - 1) / C::kRows);
+    const int64_t items = p.c.batch * p.seq_heads() * ((group + C::kRows - 1) / C::kRows);
     const int64_t resident = 152 * C::kShortPerSm;
     int ranks = 1;
     while (ranks < 8 && items * ranks * 2 <= resident && blocks > ranks * kWarps) ranks *= 2;
@@ -1097,56 +1344,63 @@ int cluster_ranks(const DecodeParams& p) {
     return blocks <= most && items * ranks <= INT32_MAX ? ranks : 0;
 }
 
-template <int D, bool kBf16, bool kE4m3, int kTiles>
+template <int D, bool kBf16, int kForm, int kTiles>
 cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
-    using C = Cfg<D, kE4m3, kTiles>;
+    using C = Cfg<D, kForm, kTiles>;
     int ranks = cluster_ranks<C>(p);
     if (ranks) {
-        auto kern = fa2_decode_kernel<D, kBf16, kE4m3, kTiles, true>;
+        auto kern = fa2_decode_kernel<D, kBf16, kForm, kTiles, true>;
         cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, slot + 1);
         if (e != cudaSuccess) return e;
         if (ranks == 1 || cluster_fits(reinterpret_cast<const void*>(kern), kThreads, C::kSmem, ranks, slot + 1)) {
-            const int64_t items = p.c.batch * p.c.hkv * ((p.heads / p.c.hkv + C::kRows - 1) / C::kRows);
+            const int64_t items = p.c.batch * p.seq_heads() * ((p.heads / p.c.hkv + C::kRows - 1) / C::kRows);
             decode_record() = ranks;
             return launch_early_cluster(kern, dim3((unsigned)(items * ranks)), dim3(kThreads), C::kSmem, stream, (unsigned)ranks, p, ranks);
         }
     }
     decode_record() = 0;
-    auto kern = fa2_decode_kernel<D, kBf16, kE4m3, kTiles, false>;
+    auto kern = fa2_decode_kernel<D, kBf16, kForm, kTiles, false>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, slot);
     if (e != cudaSuccess) return e;
     e = launch_early(kern, dim3(C::kMaxCtas), dim3(kThreads), C::kSmem, stream, p, 1);
     if (e != cudaSuccess) return e;
     const int rows = std::min(C::kRows, p.heads / p.c.hkv);
-    const int64_t items = p.c.batch * p.c.hkv * ((p.heads / p.c.hkv + C::kRows - 1) / C::kRows);
+    const int64_t items = p.c.batch * p.seq_heads() * ((p.heads / p.c.hkv + C::kRows - 1) / C::kRows);
     // The fewer rows an item has, and the fewer items (of more partial results each), the more warps
     // for a row. GB300: one key-value head, 100,000 tokens, 4 query heads 36 us with a quarter of the
     // warps for each row, 23 us with all; 8 heads 11.0 us with a quarter, 10.4 half, 11.8 all.
     auto join = [&](void (*kernel)(DecodeParams), int join_rows) {
         return launch_early(kernel, dim3(C::kMaxCtas, (unsigned)((rows + join_rows - 1) / join_rows)), dim3(kJoinThreads), 0, stream, p);
     };
-    if (rows == 1 || items <= kFewItems) return join(fa2_decode_join_kernel<D, kBf16, kE4m3, C, 1>, 1);
-    if (rows == 2 || items <= 2 * kFewItems) return join(fa2_decode_join_kernel<D, kBf16, kE4m3, C, 2>, 2);
-    return join(fa2_decode_join_kernel<D, kBf16, kE4m3, C, 4>, 4);
+    if (rows == 1 || items <= kFewItems) return join(fa2_decode_join_kernel<D, kBf16, C, 1>, 1);
+    if (rows == 2 || items <= 2 * kFewItems) return join(fa2_decode_join_kernel<D, kBf16, C, 2>, 2);
+    return join(fa2_decode_join_kernel<D, kBf16, C, 4>, 4);
 }
 
 // Up to 8 query heads a key-value head: one column tile, else two.
-template <int D, bool kBf16, bool kE4m3>
+template <int D, bool kBf16, int kForm>
 cudaError_t launch_tiles(const DecodeParams& p, cudaStream_t stream, int slot) {
-    return p.heads / p.c.hkv <= 8 ? launch_d<D, kBf16, kE4m3, 1>(p, stream, slot) : launch_d<D, kBf16, kE4m3, 2>(p, stream, slot + 2);
+    return p.heads / p.c.hkv <= 8 ? launch_d<D, kBf16, kForm, 1>(p, stream, slot) : launch_d<D, kBf16, kForm, 2>(p, stream, slot + 2);
 }
 
+// Rows of 16 bits and e4m3 codes; those of e2m1 codes are compiled apart (launch_e2m1).
 template <int D>
 cudaError_t launch_kind(const DecodeParams& p, cudaStream_t stream, int slot) {  // slots slot .. slot + 15
     const bool bf = p.c.dtype == kBf16;
-    if (p.c.e4m3) return bf ? launch_tiles<D, true, true>(p, stream, slot) : launch_tiles<D, false, true>(p, stream, slot + 4);
-    return bf ? launch_tiles<D, true, false>(p, stream, slot + 8) : launch_tiles<D, false, false>(p, stream, slot + 12);
+    if (p.c.form == kRowsE4m3)
+        return bf ? launch_tiles<D, true, kRowsE4m3>(p, stream, slot) : launch_tiles<D, false, kRowsE4m3>(p, stream, slot + 4);
+    return bf ? launch_tiles<D, true, kRows16>(p, stream, slot + 8) : launch_tiles<D, false, kRows16>(p, stream, slot + 12);
+}
+
+template <int D>
+cudaError_t launch_e2m1(const DecodeParams& p, cudaStream_t stream, int slot) {  // slots slot .. slot + 7
+    return p.c.dtype == kBf16 ? launch_tiles<D, true, kRowsE2m1>(p, stream, slot) : launch_tiles<D, false, kRowsE2m1>(p, stream, slot + 4);
 }
 
 template <int D, int kTiles>
-size_t workspace_for() {  // either type of cache
-    using C = Cfg<D, true, kTiles>;
-    constexpr int kCtas = std::max(C::kMaxCtas, Cfg<D, false, kTiles>::kMaxCtas);
+size_t workspace_for() {  // any type of cache
+    using C = Cfg<D, kRowsE4m3, kTiles>;
+    constexpr int kCtas = std::max({C::kMaxCtas, Cfg<D, kRows16, kTiles>::kMaxCtas, Cfg<D, kRowsE2m1, kTiles>::kMaxCtas});
     return (size_t)kCtas * (2 * C::kRows * (D + 4) * sizeof(float) + sizeof(Torn));
 }
 

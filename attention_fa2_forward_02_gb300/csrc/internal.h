@@ -169,16 +169,21 @@ struct RopeParams {
     int dtype;
 };
 
+// How the cache holds its rows (fa2.h, fa2_cache_type).
+enum CacheForm : int { kRows16 = FA2_CACHE_SAME, kRowsE4m3 = FA2_CACHE_E4M3, kRowsE2m1 = FA2_CACHE_E2M1 };
+
 // A paged cache and the sequences that a call goes through (fa2.h, fa2_kv_cache).
 struct PagedParams {
     char* k;
     char* v;
     uint8_t* k_exp;
     uint8_t* v_exp;
+    uint8_t* k_scale;  // e2m1: d / 16 scale bytes a row
+    uint8_t* v_scale;
     int64_t num_pages, page_stride, head_stride, slot_stride;  // strides in bytes
     int hkv, page_size, d;
     uint32_t page_mul, page_shift;  // pos / page_size = (pos + high word of pos * page_mul) >> page_shift
-    bool e4m3;
+    int form;  // CacheForm
     const int32_t* table;
     int64_t table_stride;
     int64_t room;  // pages_per_seq * page_size, at most 2^30
@@ -211,6 +216,21 @@ struct KvRowsParams {
     bool read;
 };
 
+// fa2_rope_append, and fa2_kv_append into 4-bit rows (rot 0, no queries).
+struct RopeAppendParams {
+    KvRowsParams rows;
+    const char* q;
+    char* q_out;
+    int64_t qs[2], qos[2];  // bytes: {token, head}
+    int heads;
+    const double* inv_freq;
+    const int32_t* positions;  // null: the place in the sequence
+    int rot;
+    bool interleaved;
+    float magnitude;
+    int grow;  // max(0, ceil(log2 |magnitude|))
+};
+
 struct DecodeParams {
     PagedParams c;
     const void* q;
@@ -221,14 +241,58 @@ struct DecodeParams {
     int64_t window;
     float* workspace;
     float scale;
+    // Whether each key-value head has a block table and a length of its own: c.batch, c.table and c.lens then
+    // count (sequence, head) pairs, head by head.
+    bool per_head;
+    // key-value heads behind one row of the block table
+#ifdef __CUDACC__
+    __host__ __device__
+#endif
+    int seq_heads() const { return per_head ? 1 : c.hkv; }
+};
+
+// Bounds of the pages that new tokens lie in (fa2_kv_bounds).
+struct KvBoundsParams {
+    PagedParams c;
+    int8_t* bounds;
+    uint8_t* bounds_exp;
+    const int32_t* cu_new;
+    int64_t tokens;
+};
+
+struct SelectParams {
+    const void* q;
+    int64_t q_batch, q_head;  // elements
+    const int8_t* bounds;
+    const uint8_t* bounds_exp;
+    int64_t num_pages;
+    int page_size, group, hkv, d;
+    uint32_t page_mul, page_shift;  // as in PagedParams
+    const int32_t* table;
+    int64_t table_stride, per_seq;  // pages a sequence has room for
+    const int32_t* lens;
+    int64_t batch;
+    int32_t* sel_table;
+    int32_t* sel_lens;
+    int budget, first, recent;
+    uint32_t* scores;  // the workspace: [batch, hkv, per_seq]
+    int dtype;
+    unsigned int* status;
 };
 
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
-cudaError_t launch_kv_rows(const KvRowsParams& p, cudaStream_t stream);
+cudaError_t launch_kv_rows(const KvRowsParams& p, cudaStream_t stream);  // 16-bit and e4m3 rows
+cudaError_t launch_rope_append(const RopeAppendParams& p, cudaStream_t stream);
+cudaError_t launch_kv_read_e2m1(const KvRowsParams& p, cudaStream_t stream);
+cudaError_t launch_kv_bounds(const KvBoundsParams& p, cudaStream_t stream);
+cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream);
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_d32(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_d64(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_d128(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_e2m1_d32(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_e2m1_d64(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_decode_e2m1_d128(const DecodeParams& p, cudaStream_t stream);
 size_t decode_workspace_bytes(int heads, int hkv, int d);
 
 cudaError_t launch_fwd_tc(const FwdParams& p, cudaStream_t stream);

@@ -121,29 +121,8 @@ __device__ __forceinline__ bool find_token(const KvRowsParams& p, int64_t t, int
         b = b_read;
         pos = t;
         if (pos >= bounded_len(c.lens[b], c.room, c.status)) return false;
-    } else {
-        int first = (int)t, end = (int)t + 1;
-        if (p.cu_new) {
-            // the last sequence that begins at or before row t
-            int lo = 0, hi = (int)c.batch;  // cu_new[lo] <= t < cu_new[hi], were it ascending
-            if (t < p.cu_new[0] || t >= p.cu_new[hi]) return false;
-            while (hi - lo > 1) {
-                const int mid = (lo + hi) >> 1;
-                if (p.cu_new[mid] <= t) lo = mid;
-                else hi = mid;
-            }
-            b = lo;
-            first = p.cu_new[b];
-            end = p.cu_new[b + 1];
-        } else {
-            b = (int)t;
-            if (c.lens[b] == 0) return false;
-        }
-        pos = (int64_t)c.lens[b] - end + t;
-        if (t < first || t >= end || pos < 0 || pos >= c.room) {
-            if (c.status) atomicOr(c.status, kStatusBadIndex);
-            return false;
-        }
+    } else if (!place_of_row(c, p.cu_new, t, &b, &pos)) {
+        return false;
     }
     const int at = page_of(c, (int)pos);
     const Slot s = slot_of(c, c.table[b * c.table_stride + at], (int)pos - at * c.page_size);
@@ -341,7 +320,7 @@ cudaError_t launch_type(const KvRowsParams& p, cudaStream_t stream) {
 
 cudaError_t launch_kv_rows(const KvRowsParams& p, cudaStream_t stream) {
     const bool bf = p.c.dtype == kBf16;
-    if (!p.c.e4m3)  // words are moved without a look at them
+    if (p.c.form == kRows16)  // words are moved without a look at them
         return p.read ? launch_type<true, false, true>(p, stream) : launch_type<true, false, false>(p, stream);
     if (p.read) return bf ? launch_type<true, true, true>(p, stream) : launch_type<false, true, true>(p, stream);
     return bf ? launch_type<true, true, false>(p, stream) : launch_type<false, true, false>(p, stream);

@@ -1,0 +1,447 @@
+// kv_rope.cu - new tokens' queries and keys turned by their positions, and their keys and values into the
+// pages of a cache, in one pass; the 4-bit rows of a cache, written and read back.
+//
+// As two calls (fa2_rope, fa2_kv_append) the keys are written and read once more than needed and every step
+// pays two launches. Here each row is read once and written once: bytes set the pace of prompts, the chain
+// length - page - row - store that of a step.
+//
+// A warp takes a token (and a share of its rows); kLanes lanes hold a row, 16 elements each, as two packs of 8:
+// i .. i + 7 and i + rot / 2 .. in the half layout, 16 in a row in the interleaved one, so that every pair
+// lies in one lane whichever the layout, accesses are whole 16-byte vectors, and the 8 sines and cosines a lane
+// needs are the same for all rows of the token (rope.cuh makes them from the position in fixed point).
+//
+// The 8- and 4-bit forms take a row's power of two from the row as it came (the magnitudes of 16-bit floats are
+// ordered as their bits are): a rotation by any angle makes an element no more than sqrt(2) |magnitude| times the
+// largest, so one bit more, and as many as the magnitude has, are always enough, and what the 8-bit floats lose
+// by it lies at the bottom of their range. It does not depend on how sines round.
+//
+// The 4-bit form: x 2^-e < 2^10 (turned: 2^10 sqrt(2) < 448 * 6), 16 elements' scale is max / 6 as an 8-bit float,
+// codes are x 2^-e / scale. Both quotients are rounded exactly: with r = 1 / s to nearest, q = x r, the remainder
+// x - q s is exact in one fused step and q + r (x - q s) is x / s to nearest (P. W. Markstein, "Computation of
+// elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990), which keeps every
+// tie between two codes a tie.
+#include "paged.cuh"
+#include "rope.cuh"
+
+namespace fa2 {
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kMinExp = -60, kMaxExp = 120;
+
+template <bool kBf16>
+__device__ __forceinline__ float2 widen2(uint32_t w) {
+    if constexpr (kBf16) return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+    else return __half22float2(*reinterpret_cast<__half2*>(&w));
+}
+
+// The largest finite magnitude of a row of 16-bit floats, a lane's 16 of them in `w`; kLanes lanes hold the row,
+// every lane of the warp calls it.
+template <bool kBf16, int kLanes>
+__device__ __forceinline__ float row_max(const uint32_t (&w)[8]) {
+    constexpr uint32_t kInf = kBf16 ? 0x7f80u : 0x7c00u;
+    uint32_t m = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
+#pragma unroll
+    for (int off = kLanes / 2; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
+    m = max(m & 0xffffu, m >> 16);
+    if (__any_sync(0xffffffffu, m >= kInf)) {  // rare: look again without infinities and NaN
+        m = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const uint32_t lo = w[j] & 0x7fffu, hi = (w[j] >> 16) & 0x7fffu;
+            m = max(m, max(lo < kInf ? lo : 0u, hi < kInf ? hi : 0u));
+        }
+#pragma unroll
+        for (int off = kLanes / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
+    }
+    return kBf16 ? __uint_as_float(m << 16) : __half2float(__ushort_as_half((unsigned short)m));
+}
+
+// e of a row's power of two 2^e for its largest magnitude a before any rotation, `more` for what that can add.
+template <int kForm>
+__device__ __forceinline__ int row_exp(float a, int more) {
+    int e = 0;
+    if (a > 0.f) {
+        const uint32_t bits = __float_as_uint(a);
+        const int k = (int)(bits >> 23) - 126;  // a = f 2^k, f in [1/2, 1) (a subnormal a: k = -126, and the limit below)
+        e = kForm == kRowsE2m1 ? k - 10 : k - 9 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);  // e4m3: a <= 448 2^e
+        e = max(e, kMinExp);
+    }
+    return min(e + more, kMaxExp);
+}
+
+__device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {  // nearest even; beyond 448: 448; NaN stays
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+// Eight e2m1 codes, nearest even, beyond 6: 6.
+__device__ __forceinline__ uint32_t to_e2m1x8(const float (&x)[8]) {
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+    return r;
+}
+
+// x / s to nearest, for finite x and s with r = 1 / s to nearest
+__device__ __forceinline__ float divide(float x, float s, float r) {
+    const float q = x * r;
+    return fmaf(fmaf(-q, s, x), r, q);
+}
+
+// The largest of 8 magnitudes, as bits: NaN above infinity above the finite ones.
+__device__ __forceinline__ uint32_t max_bits(const float (&x)[8]) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    return m;
+}
+
+// The scale byte of 16 elements x 2^-e whose largest magnitude has these bits.
+__device__ __forceinline__ uint32_t group_scale(uint32_t bits) {
+    if (bits > 0x7f800000u) return 0x7fu;   // a NaN
+    if (bits == 0x7f800000u) return 0x7eu;  // an infinity: 448
+    return to_e4m3x2(divide(__uint_as_float(bits), 6.f, 1.f / 6.f), 0.f) & 0xffu;
+}
+
+// The codes of 8 elements x 2^-e at a scale byte of group_scale.
+__device__ __forceinline__ uint32_t group_codes(const float (&x)[8], uint32_t scale) {
+    const uint32_t h = e4m3x2_to_f16x2(scale);
+    const float s = __half2float(__ushort_as_half((unsigned short)h));
+    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
+    float y[8];
+    if (scale < 0x7eu) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = divide(x[i], s, r);
+    } else {  // an infinity's remainder is none
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+    }
+    return to_e2m1x8(y);
+}
+
+// Where a token lies: bytes / scale bytes of the cache, head 0 (-1: its page is outside); its position (-1: none).
+struct Spot {
+    int64_t cache_off, exp_off;
+    int pos;
+};
+
+template <bool kBf16, int kForm, int kLanes, int kRows, int kTok>
+__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppendParams p, int slots_per_warp) {
+    const PagedParams& c = p.rows.c;
+    constexpr int kGroups = 32 / kLanes;
+    __shared__ uint64_t turns[64];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTok;
+    grid_begin();
+    if (p.rot) {
+        for (int i = threadIdx.x; i < p.rot / 2; i += kWarps * 32) turns[i] = turns_of(p.inv_freq[i]);
+        __syncthreads();
+    }
+    if (t0 >= p.rows.tokens) return;
+    Spot found{-1, -1, -1};
+    {
+        const int64_t t = t0 + lane % kTok;
+        int b;
+        int64_t pos;
+        if (t < p.rows.tokens && place_of_row(c, p.rows.cu_new, t, &b, &pos)) {
+            found.pos = (int)pos;
+            const int at = page_of(c, found.pos);
+            const Slot s = slot_of(c, c.table[b * c.table_stride + at], found.pos - at * c.page_size);
+            found.cache_off = s.off;
+            found.exp_off = s.exp;
+        }
+    }
+    const int li = lane % kLanes, gr = lane / kLanes;
+    // the lane's packs
+    const bool turned = 16 * li < p.rot, halves = turned && !p.interleaved;
+    const int i0 = halves ? 8 * li : 16 * li, i1 = halves ? p.rot / 2 + 8 * li : 16 * li + 8;
+    const bool on0 = i0 < c.d, on1 = i1 < c.d;
+    // 4 bits: the lane and the pack that hold the other 8 of the 16 elements around each pack
+    auto holder = [&](int pack, int* second) {  // of elements 8 pack ..
+        const int k = p.interleaved ? 0 : p.rot / 16;
+        const bool apart = pack < 2 * k;
+        *second = apart ? pack >= k : pack & 1;
+        return lane - li + (apart ? (pack < k ? pack : pack - k) : pack / 2);
+    };
+    int second0 = 0, second1 = 0, from0 = 0, from1 = 0;
+    if constexpr (kForm == kRowsE2m1) {
+        from0 = holder((i0 / 8) ^ 1, &second0) & 31;
+        from1 = holder((i1 / 8) ^ 1, &second1) & 31;
+    }
+    // rows: the queries', from a whole round on the keys', the values'
+    const int q_slots = (p.heads + kGroups - 1) / kGroups * kGroups, total = q_slots + 2 * c.hkv;
+    const int begin = blockIdx.y * slots_per_warp, stop = min(total, begin + slots_per_warp);
+
+    for (int n = 0; n < kTok; ++n) {
+        const int pos = __shfl_sync(0xffffffffu, found.pos, n);
+        const int64_t cache_off = __shfl_sync(0xffffffffu, found.cache_off, n);
+        const int64_t exp_off = kForm != kRows16 ? __shfl_sync(0xffffffffu, found.exp_off, n) : 0;
+        if (pos < 0) continue;
+        const int64_t t = t0 + n;
+        float cs[8], sn[8];
+        if (turned) {
+            const int64_t at = p.positions ? p.positions[t] : pos;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                turn_sincos((uint32_t)(((uint64_t)at * turns[8 * li + i]) >> 32), &sn[i], &cs[i]);
+                sn[i] *= p.magnitude;
+                cs[i] *= p.magnitude;
+            }
+        }
+        // a lane's 16 elements, turned: x[0 .. 7] of the first pack, x[8 .. 15] of the second
+        auto turn = [&](const uint4 (&in)[2], float (&x)[2][8], bool turns_row) {
+            const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const float2 f = widen2<kBf16>(w[j]);
+                x[j / 4][2 * (j % 4)] = f.x;
+                x[j / 4][2 * (j % 4) + 1] = f.y;
+            }
+            if (!turns_row || !turned) return;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                // as in fa2_rope: a product, then a fused one
+                float &one = p.interleaved ? x[i / 4][2 * (i % 4)] : x[0][i], &two = p.interleaved ? x[i / 4][2 * (i % 4) + 1] : x[1][i];
+                const float a = one, b = two;
+                one = a * cs[i] - b * sn[i];
+                two = b * cs[i] + a * sn[i];
+            }
+        };
+        auto packed = [&](const float (&x)[8]) {
+            return make_uint4(pack2<kBf16>(x[0], x[1]), pack2<kBf16>(x[2], x[3]), pack2<kBf16>(x[4], x[5]), pack2<kBf16>(x[6], x[7]));
+        };
+        // ---- queries
+        for (int r0 = begin + gr; r0 - gr < min(stop, q_slots); r0 += kGroups * kRows) {
+            uint4 in[kRows][2];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = r0 + i * kGroups;
+                if (r >= p.heads || r >= stop) continue;
+                const char* src = p.q + t * p.qs[0] + r * p.qs[1];
+                if (on0) in[i][0] = *reinterpret_cast<const uint4*>(src + 2 * i0);
+                if (on1) in[i][1] = *reinterpret_cast<const uint4*>(src + 2 * i1);
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = r0 + i * kGroups;
+                if (r >= p.heads || r >= stop) continue;
+                char* dst = p.q_out + t * p.qos[0] + r * p.qos[1];
+                if (turned) {
+                    float x[2][8];
+                    turn(in[i], x, true);
+                    in[i][0] = packed(x[0]);
+                    in[i][1] = packed(x[1]);
+                }
+                if (on0) *reinterpret_cast<uint4*>(dst + 2 * i0) = in[i][0];
+                if (on1) *reinterpret_cast<uint4*>(dst + 2 * i1) = in[i][1];
+            }
+        }
+        if (cache_off < 0) continue;
+        // ---- keys, then values
+        for (int r0 = max(begin, q_slots) - q_slots + gr; r0 - gr < stop - q_slots; r0 += kGroups * kRows) {
+            uint4 in[kRows][2];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                in[i][0] = in[i][1] = make_uint4(0, 0, 0, 0);
+                const int r = r0 + i * kGroups;
+                if (r >= stop - q_slots) continue;
+                const bool v = r >= c.hkv;
+                const char* src = v ? p.rows.v + t * p.rows.vs[0] + (r - c.hkv) * p.rows.vs[1] : p.rows.k + t * p.rows.ks[0] + r * p.rows.ks[1];
+                if (on0) in[i][0] = *reinterpret_cast<const uint4*>(src + 2 * i0);
+                if (on1) in[i][1] = *reinterpret_cast<const uint4*>(src + 2 * i1);
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = r0 + i * kGroups, h = r >= c.hkv ? r - c.hkv : r;
+                const bool there = r < stop - q_slots, v = r >= c.hkv;
+                char* dst = (v ? c.v : c.k) + cache_off + h * c.head_stride;
+                if constexpr (kForm == kRows16) {
+                    if (!there) continue;
+                    if (turned && !v) {
+                        float x[2][8];
+                        turn(in[i], x, true);
+                        in[i][0] = packed(x[0]);
+                        in[i][1] = packed(x[1]);
+                    }
+                    if (on0) *reinterpret_cast<uint4*>(dst + 2 * i0) = in[i][0];
+                    if (on1) *reinterpret_cast<uint4*>(dst + 2 * i1) = in[i][1];
+                } else {
+                    const uint32_t w[8] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w,
+                                           in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
+                    const bool turns_row = !v && p.rot > 0;
+                    const int e = row_exp<kForm>(row_max<kBf16, kLanes>(w), turns_row ? p.grow + (kForm == kRowsE4m3) : 0);
+                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
+                    float x[2][8];
+                    turn(in[i], x, !v);
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) x[k][j] *= inv;
+                    const int64_t byte = exp_off + (int64_t)h * c.page_size;
+                    if (there && li == 0) (v ? c.v_exp : c.k_exp)[byte] = (uint8_t)(e + 127);
+                    if constexpr (kForm == kRowsE4m3) {
+                        if (!there) continue;
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+                            if (k ? on1 : on0)
+                                *reinterpret_cast<uint2*>(dst + (k ? i1 : i0)) =
+                                    make_uint2(to_e4m3x2(x[k][0], x[k][1]) | to_e4m3x2(x[k][2], x[k][3]) << 16,
+                                               to_e4m3x2(x[k][4], x[k][5]) | to_e4m3x2(x[k][6], x[k][7]) << 16);
+                    } else {
+                        const uint32_t m0 = max_bits(x[0]), m1 = max_bits(x[1]);
+                        const uint32_t a0 = __shfl_sync(0xffffffffu, m0, from0), b0 = __shfl_sync(0xffffffffu, m1, from0);
+                        const uint32_t a1 = __shfl_sync(0xffffffffu, m0, from1), b1 = __shfl_sync(0xffffffffu, m1, from1);
+                        const uint32_t s[2] = {group_scale(max(m0, second0 ? b0 : a0)), group_scale(max(m1, second1 ? b1 : a1))};
+                        if (!there) continue;
+                        uint8_t* scales = (v ? c.v_scale : c.k_scale) + byte * (c.d / 16);
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int at = k ? i1 : i0;
+                            if (!(k ? on1 : on0)) continue;
+                            *reinterpret_cast<uint32_t*>(dst + at / 2) = group_codes(x[k], s[k]);
+                            if (at % 16 == 0) scales[at / 16] = (uint8_t)s[k];
+                        }
+                    }
+                }
+            }
+        }
+    }
+}
+
+template <bool kBf16, int kForm, int kLanes>
+cudaError_t launch_lanes(const RopeAppendParams& p, cudaStream_t stream) {
+    constexpr int kGroups = 32 / kLanes, kRows = 4, kTok = 4;
+    const int slots = (p.heads + kGroups - 1) / kGroups * kGroups + 2 * p.rows.c.hkv;
+    auto blocks = [&](int tok) { return (unsigned)((p.rows.tokens + kWarps * tok - 1) / (kWarps * tok)); };
+    // A warp takes kTok whole tokens while that gives every SM several blocks, one with fewer, and with few
+    // tokens one round of a token's rows.
+    if (blocks(kTok) >= 152 * 4)
+        return launch_early(rope_append_kernel<kBf16, kForm, kLanes, kRows, kTok>, dim3(blocks(kTok)), dim3(kWarps * 32), 0, stream, p, slots);
+    if (blocks(1) >= 152 * 2)
+        return launch_early(rope_append_kernel<kBf16, kForm, kLanes, kRows, 1>, dim3(blocks(1)), dim3(kWarps * 32), 0, stream, p, slots);
+    return launch_early(rope_append_kernel<kBf16, kForm, kLanes, 1, 1>, dim3(blocks(1), (unsigned)((slots + kGroups - 1) / kGroups)),
+                        dim3(kWarps * 32), 0, stream, p, kGroups);
+}
+
+template <bool kBf16, int kForm>
+cudaError_t launch_form(const RopeAppendParams& p, cudaStream_t stream) {
+    if (p.rows.c.d <= 32) return launch_lanes<kBf16, kForm, 2>(p, stream);
+    if (p.rows.c.d <= 64) return launch_lanes<kBf16, kForm, 4>(p, stream);
+    return launch_lanes<kBf16, kForm, 8>(p, stream);
+}
+
+// 4-bit rows back to 16 bits: as kv_rows_kernel of kv_cache.cu, a lane's 16 elements as packs of 8 that lie kLanes
+// packs apart, so that both sides of a row's lanes are one after another in memory.
+template <bool kBf16, int kLanes, int kRows, int kTok>
+__global__ void __launch_bounds__(kWarps * 32) kv_read_e2m1_kernel(const KvRowsParams p, int rows_per_warp) {
+    const PagedParams& c = p.c;
+    constexpr int kGroups = 32 / kLanes;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTok;
+    const int b = blockIdx.z;
+    grid_begin();
+    const int len = bounded_len(c.lens[b], c.room, c.status);
+    if (t0 >= p.tokens || t0 >= len) return;
+    int64_t my_off = -1, my_exp = -1;
+    {
+        const int64_t pos = t0 + lane % kTok;
+        if (pos < p.tokens && pos < len) {
+            const int at = page_of(c, (int)pos);
+            const Slot s = slot_of(c, c.table[b * c.table_stride + at], (int)pos - at * c.page_size);
+            my_off = s.off;
+            my_exp = s.exp;
+        }
+    }
+    const int li = lane % kLanes, gr = lane / kLanes;
+    const int total = 2 * c.hkv, begin = blockIdx.y * rows_per_warp, stop = min(total, begin + rows_per_warp);
+    for (int n = 0; n < kTok; ++n) {
+        const int64_t cache_off = __shfl_sync(0xffffffffu, my_off, n), exp_off = __shfl_sync(0xffffffffu, my_exp, n);
+        if (cache_off < 0) continue;
+        for (int r0 = begin + gr; r0 - gr < stop; r0 += kGroups * kRows) {
+            uint32_t codes[kRows][2], scale[kRows][2], byte[kRows];
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = r0 + i * kGroups, h = r >= c.hkv ? r - c.hkv : r;
+                if (r >= stop) continue;
+                const bool v = r >= c.hkv;
+                const char* src = (v ? c.v : c.k) + cache_off + h * c.head_stride;
+                const int64_t e = exp_off + (int64_t)h * c.page_size;
+                const uint8_t* scales = (v ? c.v_scale : c.k_scale) + e * (c.d / 16);
+                byte[i] = (v ? c.v_exp : c.k_exp)[e];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int pack = li + k * kLanes;
+                    if (8 * pack >= c.d) continue;
+                    codes[i][k] = *reinterpret_cast<const uint32_t*>(src + 4 * pack);
+                    scale[i][k] = scales[pack / 2];
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < kRows; ++i) {
+                const int r = r0 + i * kGroups, h = r >= c.hkv ? r - c.hkv : r;
+                if (r >= stop) continue;
+                const bool v = r >= c.hkv;
+                char* dst = v ? p.v + b * p.vs[0] + h * p.vs[1] + (t0 + n) * p.vs[2] : p.k + b * p.ks[0] + h * p.ks[1] + (t0 + n) * p.ks[2];
+                const float two = __uint_as_float(byte[i] << 23);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const int pack = li + k * kLanes;
+                    if (8 * pack >= c.d) continue;
+                    uint32_t f[4], o[4];
+                    e2m1x8_to_f16x8(codes[i][k], f);
+                    const uint32_t s = e4m3x2_to_f16x2(scale[i][k] * 0x101u);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const uint32_t x = hmul2(f[j], s);  // exact: 6 bits
+                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x));
+                        o[j] = pack2<kBf16>(y.x * two, y.y * two);
+                    }
+                    *reinterpret_cast<uint4*>(dst + 16 * pack) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+    }
+}
+
+template <bool kBf16, int kLanes>
+cudaError_t launch_read(const KvRowsParams& p, cudaStream_t stream) {
+    constexpr int kGroups = 32 / kLanes, kRows = 4, kTok = 2;
+    const int total = 2 * p.c.hkv;
+    const unsigned batch = (unsigned)p.c.batch;
+    auto blocks = [&](int tok) { return (p.tokens + kWarps * tok - 1) / (kWarps * tok); };
+    if (blocks(kTok) * batch >= 152 * 8) {
+        const dim3 grid((unsigned)blocks(kTok), 1, batch);
+        return launch_early(kv_read_e2m1_kernel<kBf16, kLanes, kRows, kTok>, grid, dim3(kWarps * 32), 0, stream, p, total);
+    }
+    const dim3 grid((unsigned)blocks(1), (unsigned)((total + kGroups - 1) / kGroups), batch);
+    return launch_early(kv_read_e2m1_kernel<kBf16, kLanes, 1, 1>, grid, dim3(kWarps * 32), 0, stream, p, kGroups);
+}
+
+template <bool kBf16>
+cudaError_t launch_read_lanes(const KvRowsParams& p, cudaStream_t stream) {
+    if (p.c.d <= 32) return launch_read<kBf16, 2>(p, stream);
+    if (p.c.d <= 64) return launch_read<kBf16, 4>(p, stream);
+    return launch_read<kBf16, 8>(p, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_rope_append(const RopeAppendParams& p, cudaStream_t stream) {
+    const bool bf = p.rows.c.dtype == kBf16;
+    switch (p.rows.c.form) {
+        case kRows16: return bf ? launch_form<true, kRows16>(p, stream) : launch_form<false, kRows16>(p, stream);
+        case kRowsE4m3: return bf ? launch_form<true, kRowsE4m3>(p, stream) : launch_form<false, kRowsE4m3>(p, stream);
+        default: return bf ? launch_form<true, kRowsE2m1>(p, stream) : launch_form<false, kRowsE2m1>(p, stream);
+    }
+}
+
+cudaError_t launch_kv_read_e2m1(const KvRowsParams& p, cudaStream_t stream) {
+    return p.c.dtype == kBf16 ? launch_read_lanes<true>(p, stream) : launch_read_lanes<false>(p, stream);
+}
+
+}  // namespace fa2

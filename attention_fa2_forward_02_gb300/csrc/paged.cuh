@@ -36,6 +36,35 @@ __device__ __forceinline__ Slot slot_of(const PagedParams& c, int page, int slot
     return {page * c.page_stride + slot * c.slot_stride, (int64_t)page * c.hkv * c.page_size + slot};
 }
 
+// The sequence and the position of new token t (fa2_kv_append); false: it has none.
+__device__ __forceinline__ bool place_of_row(const PagedParams& c, const int32_t* cu_new, int64_t t, int* seq, int64_t* position) {
+    int first = (int)t, end = (int)t + 1, b;
+    if (cu_new) {
+        // the last sequence that begins at or before row t
+        int lo = 0, hi = (int)c.batch;  // cu_new[lo] <= t < cu_new[hi], were it ascending
+        if (t < cu_new[0] || t >= cu_new[hi]) return false;
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (cu_new[mid] <= t) lo = mid;
+            else hi = mid;
+        }
+        b = lo;
+        first = cu_new[b];
+        end = cu_new[b + 1];
+    } else {
+        b = (int)t;
+        if (c.lens[b] == 0) return false;
+    }
+    const int64_t pos = (int64_t)c.lens[b] - end + t;
+    if (t < first || t >= end || pos < 0 || pos >= c.room) {
+        if (c.status) atomicOr(c.status, kStatusBadIndex);
+        return false;
+    }
+    *seq = b;
+    *position = pos;
+    return true;
+}
+
 // Two packed e4m3 codes -> two halves (exact).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
     uint32_t r;
@@ -47,6 +76,28 @@ __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t codes) {
 __device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t codes, uint32_t& lo, uint32_t& hi) {
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi) : "r"(codes));
+}
+
+// Eight packed e2m1 codes -> four pairs of halves, codes 2 i and 2 i + 1 in pair i (exact).
+__device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t codes, uint32_t (&r)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(codes));
+}
+
+// Four codes of each of two rows, the first row's in the lower half of the word -> four pairs of halves, code i
+// of the first and of the second row in pair i.
+__device__ __forceinline__ void e2m1_2x4_to_f16(uint32_t codes, uint32_t (&r)[4]) {
+    const uint32_t even = (codes & 0x0f0fu) | (codes >> 12 & 0xf0f0u), odd = (codes >> 4 & 0x0f0fu) | (codes >> 16 & 0xf0f0u);
+    asm("{\n\t.reg .b8 a, b, c, d, n;\n\t.reg .b16 e, o;\n\tcvt.u16.u32 e, %4;\n\tcvt.u16.u32 o, %5;\n\t"
+        "mov.b16 {a, c}, e;\n\tmov.b16 {b, d}, o;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(even), "r"(odd));
+}
+
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+    const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+    return *reinterpret_cast<const uint32_t*>(&x);
 }
 
 }  // namespace fa2

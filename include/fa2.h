@@ -459,7 +459,14 @@ fa2_status fa2_rope_backward(const void* dy, void* dx, const int32_t* positions,
  *              scale byte in k_exp, v_exp (uint8 [num_pages, n_kv_heads, page_size],
  *              contiguous): an element stands for code * 2^(byte - 127), bytes 1 to 253
  *              (fa2_kv_append writes 67 to 247; others have no meaning).
- *   head_dim   a multiple of 8 (E4M3: 16) up to 128; page_size, n_kv_heads, num_pages > 0,
+ *              FA2_CACHE_E2M1: 4-bit floats (sign, 2 exponent bits, 1 fraction bit: 0, 0.5, 1,
+ *              1.5, 2, 3, 4, 6), two a byte, the even element in the low four bits; a scale for
+ *              each 16 elements of a row in k_scale, v_scale (8-bit floats, 4 exponent, 3
+ *              fraction bits, [num_pages, n_kv_heads, page_size, head_dim / 16], contiguous,
+ *              16-byte aligned), and a byte a row in k_exp, v_exp as above: an element stands
+ *              for code * scale * 2^(byte - 127).  d = 128: 73 bytes a row, for 129 and 256.
+ *              Strides count elements (two a byte).
+ *   head_dim   a multiple of 8 (E4M3: 16, E2M1: 32) up to 128; page_size, n_kv_heads, num_pages > 0,
  *              n_kv_heads <= 1024, pages_per_seq * page_size <= 2^30 (FA2_ERR_UNSUPPORTED).
  *
  * The lengths (int32 [batch], device) and the block table are read on the device, so that a
@@ -470,7 +477,7 @@ fa2_status fa2_rope_backward(const void* dy, void* dx, const int32_t* positions,
  * masked out of the attention), and either sets the status that fa2_device_status reports as
  * FA2_ERR_BAD_INDEX.
  */
-typedef enum { FA2_CACHE_SAME = 0, FA2_CACHE_E4M3 = 1 } fa2_cache_type;
+typedef enum { FA2_CACHE_SAME = 0, FA2_CACHE_E4M3 = 1, FA2_CACHE_E2M1 = 2 } fa2_cache_type;
 typedef struct fa2_kv_cache {
     void* k;
     void* v;
@@ -480,6 +487,8 @@ typedef struct fa2_kv_cache {
     int64_t page_stride, head_stride, slot_stride;
     int32_t n_kv_heads, page_size, head_dim;
     fa2_cache_type type;
+    uint8_t* k_scale; /* read for FA2_CACHE_E2M1 only */
+    uint8_t* v_scale;
 } fa2_kv_cache;
 
 /*
@@ -497,6 +506,12 @@ typedef struct fa2_kv_cache {
  * FA2_CACHE_E4M3: a row's scale is 2^e, e the smallest integer with max|x| <= 448 * 2^e over
  * the row's finite elements (0 if they are all zero), no less than -60; codes are x / 2^e
  * (exact) rounded to nearest even; infinities become 448 * 2^e with their sign, NaN stays NaN.
+ * FA2_CACHE_E2M1: the row's power of two is 2^e, e = floor(log2 a) - 9 for a = max|x| over its
+ * finite elements (0 if they are all zero), no less than -60; 16 elements' scale is
+ * max|x| 2^-e / 6 of theirs as an 8-bit float (448 with an infinity among them, NaN with a
+ * NaN), codes are x 2^-e / scale, both rounded to nearest even, codes of magnitudes past 6 are
+ * 6, and those of a scale of 0 are 0 (of either sign).  An infinity so becomes 2688 * 2^e with
+ * its sign, and a NaN makes its 16 elements NaN.
  * Two tokens may not name one slot (a page shared by two sequences that both write it): the
  * slot's contents are then some mix of both.
  * Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_CUDA.
@@ -507,6 +522,33 @@ fa2_status fa2_kv_append(const fa2_kv_cache* cache, const void* k, const void* v
                          int64_t tokens, fa2_dtype dtype, void* stream);
 
 /*
+ * fa2_rope_append - fa2_rope on the queries and keys of new tokens and fa2_kv_append in one
+ * pass: queries are turned and written out, keys turned and stored, values stored.
+ *
+ *   q, q_out   element (token, head, d) at token * strides[0] + head * strides[1] + d, dtype,
+ *              device; q is read, q_out written and may not overlap itself; q_out may be q with
+ *              the same strides.  Both NULL with n_heads 0: keys and values alone.
+ *   inv_freq, rot_dim, interleaved, magnitude   as for fa2_rope; rot_dim a multiple of 16
+ *   positions  int32 [tokens], device: each token's position for its rotation; NULL: its place
+ *              in its sequence, which always is where it is stored
+ *   the others as for fa2_kv_append
+ * Rotated in float32, angles as in fa2_rope.  A turned key is rounded once: to dtype in a
+ * 16-bit cache, to its codes in the others, whose power of two comes from the row before its rotation
+ * with room for what that can add: with g = max(0, ceil(log2 |magnitude|)), e4m3 rows have e of
+ * fa2_kv_append for that row, plus 1 + g, e2m1 rows plus g (no more than 120).
+ * A token without a valid position is neither stored nor turned (its row of q_out stays as it
+ * was); one whose page is outside the cache is turned and not stored.  Both set the status
+ * FA2_ERR_BAD_INDEX, as for fa2_kv_append.
+ * n_heads <= 65535; the other limits and the errors are those of fa2_kv_append.
+ */
+fa2_status fa2_rope_append(const fa2_kv_cache* cache, const void* q, void* q_out, const void* k, const void* v,
+                           const int64_t q_strides[2], const int64_t q_out_strides[2], const int64_t k_strides[2],
+                           const int64_t v_strides[2], const double* inv_freq, int32_t rot_dim, int32_t interleaved,
+                           float magnitude, const int32_t* positions, const int32_t* block_table, int64_t table_stride,
+                           int64_t pages_per_seq, const int32_t* cu_new, const int32_t* seq_lens, int64_t batch,
+                           int64_t tokens, int32_t n_heads, fa2_dtype dtype, void* stream);
+
+/*
  * fa2_kv_read - copies the cached rows of each sequence out of the pages.
  *
  *   k_out, v_out  element (b, head, pos, d) at b strides[0] + head strides[1] + pos strides[2]
@@ -515,7 +557,7 @@ fa2_status fa2_kv_append(const fa2_kv_cache* cache, const void* k, const void* v
  *                 written, the others left as they were.  With [batch, heads, max_len, d]
  *                 outputs of equal lengths, fa2_forward takes them as they are.
  * FA2_CACHE_E4M3: code * 2^(byte - 127), rounded once to dtype (BF16: exact; F16 past 65504:
- * infinity).  Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_CUDA.
+ * infinity).  FA2_CACHE_E2M1: code * scale * 2^(byte - 127), the same.  Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_CUDA.
  */
 fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, const int64_t out_strides[3],
                        const int32_t* block_table, int64_t table_stride, int64_t pages_per_seq,
@@ -536,11 +578,11 @@ fa2_status fa2_kv_read(const fa2_kv_cache* cache, void* k_out, void* v_out, cons
  *   workspace  fa2_decode_workspace_size bytes, 16-byte aligned, contents do not matter;
  *              calls whose GPU work may overlap need one each
  * float32 scores, softmax statistics and sums; the product with V takes each probability as two
- * 16-bit numbers (FA2_CACHE_SAME: dtype; FA2_CACHE_E4M3: half), its rounding and what that left
- * off: within 2^-16 (BF16) or 2^-22 of it; in FA2_CACHE_E4M3 with BF16, whose results have steps
- * of 2^-8, one half, within 2^-11. In half, weights below 2^-32 of the row's largest
- * count as 0 there; in FA2_CACHE_E4M3 these weights have the value row's scale in them (rows
- * whose codes are all 0 are not among the largest), the denominator and the LSE do not. There
+ * 16-bit numbers (FA2_CACHE_SAME: dtype; the others: half), its rounding and what that left
+ * off: within 2^-16 (BF16) or 2^-22 of it; in FA2_CACHE_E4M3 and _E2M1 with BF16, whose results have
+ * steps of 2^-8, one half, within 2^-11. In half, weights below 2^-32 of the row's largest
+ * count as 0 there; in FA2_CACHE_E4M3 and _E2M1 these weights have the value row's power of two in
+ * them (rows whose codes are all 0 are not among the largest), the denominator and the LSE do not. There
  * BF16 queries are brought to half by a power of two a row: elements below 2^-29 of the row's
  * largest lose bits, below 2^-39 all of them.
  * The keys of all sequences and heads are divided evenly over the CTAs, whatever the lengths
@@ -557,6 +599,66 @@ fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_ca
                       const int32_t* block_table, int64_t table_stride, int64_t pages_per_seq,
                       const int32_t* seq_lens, int64_t batch, int32_t n_heads, int64_t window, void* workspace,
                       size_t workspace_bytes, fa2_dtype dtype, float softmax_scale, void* stream);
+
+/*
+ * Attention of one new token over some pages of a long context.  Each page has bounds, the
+ * lowest and the highest key of every channel, from which the largest score that a key of the
+ * page could have follows; the pages where that is largest are read, the others are not.
+ *
+ *   bounds      int8 [num_pages, n_kv_heads, 2, head_dim], contiguous, 16-byte aligned: the
+ *               lowest, then the highest keys' codes
+ *   bounds_exp  uint8 [num_pages, n_kv_heads], contiguous: a code stands for code * 2^(byte - 127)
+ *
+ * fa2_kv_bounds - makes the bounds of the pages that new tokens lie in, from all of the page's
+ * live keys (those before the sequence's length): call it after fa2_kv_append or
+ * fa2_rope_append, with the same cu_new and seq_lens (tokens: the rows of k and v there).
+ *   2^e, e = byte - 127 is the smallest power of two with every finite |key| <= 127 * 2^e, e no
+ *   less than -60 (0 for keys of zeros); the lowest is rounded down, the highest up, so that
+ *   low * 2^e <= key <= high * 2^e for every live key; infinities count as 127 * 2^e with their
+ *   sign, NaN not at all.
+ * Any type of cache; only k (with k_exp and k_scale) is read (v may be NULL).  A page outside the cache is
+ * skipped and sets the status FA2_ERR_BAD_INDEX, as does a token without a valid position.
+ * Two sequences may share a page only if neither has new tokens in it.
+ *
+ * fa2_select_pages - the pages to read, for each sequence and key-value head.
+ *   With the query rows of the head's group as 8-bit integers Q_h (2^e_h the smallest power of
+ *   two, e_h >= -60, with every finite |q| <= 127 * 2^e_h; rounded to nearest even; NaN counts as 0,
+ *   infinities as 127 * 2^e_h), page p has the score
+ *     max_h (2^e_h sum_c max(Q_hc low_pc, Q_hc high_pc)) * 2^e_p,
+ *   a float32 that no rounding enters (it may overflow to infinity).  The `first` first pages
+ *   of the sequence and the `recent` last ones are taken before all others, then those of the
+ *   largest scores, the earlier of two alike, up to `budget` pages.
+ *   q           element (b, h, d) as for fa2_decode;  n_heads / n_kv_heads <= 128
+ *   sel_table   int32 [batch, n_kv_heads, budget], written: the page numbers of the block
+ *               table, in the order of their positions, -1 behind them
+ *   sel_lens    int32 [batch, n_kv_heads], written: the keys in them (the sequence's last page
+ *               may be partly filled)
+ *   first, recent >= 0, first + recent <= budget;  budget * page_size <= 2^30
+ *   workspace   fa2_select_workspace_size bytes, 16-byte aligned, contents do not matter; calls
+ *               whose GPU work may overlap need one each
+ * A page outside the cache has the lowest score of all (and sets the status FA2_ERR_BAD_INDEX).
+ *
+ * fa2_decode_selected - fa2_decode over a block table and a length for each sequence and
+ * key-value head: block_table [batch, n_kv_heads, pages_per_seq] and seq_lens [batch,
+ * n_kv_heads], contiguous, as fa2_select_pages writes them; no window.  Workspace as for fa2_decode.
+ * batch * n_kv_heads <= 2^20 (FA2_ERR_UNSUPPORTED).
+ * Errors: FA2_ERR_INVALID_ARG, FA2_ERR_UNSUPPORTED, FA2_ERR_MISALIGNED, FA2_ERR_WORKSPACE,
+ *         FA2_ERR_CUDA.
+ */
+fa2_status fa2_kv_bounds(const fa2_kv_cache* cache, int8_t* bounds, uint8_t* bounds_exp, const int32_t* block_table,
+                         int64_t table_stride, int64_t pages_per_seq, const int32_t* cu_new, const int32_t* seq_lens,
+                         int64_t batch, int64_t tokens, fa2_dtype dtype, void* stream);
+size_t fa2_select_workspace_size(int64_t batch, int32_t n_kv_heads, int64_t pages_per_seq);
+fa2_status fa2_select_pages(const void* q, const int64_t q_strides[2], const int8_t* bounds, const uint8_t* bounds_exp,
+                            int64_t num_pages, int32_t page_size, int32_t n_heads, int32_t n_kv_heads, int32_t head_dim,
+                            const int32_t* block_table, int64_t table_stride, int64_t pages_per_seq,
+                            const int32_t* seq_lens, int64_t batch, int32_t* sel_table, int32_t* sel_lens, int64_t budget,
+                            int64_t first, int64_t recent, void* workspace, size_t workspace_bytes, fa2_dtype dtype,
+                            void* stream);
+fa2_status fa2_decode_selected(const void* q, const int64_t q_strides[2], const fa2_kv_cache* cache, void* o, float* lse,
+                               const int32_t* block_table, int64_t pages_per_seq, const int32_t* seq_lens, int64_t batch,
+                               int32_t n_heads, void* workspace, size_t workspace_bytes, fa2_dtype dtype,
+                               float softmax_scale, void* stream);
 
 /*
  * fa2_device_status - the watchdog word of the library's kernels.

@@ -8,6 +8,8 @@ Inputs are float64 arrays (storage values already widened exactly).
 """
 from __future__ import annotations
 
+import math
+
 import numpy as np
 
 MIN_EXP = -60
@@ -102,3 +104,112 @@ def decode_row(q, k, v, scale, live=None):
     p = np.exp(s - m)
     total = p.sum()
     return (p @ v) / total, m + np.log(total), (p @ np.abs(v)) / total, float(np.max(scale * (np.abs(k) @ np.abs(q))))
+
+
+# ---------------------------------------------------------------------------- the 4-bit rows
+E2M1_VALUES = np.array([0.0, 0.5, 1.0, 1.5, 2.0, 3.0, 4.0, 6.0])
+
+
+def _nearest_even(y, values):
+    """Indices of the ascending `values` nearest to the magnitudes y, the even index of two at the same distance."""
+    y = np.minimum(np.asarray(y, dtype=np.float64), values[-1])
+    dist = np.abs(values[None, :] - y.reshape(-1, 1))
+    low = dist.argmin(1)
+    last = len(values) - 1
+    tie = (low < last) & (dist[np.arange(len(low)), np.minimum(low + 1, last)] == dist[np.arange(len(low)), low])
+    return np.where(tie & (low % 2 == 1), low + 1, low).reshape(np.shape(y))
+
+
+def quantise_row4(x, before=None, more=0):
+    """(codes 0 .. 15 [d], scale bytes [d / 16], byte) of one row.  `before`: the row before its rotation, whose power of
+    two counts, raised by `more`."""
+    x = np.asarray(x, dtype=np.float64)
+    b = x if before is None else np.asarray(before, dtype=np.float64)
+    finite = np.abs(b[np.isfinite(b)])
+    a = finite.max() if finite.size else 0.0
+    e = min((max(math.floor(math.log2(a)) - 9, MIN_EXP) if a > 0 else 0) + more, 120)
+    y = (x * 2.0 ** -e).reshape(-1, 16)
+    codes, scales = np.zeros(y.shape, dtype=np.uint8), np.zeros(len(y), dtype=np.uint8)
+    e4m3 = e4m3_values()[:127]
+    for g, row in enumerate(y):
+        if np.isnan(row).any():
+            scales[g] = 0x7F
+            continue
+        big = np.abs(row).max()
+        scales[g] = 126 if np.isinf(big) else _nearest_even(np.array([big / 6]), e4m3)[0]
+        s = e4m3[scales[g]]
+        c = _nearest_even(np.abs(row) / s, E2M1_VALUES) if s > 0 else np.zeros(16, dtype=int)
+        codes[g] = c | np.where(np.signbit(row), 8, 0)
+    return codes.reshape(-1), scales, e + 127
+
+
+def row_values4(codes, scales, byte):
+    """What a 4-bit row stands for: codes 0 .. 15 [..., d], scale bytes [..., d / 16], bytes [...]."""
+    codes = np.asarray(codes)
+    v = E2M1_VALUES[codes & 7] * np.where(codes & 8, -1.0, 1.0)
+    s = np.repeat(e4m3_values()[np.asarray(scales)], 16, axis=-1)
+    return v * s * 2.0 ** (np.asarray(byte, dtype=np.float64)[..., None] - 127)
+
+
+def pack4(codes):
+    """Two codes a byte, the even element in the low four bits."""
+    c = np.asarray(codes, dtype=np.uint8)
+    return c[..., ::2] | (c[..., 1::2] << 4)
+
+
+# ---------------------------------------------------------------------------- bounds and selection
+def smallest_exp(a, most):
+    """The smallest e >= MIN_EXP with a <= most 2^e; 0 for a = 0."""
+    if a == 0:
+        return 0
+    e = MIN_EXP
+    while a > most * 2.0 ** e:
+        e += 1
+    return e
+
+
+def page_bounds(keys):
+    """(codes int [2, d], byte) of the live keys [n, d] of a page: lowest and highest of each channel, NaN not counted."""
+    k = np.asarray(keys, dtype=np.float64)
+    none = np.isnan(k).all(0)
+    low = np.where(none, 0.0, np.min(np.where(np.isnan(k), np.inf, k), 0))
+    high = np.where(none, 0.0, np.max(np.where(np.isnan(k), -np.inf, k), 0))
+    both = np.abs(np.stack([low, high]))
+    e = smallest_exp(both[np.isfinite(both)].max() if np.isfinite(both).any() else 0.0, 127.0)
+    return np.clip(np.stack([np.floor(low * 2.0 ** -e), np.ceil(high * 2.0 ** -e)]), -127, 127).astype(np.int64), e + 127
+
+
+def touched_pages(lens, cu_new, page_size, room):
+    """{(sequence, page number in it): live keys} of the pages that new tokens lie in."""
+    out = {}
+    for b, n in enumerate(lens):
+        count = 1 if cu_new is None else int(cu_new[b + 1]) - int(cu_new[b])
+        end = min(max(int(n), 0), room)
+        for pos in range(max(0, int(n) - count), end):
+            out[b, pos // page_size] = min(page_size, end - pos // page_size * page_size)
+    return out
+
+
+def query_integers(q):
+    """(integers [d], e) of one query row."""
+    q = np.where(np.isnan(q), 0.0, np.asarray(q, dtype=np.float64))
+    finite = np.abs(q[np.isfinite(q)])
+    e = smallest_exp(finite.max() if finite.size else 0.0, 127.0)
+    return np.clip(np.rint(q * 2.0 ** -e), -127, 127).astype(np.int64), e
+
+
+def page_score(qs, codes, byte):
+    """The score of a page with bounds codes [2, d] for the query rows qs [group, d]."""
+    best = -math.inf
+    for q in qs:
+        ints, e = query_integers(q)
+        best = max(best, int(np.maximum(ints * codes[0], ints * codes[1]).sum()) * 2.0 ** e)
+    return best * 2.0 ** (int(byte) - 127)
+
+
+def select_pages(scores, budget, first, recent):
+    """The numbers of the pages taken, ascending; scores: None for a page outside the cache."""
+    n = len(scores)
+    rank = lambda j: (0 if j < first or j >= n - recent else 1 if scores[j] is not None else 2,  # noqa: E731
+                      -scores[j] if 0 <= j < n and scores[j] is not None and not (j < first or j >= n - recent) else 0.0, j)
+    return sorted(sorted(range(n), key=rank)[:budget])

@@ -22,9 +22,9 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
         }
     }
     switch (pad_head_dim(p.c.d)) {
-        case 32: return launch_decode_d32(p, stream);
-        case 64: return launch_decode_d64(p, stream);
-        default: return launch_decode_d128(p, stream);
+        case 32: return p.per_head ? launch_selected_d32(p, stream) : launch_decode_d32(p, stream);
+        case 64: return p.per_head ? launch_selected_d64(p, stream) : launch_decode_d64(p, stream);
+        default: return p.per_head ? launch_selected_d128(p, stream) : launch_decode_d128(p, stream);
     }
 }
 

@@ -62,7 +62,7 @@ struct Cfg {
     // contexts 304 and 322), d 32 34 and 33. But three leave 168 registers: too few at d 64, 8 heads
     // (41 us with two, 50 with three; long 163 and 198), and for 16 heads (d 64 57 and 70, d 128 86
     // and 155; d 32 42 and 40).
-    static constexpr int kPerSm = kE4m3 && (D == 32 || (D == 128 && kTiles == 1)) ? 3 : 2;
+    static constexpr int kPerSm = (kE4m3 && (D == 32 || (D == 128 && kTiles == 1))) || (kE2m1 && kTiles == 1) ? 3 : 2;
     static constexpr int kMaxCtas = 152 * kPerSm;           // a fixed number: the split depends on the lengths alone
     // in one launch, where latency is more than memory: 7 windows of 1024 keys, d 64, 9.6 -> 8.8 us
     static constexpr int kShortPerSm = kTiles == 1 && kRowBytes < 256 ? 3 : kPerSm;
@@ -438,9 +438,10 @@ __device__ __forceinline__ void join_cluster(const DecodeParams& p, uint32_t par
     cluster_sync_all();  // no CTA leaves while another reads its shared memory
 }
 
+// kPerHead: block table and lengths for each (sequence, key-value head) pair, which then counts as a sequence.
 // kCluster: the CTAs of a cluster of `ranks` share the item blockIdx.x / ranks; nothing is left to
 // the second kernel.
-template <int D, bool kBf16, int kForm, int kTiles, bool kCluster>
+template <int D, bool kBf16, int kForm, int kTiles, bool kPerHead, bool kCluster>
 __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kShortPerSm : Cfg<D, kForm, kTiles>::kPerSm)
     fa2_decode_kernel(const DecodeParams p, int ranks) {
     using C = Cfg<D, kForm, kTiles>;
@@ -460,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     const PagedParams& c = p.c;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = p.heads / c.hkv, hblocks = (group + kRows - 1) / kRows;
-    const int64_t per_seq = (int64_t)p.seq_heads() * hblocks;
+    const int64_t per_seq = kPerHead ? hblocks : (int64_t)c.hkv * hblocks;
     grid_begin();
 
     Split split(0, 0);
@@ -469,7 +470,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     auto empty_rows = [&]() {
         for (int b = blockIdx.x; b < c.batch; b += gridDim.x) {
             if (range_of(p, b).len > 0) continue;
-            const int rows = group * p.seq_heads();
+            const int rows = kPerHead ? group : p.heads;
             const int64_t row0 = (int64_t)b * rows;
             for (int i = threadIdx.x; i < rows * c.d / 8; i += kThreads)
                 reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.o) + row0 * c.d)[i] = make_uint4(0, 0, 0, 0);
@@ -507,8 +508,6 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
             return s.k1 > s.k0;
         }
     };
-    // the key-value head of a segment's item
-    auto kv_head = [&](const Segment& s) { return p.per_head ? s.b % c.hkv : s.item / hblocks; };
     // this warp's blocks of segment number `number`: k0 + turn(number), + kWarps, ...
     auto turn = [&](int number) { return (warp + number) % kWarps; };
     auto count = [&](const Segment& s, int number) {
@@ -547,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     int64_t ahead_head = 0, ahead_exp = 0;                // the head's offset in a page, in its scale bytes
     auto enter = [&]() {
         if (!ahead_live) return;
-        const int hk = kv_head(ahead);
+        const int hk = kPerHead ? ahead.b % c.hkv : ahead.item / hblocks;
         ahead_left = count(ahead, ahead_number);
         ahead_key = ahead.range.base + (ahead.k0 + turn(ahead_number)) * kKeys + (kKeys < 32 ? lane % kKeys : lane);
         ahead_table = c.table + ahead.b * c.table_stride;
@@ -755,8 +754,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     const int q_row = threadIdx.x / kParts, q_part = threadIdx.x % kParts;
     uint4 q_lo, q_hi;
     auto fetch_q = [&](const Segment& s) {
-        const int hb = s.item % hblocks, head = kv_head(s) * group + hb * kRows + q_row;
-        const int b = p.per_head ? s.b / c.hkv : s.b;
+        const int hb = s.item % hblocks, head = (kPerHead ? s.b % c.hkv : s.item / hblocks) * group + hb * kRows + q_row;
+        const int b = kPerHead ? s.b / c.hkv : s.b;
         const bool on = q_row < min(kRows, group - hb * kRows);
         const uint16_t* src = static_cast<const uint16_t*>(p.q) + b * p.q_batch + (int64_t)head * p.q_head + 16 * q_part;
         q_lo = q_hi = make_uint4(0, 0, 0, 0);
@@ -784,7 +783,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     Torn ends_later{0, 0, 0, 0};
 
     for (; live; ++number) {
-        const int hb = seg.item % hblocks;
+        const int hk = seg.item / hblocks, hb = seg.item % hblocks;
+        const int head0 = hk * group + hb * kRows;        // first query head (kPerHead: of the sequence's group)
         const int rows = min(kRows, group - hb * kRows);  // query heads of the item
 
         // ---- q into shared memory, by whole warps (they exchange)
@@ -1167,7 +1167,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
         // ---- the warps' results together, kMergeRows rows at a time: a warp or two per row
         const bool whole = kCluster ? ranks == 1 : seg.k0 == 0 && seg.k1 == seg.nb;
         const int which = first_item ? 0 : 1;
-        const int64_t out_row = ((int64_t)seg.b * p.seq_heads() + seg.item / hblocks) * group + hb * kRows;  // of the first query head
+        const int64_t out_row = (int64_t)seg.b * (kPerHead ? group : p.heads) + head0;
         // where the CTA's share of an item goes: for a cluster the ring, which is done with
         float* part = kCluster ? reinterpret_cast<float*>(smem) : partial<D, kRows>(p.workspace, blockIdx.x, which);
         if constexpr (kCluster) cp_async_wait<0>();
@@ -1344,12 +1344,12 @@ int cluster_ranks(const DecodeParams& p) {
     return blocks <= most && items * ranks <= INT32_MAX ? ranks : 0;
 }
 
-template <int D, bool kBf16, int kForm, int kTiles>
+template <int D, bool kBf16, int kForm, int kTiles, bool kPerHead>
 cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
     using C = Cfg<D, kForm, kTiles>;
     int ranks = cluster_ranks<C>(p);
     if (ranks) {
-        auto kern = fa2_decode_kernel<D, kBf16, kForm, kTiles, true>;
+        auto kern = fa2_decode_kernel<D, kBf16, kForm, kTiles, kPerHead, true>;
         cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, slot + 1);
         if (e != cudaSuccess) return e;
         if (ranks == 1 || cluster_fits(reinterpret_cast<const void*>(kern), kThreads, C::kSmem, ranks, slot + 1)) {
@@ -1359,7 +1359,7 @@ cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
         }
     }
     decode_record() = 0;
-    auto kern = fa2_decode_kernel<D, kBf16, kForm, kTiles, false>;
+    auto kern = fa2_decode_kernel<D, kBf16, kForm, kTiles, kPerHead, false>;
     cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, slot);
     if (e != cudaSuccess) return e;
     e = launch_early(kern, dim3(C::kMaxCtas), dim3(kThreads), C::kSmem, stream, p, 1);
@@ -1378,23 +1378,25 @@ cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
 }
 
 // Up to 8 query heads a key-value head: one column tile, else two.
-template <int D, bool kBf16, int kForm>
+template <int D, bool kBf16, int kForm, bool kPerHead>
 cudaError_t launch_tiles(const DecodeParams& p, cudaStream_t stream, int slot) {
-    return p.heads / p.c.hkv <= 8 ? launch_d<D, kBf16, kForm, 1>(p, stream, slot) : launch_d<D, kBf16, kForm, 2>(p, stream, slot + 2);
+    return p.heads / p.c.hkv <= 8 ? launch_d<D, kBf16, kForm, 1, kPerHead>(p, stream, slot)
+                                   : launch_d<D, kBf16, kForm, 2, kPerHead>(p, stream, slot + 2);
 }
 
 // Rows of 16 bits and e4m3 codes; those of e2m1 codes are compiled apart (launch_e2m1).
-template <int D>
+template <int D, bool kPerHead>
 cudaError_t launch_kind(const DecodeParams& p, cudaStream_t stream, int slot) {  // slots slot .. slot + 15
     const bool bf = p.c.dtype == kBf16;
     if (p.c.form == kRowsE4m3)
-        return bf ? launch_tiles<D, true, kRowsE4m3>(p, stream, slot) : launch_tiles<D, false, kRowsE4m3>(p, stream, slot + 4);
-    return bf ? launch_tiles<D, true, kRows16>(p, stream, slot + 8) : launch_tiles<D, false, kRows16>(p, stream, slot + 12);
+        return bf ? launch_tiles<D, true, kRowsE4m3, kPerHead>(p, stream, slot) : launch_tiles<D, false, kRowsE4m3, kPerHead>(p, stream, slot + 4);
+    return bf ? launch_tiles<D, true, kRows16, kPerHead>(p, stream, slot + 8) : launch_tiles<D, false, kRows16, kPerHead>(p, stream, slot + 12);
 }
 
-template <int D>
+template <int D, bool kPerHead>
 cudaError_t launch_e2m1(const DecodeParams& p, cudaStream_t stream, int slot) {  // slots slot .. slot + 7
-    return p.c.dtype == kBf16 ? launch_tiles<D, true, kRowsE2m1>(p, stream, slot) : launch_tiles<D, false, kRowsE2m1>(p, stream, slot + 4);
+    return p.c.dtype == kBf16 ? launch_tiles<D, true, kRowsE2m1, kPerHead>(p, stream, slot)
+                              : launch_tiles<D, false, kRowsE2m1, kPerHead>(p, stream, slot + 4);
 }
 
 template <int D, int kTiles>

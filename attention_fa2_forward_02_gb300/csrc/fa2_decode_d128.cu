@@ -4,6 +4,6 @@
 namespace fa2 {
 
 // slots 96 .. 111 of ensure_smem_limit (the attention kernels take 0 .. 61)
-cudaError_t launch_decode_d128(const DecodeParams& p, cudaStream_t stream) { return launch_kind<128>(p, stream, 96); }
+cudaError_t launch_decode_d128(const DecodeParams& p, cudaStream_t stream) { return launch_kind<128, false>(p, stream, 96); }
 
 }  // namespace fa2

@@ -4,6 +4,6 @@
 namespace fa2 {
 
 // slots 64 .. 79 of ensure_smem_limit (the attention kernels take 0 .. 61)
-cudaError_t launch_decode_d32(const DecodeParams& p, cudaStream_t stream) { return launch_kind<32>(p, stream, 64); }
+cudaError_t launch_decode_d32(const DecodeParams& p, cudaStream_t stream) { return launch_kind<32, false>(p, stream, 64); }
 
 }  // namespace fa2

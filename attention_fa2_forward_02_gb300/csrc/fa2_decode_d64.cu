@@ -4,6 +4,6 @@
 namespace fa2 {
 
 // slots 80 .. 95 of ensure_smem_limit (the attention kernels take 0 .. 61)
-cudaError_t launch_decode_d64(const DecodeParams& p, cudaStream_t stream) { return launch_kind<64>(p, stream, 80); }
+cudaError_t launch_decode_d64(const DecodeParams& p, cudaStream_t stream) { return launch_kind<64, false>(p, stream, 80); }
 
 }  // namespace fa2

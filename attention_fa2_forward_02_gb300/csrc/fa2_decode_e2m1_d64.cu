@@ -1,9 +1,11 @@
-// fa2_decode_e2m1_d64.cu - the kernels of fa2_decode.cuh over 4-bit rows for head size 64.
+// fa2_decode_e2m1_d64.cu - the kernels of fa2_decode.cuh over 4-bit rows, for head size 64.
 #include "fa2_decode.cuh"
 
 namespace fa2 {
 
-// slots 120 .. 127 of ensure_smem_limit
-cudaError_t launch_decode_e2m1_d64(const DecodeParams& p, cudaStream_t stream) { return launch_e2m1<64>(p, stream, 120); }
+// slots 128 .. 143 of ensure_smem_limit
+cudaError_t launch_decode_e2m1_d64(const DecodeParams& p, cudaStream_t stream) {
+    return p.per_head ? launch_e2m1<64, true>(p, stream, 136) : launch_e2m1<64, false>(p, stream, 128);
+}
 
 }  // namespace fa2

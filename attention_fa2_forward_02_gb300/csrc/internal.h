@@ -245,9 +245,6 @@ struct DecodeParams {
     // count (sequence, head) pairs, head by head.
     bool per_head;
     // key-value heads behind one row of the block table
-#ifdef __CUDACC__
-    __host__ __device__
-#endif
     int seq_heads() const { return per_head ? 1 : c.hkv; }
 };
 
@@ -283,6 +280,9 @@ struct SelectParams {
 cudaError_t launch_rope(const RopeParams& p, cudaStream_t stream);
 cudaError_t launch_kv_rows(const KvRowsParams& p, cudaStream_t stream);  // 16-bit and e4m3 rows
 cudaError_t launch_rope_append(const RopeAppendParams& p, cudaStream_t stream);
+cudaError_t launch_rope_append_16(const RopeAppendParams& p, cudaStream_t stream);
+cudaError_t launch_rope_append_e4m3(const RopeAppendParams& p, cudaStream_t stream);
+cudaError_t launch_rope_append_e2m1(const RopeAppendParams& p, cudaStream_t stream);
 cudaError_t launch_kv_read_e2m1(const KvRowsParams& p, cudaStream_t stream);
 cudaError_t launch_kv_bounds(const KvBoundsParams& p, cudaStream_t stream);
 cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream);
@@ -290,6 +290,11 @@ cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_d32(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_d64(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_d128(const DecodeParams& p, cudaStream_t stream);
+// ... with a block table for each key-value head
+cudaError_t launch_selected_d32(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_selected_d64(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_selected_d128(const DecodeParams& p, cudaStream_t stream);
+// ... over 4-bit rows, either
 cudaError_t launch_decode_e2m1_d32(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_e2m1_d64(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_e2m1_d128(const DecodeParams& p, cudaStream_t stream);

@@ -1,4 +1,4 @@
-// kv_rope.cu - new tokens' queries and keys turned by their positions, and their keys and values into the
+// kv_rope.cuh - new tokens' queries and keys turned by their positions, and their keys and values into the
 // pages of a cache, in one pass; the 4-bit rows of a cache, written and read back.
 //
 // As two calls (fa2_rope, fa2_kv_append) the keys are written and read once more than needed and every step
@@ -20,6 +20,8 @@
 // x - q s is exact in one fused step and q + r (x - q s) is x / s to nearest (P. W. Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990), which keeps every
 // tie between two codes a tie.
+#pragma once
+
 #include "paged.cuh"
 #include "rope.cuh"
 
@@ -27,6 +29,7 @@ namespace fa2 {
 namespace {
 
 constexpr int kWarps = 4;
+constexpr int kPerSm = 5;
 constexpr int kMinExp = -60, kMaxExp = 120;
 
 template <bool kBf16>
@@ -130,8 +133,8 @@ struct Spot {
     int pos;
 };
 
-template <bool kBf16, int kForm, int kLanes, int kRows, int kTok>
-__global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppendParams p, int slots_per_warp) {
+template <bool kBf16, int kForm, bool kInterleaved, int kLanes, int kRows, int kTok>
+__global__ void __launch_bounds__(kWarps * 32, kPerSm) rope_append_kernel(const RopeAppendParams p, int slots_per_warp) {
     const PagedParams& c = p.rows.c;
     constexpr int kGroups = 32 / kLanes;
     __shared__ uint64_t turns[64];
@@ -158,12 +161,12 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
     }
     const int li = lane % kLanes, gr = lane / kLanes;
     // the lane's packs
-    const bool turned = 16 * li < p.rot, halves = turned && !p.interleaved;
+    const bool turned = 16 * li < p.rot, halves = turned && !kInterleaved;
     const int i0 = halves ? 8 * li : 16 * li, i1 = halves ? p.rot / 2 + 8 * li : 16 * li + 8;
     const bool on0 = i0 < c.d, on1 = i1 < c.d;
     // 4 bits: the lane and the pack that hold the other 8 of the 16 elements around each pack
     auto holder = [&](int pack, int* second) {  // of elements 8 pack ..
-        const int k = p.interleaved ? 0 : p.rot / 16;
+        const int k = kInterleaved ? 0 : p.rot / 16;
         const bool apart = pack < 2 * k;
         *second = apart ? pack >= k : pack & 1;
         return lane - li + (apart ? (pack < k ? pack : pack - k) : pack / 2);
@@ -184,13 +187,22 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
         if (pos < 0) continue;
         const int64_t t = t0 + n;
         float cs[8], sn[8];
-        if (turned) {
+        if (p.rot) {
+            // the groups of lanes need the same 8 a lane: each makes some of them
+            constexpr int kOwn = kGroups < 8 ? 8 / kGroups : 1;
             const int64_t at = p.positions ? p.positions[t] : pos;
+            float s[kOwn], c8[kOwn];
+#pragma unroll
+            for (int e = 0; e < kOwn; ++e) {
+                const int i = min(8 * li + (gr * kOwn + e) % 8, p.rot / 2 - 1);
+                turn_sincos((uint32_t)(((uint64_t)at * turns[i]) >> 32), &s[e], &c8[e]);
+                s[e] *= p.magnitude;
+                c8[e] *= p.magnitude;
+            }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                turn_sincos((uint32_t)(((uint64_t)at * turns[8 * li + i]) >> 32), &sn[i], &cs[i]);
-                sn[i] *= p.magnitude;
-                cs[i] *= p.magnitude;
+                sn[i] = __shfl_sync(0xffffffffu, s[i % kOwn], i / kOwn * kLanes + li);
+                cs[i] = __shfl_sync(0xffffffffu, c8[i % kOwn], i / kOwn * kLanes + li);
             }
         }
         // a lane's 16 elements, turned: x[0 .. 7] of the first pack, x[8 .. 15] of the second
@@ -206,7 +218,7 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 // as in fa2_rope: a product, then a fused one
-                float &one = p.interleaved ? x[i / 4][2 * (i % 4)] : x[0][i], &two = p.interleaved ? x[i / 4][2 * (i % 4) + 1] : x[1][i];
+                float &one = kInterleaved ? x[i / 4][2 * (i % 4)] : x[0][i], &two = kInterleaved ? x[i / 4][2 * (i % 4) + 1] : x[1][i];
                 const float a = one, b = two;
                 one = a * cs[i] - b * sn[i];
                 two = b * cs[i] + a * sn[i];
@@ -313,135 +325,34 @@ __global__ void __launch_bounds__(kWarps * 32) rope_append_kernel(const RopeAppe
     }
 }
 
-template <bool kBf16, int kForm, int kLanes>
+template <bool kBf16, int kForm, bool kInterleaved, int kLanes>
 cudaError_t launch_lanes(const RopeAppendParams& p, cudaStream_t stream) {
-    constexpr int kGroups = 32 / kLanes, kRows = 4, kTok = 4;
+    constexpr int kGroups = 32 / kLanes, kRows = 2, kTok = 4;
     const int slots = (p.heads + kGroups - 1) / kGroups * kGroups + 2 * p.rows.c.hkv;
     auto blocks = [&](int tok) { return (unsigned)((p.rows.tokens + kWarps * tok - 1) / (kWarps * tok)); };
     // A warp takes kTok whole tokens while that gives every SM several blocks, one with fewer, and with few
     // tokens one round of a token's rows.
     if (blocks(kTok) >= 152 * 4)
-        return launch_early(rope_append_kernel<kBf16, kForm, kLanes, kRows, kTok>, dim3(blocks(kTok)), dim3(kWarps * 32), 0, stream, p, slots);
+        return launch_early(rope_append_kernel<kBf16, kForm, kInterleaved, kLanes, kRows, kTok>, dim3(blocks(kTok)), dim3(kWarps * 32), 0, stream, p, slots);
     if (blocks(1) >= 152 * 2)
-        return launch_early(rope_append_kernel<kBf16, kForm, kLanes, kRows, 1>, dim3(blocks(1)), dim3(kWarps * 32), 0, stream, p, slots);
-    return launch_early(rope_append_kernel<kBf16, kForm, kLanes, 1, 1>, dim3(blocks(1), (unsigned)((slots + kGroups - 1) / kGroups)),
+        return launch_early(rope_append_kernel<kBf16, kForm, kInterleaved, kLanes, kRows, 1>, dim3(blocks(1)), dim3(kWarps * 32), 0, stream, p, slots);
+    return launch_early(rope_append_kernel<kBf16, kForm, kInterleaved, kLanes, 1, 1>, dim3(blocks(1), (unsigned)((slots + kGroups - 1) / kGroups)),
                         dim3(kWarps * 32), 0, stream, p, kGroups);
 }
 
-template <bool kBf16, int kForm>
+template <bool kBf16, int kForm, bool kInterleaved>
+cudaError_t launch_layout(const RopeAppendParams& p, cudaStream_t stream) {
+    if (p.rows.c.d <= 32) return launch_lanes<kBf16, kForm, kInterleaved, 2>(p, stream);
+    if (p.rows.c.d <= 64) return launch_lanes<kBf16, kForm, kInterleaved, 4>(p, stream);
+    return launch_lanes<kBf16, kForm, kInterleaved, 8>(p, stream);
+}
+
+template <int kForm>
 cudaError_t launch_form(const RopeAppendParams& p, cudaStream_t stream) {
-    if (p.rows.c.d <= 32) return launch_lanes<kBf16, kForm, 2>(p, stream);
-    if (p.rows.c.d <= 64) return launch_lanes<kBf16, kForm, 4>(p, stream);
-    return launch_lanes<kBf16, kForm, 8>(p, stream);
-}
-
-// 4-bit rows back to 16 bits: as kv_rows_kernel of kv_cache.cu, a lane's 16 elements as packs of 8 that lie kLanes
-// packs apart, so that both sides of a row's lanes are one after another in memory.
-template <bool kBf16, int kLanes, int kRows, int kTok>
-__global__ void __launch_bounds__(kWarps * 32) kv_read_e2m1_kernel(const KvRowsParams p, int rows_per_warp) {
-    const PagedParams& c = p.c;
-    constexpr int kGroups = 32 / kLanes;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTok;
-    const int b = blockIdx.z;
-    grid_begin();
-    const int len = bounded_len(c.lens[b], c.room, c.status);
-    if (t0 >= p.tokens || t0 >= len) return;
-    int64_t my_off = -1, my_exp = -1;
-    {
-        const int64_t pos = t0 + lane % kTok;
-        if (pos < p.tokens && pos < len) {
-            const int at = page_of(c, (int)pos);
-            const Slot s = slot_of(c, c.table[b * c.table_stride + at], (int)pos - at * c.page_size);
-            my_off = s.off;
-            my_exp = s.exp;
-        }
-    }
-    const int li = lane % kLanes, gr = lane / kLanes;
-    const int total = 2 * c.hkv, begin = blockIdx.y * rows_per_warp, stop = min(total, begin + rows_per_warp);
-    for (int n = 0; n < kTok; ++n) {
-        const int64_t cache_off = __shfl_sync(0xffffffffu, my_off, n), exp_off = __shfl_sync(0xffffffffu, my_exp, n);
-        if (cache_off < 0) continue;
-        for (int r0 = begin + gr; r0 - gr < stop; r0 += kGroups * kRows) {
-            uint32_t codes[kRows][2], scale[kRows][2], byte[kRows];
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int r = r0 + i * kGroups, h = r >= c.hkv ? r - c.hkv : r;
-                if (r >= stop) continue;
-                const bool v = r >= c.hkv;
-                const char* src = (v ? c.v : c.k) + cache_off + h * c.head_stride;
-                const int64_t e = exp_off + (int64_t)h * c.page_size;
-                const uint8_t* scales = (v ? c.v_scale : c.k_scale) + e * (c.d / 16);
-                byte[i] = (v ? c.v_exp : c.k_exp)[e];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int pack = li + k * kLanes;
-                    if (8 * pack >= c.d) continue;
-                    codes[i][k] = *reinterpret_cast<const uint32_t*>(src + 4 * pack);
-                    scale[i][k] = scales[pack / 2];
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < kRows; ++i) {
-                const int r = r0 + i * kGroups, h = r >= c.hkv ? r - c.hkv : r;
-                if (r >= stop) continue;
-                const bool v = r >= c.hkv;
-                char* dst = v ? p.v + b * p.vs[0] + h * p.vs[1] + (t0 + n) * p.vs[2] : p.k + b * p.ks[0] + h * p.ks[1] + (t0 + n) * p.ks[2];
-                const float two = __uint_as_float(byte[i] << 23);
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int pack = li + k * kLanes;
-                    if (8 * pack >= c.d) continue;
-                    uint32_t f[4], o[4];
-                    e2m1x8_to_f16x8(codes[i][k], f);
-                    const uint32_t s = e4m3x2_to_f16x2(scale[i][k] * 0x101u);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t x = hmul2(f[j], s);  // exact: 6 bits
-                        const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x));
-                        o[j] = pack2<kBf16>(y.x * two, y.y * two);
-                    }
-                    *reinterpret_cast<uint4*>(dst + 16 * pack) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
-            }
-        }
-    }
-}
-
-template <bool kBf16, int kLanes>
-cudaError_t launch_read(const KvRowsParams& p, cudaStream_t stream) {
-    constexpr int kGroups = 32 / kLanes, kRows = 4, kTok = 2;
-    const int total = 2 * p.c.hkv;
-    const unsigned batch = (unsigned)p.c.batch;
-    auto blocks = [&](int tok) { return (p.tokens + kWarps * tok - 1) / (kWarps * tok); };
-    if (blocks(kTok) * batch >= 152 * 8) {
-        const dim3 grid((unsigned)blocks(kTok), 1, batch);
-        return launch_early(kv_read_e2m1_kernel<kBf16, kLanes, kRows, kTok>, grid, dim3(kWarps * 32), 0, stream, p, total);
-    }
-    const dim3 grid((unsigned)blocks(1), (unsigned)((total + kGroups - 1) / kGroups), batch);
-    return launch_early(kv_read_e2m1_kernel<kBf16, kLanes, 1, 1>, grid, dim3(kWarps * 32), 0, stream, p, kGroups);
-}
-
-template <bool kBf16>
-cudaError_t launch_read_lanes(const KvRowsParams& p, cudaStream_t stream) {
-    if (p.c.d <= 32) return launch_read<kBf16, 2>(p, stream);
-    if (p.c.d <= 64) return launch_read<kBf16, 4>(p, stream);
-    return launch_read<kBf16, 8>(p, stream);
+    if (p.rows.c.dtype == kBf16)
+        return p.interleaved ? launch_layout<true, kForm, true>(p, stream) : launch_layout<true, kForm, false>(p, stream);
+    return p.interleaved ? launch_layout<false, kForm, true>(p, stream) : launch_layout<false, kForm, false>(p, stream);
 }
 
 }  // namespace
-
-cudaError_t launch_rope_append(const RopeAppendParams& p, cudaStream_t stream) {
-    const bool bf = p.rows.c.dtype == kBf16;
-    switch (p.rows.c.form) {
-        case kRows16: return bf ? launch_form<true, kRows16>(p, stream) : launch_form<false, kRows16>(p, stream);
-        case kRowsE4m3: return bf ? launch_form<true, kRowsE4m3>(p, stream) : launch_form<false, kRowsE4m3>(p, stream);
-        default: return bf ? launch_form<true, kRowsE2m1>(p, stream) : launch_form<false, kRowsE2m1>(p, stream);
-    }
-}
-
-cudaError_t launch_kv_read_e2m1(const KvRowsParams& p, cudaStream_t stream) {
-    return p.c.dtype == kBf16 ? launch_read_lanes<true>(p, stream) : launch_read_lanes<false>(p, stream);
-}
-
 }  // namespace fa2

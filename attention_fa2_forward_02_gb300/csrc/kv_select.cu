@@ -5,11 +5,11 @@
 //
 // Scores: sum_c max(q_c low_c, q_c high_c) is no less than q . k for any key within the bounds. The query's
 // 8-bit integers, split into those above zero (which meet the highest keys) and those below (the lowest), make it
-// two sums of integer products, four to an instruction: exact, so that which pages are taken does not depend on
-// the order of sums, and a float32 holds the result (below 2^21) times powers of two.
+// a sum of integer products: exact, so that which pages are taken does not depend on the order of sums, and a
+// float32 holds the result (below 2^21) times powers of two.
 //
-// Selection: the budget-th largest score by bisection on its bits, the earlier page first among equals, pages in
-// the order of their positions.
+// Selection: the budget-th largest score by counting, the earlier page first among equals, pages in the order of
+// their positions.
 #include <algorithm>
 
 #include "paged.cuh"
@@ -203,8 +203,8 @@ cudaError_t launch_bounds_form(const KvBoundsParams& p, cudaStream_t stream) {
 
 // ---------------------------------------------------------------------------- scores
 
-constexpr int kHeads = 8;       // query heads whose integers a lane holds at a time
 constexpr uint32_t kForced = 0xffffffffu;  // above every score's key; a page outside the cache: 0, below every score's
+constexpr int kSets = 2;                   // times 16 pages a warp takes at once
 
 // Unsigned numbers in the order of the floats (no NaN).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -212,122 +212,140 @@ __device__ __forceinline__ uint32_t ordered(float x) {
     return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__device__ __forceinline__ int dot4(uint32_t a, uint32_t b, int c) { return __dp4a((int)a, (int)b, c); }
+__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
 
-// The scores of pages of one sequence and key-value head: kLanes lanes a page, 16 channels a lane. The CTA first
-// makes the group's integers in shared memory, then its warps take pages in turn; heads by 8.
-template <bool kBf16, int kLanes>
+// Pages that hold a length's keys.
+__device__ __forceinline__ int pages_of(const SelectParams& p, int len) {
+    if (len == 0) return 0;
+    const uint32_t last = (uint32_t)len - 1;
+    return (int)((__umulhi(p.page_mul, last) + last) >> p.page_shift) + 1;  // as page_of
+}
+
+// The scores of pages of one sequence and key-value head, as products of 16 pages' bounds with 8 heads' integers: a row of
+// bounds is 2 d bytes, the lowest keys and then the highest, and meets the head's integers below zero and then those
+// above. Lane 4 g + t reads the 16-byte pieces t, t + 4, ... of the rows g and g + 8 straight into the left operand (a
+// product takes its 32 terms in any order, the right operand the same); kPieces of them. GB300, 16 sequences to 65536
+// in pages of 32, 8 heads of 8: 6 us with them, 39 with four-term dot products and sums over lanes.
+template <bool kBf16, int kPieces>
 __global__ void __launch_bounds__(kWarps * 32) page_scores_kernel(const SelectParams p, int row_ctas) {
-    constexpr int kGroups = 32 / kLanes;
+    constexpr int kRow = 64 * kPieces;  // bytes of a head's integers: [below zero][above], zeros behind 2 d
     extern __shared__ __align__(16) uint8_t smem[];
-    // per head kLanes * 16 bytes of its integers above zero, as many of those below; then a float 2^e a head
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int padded = (p.group + kHeads - 1) / kHeads * kHeads;
-    uint4* const ints = reinterpret_cast<uint4*>(smem);  // [head][2][kLanes]
-    float* const two = reinterpret_cast<float*>(smem + (size_t)padded * 2 * kLanes * 16);
+    const int padded = (p.group + 7) / 8 * 8;
+    float* const two = reinterpret_cast<float*>(smem + (size_t)padded * kRow);  // 2^e a head
     grid_begin();
     const int row = blockIdx.x / row_ctas, cta = blockIdx.x % row_ctas, b = row / p.hkv, hk = row % p.hkv;
-    const int64_t room = p.per_seq * p.page_size;
-    const int len = bounded_len(p.lens[b], room, p.status);
-    const int pages = len ? (int)(((__umulhi(p.page_mul, (uint32_t)(len - 1)) + (uint64_t)(uint32_t)(len - 1)) >> p.page_shift) + 1) : 0;
-    const int j_first = (cta * kWarps + warp) * kGroups, j_step = row_ctas * kWarps * kGroups;
-    if (pages <= p.budget || cta * kWarps * kGroups >= pages) return;  // all are taken; nothing left for this CTA
-    // ---- the queries' integers: kLanes lanes a head
-    const int li = lane % kLanes, gr = lane / kLanes;
-    for (int h0 = warp * kGroups; h0 < padded; h0 += kWarps * kGroups) {  // whole warps
-        const int h = h0 + gr;
-        float x[16];
-        float a = 0.f;
-        const uint16_t* src = static_cast<const uint16_t*>(p.q) + b * p.q_batch + ((int64_t)hk * p.group + h) * p.q_head + 16 * li;
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            uint4 w = make_uint4(0, 0, 0, 0);
-            if (h < p.group && 16 * li + 8 * k < p.d) w = *reinterpret_cast<const uint4*>(src + 8 * k);
-            const uint32_t ws[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = floats<kBf16>(ws[i]);
-                x[8 * k + 2 * i] = f.x == f.x ? f.x : 0.f;
-                x[8 * k + 2 * i + 1] = f.y == f.y ? f.y : 0.f;
-            }
+    const int pages = pages_of(p, bounded_len(p.lens[b], p.per_seq * p.page_size, p.status));
+    if (pages <= p.budget || (int64_t)cta * kWarps * 16 * kSets >= pages) return;  // all are taken; nothing left for this CTA
+    // ---- the queries' integers: a warp a head, 4 channels a lane (d <= 128)
+    for (int h = warp; h < padded; h += kWarps) {
+        float x[4] = {}, a = 0.f;
+        if (h < p.group && 4 * lane < p.d) {
+            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + b * p.q_batch +
+                                                            ((int64_t)hk * p.group + h) * p.q_head + 4 * lane);
+            const float2 f = floats<kBf16>(w.x), g = floats<kBf16>(w.y);
+            x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
         }
 #pragma unroll
-        for (int i = 0; i < 16; ++i) a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+        for (int i = 0; i < 4; ++i) {
+            if (x[i] != x[i]) x[i] = 0.f;
+            a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+        }
 #pragma unroll
-        for (int off = kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+        for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
         const int e = bound_exp(a);
         const float inv = exp2_of(-e);
-        uint32_t up[4] = {}, down[4] = {};
+        uint32_t up = 0, down = 0;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
+        for (int i = 0; i < 4; ++i) {
             const int q = (int)fmaxf(fminf(rintf(x[i] * inv), 127.f), -127.f);
-            up[i / 4] |= (uint32_t)max(q, 0) << (8 * (i % 4));
-            down[i / 4] |= (uint32_t)(min(q, 0) & 0xff) << (8 * (i % 4));
+            up |= (uint32_t)max(q, 0) << (8 * i);
+            down |= (uint32_t)(min(q, 0) & 0xff) << (8 * i);
         }
-        if (h < padded) {
-            ints[h * 2 * kLanes + li] = make_uint4(up[0], up[1], up[2], up[3]);
-            ints[(h * 2 + 1) * kLanes + li] = make_uint4(down[0], down[1], down[2], down[3]);
-            if (li == 0) two[h] = exp2_of(e);
+        uint32_t* ints = reinterpret_cast<uint32_t*>(smem + h * kRow);
+        if (4 * lane < p.d) {
+            ints[lane] = down;
+            ints[p.d / 4 + lane] = up;
         }
+        for (int i = p.d / 2 + lane; i < kRow / 4; i += 32) ints[i] = 0;
+        if (lane == 0) two[h] = h < p.group ? exp2_of(e) : 0.f;
     }
     __syncthreads();
+    const int g = lane >> 2, t = lane & 3;
     const int32_t* table = p.table + b * p.table_stride;
     uint32_t* out = p.scores + (int64_t)row * p.per_seq;
-    const bool whole = p.d % 16 == 0;
-    for (int h0 = 0; h0 < padded; h0 += kHeads) {
-        uint32_t up[kHeads][4], down[kHeads][4];
+    const int64_t step = (int64_t)row_ctas * kWarps * 16 * kSets;
+    // lane r < 16 kSets looks page r of the warp's up
+    auto look = [&](int64_t j) { return lane < 16 * kSets && j + lane < pages ? table[j + lane] : -1; };
+    int64_t j0 = ((int64_t)cta * kWarps + warp) * 16 * kSets;
+    int next = look(j0);
+    for (; j0 < pages; j0 += step) {
+        int64_t at = next >= 0 && next < p.num_pages ? (int64_t)next * p.hkv + hk : -1;
+        const float scale = at >= 0 ? __uint_as_float((uint32_t)p.bounds_exp[at] << 23) : 0.f;
+        if (at < 0 && lane < 16 * kSets && j0 + lane < pages && p.status) atomicOr(p.status, kStatusBadIndex);
+        uint4 a[kSets][2][kPieces];
 #pragma unroll
-        for (int h = 0; h < kHeads; ++h) {
-            const uint4 u = ints[(h0 + h) * 2 * kLanes + li], d = ints[((h0 + h) * 2 + 1) * kLanes + li];
-            up[h][0] = u.x, up[h][1] = u.y, up[h][2] = u.z, up[h][3] = u.w;
-            down[h][0] = d.x, down[h][1] = d.y, down[h][2] = d.z, down[h][3] = d.w;
-        }
-        for (int64_t j0 = j_first; j0 < pages; j0 += j_step) {
-            const int j = (int)j0 + gr;
-            const int page = j < pages ? table[j] : -1;
-            const bool good = (uint32_t)page < (uint64_t)p.num_pages && page >= 0;
-            uint4 lo = make_uint4(0, 0, 0, 0), hi = lo;
-            const int64_t at = (int64_t)page * p.hkv + hk;
-            uint32_t byte = 0;
-            if (good) {
-                const int8_t* src = p.bounds + at * 2 * p.d + 16 * li;
-                if (whole) {
-                    if (16 * li < p.d) lo = *reinterpret_cast<const uint4*>(src), hi = *reinterpret_cast<const uint4*>(src + p.d);
-                } else {
-                    if (16 * li < p.d) {
-                        const uint2 x = *reinterpret_cast<const uint2*>(src), y = *reinterpret_cast<const uint2*>(src + p.d);
-                        lo.x = x.x, lo.y = x.y, hi.x = y.x, hi.y = y.y;
-                    }
-                    if (16 * li + 8 < p.d) {
-                        const uint2 x = *reinterpret_cast<const uint2*>(src + 8), y = *reinterpret_cast<const uint2*>(src + p.d + 8);
-                        lo.z = x.x, lo.w = x.y, hi.z = y.x, hi.w = y.y;
-                    }
+        for (int s = 0; s < kSets; ++s)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                const int64_t here = __shfl_sync(0xffffffffu, at, 16 * s + 8 * r + g);
+                const int8_t* src = p.bounds + (here >= 0 ? here : 0) * 2 * p.d + 16 * t;
+#pragma unroll
+                for (int i = 0; i < kPieces; ++i) {
+                    a[s][r][i] = make_uint4(0, 0, 0, 0);
+                    if (here >= 0 && 64 * i + 16 * t < 2 * p.d) a[s][r][i] = *reinterpret_cast<const uint4*>(src + 64 * i);
                 }
-                byte = p.bounds_exp[at];
             }
-            float best = -INFINITY;
+        next = look(j0 + step);
+        float best[kSets][2];
 #pragma unroll
-            for (int h = 0; h < kHeads; ++h) {
-                int u = 0;
-                u = dot4(up[h][0], hi.x, dot4(up[h][1], hi.y, dot4(up[h][2], hi.z, dot4(up[h][3], hi.w, u))));
-                u = dot4(down[h][0], lo.x, dot4(down[h][1], lo.y, dot4(down[h][2], lo.z, dot4(down[h][3], lo.w, u))));
+        for (int s = 0; s < kSets; ++s) best[s][0] = best[s][1] = -INFINITY;
+        for (int h0 = 0; h0 < padded; h0 += 8) {
+            int c[kSets][4] = {};
 #pragma unroll
-                for (int off = kLanes / 2; off > 0; off >>= 1) u += __shfl_xor_sync(0xffffffffu, u, off);
-                if (h0 + h < p.group) best = fmaxf(best, (float)u * two[h0 + h]);
+            for (int i = 0; i < kPieces; ++i) {
+                const uint4 q = *reinterpret_cast<const uint4*>(smem + (h0 + g) * kRow + 64 * i + 16 * t);
+#pragma unroll
+                for (int s = 0; s < kSets; ++s) {
+                    mma_s8(c[s], a[s][0][i].x, a[s][1][i].x, a[s][0][i].y, a[s][1][i].y, q.x, q.y);
+                    mma_s8(c[s], a[s][0][i].z, a[s][1][i].z, a[s][0][i].w, a[s][1][i].w, q.z, q.w);
+                }
             }
-            if (j < pages && li == 0) {
-                uint32_t key = good ? ordered(best * __uint_as_float(byte << 23)) : 0u;
-                if (j < p.first || j >= pages - p.recent) key = kForced;
-                out[j] = h0 == 0 ? key : max(out[j], key);
-                if (!good && p.status) atomicOr(p.status, kStatusBadIndex);
+#pragma unroll
+            for (int n = 0; n < 2; ++n) {  // heads 2t, 2t+1
+                if (h0 + 2 * t + n >= p.group) continue;
+                const float f = two[h0 + 2 * t + n];
+#pragma unroll
+                for (int s = 0; s < kSets; ++s) {
+                    best[s][0] = fmaxf(best[s][0], (float)c[s][n] * f);
+                    best[s][1] = fmaxf(best[s][1], (float)c[s][2 + n] * f);
+                }
             }
         }
+        // ---- lane r has page r's score
+        float mine = 0.f;
+#pragma unroll
+        for (int s = 0; s < kSets; ++s)
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float x = best[s][r];
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                x = __shfl_sync(0xffffffffu, x, lane % 8 * 4);
+                if (lane / 8 == 2 * s + r) mine = x;
+            }
+        const int64_t j = j0 + lane;
+        if (lane < 16 * kSets && j < pages)
+            out[j] = j < p.first || j >= pages - p.recent ? kForced : (at >= 0 ? ordered(mine * scale) : 0u);
     }
 }
 
 // ---------------------------------------------------------------------------- selection
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kHeld = 16;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kBins = 2 * kSelThreads;
 
 // Sums over the CTA of a thread's two counts, exclusive in thread order, and their totals.
 __device__ __forceinline__ uint2 scan2(uint2 v, uint2* sums, uint2* total) {
@@ -351,15 +369,20 @@ __device__ __forceinline__ uint2 scan2(uint2 v, uint2* sums, uint2* total) {
     return make_uint2(before.x + upto.x - v.x, before.y + upto.y - v.y);
 }
 
-// A CTA takes one sequence and head. Thread i has the scores of pages i per .. in registers, kHeld at most; more are read again.
+// A CTA takes one sequence and head. Thread i has the scores of pages i per .. in registers, kHeld at most; more are read
+// again. The budget-th largest is found by counting into kBins equal parts of the range that holds it, three times at
+// the most (for 32 bits), mostly twice: the range begins as that of the scores there are.
+template <int kHeld>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
     __shared__ uint2 sums[kSelWarps];
-    __shared__ uint32_t counts[2][kSelWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ uint32_t bins[kBins];
+    __shared__ uint32_t found[3];
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) found[0] = 0xffffffffu, found[1] = 0u, found[2] = 0u;
     grid_begin();
     const int b = blockIdx.x / p.hkv;
     const int len = bounded_len(p.lens[b], p.per_seq * p.page_size, p.status);
-    const int n = len ? (int)(((__umulhi(p.page_mul, (uint32_t)(len - 1)) + (uint64_t)(uint32_t)(len - 1)) >> p.page_shift) + 1) : 0;
+    const int n = pages_of(p, len);
     const int32_t* table = p.table + b * p.table_stride;
     int32_t* dst = p.sel_table + (int64_t)blockIdx.x * p.budget;
     const int taken = min(n, p.budget);
@@ -375,64 +398,110 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams 
     }
     const uint32_t* scores = p.scores + (int64_t)blockIdx.x * p.per_seq;
     const int per = (n + kSelThreads - 1) / kSelThreads;
-    const int i0 = min((int)threadIdx.x * per, n), i1 = min(i0 + per, n);
+    const int i0 = (int)min((int64_t)threadIdx.x * per, (int64_t)n), mine = min(per, n - i0);
     const bool held = per <= kHeld;
     uint32_t key[kHeld];
+    if (held) {
 #pragma unroll
-    for (int i = 0; i < kHeld; ++i) key[i] = held && i0 + i < i1 ? scores[i0 + i] : 0u;
-    // ---- the largest x with at least `budget` keys >= x, bit by bit
-    uint32_t least = 0;
-    for (int bit = 31; bit >= 0; --bit) {
-        const uint32_t x = least | (1u << bit);
-        uint32_t mine = 0;
-        if (held) {
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i) mine += key[i] >= x;
-        } else {
-            for (int i = i0; i < i1; ++i) mine += scores[i] >= x;
+        for (int i = 0; i < kHeld; ++i) {
+            if (i < mine) key[i] = scores[i0 + i];
         }
-        mine = __reduce_add_sync(0xffffffffu, mine);
-        if (lane == 0) counts[bit & 1][warp] = mine;
-        __syncthreads();
-        uint32_t all = lane < kSelWarps ? counts[bit & 1][lane] : 0u;
-        all = __reduce_add_sync(0xffffffffu, all);
-        if (all >= (uint32_t)p.budget) least = x;
     }
-    // ---- all above it, and the earliest of those equal to it
-    uint2 mine = make_uint2(0, 0), total;
     auto each = [&](auto f) {
         if (held) {
 #pragma unroll
-            for (int i = 0; i < kHeld; ++i)
-                if (i0 + i < i1) f(i0 + i, key[i]);
+            for (int i = 0; i < kHeld; ++i) {
+                if (i < mine) f(i0 + i, key[i]);
+            }
         } else {
-            for (int i = i0; i < i1; ++i) f(i, scores[i]);
+            for (int i = 0; i < mine; ++i) f(i0 + i, scores[i0 + i]);
         }
     };
-    each([&](int, uint32_t k) { mine.x += k > least, mine.y += k == least; });
-    const uint2 before = scan2(mine, sums, &total);
-    const uint32_t equal = (uint32_t)p.budget - total.x;  // taken of those equal
+    // ---- the range of the scores that are not forced, and how many to take of those
+    uint32_t lo = 0xffffffffu, hi = 0, forced = 0;
+    each([&](int, uint32_t k) {
+        if (k == kForced) ++forced;
+        else lo = min(lo, k), hi = max(hi, k);
+    });
+    lo = __reduce_min_sync(0xffffffffu, lo);
+    hi = __reduce_max_sync(0xffffffffu, hi);
+    forced = __reduce_add_sync(0xffffffffu, forced);
+    __syncthreads();  // found is set
+    if (lane == 0) {
+        atomicMin(&found[0], lo);
+        atomicMax(&found[1], hi);
+        if (forced) atomicAdd(&found[2], forced);
+    }
+    __syncthreads();
+    lo = found[0], hi = found[1];
+    uint32_t need = (uint32_t)p.budget - found[2];
+    uint32_t least = kForced - 1, equal = 0;  // all above `least` are taken and the earliest `equal` of those equal to it
+    while (need) {
+        const uint32_t width = hi - lo;  // less one
+        const int shift = max(0, 32 - __clz(width) - 10);
+        bins[threadIdx.x] = bins[kSelThreads + threadIdx.x] = 0;
+        __syncthreads();  // (found is read)
+        each([&](int, uint32_t k) {
+            if (k >= lo && k <= hi) atomicAdd(&bins[(k - lo) >> shift], 1u);
+        });
+        __syncthreads();
+        // thread i has the parts i and i + 1 from the top, in pairs
+        const int top = kBins - 1 - 2 * (int)threadIdx.x;
+        const uint32_t c0 = bins[top], c1 = bins[top - 1];
+        uint2 total;
+        const uint32_t above = scan2(make_uint2(c0 + c1, 0), sums, &total).x;
+        if (above < need && need <= above + c0 + c1) {
+            const bool second = need > above + c0;
+            found[0] = second ? top - 1 : top;
+            found[1] = second ? above + c0 : above;
+            found[2] = second ? c1 : c0;
+        }
+        __syncthreads();
+        lo += found[0] << shift;
+        hi = min(hi, lo + ((1u << shift) - 1));
+        need -= found[1];
+        least = lo;
+        if (shift == 0 || need == found[2]) {
+            equal = shift == 0 ? need : 0xffffffffu;  // (with the whole part: its lowest and all above)
+            break;
+        }
+        if (lo == hi) {
+            equal = need;
+            break;
+        }
+    }
+    // ---- in the order of their positions
+    uint2 count = make_uint2(0, 0), total;
+    each([&](int, uint32_t k) { count.x += k > least, count.y += k == least; });
+    const uint2 before = scan2(count, sums, &total);
     uint32_t at = before.x + min(before.y, equal), seen = before.y;
     each([&](int i, uint32_t k) {
-        if (k > least || (k == least && seen < equal)) {
-            dst[at++] = table[i];
-            if (i == n - 1) p.sel_lens[blockIdx.x] = p.budget * p.page_size - (int)((int64_t)n * p.page_size - len);
-        } else if (i == n - 1) {
-            p.sel_lens[blockIdx.x] = p.budget * p.page_size;
-        }
+        const bool take = k > least || (k == least && seen < equal);
         seen += k == least;
+        if (take) dst[at++] = table[i];
+        if (i == n - 1) p.sel_lens[blockIdx.x] = p.budget * p.page_size - (take ? (int)((int64_t)n * p.page_size - len) : 0);
     });
 }
 
-template <bool kBf16, int kLanes>
+template <bool kBf16, int kPieces>
 cudaError_t launch_scores(const SelectParams& p, cudaStream_t stream) {
-    const int padded = (p.group + kHeads - 1) / kHeads * kHeads;
-    const size_t smem = (size_t)padded * (2 * kLanes * 16 + sizeof(float));
-    // As many CTAs for a sequence and head as fill the SMs kResident times over, at most one for each kPages pages.
-    constexpr int kPages = 64, kResident = 5;
+    const int padded = (p.group + 7) / 8 * 8;
+    const size_t smem = (size_t)padded * (64 * kPieces + sizeof(float));  // 33 KB at most
+    // As many CTAs for a sequence and head as fill the SMs kResident times over, at most one for each round of pages.
+    constexpr int kPages = kWarps * 16 * kSets, kResident = 4;
     const int64_t rows = p.batch * p.hkv, most = (p.per_seq + kPages - 1) / kPages;
     const int64_t row_ctas = std::max<int64_t>(1, std::min(most, (152 * kResident + rows - 1) / rows));
-    return launch_early(page_scores_kernel<kBf16, kLanes>, dim3((unsigned)(rows * row_ctas)), dim3(kWarps * 32), smem, stream, p, (int)row_ctas);
+    return launch_early(page_scores_kernel<kBf16, kPieces>, dim3((unsigned)(rows * row_ctas)), dim3(kWarps * 32), smem, stream, p, (int)row_ctas);
+}
+
+template <bool kBf16>
+cudaError_t launch_scores_type(const SelectParams& p, cudaStream_t stream) {
+    switch ((p.d + 31) / 32) {
+        case 1: return launch_scores<kBf16, 1>(p, stream);
+        case 2: return launch_scores<kBf16, 2>(p, stream);
+        case 3: return launch_scores<kBf16, 3>(p, stream);
+        default: return launch_scores<kBf16, 4>(p, stream);
+    }
 }
 
 }  // namespace
@@ -447,14 +516,13 @@ cudaError_t launch_kv_bounds(const KvBoundsParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream) {
-    const bool bf = p.dtype == kBf16;
-    cudaError_t e = cudaSuccess;
-    if (p.per_seq <= p.budget) {}  // every page is taken, without a look at the bounds
-    else if (p.d <= 32) e = bf ? launch_scores<true, 2>(p, stream) : launch_scores<false, 2>(p, stream);
-    else if (p.d <= 64) e = bf ? launch_scores<true, 4>(p, stream) : launch_scores<false, 4>(p, stream);
-    else e = bf ? launch_scores<true, 8>(p, stream) : launch_scores<false, 8>(p, stream);
-    if (e != cudaSuccess) return e;
-    return launch_early(select_kernel, dim3((unsigned)(p.batch * p.hkv)), dim3(kSelThreads), 0, stream, p);
+    if (p.per_seq > p.budget) {  // else every page is taken, without a look at the bounds
+        const cudaError_t e = p.dtype == kBf16 ? launch_scores_type<true>(p, stream) : launch_scores_type<false>(p, stream);
+        if (e != cudaSuccess) return e;
+    }
+    // (by the table's width: the lengths are on the device)
+    auto kern = p.per_seq <= 4 * kSelThreads ? select_kernel<4> : select_kernel<16>;
+    return launch_early(kern, dim3((unsigned)(p.batch * p.hkv)), dim3(kSelThreads), 0, stream, p);
 }
 
 }  // namespace fa2

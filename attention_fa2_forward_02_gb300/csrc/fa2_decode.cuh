@@ -82,7 +82,8 @@ struct Cfg {
     static constexpr int kScaleRow = D / 16;                // e2m1: scale bytes of a key
     static constexpr int kScales = kE2m1 ? kKeys * kScaleRow : 0;  // and of a block's keys, or values
     static constexpr int kStage = 2 * kTile + kInfo + 2 * kScales;
-    static constexpr int kStages = 2;
+    // 4-bit rows: a block of 4.7 KB is too little in flight a warp; two stages 69.6 us in the batch of 32, three 0
+    static constexpr int kStages = kE2m1 && D == 128 ? 3 : 2;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kQ = kRows * D * 2;                // q as the first product takes it
     static constexpr int kPitch = kCodes ? D + 8 : D + 4;    // floats a row at the end of an item (no bank twice)
@@ -167,12 +168,17 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     return v;
 }
 
+// The lower or the upper half of a pair, twice.
+__device__ __forceinline__ uint32_t twice(uint32_t pair, bool upper) {
+    const __half2 x = *reinterpret_cast<const __half2*>(&pair), y = upper ? __high2half2(x) : __low2half2(x);
+    return *reinterpret_cast<const uint32_t*>(&y);
+}
+
 // A key's scales of groups `half`, half + 2, ... as pairs of the same half number; `row`: its D / 16 bytes.
 template <int D>
 __device__ __forceinline__ void key_scales(uint32_t row, int half, uint32_t (&s)[D / 32]) {
     if constexpr (D == 32) {
-        const uint32_t f = e4m3x2_to_f16x2(ld_shared_u16(row));
-        s[0] = __byte_perm(f, 0, half ? 0x3232 : 0x1010);
+        s[0] = twice(e4m3x2_to_f16x2(ld_shared_u16(row)), half);
     } else {
         uint32_t w;
         if constexpr (D == 128) {
@@ -184,7 +190,7 @@ __device__ __forceinline__ void key_scales(uint32_t row, int half, uint32_t (&s)
         uint32_t f[2];
         e4m3x4_to_f16x4(w, f[0], f[1]);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) s[i] = __byte_perm(f[i / 2], 0, i % 2 ? 0x3232 : 0x1010);
+        for (int i = 0; i < D / 32; ++i) s[i] = twice(f[i / 2], i % 2);
     }
 }
 
@@ -548,12 +554,17 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
         if (!ahead_live) return;
         const int hk = kPerHead ? ahead.b % c.hkv : ahead.item / hblocks;
         ahead_left = count(ahead, ahead_number);
-        ahead_key = ahead.range.base + (ahead.k0 + turn(ahead_number)) * kKeys + (kKeys < 32 ? lane % kKeys : lane);
+        ahead_key = ahead.range.base + (ahead.k0 + turn(ahead_number)) * kKeys + (kE2m1 ? 0 : (kKeys < 32 ? lane % kKeys : lane));
         ahead_table = c.table + ahead.b * c.table_stride;
         ahead_head = hk * c.head_stride;
         ahead_exp = (int64_t)hk * c.page_size;
     };
     enter();
+    // e2m1, and pages of whole sixteens of keys: kTeam lanes look 16 keys of a block up, which lie after one another in
+    // a page, and copy them: no address crosses lanes. (One key a lane, as below, took 390 instructions a block of 32
+    // keys, more than its products.)
+    const bool sixteens = c.page_size % 16 == 0, by_sixteens = kE2m1 && sixteens;
+    constexpr int kTeam = kE2m1 ? 512 / kKeys : 32;
     int page[C::kLooks], slot[C::kLooks];  // slot -1: no such key
     int64_t head_off = 0, head_exp = 0;    // and the block's head
     bool found = false;
@@ -567,9 +578,22 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
         if (!found) return;
         head_off = ahead_head;
         head_exp = ahead_exp;
+        if (by_sixteens) {
+            const int key = ahead_key + 16 * (lane / kTeam);
+            page[0] = 0;
+            slot[0] = -1;
+            if (key + 15 >= ahead.range.first && key < ahead.range.len) {
+                const int at = page_of(c, key);
+                page[0] = ahead_table[at];
+                slot[0] = key - at * c.page_size;
+            }
+            ahead_key += kWarps * kKeys;
+            --ahead_left;
+            return;
+        }
 #pragma unroll
         for (int j = 0; j < C::kLooks; ++j) {
-            const int key = ahead_key + 32 * j;
+            const int key = ahead_key + (kE2m1 ? lane : 0) + 32 * j;
             page[j] = 0;
             slot[j] = -1;
             if (key >= ahead.range.first && key < ahead.range.len) {
@@ -585,58 +609,82 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     const int lane_bytes = lane % C::kChunks * 16 < (kE2m1 ? c.d / 2 : (kE4m3 ? c.d : 2 * c.d)) ? 16 : 0;
     const int64_t lane_off = lane / C::kChunks * c.slot_stride + (lane_bytes ? lane % C::kChunks * 16 : 0);
     const int64_t rows_off = 32 / C::kChunks * c.slot_stride;
-    const bool sixteens = c.page_size % 16 == 0;
     const bool half_lines = c.d * 2 % 128 != 0;
     int fill = 0;                        // the stage to fill next
     uint32_t ka[C::kLooks], ve[C::kLooks];  // scale bytes of the block loaded last; ve 256: the key does not count
     int info_stage = -1;                 // and its stage, while they are not stored
-    // e2m1: the scale bytes of the keys `some` at `at` into K's and V's scales at `dst`, rows of kScaleRow bytes.
-    // The scale bytes of keys that follow one another in a page do so too: 16 keys of whole rows are D
-    // contiguous bytes. Those of keys among them that do not count come along, and store_info clears them.
+    // e2m1, key by key: the scale bytes of the keys `some` at `at` into K's and V's scales at `dst`
     auto load_scales = [&](uint32_t dst, const uint32_t (&some)[C::kLooks], const int64_t (&at)[C::kLooks]) {
         if constexpr (kE2m1) {
-            constexpr int kPer = D / 16;  // 16-byte pieces of 16 keys' scale bytes
-            const int row = c.d / 16;     // bytes a key has in memory
-            if (sixteens) {
-                // pieces 0 .. kKeys / 16 * kPer - 1 of K, then those of V; with d < D rows of d / 16 bytes, widened by store_info
+            const int row = c.d / 16;  // bytes a key has in memory
 #pragma unroll
-                for (int i0 = 0; i0 < 2 * kKeys / 16 * kPer; i0 += 32) {  // (of D = 32 only half a warp's worth)
-                    const int i = i0 + lane, n = i % (kKeys / 16 * kPer), r = n / kPer * 16, piece = n % kPer;
-                    const uint32_t there = (some[0] >> (r & 31)) & 0xffffu, there1 = (some[C::kLooks - 1] >> (r & 31)) & 0xffffu;
-                    const uint32_t set = r < 32 ? there : there1;
-                    const int one = set ? __ffs(set) - 1 : 0;
-                    const int64_t a0 = __shfl_sync(0xffffffffu, at[0], (r & 31) + one);
-                    const int64_t a1 = __shfl_sync(0xffffffffu, at[C::kLooks - 1], (r & 31) + one);
-                    const bool on = set && piece < row, used = i < 2 * kKeys / 16 * kPer;
-                    const uint8_t* src = (i < kKeys / 16 * kPer ? c.k_scale : c.v_scale) + (on ? ((r < 32 ? a0 : a1) - one) * row + piece * 16 : 0);
-                    const uint32_t to = dst + (i < kKeys / 16 * kPer ? 0 : C::kScales) + n / kPer * (16 * C::kScaleRow) + piece * 16;
-                    if (used) cp_async16<true>(to, src, on ? 16 : 0, true);
-                }
-            } else {
-#pragma unroll
-                for (int j = 0; j < C::kLooks; ++j) {
-                    const bool on = (some[j] >> lane) & 1u;
-                    const uint8_t *ks = c.k_scale + (on ? at[j] * row : 0), *vs = c.v_scale + (on ? at[j] * row : 0);
-                    const uint32_t to = dst + (lane + 32 * j) * C::kScaleRow;
-                    if (D >= 64 && row == kPer) {
-                        cp_async_small<kPer>(to, ks, on);
-                        cp_async_small<kPer>(to + C::kScales, vs, on);
-                    } else {  // rows of 2 or 6 bytes have no asynchronous copy
-                        for (int e = 0; e < row; e += 2) {
-                            st_shared_u16(to + e, on ? *reinterpret_cast<const uint16_t*>(ks + e) : 0);
-                            st_shared_u16(to + C::kScales + e, on ? *reinterpret_cast<const uint16_t*>(vs + e) : 0);
-                        }
-                        for (int e = row; e < kPer; e += 2) {
-                            st_shared_u16(to + e, 0);
-                            st_shared_u16(to + C::kScales + e, 0);
-                        }
+            for (int j = 0; j < C::kLooks; ++j) {
+                const bool on = (some[j] >> lane) & 1u;
+                const uint8_t *ks = c.k_scale + (on ? at[j] * row : 0), *vs = c.v_scale + (on ? at[j] * row : 0);
+                const uint32_t to = dst + (lane + 32 * j) * C::kScaleRow;
+                if (D >= 64 && row == C::kScaleRow) {
+                    cp_async_small<C::kScaleRow>(to, ks, on);
+                    cp_async_small<C::kScaleRow>(to + C::kScales, vs, on);
+                } else {  // rows of 2 or 6 bytes have no asynchronous copy
+                    for (int e = 0; e < C::kScaleRow; e += 2) {
+                        st_shared_u16(to + e, on && e < row ? *reinterpret_cast<const uint16_t*>(ks + e) : 0);
+                        st_shared_u16(to + C::kScales + e, on && e < row ? *reinterpret_cast<const uint16_t*>(vs + e) : 0);
                     }
                 }
             }
         }
     };
+    // e2m1, by sixteens: this lane's pieces of its team's 16 keys. A team's rows are copied whole if any of them counts (a
+    // page holds all 16), and not at all otherwise: a code that does not count is finite whatever it is. Scales are not,
+    // and become zeros (here where none counts, else in tidy_scales).
+    const int mate = lane % kTeam, mate_row = mate / C::kChunks, mate_piece = mate % C::kChunks;
+    constexpr int kTeamRows = kTeam / C::kChunks;  // rows a copy covers
+    uint32_t untidy = 0;  // bit n: the block loaded n loads ago has keys that do not count
+    auto load_sixteens = [&](uint32_t st) {
+        if constexpr (kE2m1) {
+            const int key0 = ahead_key - kWarps * kKeys + 16 * (lane / kTeam);  // of the team
+            Slot s{-1, -1};
+            if (slot[0] >= 0) s = slot_of(c, page[0], slot[0]);
+            const bool there = s.off >= 0;
+            const int64_t o = (there ? s.off + mate_row * c.slot_stride : 0) + head_off + mate_piece * 16;
+            const char *ks = c.k + o, *vs = c.v + o;
+            if (there && 32 * mate_piece < c.d) {
+#pragma unroll
+                for (int i = 0; i < 16 / kTeamRows; ++i) {
+                    const uint32_t dst = st + swizzle<C::kChunks>(16 * (lane / kTeam) + i * kTeamRows + mate_row, mate_piece) * 16;
+                    cp_async16<true>(dst, ks, 16, true);
+                    cp_async16<true>(dst + C::kTile, vs, 16, true);
+                    ks += kTeamRows * c.slot_stride;
+                    vs += kTeamRows * c.slot_stride;
+                }
+            }
+            const int64_t e = s.exp + head_exp;
+            // 16 keys' scale bytes are d contiguous ones, D / 16 pieces of K and as many of V (d = 96: rows of 6 bytes, widened later)
+            constexpr int kPer = D / 16;
+            const int side = mate / kPer, piece = mate % kPer;
+            if (side < 2 && 16 * piece < c.d) {
+                const uint32_t dst = st + 2 * C::kTile + C::kInfo + side * C::kScales + 16 * (lane / kTeam) * C::kScaleRow + piece * 16;
+                cp_async16<true>(dst, (side ? c.v_scale : c.k_scale) + (there ? e * (c.d / 16) + piece * 16 : 0), there ? 16 : 0, true);
+            }
+            constexpr int kMine = 16 / kTeam;  // keys whose scale's exponents this lane reads
+            bool all = true;
+#pragma unroll
+            for (int j = 0; j < kMine; ++j) {
+                const int n = mate * kMine + j;
+                const bool on = there && key0 + n >= ahead.range.first && key0 + n < ahead.range.len;
+                ka[j] = on ? c.k_exp[e + n] : 127u;
+                ve[j] = on ? c.v_exp[e + n] : 256u;
+                all = all && on;
+            }
+            untidy |= __any_sync(0xffffffffu, !all);
+        }
+    };
     auto load = [&]() {  // copies the block looked up last into the next stage; commits one group
-        if (found) {
+        if constexpr (kE2m1) untidy <<= 1;
+        if (found && by_sixteens) {
+            load_sixteens(my_addr + fill * C::kStage);
+            info_stage = fill;
+        } else if (found) {
             const uint32_t st = my_addr + fill * C::kStage;
             const char* kbase = c.k + head_off;
             const char* vbase = c.v + head_off;
@@ -659,7 +707,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                 }
             }
             constexpr int kStep = 32 / C::kChunks;  // rows a copy instruction of the warp covers
-            if (sixteens) {  // 16 keys lie after one another in a page: the address of one tells the others'
+            if (sixteens && !kE2m1) {  // 16 keys lie after one another in a page: the address of one tells the others'
 #pragma unroll
                 for (int r = 0; r < kKeys; r += 16) {
                     const uint32_t there = (some[r / 32] >> (r & 31)) & 0xffffu;
@@ -669,7 +717,6 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                     const char *ks = kbase + o, *vs = vbase + o;
 #pragma unroll
                     for (int i = 0; i < 16; i += kStep) {
-                        if (kStep > 16 && lane >= 16) break;  // 16 rows are all there is
                         const int bytes = (there >> (i + lane / C::kChunks)) & 1u ? lane_bytes : 0;
                         const uint32_t dst = st + swizzle<C::kChunks>(r + i + lane / C::kChunks, lane % C::kChunks) * 16;
                         cp_async16<C::kHalfLines>(dst, ks, bytes, half_lines);
@@ -700,16 +747,13 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
         cp_async_commit();
         fill = fill + 1 == S ? 0 : fill + 1;
     };
-    // e2m1, once a block's copies are done: rows of d / 16 scale bytes to kScaleRow, and zeros for keys that do
-    // not count, so that whatever lies there (a NaN) times a code of zero is zero.
-    auto tidy_scales = [&](uint32_t scales) {
+    // e2m1, by sixteens, before a block is used: rows of d / 16 scale bytes to kScaleRow, and zeros for keys that do
+    // not count, so that whatever lies there (a NaN) times any code is zero.
+    auto tidy_scales = [&](uint8_t* stage) {
         if constexpr (kE2m1) {
-            const bool widen = D == 128 && sixteens && c.d < D;
-            bool clear = false;
-#pragma unroll
-            for (int j = 0; j < C::kLooks; ++j) clear |= ve[j] >= 256;
-            if (!widen && !__any_sync(0xffffffffu, clear)) return;
-            __syncwarp();  // other lanes' copies
+            const bool widen = D == 128 && by_sixteens && c.d < D;
+            if (!widen && !(untidy >> (S - 2) & 1u)) return;
+            const uint32_t scales = smem_u32(stage) + 2 * C::kTile + C::kInfo;
             uint32_t w[C::kLooks][2][2];
             if (widen) {
 #pragma unroll
@@ -726,25 +770,26 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
             }
 #pragma unroll
             for (int j = 0; j < C::kLooks; ++j) {
-                if (!widen && ve[j] < 256) continue;
+                const bool counts = reinterpret_cast<const float2*>(stage + 2 * C::kTile)[lane + 32 * j].y > -INFINITY;
+                if (!widen && counts) continue;
 #pragma unroll
                 for (int side = 0; side < 2; ++side) {
                     const uint32_t to = scales + side * C::kScales + (lane + 32 * j) * C::kScaleRow;
-                    const bool keep = widen && ve[j] < 256;
+                    const bool keep = widen && counts;
                     if constexpr (D == 128) st_shared_v2(to, keep ? w[j][side][0] : 0, keep ? w[j][side][1] : 0);
                     else if constexpr (D == 64) st_shared_u32(to, 0);
                     else st_shared_u16(to, 0);
                 }
             }
+            __syncwarp();
         }
     };
     auto store_info = [&]() {  // codes: the key's scale, and the value scale's exponent (-infinity: masked)
         if constexpr (kCodes) {
             if (info_stage < 0) return;
-            if constexpr (kE2m1) tidy_scales(smem_u32(my + info_stage * C::kStage + 2 * C::kTile + C::kInfo));
 #pragma unroll
             for (int j = 0; j < C::kLooks; ++j)
-                reinterpret_cast<float2*>(my + info_stage * C::kStage + 2 * C::kTile)[lane + 32 * j] =
+                reinterpret_cast<float2*>(my + info_stage * C::kStage + 2 * C::kTile)[by_sixteens ? lane * C::kLooks + j : lane + 32 * j] =
                     make_float2(__uint_as_float(ka[j] << 23), ve[j] < 256 ? (float)((int)ve[j] - 127) : -INFINITY);
             info_stage = -1;
         }
@@ -768,7 +813,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     for (int i = 0; i < S - 1; ++i) {
         load();
         look();
-        if constexpr (!kE2m1) store_info();  // (it clears scales behind their copies: in the loop, once those are done)
+        store_info();
     }
 
     if constexpr (!kCluster) empty_rows();
@@ -877,6 +922,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
             cp_async_wait<S - 2>();
             store_info();
             __syncwarp();
+            tidy_scales(my + use * C::kStage);
             load();
             look();
             const uint32_t kt = my_addr + use * C::kStage, vt = kt + C::kTile;

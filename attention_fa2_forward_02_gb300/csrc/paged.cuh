@@ -89,9 +89,8 @@ __device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t codes, uint32_t (&r)[4]
 // of the first and of the second row in pair i.
 __device__ __forceinline__ void e2m1_2x4_to_f16(uint32_t codes, uint32_t (&r)[4]) {
     const uint32_t even = (codes & 0x0f0fu) | (codes >> 12 & 0xf0f0u), odd = (codes >> 4 & 0x0f0fu) | (codes >> 16 & 0xf0f0u);
-    asm("{\n\t.reg .b8 a, b, c, d, n;\n\t.reg .b16 e, o;\n\tcvt.u16.u32 e, %4;\n\tcvt.u16.u32 o, %5;\n\t"
-        "mov.b16 {a, c}, e;\n\tmov.b16 {b, d}, o;\n\tcvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+    asm("{\n\t.reg .b8 a, b, c, d, n, m;\n\tmov.b32 {a, c, n, m}, %4;\n\tmov.b32 {b, d, n, m}, %5;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(even), "r"(odd));
 }
 

@@ -86,12 +86,15 @@ __device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t codes, uint32_t (&r)[4]
 }
 
 // Four codes of each of two rows, the first row's in the lower half of the word -> four pairs of halves, code i
-// of the first and of the second row in pair i.
+// of the first and of the second row in pair i. (Converted first, paired after: 8 instructions; pairs of codes made of
+// nibbles first take 11, and the unit that does them is the decode's busiest.)
 __device__ __forceinline__ void e2m1_2x4_to_f16(uint32_t codes, uint32_t (&r)[4]) {
-    const uint32_t even = (codes & 0x0f0fu) | (codes >> 12 & 0xf0f0u), odd = (codes >> 4 & 0x0f0fu) | (codes >> 16 & 0xf0f0u);
-    asm("{\n\t.reg .b8 a, b, c, d, n, m;\n\tmov.b32 {a, c, n, m}, %4;\n\tmov.b32 {b, d, n, m}, %5;\n\t"
-        "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\tcvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(even), "r"(odd));
+    uint32_t x[4];
+    e2m1x8_to_f16x8(codes, x);
+    r[0] = __byte_perm(x[0], x[2], 0x5410);
+    r[1] = __byte_perm(x[0], x[2], 0x7632);
+    r[2] = __byte_perm(x[1], x[3], 0x5410);
+    r[3] = __byte_perm(x[1], x[3], 0x7632);
 }
 
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {

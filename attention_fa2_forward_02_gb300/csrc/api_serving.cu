@@ -87,7 +87,7 @@ fa2_status paged(const fa2_kv_cache* c, const int32_t* table, int64_t table_stri
         pages_per_seq > kMaxLen || pages_per_seq * c->page_size > kMaxLen)
         return FA2_ERR_UNSUPPORTED;
     const int64_t bits = e2m1 ? 4 : (e4m3 ? 8 : 16);
-    if (e2m1 && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16))) return FA2_ERR_MISALIGNED;
+    if (e2m1 && (!aligned(c->k_scale, 16) || !aligned(c->v_scale, 16) || !aligned(c->k_exp, 16) || !aligned(c->v_exp, 16))) return FA2_ERR_MISALIGNED;
     if (!aligned(c->k, 16) || !aligned(c->v, 16) || !aligned(table, 4) || !aligned(lens, 4)) return FA2_ERR_MISALIGNED;
     for (int i = 0; i < 3; ++i)
         if (sizes[i] > 1 && strides[i] * bits % 128 != 0) return FA2_ERR_MISALIGNED;
@@ -168,6 +168,9 @@ fa2_status decode_call(const void* q, const int64_t* q_strides, const fa2_kv_cac
     p.window = window < p.c.room ? window : 0;  // as wide as the table: all keys
     p.workspace = static_cast<float*>(workspace);
     p.scale = softmax_scale;
+    p.by_sixteens = p.c.page_size % 16 == 0 &&
+                    (double)p.c.num_pages * p.c.page_stride + (double)p.c.hkv * p.c.head_stride + (double)p.c.page_size * p.c.slot_stride < 16.0 * UINT32_MAX &&
+                    p.c.num_pages * p.c.hkv * p.c.page_size < UINT32_MAX;
     if (per_head) {
         if (batch * cache->n_kv_heads > (1 << 20)) return FA2_ERR_UNSUPPORTED;
         p.per_head = true;

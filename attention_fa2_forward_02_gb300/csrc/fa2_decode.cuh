@@ -81,7 +81,8 @@ struct Cfg {
     static constexpr int kInfo = kCodes ? kKeys * 8 : 16;   // codes: a float2 per key; else the keys that count, as bits
     static constexpr int kScaleRow = D / 16;                // e2m1: scale bytes of a key
     static constexpr int kScales = kE2m1 ? kKeys * kScaleRow : 0;  // and of a block's keys, or values
-    static constexpr int kStage = 2 * kTile + kInfo + 2 * kScales;
+    static constexpr int kExps = 2 * kTile + kInfo + 2 * kScales;  // e2m1: bytes of K's, then V's powers of two
+    static constexpr int kStage = kExps + (kE2m1 ? 2 * kKeys : 0);
     // 4-bit rows: a block of 4.7 KB is too little in flight a warp; two stages 69.6 us in the batch of 32, three 0
     static constexpr int kStages = kE2m1 && D == 128 ? 3 : 2;
     static constexpr int kRing = kWarps * kStages * kStage;
@@ -550,6 +551,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     int ahead_number = 0, ahead_left = 0, ahead_key = 0;  // blocks of this warp left, the next one's first key
     const int32_t* ahead_table = nullptr;
     int64_t ahead_head = 0, ahead_exp = 0;                // the head's offset in a page, in its scale bytes
+    uint32_t ahead_head16 = 0, ahead_head_key = 0;        // (by sixteens)
     auto enter = [&]() {
         if (!ahead_live) return;
         const int hk = kPerHead ? ahead.b % c.hkv : ahead.item / hblocks;
@@ -558,15 +560,18 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
         ahead_table = c.table + ahead.b * c.table_stride;
         ahead_head = hk * c.head_stride;
         ahead_exp = (int64_t)hk * c.page_size;
+        ahead_head16 = (uint32_t)hk * (uint32_t)(c.head_stride >> 4);
+        ahead_head_key = (uint32_t)(hk * c.page_size);
     };
     enter();
     // e2m1, and pages of whole sixteens of keys: kTeam lanes look 16 keys of a block up, which lie after one another in
     // a page, and copy them: no address crosses lanes. (One key a lane, as below, took 390 instructions a block of 32
     // keys, more than its products.)
-    const bool sixteens = c.page_size % 16 == 0, by_sixteens = kE2m1 && sixteens;
+    const bool sixteens = c.page_size % 16 == 0, by_sixteens = kE2m1 && p.by_sixteens;
     constexpr int kTeam = kE2m1 ? 512 / kKeys : 32;
     int page[C::kLooks], slot[C::kLooks];  // slot -1: no such key
     int64_t head_off = 0, head_exp = 0;    // and the block's head
+    uint32_t head16 = 0, head_key = 0;     // (by sixteens)
     bool found = false;
     auto look = [&]() {  // the next block of this warp, if there is one
         while (ahead_live && ahead_left == 0) {
@@ -579,6 +584,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
         head_off = ahead_head;
         head_exp = ahead_exp;
         if (by_sixteens) {
+            head16 = ahead_head16;
+            head_key = ahead_head_key;
             const int key = ahead_key + 16 * (lane / kTeam);
             page[0] = 0;
             slot[0] = -1;
@@ -637,53 +644,43 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     // e2m1, by sixteens: this lane's pieces of its team's 16 keys. A team's rows are copied whole if any of them counts (a
     // page holds all 16), and not at all otherwise: a code that does not count is finite whatever it is. Scales are not,
     // and become zeros (here where none counts, else in tidy_scales).
-    const int mate = lane % kTeam, mate_row = mate / C::kChunks, mate_piece = mate % C::kChunks;
+    const int team = lane / kTeam, mate = lane % kTeam, mate_row = mate / C::kChunks, mate_piece = mate % C::kChunks;
     constexpr int kTeamRows = kTeam / C::kChunks;  // rows a copy covers
-    uint32_t untidy = 0;  // bit n: the block loaded n loads ago has keys that do not count
+    const uint32_t step16 = (uint32_t)(c.slot_stride >> 4), mate16 = mate_row * step16 + mate_piece;
+    const bool mate_on = 32 * mate_piece < c.d;
+    // scale bytes: 16 keys' are d contiguous ones, D / 16 pieces of K and as many of V (d = 96: rows of 6 bytes, widened
+    // later); after those, for the powers of two, a piece of K and a piece of V
+    constexpr int kPer = D / 16;
+    const int scale_side = mate / kPer, scale_piece = mate % kPer;
+    const bool scale_on = scale_side < 2 && 16 * scale_piece < c.d;
     auto load_sixteens = [&](uint32_t st) {
         if constexpr (kE2m1) {
-            const int key0 = ahead_key - kWarps * kKeys + 16 * (lane / kTeam);  // of the team
-            Slot s{-1, -1};
-            if (slot[0] >= 0) s = slot_of(c, page[0], slot[0]);
-            const bool there = s.off >= 0;
-            const int64_t o = (there ? s.off + mate_row * c.slot_stride : 0) + head_off + mate_piece * 16;
-            const char *ks = c.k + o, *vs = c.v + o;
-            if (there && 32 * mate_piece < c.d) {
+            const bool there = slot[0] >= 0 && (uint32_t)page[0] < (uint64_t)c.num_pages;
+            if (slot[0] >= 0 && !there && c.status) atomicOr(c.status, kStatusBadIndex);
+            // in units of 16 bytes, and of keys: within 32 bits (by_sixteens)
+            const uint32_t o = there ? (uint32_t)page[0] * (uint32_t)(c.page_stride >> 4) + (uint32_t)slot[0] * step16 + head16 + mate16 : 0u;
+            const uint32_t e = there ? (uint32_t)page[0] * (uint32_t)(c.hkv * c.page_size) + (uint32_t)slot[0] + head_key : 0u;
+            if (there && mate_on) {
+                const char *ks = c.k + (uint64_t)o * 16, *vs = c.v + (uint64_t)o * 16;
 #pragma unroll
                 for (int i = 0; i < 16 / kTeamRows; ++i) {
-                    const uint32_t dst = st + swizzle<C::kChunks>(16 * (lane / kTeam) + i * kTeamRows + mate_row, mate_piece) * 16;
+                    const uint32_t dst = st + swizzle<C::kChunks>(16 * team + i * kTeamRows + mate_row, mate_piece) * 16;
                     cp_async16<true>(dst, ks, 16, true);
                     cp_async16<true>(dst + C::kTile, vs, 16, true);
                     ks += kTeamRows * c.slot_stride;
                     vs += kTeamRows * c.slot_stride;
                 }
             }
-            const int64_t e = s.exp + head_exp;
-            // 16 keys' scale bytes are d contiguous ones, D / 16 pieces of K and as many of V (d = 96: rows of 6 bytes, widened later)
-            constexpr int kPer = D / 16;
-            const int side = mate / kPer, piece = mate % kPer;
-            if (side < 2 && 16 * piece < c.d) {
-                const uint32_t dst = st + 2 * C::kTile + C::kInfo + side * C::kScales + 16 * (lane / kTeam) * C::kScaleRow + piece * 16;
-                cp_async16<true>(dst, (side ? c.v_scale : c.k_scale) + (there ? e * (c.d / 16) + piece * 16 : 0), there ? 16 : 0, true);
-            }
-            constexpr int kMine = 16 / kTeam;  // keys whose scale's exponents this lane reads
-            bool all = true;
-#pragma unroll
-            for (int j = 0; j < kMine; ++j) {
-                const int n = mate * kMine + j;
-                const bool on = there && key0 + n >= ahead.range.first && key0 + n < ahead.range.len;
-                ka[j] = on ? c.k_exp[e + n] : 127u;
-                ve[j] = on ? c.v_exp[e + n] : 256u;
-                all = all && on;
-            }
-            untidy |= __any_sync(0xffffffffu, !all);
+            const int bytes = there ? 16 : 0;  // else zeros
+            if (scale_on)
+                cp_async16<true>(st + 2 * C::kTile + C::kInfo + scale_side * C::kScales + 16 * team * C::kScaleRow + scale_piece * 16,
+                                 (scale_side ? c.v_scale : c.k_scale) + ((uint64_t)e * (uint32_t)(c.d / 16) + (there ? scale_piece * 16 : 0)), bytes, true);
+            if (mate < 2) cp_async16<true>(st + C::kExps + mate * kKeys + 16 * team, (mate ? c.v_exp : c.k_exp) + e, bytes, true);
         }
     };
     auto load = [&]() {  // copies the block looked up last into the next stage; commits one group
-        if constexpr (kE2m1) untidy <<= 1;
         if (found && by_sixteens) {
             load_sixteens(my_addr + fill * C::kStage);
-            info_stage = fill;
         } else if (found) {
             const uint32_t st = my_addr + fill * C::kStage;
             const char* kbase = c.k + head_off;
@@ -747,38 +744,49 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
         cp_async_commit();
         fill = fill + 1 == S ? 0 : fill + 1;
     };
-    // e2m1, by sixteens, before a block is used: rows of d / 16 scale bytes to kScaleRow, and zeros for keys that do
-    // not count, so that whatever lies there (a NaN) times any code is zero.
-    auto tidy_scales = [&](uint8_t* stage) {
+    // e2m1, by sixteens, before a block of keys key0 .. of the range is used: its info from the bytes of its powers of two (0:
+    // the page is not there); rows of d / 16 scale bytes to kScaleRow; and zeros for the scales of keys that do not count, so
+    // that whatever lies there (a NaN) times any code is zero.
+    auto tidy = [&](uint8_t* stage, int key0, const Range& range) {
         if constexpr (kE2m1) {
-            const bool widen = D == 128 && by_sixteens && c.d < D;
-            if (!widen && !(untidy >> (S - 2) & 1u)) return;
-            const uint32_t scales = smem_u32(stage) + 2 * C::kTile + C::kInfo;
-            uint32_t w[C::kLooks][2][2];
-            if (widen) {
-#pragma unroll
-                for (int j = 0; j < C::kLooks; ++j)
-#pragma unroll
-                    for (int side = 0; side < 2; ++side) {
-                        // 16 keys' rows of d / 16 bytes lie together at the beginning of their 16 kScaleRow bytes
-                        const int key = lane + 32 * j;
-                        const uint32_t from = scales + side * C::kScales + key / 16 * (16 * C::kScaleRow) + key % 16 * (c.d / 16);
-                        w[j][side][0] = ld_shared_u16(from) | ld_shared_u16(from + 2) << 16;
-                        w[j][side][1] = ld_shared_u16(from + 4);
-                    }
-                __syncwarp();
-            }
+            if (!by_sixteens) return;
+            const bool widen = D == 128 && c.d < D;
+            bool counts[C::kLooks], all = true;
 #pragma unroll
             for (int j = 0; j < C::kLooks; ++j) {
-                const bool counts = reinterpret_cast<const float2*>(stage + 2 * C::kTile)[lane + 32 * j].y > -INFINITY;
-                if (!widen && counts) continue;
+                const int r = lane + 32 * j, key = key0 + r;
+                const uint32_t k = stage[C::kExps + r], v = stage[C::kExps + kKeys + r];
+                counts[j] = v != 0 && key >= range.first && key < range.len;
+                all = all && counts[j];
+                reinterpret_cast<float2*>(stage + 2 * C::kTile)[r] = make_float2(__uint_as_float(k << 23), counts[j] ? (float)((int)v - 127) : -INFINITY);
+            }
+            if (widen || __any_sync(0xffffffffu, !all)) {
+                const uint32_t scales = smem_u32(stage) + 2 * C::kTile + C::kInfo;
+                uint32_t w[C::kLooks][2][2];
+                if (widen) {
 #pragma unroll
-                for (int side = 0; side < 2; ++side) {
-                    const uint32_t to = scales + side * C::kScales + (lane + 32 * j) * C::kScaleRow;
-                    const bool keep = widen && counts;
-                    if constexpr (D == 128) st_shared_v2(to, keep ? w[j][side][0] : 0, keep ? w[j][side][1] : 0);
-                    else if constexpr (D == 64) st_shared_u32(to, 0);
-                    else st_shared_u16(to, 0);
+                    for (int j = 0; j < C::kLooks; ++j)
+#pragma unroll
+                        for (int side = 0; side < 2; ++side) {
+                            // 16 keys' rows of d / 16 bytes lie together at the beginning of their 16 kScaleRow bytes
+                            const int r = lane + 32 * j;
+                            const uint32_t from = scales + side * C::kScales + r / 16 * (16 * C::kScaleRow) + r % 16 * (c.d / 16);
+                            w[j][side][0] = ld_shared_u16(from) | ld_shared_u16(from + 2) << 16;
+                            w[j][side][1] = ld_shared_u16(from + 4);
+                        }
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int j = 0; j < C::kLooks; ++j) {
+                    if (!widen && counts[j]) continue;
+#pragma unroll
+                    for (int side = 0; side < 2; ++side) {
+                        const uint32_t to = scales + side * C::kScales + (lane + 32 * j) * C::kScaleRow;
+                        const bool keep = widen && counts[j];
+                        if constexpr (D == 128) st_shared_v2(to, keep ? w[j][side][0] : 0, keep ? w[j][side][1] : 0);
+                        else if constexpr (D == 64) st_shared_u32(to, 0);
+                        else st_shared_u16(to, 0);
+                    }
                 }
             }
             __syncwarp();
@@ -789,7 +797,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
             if (info_stage < 0) return;
 #pragma unroll
             for (int j = 0; j < C::kLooks; ++j)
-                reinterpret_cast<float2*>(my + info_stage * C::kStage + 2 * C::kTile)[by_sixteens ? lane * C::kLooks + j : lane + 32 * j] =
+                reinterpret_cast<float2*>(my + info_stage * C::kStage + 2 * C::kTile)[lane + 32 * j] =
                     make_float2(__uint_as_float(ka[j] << 23), ve[j] < 256 ? (float)((int)ve[j] - 127) : -INFINITY);
             info_stage = -1;
         }
@@ -918,11 +926,13 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
             ml[h][0] = ml[h][1] = kNoScore;
         }
 
+        int here = seg.range.base + (seg.k0 + turn(number)) * kKeys;  // the block's first key
         for (int i = count(seg, number); i > 0; --i) {
             cp_async_wait<S - 2>();
             store_info();
             __syncwarp();
-            tidy_scales(my + use * C::kStage);
+            tidy(my + use * C::kStage, here, seg.range);
+            here += kWarps * kKeys;
             load();
             look();
             const uint32_t kt = my_addr + use * C::kStage, vt = kt + C::kTile;
@@ -1061,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                 }
             }
             float mx[kTiles][2];
-            auto grows = [&]() {  // the block's maxima; whether one is well above the running maximum
+            auto grows = [&]() {  // this lane's maxima of the block; whether any lane's is well above the running maximum
                 bool grow = false;
 #pragma unroll
                 for (int h = 0; h < kTiles; ++h)
@@ -1070,8 +1080,6 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                         mx[h][n] = fmaxf(sc[0][h][n], sc[0][h][2 + n]);
 #pragma unroll
                         for (int j = 1; j < kMt; ++j) mx[h][n] = fmax3(mx[h][n], sc[j][h][n], sc[j][h][2 + n]);
-#pragma unroll
-                        for (int off = 4; off < 32; off <<= 1) mx[h][n] = fmaxf(mx[h][n], __shfl_xor_sync(0xffffffffu, mx[h][n], off));
                         grow |= mx[h][n] - m[h][n] > kRescale + kLift;  // exact where it matters; m + kRescale is not, past 2^26
                     }
                 return __any_sync(0xffffffffu, grow);
@@ -1114,6 +1122,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                 for (int h = 0; h < kTiles; ++h)
 #pragma unroll
                     for (int n = 0; n < 2; ++n) {
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) mx[h][n] = fmaxf(mx[h][n], __shfl_xor_sync(0xffffffffu, mx[h][n], off));
                         const float m_new = fmaxf(m[h][n], mx[h][n] - kLift);
                         const float f = m_new == -INFINITY ? 1.f : ex2_approx(m[h][n] - m_new);
                         m[h][n] = m_new;

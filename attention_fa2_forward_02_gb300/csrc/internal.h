@@ -244,6 +244,8 @@ struct DecodeParams {
     // Whether each key-value head has a block table and a length of its own: c.batch, c.table and c.lens then
     // count (sequence, head) pairs, head by head.
     bool per_head;
+    // 4-bit rows: whole sixteens of keys in a page, offsets in units of 16 bytes and of keys that 32 bits hold
+    bool by_sixteens;
     // key-value heads behind one row of the block table
     int seq_heads() const { return per_head ? 1 : c.hkv; }
 };

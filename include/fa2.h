@@ -462,9 +462,9 @@ fa2_status fa2_rope_backward(const void* dy, void* dx, const int32_t* positions,
  *              FA2_CACHE_E2M1: 4-bit floats (sign, 2 exponent bits, 1 fraction bit: 0, 0.5, 1,
  *              1.5, 2, 3, 4, 6), two a byte, the even element in the low four bits; a scale for
  *              each 16 elements of a row in k_scale, v_scale (8-bit floats, 4 exponent, 3
- *              fraction bits, [num_pages, n_kv_heads, page_size, head_dim / 16], contiguous,
- *              16-byte aligned), and a byte a row in k_exp, v_exp as above: an element stands
- *              for code * scale * 2^(byte - 127).  d = 128: 73 bytes a row, for 129 and 256.
+ *              fraction bits, [num_pages, n_kv_heads, page_size, head_dim / 16], contiguous),
+ *              and a byte a row in k_exp, v_exp as above; all four 16-byte aligned.  An element
+ *              stands for code * scale * 2^(byte - 127).  d = 128: 73 bytes a row, for 129 and 256.
  *              Strides count elements (two a byte).
  *   head_dim   a multiple of 8 (E4M3: 16, E2M1: 32) up to 128; page_size, n_kv_heads, num_pages > 0,
  *              n_kv_heads <= 1024, pages_per_seq * page_size <= 2^30 (FA2_ERR_UNSUPPORTED).

@@ -18,7 +18,7 @@ def lib():
 
 def cache4(**kw):
     """4-bit pages; strides count elements."""
-    return cache(**({"type": 2, "k_exp": 0x1001, "v_exp": 0x1001, "k_scale": 0x1000, "v_scale": 0x1000} | kw))
+    return cache(**({"type": 2, "k_exp": 0x1000, "v_exp": 0x1000, "k_scale": 0x1000, "v_scale": 0x1000} | kw))
 
 
 @pytest.mark.parametrize("call", [append, read, decode])
@@ -26,7 +26,7 @@ def cache4(**kw):
     ({"k_exp": None}, INVALID), ({"v_exp": None}, INVALID), ({"k_scale": None}, INVALID), ({"v_scale": None}, INVALID), ({"type": 3}, INVALID),
     ({"head_dim": 48}, UNSUPPORTED), ({"head_dim": 16}, UNSUPPORTED), ({"head_dim": 160, "slot_stride": 160, "head_stride": 2560, "page_stride": 10240},
                                                                        UNSUPPORTED),
-    ({"k_scale": 0x1008}, MISALIGNED), ({"v_scale": 0x1001}, MISALIGNED), ({"k": 0x1008}, MISALIGNED),
+    ({"k_exp": 0x1008}, MISALIGNED), ({"v_exp": 0x1001}, MISALIGNED), ({"k_scale": 0x1008}, MISALIGNED), ({"v_scale": 0x1001}, MISALIGNED), ({"k": 0x1008}, MISALIGNED),
     ({"slot_stride": 80, "head_stride": 16 * 80, "page_stride": 64 * 80}, MISALIGNED), ({"slot_stride": 32}, INVALID),
 ])
 def test_four_bit_cache_validation(lib, call, kw, want):

@@ -1387,7 +1387,10 @@ __global__ void __launch_bounds__(kJoinThreads) fa2_decode_join_kernel(const Dec
 // lengths themselves, in two launches. GB300, 8 heads of d = 128, bf16, two launches against one:
 // 1 sequence of 1000 8.5 / 6.7 us, of 2000 9.2 / 8.5; 30 of up to 200 11.0 / 8.8; 64 of up to 500
 // (8 blocks a warp) 23.4 / 21.5; past the limit 8 of up to 2000 13.0 / 15.2 (8 blocks a warp).
-template <typename C>
+//
+// With a table for each key-value head all rows are as a rule equally long (what fa2_select_pages gives), which the two
+// launches' division has nothing to add to: any number of CTAs that are resident at once, up to 16 blocks a warp.
+template <typename C, bool kPerHead>
 int cluster_ranks(const DecodeParams& p) {
     const int64_t keys = p.window > 0 && p.window + 15 < p.c.room ? p.window + 15 : p.c.room;
     const int64_t blocks = (keys + C::kKeys - 1) / C::kKeys;
@@ -1395,6 +1398,10 @@ int cluster_ranks(const DecodeParams& p) {
     const int64_t items = p.c.batch * p.seq_heads() * ((group + C::kRows - 1) / C::kRows);
     const int64_t resident = 152 * C::kShortPerSm;
     int ranks = 1;
+    if constexpr (kPerHead) {
+        ranks = (int)std::max<int64_t>(1, std::min<int64_t>({8, resident / items, (blocks + kWarps - 1) / kWarps}));
+        return blocks <= (int64_t)ranks * kWarps * 16 && items * ranks <= INT32_MAX ? ranks : 0;
+    }
     while (ranks < 8 && items * ranks * 2 <= resident && blocks > ranks * kWarps) ranks *= 2;
     const int64_t most = (int64_t)ranks * kWarps * (items > resident ? 8 : 4);
     return blocks <= most && items * ranks <= INT32_MAX ? ranks : 0;
@@ -1403,12 +1410,13 @@ int cluster_ranks(const DecodeParams& p) {
 template <int D, bool kBf16, int kForm, int kTiles, bool kPerHead>
 cudaError_t launch_d(const DecodeParams& p, cudaStream_t stream, int slot) {
     using C = Cfg<D, kForm, kTiles>;
-    int ranks = cluster_ranks<C>(p);
+    int ranks = cluster_ranks<C, kPerHead>(p);
     if (ranks) {
         auto kern = fa2_decode_kernel<D, kBf16, kForm, kTiles, kPerHead, true>;
         cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), C::kSmem, slot + 1);
         if (e != cudaSuccess) return e;
-        if (ranks == 1 || cluster_fits(reinterpret_cast<const void*>(kern), kThreads, C::kSmem, ranks, slot + 1)) {
+        const int ask = ranks <= 2 ? ranks : (ranks <= 4 ? 4 : 8);
+        if (ranks == 1 || cluster_fits(reinterpret_cast<const void*>(kern), kThreads, C::kSmem, ask, slot + 1)) {
             const int64_t items = p.c.batch * p.seq_heads() * ((p.heads / p.c.hkv + C::kRows - 1) / C::kRows);
             decode_record() = ranks;
             return launch_early_cluster(kern, dim3((unsigned)(items * ranks)), dim3(kThreads), C::kSmem, stream, (unsigned)ranks, p, ranks);

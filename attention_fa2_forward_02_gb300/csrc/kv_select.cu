@@ -204,7 +204,7 @@ cudaError_t launch_bounds_form(const KvBoundsParams& p, cudaStream_t stream) {
 // ---------------------------------------------------------------------------- scores
 
 constexpr uint32_t kForced = 0xffffffffu;  // above every score's key; a page outside the cache: 0, below every score's
-constexpr int kSets = 2;                   // times 16 pages a warp takes at once
+constexpr int kSets = 1;                   // times 16 pages a warp takes at once
 
 // Unsigned numbers in the order of the floats (no NaN).
 __device__ __forceinline__ uint32_t ordered(float x) {
@@ -488,7 +488,7 @@ cudaError_t launch_scores(const SelectParams& p, cudaStream_t stream) {
     const int padded = (p.group + 7) / 8 * 8;
     const size_t smem = (size_t)padded * (64 * kPieces + sizeof(float));  // 33 KB at most
     // As many CTAs for a sequence and head as fill the SMs kResident times over, at most one for each round of pages.
-    constexpr int kPages = kWarps * 16 * kSets, kResident = 4;
+    constexpr int kPages = kWarps * 16 * kSets, kResident = 6;
     const int64_t rows = p.batch * p.hkv, most = (p.per_seq + kPages - 1) / kPages;
     const int64_t row_ctas = std::max<int64_t>(1, std::min(most, (152 * kResident + rows - 1) / rows));
     return launch_early(page_scores_kernel<kBf16, kPieces>, dim3((unsigned)(rows * row_ctas)), dim3(kWarps * 32), smem, stream, p, (int)row_ctas);

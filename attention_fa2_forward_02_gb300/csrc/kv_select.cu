@@ -204,17 +204,19 @@ cudaError_t launch_bounds_form(const KvBoundsParams& p, cudaStream_t stream) {
 // ---------------------------------------------------------------------------- scores
 
 constexpr uint32_t kForced = 0xffffffffu;  // above every score's key; a page outside the cache: 0, below every score's
-constexpr int kSets = 1;                   // times 16 pages a warp takes at once
+constexpr int kSelWarps = 8, kSelThreads = kSelWarps * 32, kSelPerSm = 2;
+constexpr int kWideThreads = 1024;
+constexpr int kBins = 1024;
 
-// Unsigned numbers in the order of the floats (no NaN).
+// Unsigned numbers in the order of the floats (no NaN; -0 as 0).
 __device__ __forceinline__ uint32_t ordered(float x) {
-    const uint32_t b = __float_as_uint(x);
+    const uint32_t b = __float_as_uint(x + 0.f);
     return b ^ ((b >> 31) ? 0xffffffffu : 0x80000000u);
 }
 
-__device__ __forceinline__ void mma_s8(int (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm("mma.sync.aligned.m16n8k32.row.col.s32.s8.s8.s32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-        : "+r"(c[0]), "+r"(c[1]), "+r"(c[2]), "+r"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3]) : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
 // Pages that hold a length's keys.
@@ -224,130 +226,173 @@ __device__ __forceinline__ int pages_of(const SelectParams& p, int len) {
     return (int)((__umulhi(p.page_mul, last) + last) >> p.page_shift) + 1;  // as page_of
 }
 
-// The scores of pages of one sequence and key-value head, as products of 16 pages' bounds with 8 heads' integers: a row of
-// bounds is 2 d bytes, the lowest keys and then the highest, and meets the head's integers below zero and then those
-// above. Lane 4 g + t reads the 16-byte pieces t, t + 4, ... of the rows g and g + 8 straight into the left operand (a
-// product takes its 32 terms in any order, the right operand the same); kPieces of them. GB300, 16 sequences to 65536
-// in pages of 32, 8 heads of 8: 6 us with them, 39 with four-term dot products and sums over lanes.
-template <bool kBf16, int kPieces>
-__global__ void __launch_bounds__(kWarps * 32) page_scores_kernel(const SelectParams p, int row_ctas) {
-    constexpr int kRow = 64 * kPieces;  // bytes of a head's integers: [below zero][above], zeros behind 2 d
-    extern __shared__ __align__(16) uint8_t smem[];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int padded = (p.group + 7) / 8 * 8;
-    float* const two = reinterpret_cast<float*>(smem + (size_t)padded * kRow);  // 2^e a head
-    grid_begin();
-    const int row = blockIdx.x / row_ctas, cta = blockIdx.x % row_ctas, b = row / p.hkv, hk = row % p.hkv;
-    const int pages = pages_of(p, bounded_len(p.lens[b], p.per_seq * p.page_size, p.status));
-    if (pages <= p.budget || (int64_t)cta * kWarps * 16 * kSets >= pages) return;  // all are taken; nothing left for this CTA
-    // ---- the queries' integers: a warp a head, 4 channels a lane (d <= 128)
-    for (int h = warp; h < padded; h += kWarps) {
-        float x[4] = {}, a = 0.f;
-        if (h < p.group && 4 * lane < p.d) {
-            const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + b * p.q_batch +
-                                                            ((int64_t)hk * p.group + h) * p.q_head + 4 * lane);
-            const float2 f = floats<kBf16>(w.x), g = floats<kBf16>(w.y);
-            x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (x[i] != x[i]) x[i] = 0.f;
-            a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
-        }
-#pragma unroll
-        for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-        const int e = bound_exp(a);
-        const float inv = exp2_of(-e);
-        uint32_t up = 0, down = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int q = (int)fmaxf(fminf(rintf(x[i] * inv), 127.f), -127.f);
-            up |= (uint32_t)max(q, 0) << (8 * i);
-            down |= (uint32_t)(min(q, 0) & 0xff) << (8 * i);
-        }
-        uint32_t* ints = reinterpret_cast<uint32_t*>(smem + h * kRow);
-        if (4 * lane < p.d) {
-            ints[lane] = down;
-            ints[p.d / 4 + lane] = up;
-        }
-        for (int i = p.d / 2 + lane; i < kRow / 4; i += 32) ints[i] = 0;
-        if (lane == 0) two[h] = h < p.group ? exp2_of(e) : 0.f;
-    }
-    __syncthreads();
-    const int g = lane >> 2, t = lane & 3;
-    const int32_t* table = p.table + b * p.table_stride;
-    uint32_t* out = p.scores + (int64_t)row * p.per_seq;
-    const int64_t step = (int64_t)row_ctas * kWarps * 16 * kSets;
-    // lane r < 16 kSets looks page r of the warp's up
-    auto look = [&](int64_t j) { return lane < 16 * kSets && j + lane < pages ? table[j + lane] : -1; };
-    int64_t j0 = ((int64_t)cta * kWarps + warp) * 16 * kSets;
-    int next = look(j0);
-    for (; j0 < pages; j0 += step) {
-        int64_t at = next >= 0 && next < p.num_pages ? (int64_t)next * p.hkv + hk : -1;
-        const float scale = at >= 0 ? __uint_as_float((uint32_t)p.bounds_exp[at] << 23) : 0.f;
-        if (at < 0 && lane < 16 * kSets && j0 + lane < pages && p.status) atomicOr(p.status, kStatusBadIndex);
-        uint4 a[kSets][2][kPieces];
-#pragma unroll
-        for (int s = 0; s < kSets; ++s)
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                const int64_t here = __shfl_sync(0xffffffffu, at, 16 * s + 8 * r + g);
-                const int8_t* src = p.bounds + (here >= 0 ? here : 0) * 2 * p.d + 16 * t;
-#pragma unroll
-                for (int i = 0; i < kPieces; ++i) {
-                    a[s][r][i] = make_uint4(0, 0, 0, 0);
-                    if (here >= 0 && 64 * i + 16 * t < 2 * p.d) a[s][r][i] = *reinterpret_cast<const uint4*>(src + 64 * i);
-                }
+// The query's side of the scores of one sequence and key-value head, in shared memory: a head's integers as halves,
+// those below zero (which meet the lowest keys) and then those above, zeros behind 2 d; kPieces = ceil(d / 32).
+template <int kPieces>
+struct Queries {
+    static constexpr int kRow = 128 * kPieces + 16;  // bytes a head, 8 rows in different banks
+    static __host__ __device__ constexpr size_t bytes(int group) { return (size_t)((group + 7) / 8 * 8) * (kRow + sizeof(float2)); }
+    uint8_t* rows;
+    float2* stats;  // a head's -128 times the sum of its integers, and 2^e (0: no such head)
+    __device__ Queries(uint8_t* smem, int padded) : rows(smem), stats(reinterpret_cast<float2*>(smem + (size_t)padded * kRow)) {}
+
+    // A warp a head, 4 channels a lane (d <= 128); every thread of the CTA calls it.
+    template <bool kBf16>
+    __device__ __forceinline__ void make(const SelectParams& p, int b, int hk) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, padded = (p.group + 7) / 8 * 8;
+        for (int h = warp; h < padded; h += kSelWarps) {
+            float x[4] = {}, a = 0.f;
+            if (h < p.group && 4 * lane < p.d) {
+                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + b * p.q_batch +
+                                                                ((int64_t)hk * p.group + h) * p.q_head + 4 * lane);
+                const float2 f = floats<kBf16>(w.x), g = floats<kBf16>(w.y);
+                x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
             }
-        next = look(j0 + step);
-        float best[kSets][2];
 #pragma unroll
-        for (int s = 0; s < kSets; ++s) best[s][0] = best[s][1] = -INFINITY;
-        for (int h0 = 0; h0 < padded; h0 += 8) {
-            int c[kSets][4] = {};
+            for (int i = 0; i < 4; ++i) {
+                if (x[i] != x[i]) x[i] = 0.f;
+                a = fmaxf(a, fabsf(x[i]) < INFINITY ? fabsf(x[i]) : 0.f);
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
+            const int e = bound_exp(a);
+            const float inv = exp2_of(-e);
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                x[i] = fmaxf(fminf(rintf(x[i] * inv), 127.f), -127.f);
+                sum += x[i];
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            uint2* dst = reinterpret_cast<uint2*>(rows + (size_t)h * kRow);  // 4 halves each
+            if (4 * lane < p.d) {
+                dst[lane] = make_uint2(pack2<false>(fminf(x[0], 0.f), fminf(x[1], 0.f)), pack2<false>(fminf(x[2], 0.f), fminf(x[3], 0.f)));
+                dst[p.d / 4 + lane] = make_uint2(pack2<false>(fmaxf(x[0], 0.f), fmaxf(x[1], 0.f)), pack2<false>(fmaxf(x[2], 0.f), fmaxf(x[3], 0.f)));
+            }
+            for (int i = p.d / 2 + lane; i < 16 * kPieces; i += 32) dst[i] = make_uint2(0, 0);
+            if (lane == 0) stats[h] = make_float2(-128.f * sum, h < p.group ? exp2_of(e) : 0.f);
+        }
+        __syncthreads();
+    }
+};
+
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool on) {  // else zeros
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(on ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ uint4 load16(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+// Scores of pages tile * 16 .. of the sequence, tiles first, first + step, ...: put(page, key). The left operand's rows are
+// the bounds of 16 pages, the right one's columns 8 heads' integers. Lane 4 g + t takes the 16-byte pieces t, t + 4, ...
+// of the rows g and g + 8 (a product takes its terms in any order, both operands the same). A code plus 128, as a half's
+// bits, is that many times 2^-24: two instructions for two codes, and the products' sums, of no more than 22 bits, are
+// exact. (GB300, products a quarter of an SM can begin: one of 8-bit integers, 32 terms, every 63 cycles, one of halves,
+// 16 terms, every 8; sums of four products 2 cycles for a 512th of either's 8192.)
+// A page's number and its bounds follow one another from far away, 2 us and more: kDepth tiles are on their way or in
+// use a warp, the first ones while `meanwhile` runs. (In registers they would not fit, and a register that is spilled
+// waits for its load: 35 us for 42 MB that way.)
+constexpr int kDepth = 3;
+template <int kPieces, typename Meanwhile, typename Put>
+__device__ __forceinline__ void score_tiles(const SelectParams& p, const Queries<kPieces>& q, uint8_t* ring, const int32_t* table, int hk, int pages,
+                                            int first, int step, Meanwhile meanwhile, Put put) {
+    constexpr int kRow = 64 * kPieces, kFlip = kPieces % 2 == 0 ? 4 : 0;  // pieces of every other row change places: no bank twice
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t q_at = smem_u32(q.rows), my = smem_u32(ring) + (threadIdx.x >> 5) * (kDepth * 16 * kRow);
+    const int per_row = p.d / 8;  // pieces
+    auto look = [&](int64_t tile) { return lane < 16 && tile * 16 + lane < pages ? table[tile * 16 + lane] : -1; };
+    // a tile's copies, one group of them; lane r has page r's power of two, or -1
+    auto fetch = [&](int64_t tile, int page, uint32_t at) {
+        float scale = -1.f;
+        if (tile * 16 < pages) {
+            const int64_t row = page >= 0 && page < p.num_pages ? (int64_t)page * p.hkv + hk : -1;
+            if (row >= 0) scale = __uint_as_float((uint32_t)p.bounds_exp[row] << 23);
+#pragma unroll
+            for (int i = 0; i < 2 * kPieces; ++i) {  // 32 pieces at a time, row by row
+                const int n = 32 * i + lane, r = n / (4 * kPieces), piece = n % (4 * kPieces);
+                const int64_t here = __shfl_sync(0xffffffffu, row, r);
+                const bool on = here >= 0 && piece < per_row;
+                copy16(at + r * kRow + (piece ^ (r % 2 * kFlip)) * 16, p.bounds + (on ? here * 2 * p.d + 16 * piece : 0), on);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        return scale;
+    };
+    auto finish = [&](int64_t tile, uint32_t at, float scale) {
+        float best[2] = {-INFINITY, -INFINITY};
+        for (int h0 = 0; h0 < p.group; h0 += 8) {
+            float c[4] = {};
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
-                const uint4 q = *reinterpret_cast<const uint4*>(smem + (h0 + g) * kRow + 64 * i + 16 * t);
+                const uint32_t b = q_at + (uint32_t)(h0 + g) * Queries<kPieces>::kRow + 128 * i + 32 * t;
+                const uint4 b0 = load16(b), b1 = load16(b + 16);
+                const uint32_t a = at + g * kRow + ((4 * i + t) ^ (g % 2 * kFlip)) * 16;  // (g + 8 is as odd as g)
+                const uint4 u4 = load16(a), v4 = load16(a + 8 * kRow);
+                const uint32_t bs[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
+                const uint32_t u[4] = {u4.x, u4.y, u4.z, u4.w}, v[4] = {v4.x, v4.y, v4.z, v4.w};
 #pragma unroll
-                for (int s = 0; s < kSets; ++s) {
-                    mma_s8(c[s], a[s][0][i].x, a[s][1][i].x, a[s][0][i].y, a[s][1][i].y, q.x, q.y);
-                    mma_s8(c[s], a[s][0][i].z, a[s][1][i].z, a[s][0][i].w, a[s][1][i].w, q.z, q.w);
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t y = u[w] ^ 0x80808080u, z = v[w] ^ 0x80808080u;
+                    mma_f16(c, __byte_perm(y, 0, 0x4140), __byte_perm(z, 0, 0x4140), __byte_perm(y, 0, 0x4342), __byte_perm(z, 0, 0x4342), bs[2 * w],
+                            bs[2 * w + 1]);
                 }
             }
 #pragma unroll
             for (int n = 0; n < 2; ++n) {  // heads 2t, 2t+1
                 if (h0 + 2 * t + n >= p.group) continue;
-                const float f = two[h0 + 2 * t + n];
-#pragma unroll
-                for (int s = 0; s < kSets; ++s) {
-                    best[s][0] = fmaxf(best[s][0], (float)c[s][n] * f);
-                    best[s][1] = fmaxf(best[s][1], (float)c[s][2 + n] * f);
-                }
+                const float2 s = q.stats[h0 + 2 * t + n];
+                best[0] = fmaxf(best[0], fmaf(c[n], 0x1p24f, s.x) * s.y);
+                best[1] = fmaxf(best[1], fmaf(c[2 + n], 0x1p24f, s.x) * s.y);
             }
         }
-        // ---- lane r has page r's score
-        float mine = 0.f;
+        // lane r has page r's score
+        float score = 0.f;
 #pragma unroll
-        for (int s = 0; s < kSets; ++s)
+        for (int r = 0; r < 2; ++r) {
+            float y = best[r];
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 1));
+            y = fmaxf(y, __shfl_xor_sync(0xffffffffu, y, 2));
+            y = __shfl_sync(0xffffffffu, y, lane % 8 * 4);
+            if (lane / 8 == r) score = y;
+        }
+        const int64_t j = tile * 16 + lane;
+        if (lane < 16 && j < pages) {
+            if (scale < 0.f && p.status) atomicOr(p.status, kStatusBadIndex);
+            put((int)j, j < p.first || j >= pages - p.recent ? kForced : (scale >= 0.f ? ordered(score * scale) : 0u));
+        }
+    };
+    int64_t tile = first;
+    float scales[kDepth - 1];
+    int ahead[kDepth];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                float x = best[s][r];
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                x = __shfl_sync(0xffffffffu, x, lane % 8 * 4);
-                if (lane / 8 == 2 * s + r) mine = x;
-            }
-        const int64_t j = j0 + lane;
-        if (lane < 16 * kSets && j < pages)
-            out[j] = j < p.first || j >= pages - p.recent ? kForced : (at >= 0 ? ordered(mine * scale) : 0u);
+    for (int i = 0; i < kDepth; ++i) ahead[i] = look(tile + i * (int64_t)step);
+#pragma unroll
+    for (int i = 0; i < kDepth - 1; ++i) scales[i] = fetch(tile + i * (int64_t)step, ahead[i], my + i * 16 * kRow);
+    int next = ahead[kDepth - 1];
+    meanwhile();
+    int use = 0, fill = kDepth - 1;
+    for (; tile * 16 < pages; tile += step) {  // (no warp waits for another in here)
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
+        __syncwarp();  // the tile is there for all lanes, and the one before is done with
+        const float scale = scales[0];
+#pragma unroll
+        for (int i = 0; i + 1 < kDepth - 1; ++i) scales[i] = scales[i + 1];
+        scales[kDepth - 2] = fetch(tile + (kDepth - 1) * (int64_t)step, next, my + fill * 16 * kRow);
+        next = look(tile + kDepth * (int64_t)step);
+        finish(tile, my + use * 16 * kRow, scale);
+        use = use + 1 == kDepth ? 0 : use + 1;
+        fill = fill + 1 == kDepth ? 0 : fill + 1;
     }
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
 }
 
 // ---------------------------------------------------------------------------- selection
 
-constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32, kBins = 2 * kSelThreads;
-
 // Sums over the CTA of a thread's two counts, exclusive in thread order, and their totals.
+template <int kThreads>
 __device__ __forceinline__ uint2 scan2(uint2 v, uint2* sums, uint2* total) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     uint2 upto = v;
@@ -361,7 +406,7 @@ __device__ __forceinline__ uint2 scan2(uint2 v, uint2* sums, uint2* total) {
     __syncthreads();
     uint2 before = make_uint2(0, 0), all = before;
 #pragma unroll
-    for (int w = 0; w < kSelWarps; ++w) {
+    for (int w = 0; w < kThreads / 32; ++w) {
         if (w < warp) before.x += sums[w].x, before.y += sums[w].y;
         all.x += sums[w].x, all.y += sums[w].y;
     }
@@ -369,138 +414,223 @@ __device__ __forceinline__ uint2 scan2(uint2 v, uint2* sums, uint2* total) {
     return make_uint2(before.x + upto.x - v.x, before.y + upto.y - v.y);
 }
 
-// A CTA takes one sequence and head. Thread i has the scores of pages i per .. in registers, kHeld at most; more are read
-// again. The budget-th largest is found by counting into kBins equal parts of the range that holds it, three times at
-// the most (for 32 bits), mostly twice: the range begins as that of the scores there are.
-template <int kHeld>
-__global__ void __launch_bounds__(kSelThreads) select_kernel(const SelectParams p) {
-    __shared__ uint2 sums[kSelWarps];
-    __shared__ uint32_t bins[kBins];
-    __shared__ uint32_t found[3];
+struct SelectSmem {
+    uint2 sums[32];
+    uint32_t bins[kBins];
+    uint32_t found[3];
+    uint32_t few, list[32];
+};
+
+// All pages of row `row` (a sequence and head): there are no more than the budget.
+__device__ __forceinline__ void take_all(const SelectParams& p, int row, const int32_t* table, int n, int len) {
+    int32_t* dst = p.sel_table + (int64_t)row * p.budget;
+    for (int i = threadIdx.x; i < p.budget; i += blockDim.x) {
+        const int page = i < n ? table[i] : -1;
+        dst[i] = page;
+        if (i < n && (page < 0 || page >= p.num_pages) && p.status) atomicOr(p.status, kStatusBadIndex);
+    }
+    if (threadIdx.x == 0) p.sel_lens[row] = len;
+}
+
+// The budget of row `row` out of n > budget pages with keys key(0) .. key(n - 1). The budget-th largest is found by counting
+// into kBins equal parts of the range that holds it, three times at the most (for 32 bits), mostly twice: the range
+// begins as that of the scores there are.
+template <int kThreads, typename Key>
+__device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm, int row, const int32_t* table, int n, int len, Key key) {
     const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) found[0] = 0xffffffffu, found[1] = 0u, found[2] = 0u;
-    grid_begin();
-    const int b = blockIdx.x / p.hkv;
-    const int len = bounded_len(p.lens[b], p.per_seq * p.page_size, p.status);
-    const int n = pages_of(p, len);
-    const int32_t* table = p.table + b * p.table_stride;
-    int32_t* dst = p.sel_table + (int64_t)blockIdx.x * p.budget;
-    const int taken = min(n, p.budget);
-    for (int i = taken + threadIdx.x; i < p.budget; i += kSelThreads) dst[i] = -1;
-    if (n <= p.budget) {
-        for (int i = threadIdx.x; i < n; i += kSelThreads) {
-            const int page = table[i];
-            dst[i] = page;
-            if ((page < 0 || page >= p.num_pages) && p.status) atomicOr(p.status, kStatusBadIndex);
-        }
-        if (threadIdx.x == 0) p.sel_lens[blockIdx.x] = len;
-        return;
-    }
-    const uint32_t* scores = p.scores + (int64_t)blockIdx.x * p.per_seq;
-    const int per = (n + kSelThreads - 1) / kSelThreads;
-    const int i0 = (int)min((int64_t)threadIdx.x * per, (int64_t)n), mine = min(per, n - i0);
-    const bool held = per <= kHeld;
-    uint32_t key[kHeld];
-    if (held) {
-#pragma unroll
-        for (int i = 0; i < kHeld; ++i) {
-            if (i < mine) key[i] = scores[i0 + i];
-        }
-    }
-    auto each = [&](auto f) {
-        if (held) {
-#pragma unroll
-            for (int i = 0; i < kHeld; ++i) {
-                if (i < mine) f(i0 + i, key[i]);
-            }
-        } else {
-            for (int i = 0; i < mine; ++i) f(i0 + i, scores[i0 + i]);
-        }
-    };
     // ---- the range of the scores that are not forced, and how many to take of those
     uint32_t lo = 0xffffffffu, hi = 0, forced = 0;
-    each([&](int, uint32_t k) {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const uint32_t k = key(i);
         if (k == kForced) ++forced;
         else lo = min(lo, k), hi = max(hi, k);
-    });
+    }
+    if (threadIdx.x == 0) sm.found[0] = 0xffffffffu, sm.found[1] = 0u, sm.found[2] = 0u, sm.few = 0;
     lo = __reduce_min_sync(0xffffffffu, lo);
     hi = __reduce_max_sync(0xffffffffu, hi);
     forced = __reduce_add_sync(0xffffffffu, forced);
-    __syncthreads();  // found is set
+    __syncthreads();
     if (lane == 0) {
-        atomicMin(&found[0], lo);
-        atomicMax(&found[1], hi);
-        if (forced) atomicAdd(&found[2], forced);
+        atomicMin(&sm.found[0], lo);
+        atomicMax(&sm.found[1], hi);
+        if (forced) atomicAdd(&sm.found[2], forced);
     }
     __syncthreads();
-    lo = found[0], hi = found[1];
-    uint32_t need = (uint32_t)p.budget - found[2];
+    lo = sm.found[0], hi = sm.found[1];
+    uint32_t need = (uint32_t)p.budget - sm.found[2];
     uint32_t least = kForced - 1, equal = 0;  // all above `least` are taken and the earliest `equal` of those equal to it
     while (need) {
-        const uint32_t width = hi - lo;  // less one
-        const int shift = max(0, 32 - __clz(width) - 10);
-        bins[threadIdx.x] = bins[kSelThreads + threadIdx.x] = 0;
+        const int shift = max(0, 22 - __clz(hi - lo));  // (hi - lo) >> shift < kBins
+        for (int i = threadIdx.x; i < kBins; i += kThreads) sm.bins[i] = 0;
         __syncthreads();  // (found is read)
-        each([&](int, uint32_t k) {
-            if (k >= lo && k <= hi) atomicAdd(&bins[(k - lo) >> shift], 1u);
-        });
+        for (int i = threadIdx.x; i < n; i += kThreads) {
+            const uint32_t k = key(i);
+            if (k >= lo && k <= hi) atomicAdd(&sm.bins[(k - lo) >> shift], 1u);
+        }
         __syncthreads();
-        // thread i has the parts i and i + 1 from the top, in pairs
-        const int top = kBins - 1 - 2 * (int)threadIdx.x;
-        const uint32_t c0 = bins[top], c1 = bins[top - 1];
+        // thread i has kPer parts from the top
+        constexpr int kPer = kBins / kThreads;
+        const int top = kBins - 1 - kPer * (int)threadIdx.x;
+        uint32_t c[kPer], all = 0;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) all += c[i] = sm.bins[top - i];
         uint2 total;
-        const uint32_t above = scan2(make_uint2(c0 + c1, 0), sums, &total).x;
-        if (above < need && need <= above + c0 + c1) {
-            const bool second = need > above + c0;
-            found[0] = second ? top - 1 : top;
-            found[1] = second ? above + c0 : above;
-            found[2] = second ? c1 : c0;
+        uint32_t above = scan2<kThreads>(make_uint2(all, 0), sm.sums, &total).x;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) {
+            if (above < need && need <= above + c[i]) sm.found[0] = top - i, sm.found[1] = above, sm.found[2] = c[i];
+            above += c[i];
         }
         __syncthreads();
-        lo += found[0] << shift;
+        lo += sm.found[0] << shift;
         hi = min(hi, lo + ((1u << shift) - 1));
-        need -= found[1];
+        need -= sm.found[1];
         least = lo;
-        if (shift == 0 || need == found[2]) {
-            equal = shift == 0 ? need : 0xffffffffu;  // (with the whole part: its lowest and all above)
-            break;
-        }
-        if (lo == hi) {
+        if (shift == 0) {
             equal = need;
             break;
         }
+        if (need == sm.found[2]) {  // the whole part: its lowest and all above
+            equal = 0xffffffffu;
+            break;
+        }
+        const uint32_t left = sm.found[2];
+        if (left <= 32) {  // each warp ranks them
+            for (int i = threadIdx.x; i < n; i += kThreads) {
+                const uint32_t k = key(i);
+                if (k >= lo && k <= hi) sm.list[atomicAdd(&sm.few, 1u)] = k;
+            }
+            __syncthreads();
+            const uint32_t mine = lane < (int)left ? sm.list[lane] : 0u;
+            uint32_t above_it = 0, alike = 0;
+            for (uint32_t i = 0; i < left; ++i) above_it += sm.list[i] > mine, alike += sm.list[i] == mine;
+            const uint32_t who = __ballot_sync(0xffffffffu, lane < (int)left && above_it < need && need <= above_it + alike);
+            least = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
+            equal = need - __shfl_sync(0xffffffffu, above_it, __ffs(who) - 1);
+            break;
+        }
     }
-    // ---- in the order of their positions
+    // ---- in the order of their positions: thread i has pages i per ..
+    const int per = (n + kThreads - 1) / kThreads;
+    const int i0 = (int)min((int64_t)threadIdx.x * per, (int64_t)n), i1 = min(i0 + per, n);
     uint2 count = make_uint2(0, 0), total;
-    each([&](int, uint32_t k) { count.x += k > least, count.y += k == least; });
-    const uint2 before = scan2(count, sums, &total);
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t k = key(i);
+        count.x += k > least, count.y += k == least;
+    }
+    const uint2 before = scan2<kThreads>(count, sm.sums, &total);
     uint32_t at = before.x + min(before.y, equal), seen = before.y;
-    each([&](int i, uint32_t k) {
+    // first the pages' places, then, side by side, what the table has there
+    int32_t* dst = p.sel_table + (int64_t)row * p.budget;
+    const bool listed = p.budget <= kBins;
+    for (int i = i0; i < i1; ++i) {
+        const uint32_t k = key(i);
         const bool take = k > least || (k == least && seen < equal);
         seen += k == least;
-        if (take) dst[at++] = table[i];
-        if (i == n - 1) p.sel_lens[blockIdx.x] = p.budget * p.page_size - (take ? (int)((int64_t)n * p.page_size - len) : 0);
-    });
+        if (take) {
+            if (listed) sm.bins[at++] = i;
+            else dst[at++] = i;
+        }
+        if (i == n - 1) p.sel_lens[row] = p.budget * p.page_size - (take ? (int)((int64_t)n * p.page_size - len) : 0);
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < p.budget; i += kThreads) dst[i] = table[listed ? (int)sm.bins[i] : dst[i]];
+}
+
+constexpr size_t ring_bytes(int pieces) { return (size_t)kSelWarps * kDepth * 16 * 64 * pieces; }
+
+// The CTAs of a cluster of `ranks` share a sequence and head: all make scores, in the first one's shared memory, which selects.
+template <bool kBf16, int kPieces>
+__global__ void __launch_bounds__(kSelThreads, kSelPerSm) select_kernel(const SelectParams p, int ranks) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ SelectSmem sm;
+    const int padded = (p.group + 7) / 8 * 8, row = blockIdx.x / ranks, rank = blockIdx.x % ranks, b = row / p.hkv, hk = row % p.hkv;
+    Queries<kPieces> q(smem, padded);
+    uint8_t* const ring = smem + Queries<kPieces>::bytes(p.group);
+    uint32_t* scores = reinterpret_cast<uint32_t*>(ring + ring_bytes(kPieces));
+    grid_begin();
+    const int len = bounded_len(p.lens[b], p.per_seq * p.page_size, p.status), n = pages_of(p, len);
+    const int32_t* table = p.table + b * p.table_stride;
+    if (n <= p.budget) {  // of the whole cluster
+        if (rank == 0) take_all(p, row, table, n, len);
+        return;
+    }
+    const uint32_t to = cluster_map(smem_u32(scores), 0);
+    score_tiles<kPieces>(
+        p, q, ring, table, hk, n, rank * kSelWarps + (int)(threadIdx.x >> 5), ranks * kSelWarps, [&] { q.template make<kBf16>(p, b, hk); },
+        [&](int j, uint32_t key) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 4 * j), "r"(key) : "memory"); });
+    cluster_sync_all();
+    if (rank == 0) select_row<kSelThreads>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
+}
+
+// The same for tables too wide for that, in two launches through the workspace.
+template <bool kBf16, int kPieces>
+__global__ void __launch_bounds__(kSelThreads, kSelPerSm) wide_scores_kernel(const SelectParams p, int row_ctas) {
+    extern __shared__ __align__(16) uint8_t smem[];
+    const int padded = (p.group + 7) / 8 * 8, row = blockIdx.x / row_ctas, cta = blockIdx.x % row_ctas, b = row / p.hkv, hk = row % p.hkv;
+    Queries<kPieces> q(smem, padded);
+    grid_begin();
+    const int n = pages_of(p, bounded_len(p.lens[b], p.per_seq * p.page_size, p.status));
+    if (n <= p.budget || (int64_t)cta * kSelWarps * 16 >= n) return;
+    uint32_t* out = p.scores + (int64_t)row * p.per_seq;
+    score_tiles<kPieces>(
+        p, q, smem + Queries<kPieces>::bytes(p.group), p.table + b * p.table_stride, hk, n, cta * kSelWarps + (int)(threadIdx.x >> 5), row_ctas * kSelWarps,
+        [&] { q.template make<kBf16>(p, b, hk); }, [&](int j, uint32_t key) { out[j] = key; });
+}
+__global__ void __launch_bounds__(kWideThreads) wide_select_kernel(const SelectParams p) {
+    __shared__ SelectSmem sm;
+    const int row = blockIdx.x, b = row / p.hkv;
+    grid_begin();
+    const int len = bounded_len(p.lens[b], p.per_seq * p.page_size, p.status), n = pages_of(p, len);
+    const int32_t* table = p.table + b * p.table_stride;
+    if (n <= p.budget) return take_all(p, row, table, n, len);
+    const uint32_t* scores = p.scores + (int64_t)row * p.per_seq;
+    select_row<kWideThreads>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
+}
+// Tables no wider than the budget: every page is taken, without a look at the bounds.
+__global__ void __launch_bounds__(kSelThreads) take_all_kernel(const SelectParams p) {
+    const int row = blockIdx.x, b = row / p.hkv;
+    grid_begin();
+    const int len = bounded_len(p.lens[b], p.per_seq * p.page_size, p.status);
+    take_all(p, row, p.table + b * p.table_stride, pages_of(p, len), len);
 }
 
 template <bool kBf16, int kPieces>
-cudaError_t launch_scores(const SelectParams& p, cudaStream_t stream) {
-    const int padded = (p.group + 7) / 8 * 8;
-    const size_t smem = (size_t)padded * (64 * kPieces + sizeof(float));  // 33 KB at most
-    // As many CTAs for a sequence and head as fill the SMs kResident times over, at most one for each round of pages.
-    constexpr int kPages = kWarps * 16 * kSets, kResident = 6;
-    const int64_t rows = p.batch * p.hkv, most = (p.per_seq + kPages - 1) / kPages;
-    const int64_t row_ctas = std::max<int64_t>(1, std::min(most, (152 * kResident + rows - 1) / rows));
-    return launch_early(page_scores_kernel<kBf16, kPieces>, dim3((unsigned)(rows * row_ctas)), dim3(kWarps * 32), smem, stream, p, (int)row_ctas);
+cudaError_t launch_pieces(const SelectParams& p, cudaStream_t stream) {
+    const int64_t rows = p.batch * p.hkv, tiles = (p.per_seq + 15) / 16, resident = 152 * kSelPerSm;
+    const size_t q_bytes = Queries<kPieces>::bytes(p.group);  // 68 KB at most
+    // One launch while a warp has no more than kRounds tiles (by the table's width: the lengths are on the device) and the
+    // scores fit beside the queries.
+    constexpr int kRounds = 8, kMostPages = 12 * 1024;
+    const int64_t most = (tiles + kSelWarps - 1) / kSelWarps;
+    const int ranks = (int)std::max<int64_t>(1, std::min<int64_t>({8, resident / rows, most}));
+    const int slot = 208 + 4 * kBf16 + kPieces - 1;
+    if (tiles <= (int64_t)ranks * kSelWarps * kRounds && p.per_seq <= kMostPages && rows * ranks <= INT32_MAX) {
+        auto kern = select_kernel<kBf16, kPieces>;
+        constexpr int kSmem = 217 * 1024;  // 68 + 96 + 48 KB at most
+        cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), kSmem, slot);
+        if (e != cudaSuccess) return e;
+        const size_t smem = q_bytes + ring_bytes(kPieces) + (size_t)p.per_seq * sizeof(uint32_t);
+        const int ask = ranks <= 2 ? ranks : (ranks <= 4 ? 4 : 8);
+        if (ranks == 1 || cluster_fits(reinterpret_cast<const void*>(kern), kSelThreads, kSmem, ask, slot))
+            return launch_early_cluster(kern, dim3((unsigned)(rows * ranks)), dim3(kSelThreads), smem, stream, (unsigned)ranks, p, ranks);
+    }
+    auto kern = wide_scores_kernel<kBf16, kPieces>;
+    cudaError_t e = ensure_smem_limit(reinterpret_cast<const void*>(kern), 168 * 1024, slot + 8);
+    if (e != cudaSuccess) return e;
+    const int64_t row_ctas = std::max<int64_t>(1, std::min(most, resident / rows));
+    e = launch_early(kern, dim3((unsigned)(rows * row_ctas)), dim3(kSelThreads), q_bytes + ring_bytes(kPieces), stream, p, (int)row_ctas);
+    if (e != cudaSuccess) return e;
+    return launch_early(wide_select_kernel, dim3((unsigned)rows), dim3(kWideThreads), 0, stream, p);
 }
 
 template <bool kBf16>
-cudaError_t launch_scores_type(const SelectParams& p, cudaStream_t stream) {
+cudaError_t launch_select_type(const SelectParams& p, cudaStream_t stream) {
     switch ((p.d + 31) / 32) {
-        case 1: return launch_scores<kBf16, 1>(p, stream);
-        case 2: return launch_scores<kBf16, 2>(p, stream);
-        case 3: return launch_scores<kBf16, 3>(p, stream);
-        default: return launch_scores<kBf16, 4>(p, stream);
+        case 1: return launch_pieces<kBf16, 1>(p, stream);
+        case 2: return launch_pieces<kBf16, 2>(p, stream);
+        case 3: return launch_pieces<kBf16, 3>(p, stream);
+        default: return launch_pieces<kBf16, 4>(p, stream);
     }
 }
 
@@ -516,13 +646,8 @@ cudaError_t launch_kv_bounds(const KvBoundsParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_select_pages(const SelectParams& p, cudaStream_t stream) {
-    if (p.per_seq > p.budget) {  // else every page is taken, without a look at the bounds
-        const cudaError_t e = p.dtype == kBf16 ? launch_scores_type<true>(p, stream) : launch_scores_type<false>(p, stream);
-        if (e != cudaSuccess) return e;
-    }
-    // (by the table's width: the lengths are on the device)
-    auto kern = p.per_seq <= 4 * kSelThreads ? select_kernel<4> : select_kernel<16>;
-    return launch_early(kern, dim3((unsigned)(p.batch * p.hkv)), dim3(kSelThreads), 0, stream, p);
+    if (p.per_seq <= p.budget) return launch_early(take_all_kernel, dim3((unsigned)(p.batch * p.hkv)), dim3(kSelThreads), 0, stream, p);
+    return p.dtype == kBf16 ? launch_select_type<true>(p, stream) : launch_select_type<false>(p, stream);
 }
 
 }  // namespace fa2

@@ -264,6 +264,26 @@ def test_extreme_queries_and_bounds():
         S.page_score = exact
 
 
+@pytest.mark.parametrize("d", [128, 96, 40])
+def test_the_largest_sums_are_exact(d):
+    """Integers of 125 to 127 on both sides, all signs alike or nearly so: sums up to 2^21 that differ by little."""
+    torch = G.require_gpu()
+    c = Cache("sel/sums", [4000, 3999], 8, 2, d)
+    raw = synth.counter_u16(f"sel/sums/{d}", (c.pages, 2, 2, d)).astype(np.int64)
+    codes = np.where(np.arange(2)[:, None] == 1, 127 - raw % 3, 125 - raw % 3)
+    codes[::2] = -codes[::2, :, ::-1]
+    byte = np.full((c.pages, 2), 127, dtype=np.uint8)
+    ints = 127.0 - synth.counter_u16(f"sel/sums/q{d}", (2, 6, d)) % 3
+    ints[:, :, 0] = 127.0
+    ints[0, ::2] *= -1
+    ints[1, 1, ::7] *= -1
+    x = synth.to_storage(ints, "bf16")
+    for budget in (5, 100, 499):
+        table, lens = select(c, G.to_device(x, "bf16"), torch.from_numpy(codes.astype(np.int8)).cuda(), torch.from_numpy(byte).cuda(), budget, 0, 1)
+        check_selection(c, synth.widen(x, "bf16"), codes, byte, table, lens, budget, 0, 1)
+    binding.fa2_device_status()
+
+
 def test_bad_pages_come_last():
     torch = G.require_gpu()
     c = Cache("sel/bad", [320, 64], 16, 2, 32)

@@ -16,7 +16,7 @@
 // by it lies at the bottom of their range. It does not depend on how sines round.
 //
 // The 4-bit form: x 2^-e < 2^10 (turned: 2^10 sqrt(2) < 448 * 6), 16 elements' scale is max / 6 as an 8-bit float,
-// codes are x 2^-e / scale. Both quotients are rounded exactly: with r = 1 / s to nearest, q = x r, the remainder
+// codes are x 2^-e / scale, the scales' reciprocals a table. Both quotients are rounded exactly: with r = 1 / s to nearest, q = x r, the remainder
 // x - q s is exact in one fused step and q + r (x - q s) is x / s to nearest (P. W. Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", IBM J. Res. Dev. 34, 1990), which keeps every
 // tie between two codes a tie.
@@ -38,18 +38,41 @@ __device__ __forceinline__ float2 widen2(uint32_t w) {
     else return __half22float2(*reinterpret_cast<__half2*>(&w));
 }
 
-// The largest finite magnitude of a row of 16-bit floats, a lane's 16 of them in `w`; kLanes lanes hold the row,
-// every lane of the warp calls it.
+// Two float32 products, or fused products and sums, in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 w, {%6, %7};\n\tfma.rn.f32x2 z, x, y, w;\n\t"
+        "mov.b64 {%0, %1}, z;\n\t}"
+        : "=f"(r.x), "=f"(r.y) : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+
+// The larger magnitudes of the even and of the odd elements of 8 16-bit floats: their bits are ordered as they are.
+__device__ __forceinline__ uint32_t pack_max(const uint4& w) {
+    const uint32_t k = 0x7fff7fffu;
+    return __vmaxu2(__vmaxu2(w.x & k, w.y & k), __vmaxu2(w.z & k, w.w & k));
+}
+template <bool kBf16>
+__device__ __forceinline__ float magnitude_of(uint32_t bits) {
+    return kBf16 ? __uint_as_float(bits << 16) : __half2float(__ushort_as_half((unsigned short)bits));
+}
+
+// The largest finite magnitude of a row, a lane's 16 elements in `in`, `m` their pack_max; kLanes lanes hold the row, every lane
+// of the warp calls it.
 template <bool kBf16, int kLanes>
-__device__ __forceinline__ float row_max(const uint32_t (&w)[8]) {
+__device__ __forceinline__ float row_max(const uint4 (&in)[2], uint32_t m) {
     constexpr uint32_t kInf = kBf16 ? 0x7f80u : 0x7c00u;
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) m = __vmaxu2(m, w[j] & 0x7fff7fffu);
 #pragma unroll
     for (int off = kLanes / 2; off > 0; off >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, off));
     m = max(m & 0xffffu, m >> 16);
     if (__any_sync(0xffffffffu, m >= kInf)) {  // rare: look again without infinities and NaN
+        const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
         m = 0;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -59,7 +82,7 @@ __device__ __forceinline__ float row_max(const uint32_t (&w)[8]) {
 #pragma unroll
         for (int off = kLanes / 2; off > 0; off >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, off));
     }
-    return kBf16 ? __uint_as_float(m << 16) : __half2float(__ushort_as_half((unsigned short)m));
+    return magnitude_of<kBf16>(m);
 }
 
 // e of a row's power of two 2^e for its largest magnitude a before any rotation, `more` for what that can add.
@@ -74,6 +97,7 @@ __device__ __forceinline__ int row_exp(float a, int more) {
     }
     return min(e + more, kMaxExp);
 }
+__device__ __forceinline__ float exp2_of(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }  // -126 <= e <= 127
 
 __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {  // nearest even; beyond 448: 448; NaN stays
     uint16_t r;
@@ -82,11 +106,11 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float lo, float hi) {  // nearest 
 }
 
 // Eight e2m1 codes, nearest even, beyond 6: 6.
-__device__ __forceinline__ uint32_t to_e2m1x8(const float (&x)[8]) {
+__device__ __forceinline__ uint32_t to_e2m1x8(const float2 (&x)[4]) {
     uint32_t r;
     asm("{\n\t.reg .b8 a, b, c, d;\n\tcvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
         "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\tmov.b32 %0, {a, b, c, d};\n\t}"
-        : "=r"(r) : "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]));
+        : "=r"(r) : "f"(x[0].x), "f"(x[0].y), "f"(x[1].x), "f"(x[1].y), "f"(x[2].x), "f"(x[2].y), "f"(x[3].x), "f"(x[3].y));
     return r;
 }
 
@@ -97,32 +121,36 @@ __device__ __forceinline__ float divide(float x, float s, float r) {
 }
 
 // The largest of 8 magnitudes, as bits: NaN above infinity above the finite ones.
-__device__ __forceinline__ uint32_t max_bits(const float (&x)[8]) {
+__device__ __forceinline__ uint32_t max_bits(const float2 (&x)[4]) {
     uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = max(m, __float_as_uint(x[i]) & 0x7fffffffu);
+    for (int i = 0; i < 4; ++i) m = max(m, max(__float_as_uint(x[i].x) & 0x7fffffffu, __float_as_uint(x[i].y) & 0x7fffffffu));
     return m;
 }
 
-// The scale byte of 16 elements x 2^-e whose largest magnitude has these bits.
-__device__ __forceinline__ uint32_t group_scale(uint32_t bits) {
+// The scale byte of 16 elements whose largest magnitude has these bits, at a row's power of two 2^-e = inv.
+__device__ __forceinline__ uint32_t group_scale(uint32_t bits, float inv) {
     if (bits > 0x7f800000u) return 0x7fu;   // a NaN
     if (bits == 0x7f800000u) return 0x7eu;  // an infinity: 448
-    return to_e4m3x2(divide(__uint_as_float(bits), 6.f, 1.f / 6.f), 0.f) & 0xffu;
+    return to_e4m3x2(divide(__uint_as_float(bits) * inv, 6.f, 1.f / 6.f), 0.f) & 0xffu;
 }
 
-// The codes of 8 elements x 2^-e at a scale byte of group_scale.
-__device__ __forceinline__ uint32_t group_codes(const float (&x)[8], uint32_t scale) {
-    const uint32_t h = e4m3x2_to_f16x2(scale);
-    const float s = __half2float(__ushort_as_half((unsigned short)h));
-    const float r = s > 0.f ? __frcp_rn(s) : 0.f;
-    float y[8];
+// The codes of 8 elements at a scale byte of group_scale and a row's power of two; `reciprocal[i]`: what scale byte i stands for, and
+// 1 over that (0 for 0). The powers of two go with the scale: x / (s 2^e), exactly x 2^-e / s.
+__device__ __forceinline__ uint32_t group_codes(const float2 (&x)[4], uint32_t scale, float two, float inv, const float2* reciprocal) {
+    const float2 f = reciprocal[scale];
+    const float s = f.x * two, r = f.y * inv;
+    float2 y[4];
     if (scale < 0x7eu) {
+        const float2 r2 = make_float2(r, r), s2 = make_float2(-s, -s);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = divide(x[i], s, r);
+        for (int i = 0; i < 4; ++i) {  // divide, two at a time
+            const float2 q = mul2(x[i], r2);
+            y[i] = fma2(fma2(q, s2, x[i]), r2, q);
+        }
     } else {  // an infinity's remainder is none
 #pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] = __fdiv_rn(x[i], s);
+        for (int i = 0; i < 4; ++i) y[i] = make_float2(__fdiv_rn(x[i].x * inv, f.x), __fdiv_rn(x[i].y * inv, f.x));
     }
     return to_e2m1x8(y);
 }
@@ -138,13 +166,17 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rope_append_kernel(const 
     const PagedParams& c = p.rows.c;
     constexpr int kGroups = 32 / kLanes;
     __shared__ uint64_t turns[64];
+    __shared__ float2 reciprocal[kForm == kRowsE2m1 ? 128 : 1];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t t0 = ((int64_t)blockIdx.x * kWarps + warp) * kTok;
-    grid_begin();
-    if (p.rot) {
-        for (int i = threadIdx.x; i < p.rot / 2; i += kWarps * 32) turns[i] = turns_of(p.inv_freq[i]);
-        __syncthreads();
+    if constexpr (kForm == kRowsE2m1) {
+        const float s = __half2float(__ushort_as_half((unsigned short)e4m3x2_to_f16x2(threadIdx.x & 127)));
+        reciprocal[threadIdx.x & 127] = make_float2(s, s > 0.f ? __frcp_rn(s) : 0.f);
     }
+    grid_begin();
+    if (p.rot)
+        for (int i = threadIdx.x; i < p.rot / 2; i += kWarps * 32) turns[i] = turns_of(p.inv_freq[i]);
+    __syncthreads();
     if (t0 >= p.rows.tokens) return;
     Spot found{-1, -1, -1};
     {
@@ -165,11 +197,12 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rope_append_kernel(const 
     const int i0 = halves ? 8 * li : 16 * li, i1 = halves ? p.rot / 2 + 8 * li : 16 * li + 8;
     const bool on0 = i0 < c.d, on1 = i1 < c.d;
     // 4 bits: the lane and the pack that hold the other 8 of the 16 elements around each pack
+    const bool apart = !kInterleaved && p.rot;  // (else the lane itself)
     auto holder = [&](int pack, int* second) {  // of elements 8 pack ..
-        const int k = kInterleaved ? 0 : p.rot / 16;
-        const bool apart = pack < 2 * k;
-        *second = apart ? pack >= k : pack & 1;
-        return lane - li + (apart ? (pack < k ? pack : pack - k) : pack / 2);
+        const int k = apart ? p.rot / 16 : 0;
+        const bool half = pack < 2 * k;
+        *second = half ? pack >= k : pack & 1;
+        return lane - li + (half ? (pack < k ? pack : pack - k) : pack / 2);
     };
     int second0 = 0, second1 = 0, from0 = 0, from1 = 0;
     if constexpr (kForm == kRowsE2m1) {
@@ -186,7 +219,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rope_append_kernel(const 
         const int64_t exp_off = kForm != kRows16 ? __shfl_sync(0xffffffffu, found.exp_off, n) : 0;
         if (pos < 0) continue;
         const int64_t t = t0 + n;
-        float cs[8], sn[8];
+        float2 cs[4], sn[4], ns[4];  // of pairs 2 i, 2 i + 1; ns = -sn
         if (p.rot) {
             // the groups of lanes need the same 8 a lane: each makes some of them
             constexpr int kOwn = kGroups < 8 ? 8 / kGroups : 1;
@@ -201,31 +234,49 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rope_append_kernel(const 
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                sn[i] = __shfl_sync(0xffffffffu, s[i % kOwn], i / kOwn * kLanes + li);
-                cs[i] = __shfl_sync(0xffffffffu, c8[i % kOwn], i / kOwn * kLanes + li);
+                (i % 2 ? sn[i / 2].y : sn[i / 2].x) = __shfl_sync(0xffffffffu, s[i % kOwn], i / kOwn * kLanes + li);
+                (i % 2 ? cs[i / 2].y : cs[i / 2].x) = __shfl_sync(0xffffffffu, c8[i % kOwn], i / kOwn * kLanes + li);
             }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ns[i] = make_float2(-sn[i].x, -sn[i].y);
         }
-        // a lane's 16 elements, turned: x[0 .. 7] of the first pack, x[8 .. 15] of the second
-        auto turn = [&](const uint4 (&in)[2], float (&x)[2][8], bool turns_row) {
+        // a lane's 16 elements as pairs: `one` the first and `two` the second elements of pairs 2 i, 2 i + 1. Half layout: the
+        // elements of the first pack, of the second; interleaved: the even ones, the odd ones.
+        auto unpack = [&](const uint4 (&in)[2], float2 (&one)[4], float2 (&two)[4]) {
             const uint32_t w[8] = {in[0].x, in[0].y, in[0].z, in[0].w, in[1].x, in[1].y, in[1].z, in[1].w};
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const float2 f = widen2<kBf16>(w[j]);
-                x[j / 4][2 * (j % 4)] = f.x;
-                x[j / 4][2 * (j % 4) + 1] = f.y;
-            }
-            if (!turns_row || !turned) return;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                // as in fa2_rope: a product, then a fused one
-                float &one = kInterleaved ? x[i / 4][2 * (i % 4)] : x[0][i], &two = kInterleaved ? x[i / 4][2 * (i % 4) + 1] : x[1][i];
-                const float a = one, b = two;
-                one = a * cs[i] - b * sn[i];
-                two = b * cs[i] + a * sn[i];
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = widen2<kBf16>(kInterleaved ? w[2 * i] : w[i]), g = widen2<kBf16>(kInterleaved ? w[2 * i + 1] : w[4 + i]);
+                one[i] = kInterleaved ? make_float2(f.x, g.x) : f;
+                two[i] = kInterleaved ? make_float2(f.y, g.y) : g;
             }
         };
-        auto packed = [&](const float (&x)[8]) {
-            return make_uint4(pack2<kBf16>(x[0], x[1]), pack2<kBf16>(x[2], x[3]), pack2<kBf16>(x[4], x[5]), pack2<kBf16>(x[6], x[7]));
+        auto turn = [&](float2 (&one)[4], float2 (&two)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 a = one[i], b = two[i];
+                one[i] = fma2(a, cs[i], mul2(b, ns[i]));
+                two[i] = fma2(b, cs[i], mul2(a, sn[i]));
+            }
+        };
+        // the first (k = 0) or second pack's elements in order
+        auto pack = [&](const float2 (&one)[4], const float2 (&two)[4], int k, float2 (&x)[4]) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int j = 2 * k + i / 2;
+                if constexpr (kInterleaved) x[i] = i % 2 ? make_float2(one[j].y, two[j].y) : make_float2(one[j].x, two[j].x);
+                else x[i] = k ? two[i] : one[i];
+            }
+        };
+        auto turn_words = [&](uint4 (&in)[2]) {
+            float2 one[4], two[4], x[4];
+            unpack(in, one, two);
+            turn(one, two);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                pack(one, two, k, x);
+                in[k] = make_uint4(pack2<kBf16>(x[0].x, x[0].y), pack2<kBf16>(x[1].x, x[1].y), pack2<kBf16>(x[2].x, x[2].y), pack2<kBf16>(x[3].x, x[3].y));
+            }
         };
         // ---- queries
         for (int r0 = begin + gr; r0 - gr < min(stop, q_slots); r0 += kGroups * kRows) {
@@ -243,12 +294,7 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rope_append_kernel(const 
                 const int r = r0 + i * kGroups;
                 if (r >= p.heads || r >= stop) continue;
                 char* dst = p.q_out + t * p.qos[0] + r * p.qos[1];
-                if (turned) {
-                    float x[2][8];
-                    turn(in[i], x, true);
-                    in[i][0] = packed(x[0]);
-                    in[i][1] = packed(x[1]);
-                }
+                if (turned) turn_words(in[i]);
                 if (on0) *reinterpret_cast<uint4*>(dst + 2 * i0) = in[i][0];
                 if (on1) *reinterpret_cast<uint4*>(dst + 2 * i1) = in[i][1];
             }
@@ -270,30 +316,27 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rope_append_kernel(const 
 #pragma unroll
             for (int i = 0; i < kRows; ++i) {
                 const int r = r0 + i * kGroups, h = r >= c.hkv ? r - c.hkv : r;
-                const bool there = r < stop - q_slots, v = r >= c.hkv;
+                const bool there = r < stop - q_slots, v = r >= c.hkv, turns = turned && !v;
                 char* dst = (v ? c.v : c.k) + cache_off + h * c.head_stride;
                 if constexpr (kForm == kRows16) {
                     if (!there) continue;
-                    if (turned && !v) {
-                        float x[2][8];
-                        turn(in[i], x, true);
-                        in[i][0] = packed(x[0]);
-                        in[i][1] = packed(x[1]);
-                    }
+                    if (turns) turn_words(in[i]);
                     if (on0) *reinterpret_cast<uint4*>(dst + 2 * i0) = in[i][0];
                     if (on1) *reinterpret_cast<uint4*>(dst + 2 * i1) = in[i][1];
                 } else {
-                    const uint32_t w[8] = {in[i][0].x, in[i][0].y, in[i][0].z, in[i][0].w,
-                                           in[i][1].x, in[i][1].y, in[i][1].z, in[i][1].w};
-                    const bool turns_row = !v && p.rot > 0;
-                    const int e = row_exp<kForm>(row_max<kBf16, kLanes>(w), turns_row ? p.grow + (kForm == kRowsE4m3) : 0);
-                    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e
-                    float x[2][8];
-                    turn(in[i], x, !v);
+                    const uint32_t p0 = pack_max(in[i][0]), p1 = pack_max(in[i][1]);
+                    const int e = row_exp<kForm>(row_max<kBf16, kLanes>(in[i], __vmaxu2(p0, p1)),
+                                                 !v && p.rot ? p.grow + (kForm == kRowsE4m3) : 0);
+                    const float inv = exp2_of(-e);
+                    float2 one[4], two[4], x[2][4];
+                    unpack(in[i], one, two);
+                    if (turns) turn(one, two);
+                    if constexpr (kForm == kRowsE4m3) {
 #pragma unroll
-                    for (int k = 0; k < 2; ++k)
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) x[k][j] *= inv;
+                        for (int j = 0; j < 4; ++j) one[j] = mul2(one[j], make_float2(inv, inv)), two[j] = mul2(two[j], make_float2(inv, inv));
+                    }
+                    pack(one, two, 0, x[0]);
+                    pack(one, two, 1, x[1]);
                     const int64_t byte = exp_off + (int64_t)h * c.page_size;
                     if (there && li == 0) (v ? c.v_exp : c.k_exp)[byte] = (uint8_t)(e + 127);
                     if constexpr (kForm == kRowsE4m3) {
@@ -302,21 +345,35 @@ __global__ void __launch_bounds__(kWarps * 32, kPerSm) rope_append_kernel(const 
                         for (int k = 0; k < 2; ++k)
                             if (k ? on1 : on0)
                                 *reinterpret_cast<uint2*>(dst + (k ? i1 : i0)) =
-                                    make_uint2(to_e4m3x2(x[k][0], x[k][1]) | to_e4m3x2(x[k][2], x[k][3]) << 16,
-                                               to_e4m3x2(x[k][4], x[k][5]) | to_e4m3x2(x[k][6], x[k][7]) << 16);
+                                    make_uint2(to_e4m3x2(x[k][0].x, x[k][0].y) | to_e4m3x2(x[k][1].x, x[k][1].y) << 16,
+                                               to_e4m3x2(x[k][2].x, x[k][2].y) | to_e4m3x2(x[k][3].x, x[k][3].y) << 16);
                     } else {
-                        const uint32_t m0 = max_bits(x[0]), m1 = max_bits(x[1]);
-                        const uint32_t a0 = __shfl_sync(0xffffffffu, m0, from0), b0 = __shfl_sync(0xffffffffu, m1, from0);
-                        const uint32_t a1 = __shfl_sync(0xffffffffu, m0, from1), b1 = __shfl_sync(0xffffffffu, m1, from1);
-                        const uint32_t s[2] = {group_scale(max(m0, second0 ? b0 : a0)), group_scale(max(m1, second1 ? b1 : a1))};
+                        uint32_t m0, m1;
+                        if (turns) {
+                            m0 = max_bits(x[0]);
+                            m1 = max_bits(x[1]);
+                        } else {
+                            m0 = __float_as_uint(magnitude_of<kBf16>(max(p0 & 0xffffu, p0 >> 16)));
+                            m1 = __float_as_uint(magnitude_of<kBf16>(max(p1 & 0xffffu, p1 >> 16)));
+                        }
+                        if (apart) {  // of the whole call
+                            const uint32_t a0 = __shfl_sync(0xffffffffu, m0, from0), b0 = __shfl_sync(0xffffffffu, m1, from0);
+                            const uint32_t a1 = __shfl_sync(0xffffffffu, m0, from1), b1 = __shfl_sync(0xffffffffu, m1, from1);
+                            m0 = max(m0, second0 ? b0 : a0);
+                            m1 = max(m1, second1 ? b1 : a1);
+                        } else {
+                            m0 = m1 = max(m0, m1);
+                        }
                         if (!there) continue;
+                        const uint32_t s0 = group_scale(m0, inv), s1 = apart ? group_scale(m1, inv) : s0;
                         uint8_t* scales = (v ? c.v_scale : c.k_scale) + byte * (c.d / 16);
+                        const float power = exp2_of(e);
 #pragma unroll
                         for (int k = 0; k < 2; ++k) {
                             const int at = k ? i1 : i0;
                             if (!(k ? on1 : on0)) continue;
-                            *reinterpret_cast<uint32_t*>(dst + at / 2) = group_codes(x[k], s[k]);
-                            if (at % 16 == 0) scales[at / 16] = (uint8_t)s[k];
+                            *reinterpret_cast<uint32_t*>(dst + at / 2) = group_codes(x[k], k ? s1 : s0, power, inv, reciprocal);
+                            if (at % 16 == 0) scales[at / 16] = (uint8_t)(k ? s1 : s0);
                         }
                     }
                 }

@@ -36,7 +36,7 @@ EncodeTiledFn encode_fn() {
 }
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSlots = 224;
+constexpr int kMaxSlots = 288;
 std::mutex g_mu;
 unsigned int* g_status_ptr[kMaxDevices] = {};
 std::atomic<uint64_t> g_smem_done[kMaxSlots];

@@ -16,9 +16,9 @@ size_t decode_workspace_bytes(int heads, int hkv, int d) {
 cudaError_t launch_decode(const DecodeParams& p, cudaStream_t stream) {
     if (p.c.form == kRowsE2m1) {
         switch (pad_head_dim(p.c.d)) {
-            case 32: return launch_decode_e2m1_d32(p, stream);
-            case 64: return launch_decode_e2m1_d64(p, stream);
-            default: return launch_decode_e2m1_d128(p, stream);
+            case 32: return p.per_head ? launch_selected_e2m1_d32(p, stream) : launch_decode_e2m1_d32(p, stream);
+            case 64: return p.per_head ? launch_selected_e2m1_d64(p, stream) : launch_decode_e2m1_d64(p, stream);
+            default: return p.per_head ? launch_selected_e2m1_d128(p, stream) : launch_decode_e2m1_d128(p, stream);
         }
     }
     switch (pad_head_dim(p.c.d)) {

@@ -53,7 +53,8 @@ constexpr float kNoScore = -3.402823466e38f;  // a maximum of no scores, from wh
 // D: the head size's kernel; kForm: the cache's type (CacheForm); kTiles: query heads per item / 8.
 template <int D, int kForm, int kTiles>
 struct Cfg {
-    static constexpr bool kCodes = kForm != kRows16, kE4m3 = kForm == kRowsE4m3, kE2m1 = kForm == kRowsE2m1;
+    static constexpr bool kCodes = kForm != kRows16, kE4m3 = kForm == kRowsE4m3, kE2m1 = kForm >= kRowsE2m1;
+    static constexpr bool kSixteens = kForm == kRowsE2m1By16;  // (DecodeParams::by_sixteens)
     static constexpr int kRowBytes = kE2m1 ? D / 2 : (kE4m3 ? D : 2 * D);
     static constexpr int kRows = 8 * kTiles;                // query heads per item
     // CTAs an SM. 16-bit rows keep memory busy with two, and three read unevenly fast (21 sequences of
@@ -567,7 +568,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     // e2m1, and pages of whole sixteens of keys: kTeam lanes look 16 keys of a block up, which lie after one another in
     // a page, and copy them: no address crosses lanes. (One key a lane, as below, took 390 instructions a block of 32
     // keys, more than its products.)
-    const bool sixteens = c.page_size % 16 == 0, by_sixteens = kE2m1 && p.by_sixteens;
+    const bool sixteens = c.page_size % 16 == 0, by_sixteens = C::kSixteens;
     constexpr int kTeam = kE2m1 ? 512 / kKeys : 32;
     int page[C::kLooks], slot[C::kLooks];  // slot -1: no such key
     int64_t head_off = 0, head_exp = 0;    // and the block's head
@@ -1458,9 +1459,12 @@ cudaError_t launch_kind(const DecodeParams& p, cudaStream_t stream, int slot) { 
 }
 
 template <int D, bool kPerHead>
-cudaError_t launch_e2m1(const DecodeParams& p, cudaStream_t stream, int slot) {  // slots slot .. slot + 7
-    return p.c.dtype == kBf16 ? launch_tiles<D, true, kRowsE2m1, kPerHead>(p, stream, slot)
-                              : launch_tiles<D, false, kRowsE2m1, kPerHead>(p, stream, slot + 4);
+cudaError_t launch_e2m1(const DecodeParams& p, cudaStream_t stream, int slot) {  // slots slot .. slot + 15
+    if (p.by_sixteens)
+        return p.c.dtype == kBf16 ? launch_tiles<D, true, kRowsE2m1By16, kPerHead>(p, stream, slot)
+                                  : launch_tiles<D, false, kRowsE2m1By16, kPerHead>(p, stream, slot + 4);
+    return p.c.dtype == kBf16 ? launch_tiles<D, true, kRowsE2m1, kPerHead>(p, stream, slot + 8)
+                              : launch_tiles<D, false, kRowsE2m1, kPerHead>(p, stream, slot + 12);
 }
 
 template <int D, int kTiles>

@@ -4,8 +4,6 @@
 namespace fa2 {
 
 // slots 144 .. 159 of ensure_smem_limit
-cudaError_t launch_decode_e2m1_d128(const DecodeParams& p, cudaStream_t stream) {
-    return p.per_head ? launch_e2m1<128, true>(p, stream, 152) : launch_e2m1<128, false>(p, stream, 144);
-}
+cudaError_t launch_decode_e2m1_d128(const DecodeParams& p, cudaStream_t stream) { return launch_e2m1<128, false>(p, stream, 144); }
 
 }  // namespace fa2

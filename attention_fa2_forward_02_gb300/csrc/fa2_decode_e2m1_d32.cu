@@ -4,8 +4,6 @@
 namespace fa2 {
 
 // slots 112 .. 127 of ensure_smem_limit
-cudaError_t launch_decode_e2m1_d32(const DecodeParams& p, cudaStream_t stream) {
-    return p.per_head ? launch_e2m1<32, true>(p, stream, 120) : launch_e2m1<32, false>(p, stream, 112);
-}
+cudaError_t launch_decode_e2m1_d32(const DecodeParams& p, cudaStream_t stream) { return launch_e2m1<32, false>(p, stream, 112); }
 
 }  // namespace fa2

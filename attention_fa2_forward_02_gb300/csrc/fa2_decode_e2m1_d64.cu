@@ -4,8 +4,6 @@
 namespace fa2 {
 
 // slots 128 .. 143 of ensure_smem_limit
-cudaError_t launch_decode_e2m1_d64(const DecodeParams& p, cudaStream_t stream) {
-    return p.per_head ? launch_e2m1<64, true>(p, stream, 136) : launch_e2m1<64, false>(p, stream, 128);
-}
+cudaError_t launch_decode_e2m1_d64(const DecodeParams& p, cudaStream_t stream) { return launch_e2m1<64, false>(p, stream, 128); }
 
 }  // namespace fa2

@@ -170,7 +170,7 @@ struct RopeParams {
 };
 
 // How the cache holds its rows (fa2.h, fa2_cache_type).
-enum CacheForm : int { kRows16 = FA2_CACHE_SAME, kRowsE4m3 = FA2_CACHE_E4M3, kRowsE2m1 = FA2_CACHE_E2M1 };
+enum CacheForm : int { kRows16 = FA2_CACHE_SAME, kRowsE4m3 = FA2_CACHE_E4M3, kRowsE2m1 = FA2_CACHE_E2M1, kRowsE2m1By16 /* the decode's kernels alone */ };
 
 // A paged cache and the sequences that a call goes through (fa2.h, fa2_kv_cache).
 struct PagedParams {
@@ -296,7 +296,10 @@ cudaError_t launch_decode_d128(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_selected_d32(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_selected_d64(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_selected_d128(const DecodeParams& p, cudaStream_t stream);
-// ... over 4-bit rows, either
+// ... over 4-bit rows
+cudaError_t launch_selected_e2m1_d32(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_selected_e2m1_d64(const DecodeParams& p, cudaStream_t stream);
+cudaError_t launch_selected_e2m1_d128(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_e2m1_d32(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_e2m1_d64(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_e2m1_d128(const DecodeParams& p, cudaStream_t stream);

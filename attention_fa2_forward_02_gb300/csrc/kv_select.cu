@@ -391,31 +391,27 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, const Queries
 
 // ---------------------------------------------------------------------------- selection
 
-// Sums over the CTA of a thread's two counts, exclusive in thread order, and their totals.
-template <int kThreads>
-__device__ __forceinline__ uint2 scan2(uint2 v, uint2* sums, uint2* total) {
+// Sums over the CTA of a thread's two counts, packed as the halves of T, exclusive in thread order.
+template <int kThreads, typename T>
+__device__ __forceinline__ T scan(T v, T* sums) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    uint2 upto = v;
+    T upto = v;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const uint32_t x = __shfl_up_sync(0xffffffffu, upto.x, off), y = __shfl_up_sync(0xffffffffu, upto.y, off);
-        if (lane >= off) upto.x += x, upto.y += y;
+        const T x = __shfl_up_sync(0xffffffffu, upto, off);
+        if (lane >= off) upto += x;
     }
     __syncthreads();
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
-    uint2 before = make_uint2(0, 0), all = before;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before.x += sums[w].x, before.y += sums[w].y;
-        all.x += sums[w].x, all.y += sums[w].y;
-    }
-    *total = all;
-    return make_uint2(before.x + upto.x - v.x, before.y + upto.y - v.y);
+    T before = 0;
+#pragma unroll 1  // (a kernel that runs once waits for its instructions: few of them)
+    for (int w = 0; w < warp; ++w) before += sums[w];
+    return before + upto - v;
 }
 
 struct SelectSmem {
-    uint2 sums[32];
+    unsigned long long sums[32];
     uint32_t bins[kBins];
     uint32_t found[3];
     uint32_t few, list[32];
@@ -435,11 +431,16 @@ __device__ __forceinline__ void take_all(const SelectParams& p, int row, const i
 // The budget of row `row` out of n > budget pages with keys key(0) .. key(n - 1). The budget-th largest is found by counting
 // into kBins equal parts of the range that holds it, three times at the most (for 32 bits), mostly twice: the range
 // begins as that of the scores there are.
-template <int kThreads, typename Key>
+// T: two counts of pages in one, 16 bits each (n < 2^16) or 32.
+template <int kThreads, typename T, typename Key>
 __device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm, int row, const int32_t* table, int n, int len, Key key) {
+    constexpr int kHalf = 4 * sizeof(T);  // bits of a count
+    constexpr T kOne = (T)1 << kHalf, kLow = kOne - 1;
+    T* const sums = reinterpret_cast<T*>(sm.sums);
     const int lane = threadIdx.x & 31;
     // ---- the range of the scores that are not forced, and how many to take of those
     uint32_t lo = 0xffffffffu, hi = 0, forced = 0;
+#pragma unroll 1
     for (int i = threadIdx.x; i < n; i += kThreads) {
         const uint32_t k = key(i);
         if (k == kForced) ++forced;
@@ -463,6 +464,7 @@ __device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm
         const int shift = max(0, 22 - __clz(hi - lo));  // (hi - lo) >> shift < kBins
         for (int i = threadIdx.x; i < kBins; i += kThreads) sm.bins[i] = 0;
         __syncthreads();  // (found is read)
+#pragma unroll 1
         for (int i = threadIdx.x; i < n; i += kThreads) {
             const uint32_t k = key(i);
             if (k >= lo && k <= hi) atomicAdd(&sm.bins[(k - lo) >> shift], 1u);
@@ -474,8 +476,7 @@ __device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm
         uint32_t c[kPer], all = 0;
 #pragma unroll
         for (int i = 0; i < kPer; ++i) all += c[i] = sm.bins[top - i];
-        uint2 total;
-        uint32_t above = scan2<kThreads>(make_uint2(all, 0), sm.sums, &total).x;
+        uint32_t above = (uint32_t)scan<kThreads>((T)all, sums);
 #pragma unroll
         for (int i = 0; i < kPer; ++i) {
             if (above < need && need <= above + c[i]) sm.found[0] = top - i, sm.found[1] = above, sm.found[2] = c[i];
@@ -496,6 +497,7 @@ __device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm
         }
         const uint32_t left = sm.found[2];
         if (left <= 32) {  // each warp ranks them
+#pragma unroll 1
             for (int i = threadIdx.x; i < n; i += kThreads) {
                 const uint32_t k = key(i);
                 if (k >= lo && k <= hi) sm.list[atomicAdd(&sm.few, 1u)] = k;
@@ -503,6 +505,7 @@ __device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm
             __syncthreads();
             const uint32_t mine = lane < (int)left ? sm.list[lane] : 0u;
             uint32_t above_it = 0, alike = 0;
+#pragma unroll 1
             for (uint32_t i = 0; i < left; ++i) above_it += sm.list[i] > mine, alike += sm.list[i] == mine;
             const uint32_t who = __ballot_sync(0xffffffffu, lane < (int)left && above_it < need && need <= above_it + alike);
             least = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
@@ -513,16 +516,18 @@ __device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm
     // ---- in the order of their positions: thread i has pages i per ..
     const int per = (n + kThreads - 1) / kThreads;
     const int i0 = (int)min((int64_t)threadIdx.x * per, (int64_t)n), i1 = min(i0 + per, n);
-    uint2 count = make_uint2(0, 0), total;
+    T count = 0;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         const uint32_t k = key(i);
-        count.x += k > least, count.y += k == least;
+        count += (k > least ? (T)1 : (T)0) + (k == least ? kOne : (T)0);
     }
-    const uint2 before = scan2<kThreads>(count, sm.sums, &total);
-    uint32_t at = before.x + min(before.y, equal), seen = before.y;
+    const T before = scan<kThreads>(count, sums);
+    uint32_t seen = (uint32_t)(before >> kHalf), at = (uint32_t)(before & kLow) + min(seen, equal);
     // first the pages' places, then, side by side, what the table has there
     int32_t* dst = p.sel_table + (int64_t)row * p.budget;
     const bool listed = p.budget <= kBins;
+#pragma unroll 1
     for (int i = i0; i < i1; ++i) {
         const uint32_t k = key(i);
         const bool take = k > least || (k == least && seen < equal);
@@ -560,7 +565,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) select_kernel(const Se
         p, q, ring, table, hk, n, rank * kSelWarps + (int)(threadIdx.x >> 5), ranks * kSelWarps, [&] { q.template make<kBf16>(p, b, hk); },
         [&](int j, uint32_t key) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 4 * j), "r"(key) : "memory"); });
     cluster_sync_all();
-    if (rank == 0) select_row<kSelThreads>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
+    if (rank == 0) select_row<kSelThreads, uint32_t>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
 }
 
 // The same for tables too wide for that, in two launches through the workspace.
@@ -585,7 +590,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_select_kernel(const SelectP
     const int32_t* table = p.table + b * p.table_stride;
     if (n <= p.budget) return take_all(p, row, table, n, len);
     const uint32_t* scores = p.scores + (int64_t)row * p.per_seq;
-    select_row<kWideThreads>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
+    select_row<kWideThreads, unsigned long long>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
 }
 // Tables no wider than the budget: every page is taken, without a look at the bounds.
 __global__ void __launch_bounds__(kSelThreads) take_all_kernel(const SelectParams p) {

@@ -161,7 +161,7 @@ fa2_status decode_call(const void* q, const int64_t* q_strides, const fa2_kv_cac
     for (int i = 0; i < 2; ++i)
         if (sizes[i] > 1 && q_strides[i] % 8 != 0) return FA2_ERR_MISALIGNED;
     if (!workspace || !aligned(workspace, 16) ||
-        workspace_bytes < decode_workspace_bytes(n_heads, cache->n_kv_heads, cache->head_dim))
+        workspace_bytes < decode_workspace_bytes(n_heads, cache->n_kv_heads, cache->head_dim, cache->type == FA2_CACHE_E2M1))
         return FA2_ERR_WORKSPACE;
     p.q = q; p.q_batch = q_strides[0]; p.q_head = q_strides[1];
     p.o = o; p.lse = lse; p.heads = n_heads;
@@ -323,7 +323,8 @@ size_t fa2_decode_workspace_size(int64_t batch, int32_t n_heads, int32_t n_kv_he
     if (batch <= 0 || n_heads <= 0 || n_kv_heads <= 0 || n_heads % n_kv_heads != 0 || head_dim <= 0 || head_dim > 128 ||
         head_dim % 8 != 0)
         return 0;
-    return decode_workspace_bytes(n_heads, n_kv_heads, head_dim);
+    const size_t others = decode_workspace_bytes(n_heads, n_kv_heads, head_dim, false), e2m1 = decode_workspace_bytes(n_heads, n_kv_heads, head_dim, true);
+    return others > e2m1 ? others : e2m1;
 }
 
 fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_cache* cache, void* o, float* lse,

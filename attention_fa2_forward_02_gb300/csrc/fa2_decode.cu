@@ -4,12 +4,12 @@
 
 namespace fa2 {
 
-size_t decode_workspace_bytes(int heads, int hkv, int d) {
+size_t decode_workspace_bytes(int heads, int hkv, int d, bool e2m1) {
     const bool one = heads / hkv <= 8;
     switch (pad_head_dim(d)) {
-        case 32: return one ? workspace_for<32, 1>() : workspace_for<32, 2>();
-        case 64: return one ? workspace_for<64, 1>() : workspace_for<64, 2>();
-        default: return one ? workspace_for<128, 1>() : workspace_for<128, 2>();
+        case 32: return one ? workspace_for<32, 1>(e2m1) : workspace_for<32, 2>(e2m1);
+        case 64: return one ? workspace_for<64, 1>(e2m1) : workspace_for<64, 2>(e2m1);
+        default: return one ? workspace_for<128, 1>(e2m1) : workspace_for<128, 2>(e2m1);
     }
 }
 

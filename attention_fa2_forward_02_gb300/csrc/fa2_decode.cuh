@@ -1468,10 +1468,10 @@ cudaError_t launch_e2m1(const DecodeParams& p, cudaStream_t stream, int slot) { 
 }
 
 template <int D, int kTiles>
-size_t workspace_for() {  // any type of cache
+size_t workspace_for(bool e2m1) {
     using C = Cfg<D, kRowsE4m3, kTiles>;
-    constexpr int kCtas = std::max({C::kMaxCtas, Cfg<D, kRows16, kTiles>::kMaxCtas, Cfg<D, kRowsE2m1, kTiles>::kMaxCtas});
-    return (size_t)kCtas * (2 * C::kRows * (D + 4) * sizeof(float) + sizeof(Torn));
+    const int ctas = e2m1 ? Cfg<D, kRowsE2m1, kTiles>::kMaxCtas : std::max(C::kMaxCtas, Cfg<D, kRows16, kTiles>::kMaxCtas);
+    return (size_t)ctas * (2 * C::kRows * (D + 4) * sizeof(float) + sizeof(Torn));
 }
 
 }  // namespace

@@ -303,7 +303,7 @@ cudaError_t launch_selected_e2m1_d128(const DecodeParams& p, cudaStream_t stream
 cudaError_t launch_decode_e2m1_d32(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_e2m1_d64(const DecodeParams& p, cudaStream_t stream);
 cudaError_t launch_decode_e2m1_d128(const DecodeParams& p, cudaStream_t stream);
-size_t decode_workspace_bytes(int heads, int hkv, int d);
+size_t decode_workspace_bytes(int heads, int hkv, int d, bool e2m1);  // for the 4-bit cache, for the others
 
 cudaError_t launch_fwd_tc(const FwdParams& p, cudaStream_t stream);
 cudaError_t launch_fwd_f32(const FwdParams& p, cudaStream_t stream);

@@ -732,7 +732,8 @@ typedef struct fa2_launch_info {
 fa2_status fa2_last_launch_info(fa2_launch_info* info);
 
 /*
- * fa2_last_decode_info - how the calling host thread's most recent fa2_decode divided its work:
+ * fa2_last_decode_info - how the calling host thread's most recent fa2_decode or
+ * fa2_decode_selected divided its work:
  *   *ctas_per_item   CTAs of a thread-block cluster that shared each sequence's key-value head
  *                    (and 8 or 16 of its query heads), 1 to 8, in one launch; 0: all keys divided
  *                    evenly over the CTAs, whatever the lengths, in two launches; -1 before any

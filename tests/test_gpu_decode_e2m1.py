@@ -158,6 +158,27 @@ def test_offsets_past_2_32_bytes():
     check(c, synth.widen(q, "bf16"), o, lse, 2, 0.125)
 
 
+def test_offsets_past_2_36_bytes():
+    """Pages further apart than 32 bits of 16 bytes reach."""
+    torch = G.require_gpu()
+    free, _ = torch.cuda.mem_get_info()
+    stride = (1 << 35) + (1 << 30)
+    if free < 2 * stride + (16 << 30):
+        pytest.skip("not enough memory for two far pages")
+    c = Cache4("decode4/farther", [30, 16], 16, 2, 64, spare=0)
+    buf = torch.empty(2 * stride + 2 * 2 * 16 * 32, dtype=torch.uint8, device="cuda")
+    pools = []
+    for i, s in enumerate("kv"):  # K's and V's pages side by side in one buffer
+        far = buf[i * 2 * 16 * 32:].as_strided((c.pages, 2, 16, 32), (stride, 16 * 32, 32, 1))
+        far.copy_(c.dev[s])
+        pools.append(far)
+    q = synth.tensor("decode4/farther/q", (2, 4, 64), "bf16")
+    o, lse = G.empty((2, 4, 64), "bf16"), torch.empty(2, 4, device="cuda")
+    binding.fa2_decode(G.to_device(q, "bf16"), *pools, o, lse, c.table_dev, c.lens_dev, workspace(2, 4, 2, 64), 0.125, **c.exps())
+    binding.fa2_device_status()
+    check(c, synth.widen(q, "bf16"), o, lse, 2, 0.125)
+
+
 def test_same_bits_again_and_on_another_stream():
     torch = G.require_gpu()
     c, q, o, lse = run("decode4/again", [3000, 77, 900], 16, 2, 4, 128)

@@ -170,7 +170,7 @@ fa2_status decode_call(const void* q, const int64_t* q_strides, const fa2_kv_cac
     p.scale = softmax_scale;
     p.by_sixteens = p.c.page_size % 16 == 0 &&
                     (double)p.c.num_pages * p.c.page_stride + (double)p.c.hkv * p.c.head_stride + (double)p.c.page_size * p.c.slot_stride < 16.0 * UINT32_MAX &&
-                    p.c.num_pages * p.c.hkv * p.c.page_size < UINT32_MAX;
+                    (double)p.c.num_pages * p.c.hkv * p.c.page_size < UINT32_MAX;
     if (per_head) {
         if (batch * cache->n_kv_heads > (1 << 20)) return FA2_ERR_UNSUPPORTED;
         p.per_head = true;

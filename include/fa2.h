@@ -607,7 +607,8 @@ fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_ca
  *
  *   bounds      int8 [num_pages, n_kv_heads, 2, head_dim], contiguous, 16-byte aligned: the
  *               lowest, then the highest keys' codes
- *   bounds_exp  uint8 [num_pages, n_kv_heads], contiguous: a code stands for code * 2^(byte - 127)
+ *   bounds_exp  uint8 [num_pages, n_kv_heads], contiguous: a code stands for code * 2^(byte - 127),
+ *               bytes 1 to 254
  *
  * fa2_kv_bounds - makes the bounds of the pages that new tokens lie in, from all of the page's
  * live keys (those before the sequence's length): call it after fa2_kv_append or

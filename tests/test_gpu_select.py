@@ -264,6 +264,33 @@ def test_extreme_queries_and_bounds():
         S.page_score = exact
 
 
+def test_powers_that_are_none_select_within_the_budget():
+    """Bytes 0 and 255 (bounds never made) stand for 0 and infinity: a score that is then no number is the lowest of a page of the
+    cache, and no more pages than the budget are taken."""
+    torch = G.require_gpu()
+    c = Cache("sel/none", [1600, 1000, 1300], 16, 2, 64)
+    codes = np.sort((synth.counter_u16("sel/none/bounds", (c.pages, 2, 2, 64)) % 255).astype(np.int64) - 127, axis=2)
+    byte = np.array([0, 255, 127, 100], dtype=np.uint8)[synth.counter_u16("sel/none/exp", (c.pages, 2)) % 4]
+    q = synth.widen(synth.tensor("sel/none/q", (3, 6, 64), "bf16"), "bf16")
+    q[1], q[2] = 0, q[2] * 2.0 ** 120
+    x = synth.to_storage(q, "bf16")
+
+    def score(qs, codes, byte):
+        best = max(S.page_score([one], codes, 127) for one in qs)
+        best = math.copysign(math.inf, best) if abs(best) >= 2.0 ** 128 else best
+        two = 0.0 if byte == 0 else math.inf if byte == 255 else 2.0 ** (int(byte) - 127)
+        s = best * two
+        return -math.inf if math.isnan(s) else s
+    for budget, first, recent in ((20, 1, 1), (1, 0, 0), (60, 3, 9)):
+        table, lens = select(c, G.to_device(x, "bf16"), torch.from_numpy(codes.astype(np.int8)).cuda(), torch.from_numpy(byte).cuda(), budget, first, recent)
+        for b in range(3):
+            pages = c.table[b, : -(-c.lens[b] // 16)]
+            for h in range(2):
+                scores = [score(synth.widen(x, "bf16")[b, 3 * h:3 * h + 3], codes[p, h], byte[p, h]) for p in pages]
+                assert table[b, h].tolist() == [int(pages[j]) for j in S.select_pages(scores, budget, first, recent)], (b, h)
+    binding.fa2_device_status()
+
+
 @pytest.mark.parametrize("d", [128, 96, 40])
 def test_the_largest_sums_are_exact(d):
     """Integers of 125 to 127 on both sides, all signs alike or nearly so: sums up to 2^21 that differ by little."""

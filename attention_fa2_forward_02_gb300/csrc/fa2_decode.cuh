@@ -29,6 +29,13 @@
 // others' and next to nothing in O: they do not raise m. Codes are exact in half; q (bfloat16) is
 // brought to half exactly by a power of two of its row's largest element.
 //
+// The 4-bit cache is the same with code * scale, 6 bits and exact in half, in the place of the code: K's and V's
+// operands are made in registers (a byte of two codes to a pair of halves, times the group's scale; the lanes' pieces
+// of a row are permuted alike on both sides of a product, so no element moves between lanes). That and the products
+// bound it, not its 73 bytes a row: about 350 instructions for 16 keys of 128, issued in 57 of 100 cycles. GB300, 32
+// sequences of up to 8192 (d 128, 8 heads on each of 8, 193 MB): 57 us, 3.4 TB/s; 21 of up to 65536 (d 64, half, 507
+// MB): 170 us, 3.0 TB/s, where each weight takes two products.
+//
 // Contexts that can only be short (by the block table's width, or the window) take one launch: the
 // CTAs of a thread-block cluster share an item and join their results in distributed shared
 // memory. GB300, one sequence of 1000 tokens, 8 heads: 8.5 us in two launches, 6.7 in one.
@@ -62,7 +69,8 @@ struct Cfg {
     // sequences of up to 8192, a one-token one among them, d 128 76 us with two and 65 with three (long
     // contexts 304 and 322), d 32 34 and 33. But three leave 168 registers: too few at d 64, 8 heads
     // (41 us with two, 50 with three; long 163 and 198), and for 16 heads (d 64 57 and 70, d 128 86
-    // and 155; d 32 42 and 40).
+    // and 155; d 32 42 and 40). 4-bit rows have the most to do: batch of 32, d 128, 75 us with two and 70 with three
+    // (four spill: 76).
     static constexpr int kPerSm = (kE4m3 && (D == 32 || (D == 128 && kTiles == 1))) || (kE2m1 && kTiles == 1) ? 3 : 2;
     static constexpr int kMaxCtas = 152 * kPerSm;           // a fixed number: the split depends on the lengths alone
     // in one launch, where latency is more than memory: 7 windows of 1024 keys, d 64, 9.6 -> 8.8 us
@@ -84,7 +92,8 @@ struct Cfg {
     static constexpr int kScales = kE2m1 ? kKeys * kScaleRow : 0;  // and of a block's keys, or values
     static constexpr int kExps = 2 * kTile + kInfo + 2 * kScales;  // e2m1: bytes of K's, then V's powers of two
     static constexpr int kStage = kExps + (kE2m1 ? 2 * kKeys : 0);
-    // 4-bit rows: a block of 4.7 KB is too little in flight a warp; two stages 69.6 us in the batch of 32, three 0
+    // 4-bit rows at d 128: a block of 4.7 KB is too little on its way a warp. Batch of 32 69.6 us with two stages, 65.0
+    // with three (and keys looked up by teams of lanes, below); d 64, whose blocks hold 64 keys: no gain from three or four.
     static constexpr int kStages = kE2m1 && D == 128 ? 3 : 2;
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kQ = kRows * D * 2;                // q as the first product takes it
@@ -568,7 +577,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     // e2m1, and pages of whole sixteens of keys: kTeam lanes look 16 keys of a block up, which lie after one another in
     // a page, and copy them: no address crosses lanes. (One key a lane, as below, took 390 instructions a block of 32
     // keys, more than its products.)
-    const bool sixteens = c.page_size % 16 == 0, by_sixteens = C::kSixteens;
+    const bool sixteens = c.page_size % 16 == 0;
+    constexpr bool by_sixteens = C::kSixteens;
     constexpr int kTeam = kE2m1 ? 512 / kKeys : 32;
     int page[C::kLooks], slot[C::kLooks];  // slot -1: no such key
     int64_t head_off = 0, head_exp = 0;    // and the block's head

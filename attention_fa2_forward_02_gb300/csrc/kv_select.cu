@@ -2,9 +2,10 @@
 //
 // Bounds: the lowest and the highest key of every channel, as 8-bit integers at a power of two of the page and
 // head, rounded outwards: for 16 tokens of 128 channels in 16 bits 257 bytes for 8192 of keys and values. From 16-bit
-// keys memory sets the pace; codes have to be widened and compared one pair at a time, which does (60 of 100 cycles of the
-// integer and comparison unit): GB300, 9 prompts of up to 16384 tokens, 8 heads of e4m3 keys, 66 MB, 24 us, 2.7
-// TB/s. The pages of a step of 33 sequences take 3.5 us: a launch and four reads one after another.
+// keys memory sets the pace (GB300, 9 prompts of up to 16384 tokens, 8 heads, 132 MB, 27 us, 4.9 TB/s); codes have to be
+// widened and are compared two at a time, which does (60 of 100 cycles of the integer and comparison unit): e4m3, 66 MB,
+// 19 us, 3.5 TB/s; 24 when they were compared as bfloat16, by way of float32. Half of a page's 930 instructions find
+// it and make its codes, as many as 32 rows of 128 take; larger pages have fewer. The pages of a step of 33 sequences take 3.5 us: a launch and four reads one after another.
 //
 // Scores: sum_c max(q_c low_c, q_c high_c) is no less than q . k for any key within the bounds. The query's
 // 8-bit integers, split into those above zero (which meet the highest keys) and those below (the lowest), make it
@@ -51,13 +52,128 @@ __device__ __forceinline__ float2 floats(uint32_t w) {
     else return __half22float2(*reinterpret_cast<const __half2*>(&w));
 }
 
-// A warp takes one page of one sequence and one head: groups of kLanes lanes read slots in turn, 8 channels a lane.
+// Lowest and highest of a lane's 16 channels over a page's rows, a group of kLanes lanes a row, kUnroll rows of each group at
+// once. There is no other row or channel to skip: those behind the last one are the last one again.
+template <int kForm, int kLanes>
+struct PageKeys {
+    static constexpr int kGroups = 32 / kLanes, kUnroll = kForm == kRows16 ? 4 : 8, kStep = kGroups * kUnroll;
+    static constexpr int kWords = kForm == kRows16 ? 8 : (kForm == kRowsE4m3 ? 4 : 2);
+    const PagedParams& c;
+    const char *base, *second;  // of the lane's channels; 16-bit rows: of its last 8
+    int64_t exp0;
+    int live, gr, part;  // part: number of its 16 channels
+    uint32_t k[kUnroll][kWords];
+    uint32_t byte[kUnroll], scale[kUnroll];
+
+    __device__ __forceinline__ void load(int s0) {  // rows s0 + gr, + kGroups, ...
+#pragma unroll
+        for (int n = 0; n < kUnroll; ++n) {
+            if (s0 + n * kGroups >= live) continue;
+            const int s = min(s0 + gr + n * kGroups, live - 1);
+            const char* row = base + s * c.slot_stride;
+            if constexpr (kForm == kRows16) {
+                const uint4 x = *reinterpret_cast<const uint4*>(row), y = *reinterpret_cast<const uint4*>(second + s * c.slot_stride);
+                k[n][0] = x.x, k[n][1] = x.y, k[n][2] = x.z, k[n][3] = x.w;
+                k[n][4] = y.x, k[n][5] = y.y, k[n][6] = y.z, k[n][7] = y.w;
+            } else if constexpr (kForm == kRowsE4m3) {
+                const uint4 x = *reinterpret_cast<const uint4*>(row);
+                k[n][0] = x.x, k[n][1] = x.y, k[n][2] = x.z, k[n][3] = x.w;
+                byte[n] = c.k_exp[exp0 + s];
+            } else {
+                const uint2 x = *reinterpret_cast<const uint2*>(row);
+                k[n][0] = x.x, k[n][1] = x.y;
+                byte[n] = c.k_exp[exp0 + s];
+                scale[n] = c.k_scale[(exp0 + s) * (c.d / 16) + part];
+            }
+        }
+    }
+
+    // The first rows are loaded. kHalf (codes): compared as halves at the power of two `top`; else as 16-bit floats that
+    // hold every element. The groups then share the channels: from word w on, `words` pairs of each lane's 8, in l and u.
+    template <bool kBf16, bool kHalf>
+    __device__ __forceinline__ void compare(uint32_t top, int* w, float (&l)[kLanes == 8 ? 4 : 2], float (&u)[kLanes == 8 ? 4 : 2]) {
+        constexpr bool kPairBf16 = !kHalf && (kBf16 || kForm != kRows16);
+        using T = typename Pair<kPairBf16>::T;
+        constexpr uint32_t kInf2 = kPairBf16 ? 0x7f807f80u : 0x7c007c00u;
+        auto widen = [&](uint32_t word) { return *reinterpret_cast<T*>(&word); };
+        auto bits = [&](T x) { return *reinterpret_cast<uint32_t*>(&x); };
+        uint32_t lo[8], hi[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) lo[i] = kInf2, hi[i] = kInf2 | 0x80008000u;
+        const uint32_t one = (15u - top) * 0x04000400u;  // 2^-top as two halves' bits, to which a byte adds
+        for (int s0 = 0; s0 < live; s0 += kStep) {
+            if (s0) load(s0);
+#pragma unroll
+            for (int n = 0; n < kUnroll; ++n) {
+                if (s0 + n * kGroups >= live) continue;
+                uint32_t x[8];
+                if constexpr (kForm == kRows16) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[i] = k[n][i];
+                } else {
+                    uint32_t s = 0;
+                    if constexpr (kHalf) s = byte[n] * 0x04000400u + one;
+                    if constexpr (kForm == kRowsE4m3) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) e4m3x4_to_f16x4(k[n][i], x[2 * i], x[2 * i + 1]);
+                    } else {
+                        uint32_t f[2][4];
+                        e2m1x8_to_f16x8(k[n][0], f[0]);
+                        e2m1x8_to_f16x8(k[n][1], f[1]);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = f[i / 4][i % 4];
+                        const uint32_t of16 = e4m3x2_to_f16x2(scale[n] * 0x101u);
+                        s = kHalf ? hmul2(of16, s) : of16;
+                    }
+                    if constexpr (kHalf || kForm == kRowsE2m1) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = hmul2(x[i], s);
+                    }
+                    if constexpr (!kHalf) {
+                        const float two = __uint_as_float(byte[n] << 23);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));
+                            x[i] = pack2<true>(y.x * two, y.y * two);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {  // (a NaN is not taken)
+                    lo[i] = bits(__hmin2(widen(lo[i]), widen(x[i])));
+                    hi[i] = bits(__hmax2(widen(hi[i]), widen(x[i])));
+                }
+            }
+        }
+        // two groups of lanes at a time join their words, each a half of them
+        *w = 0;
+#pragma unroll
+        for (int off = kLanes, words = 8; off < 32; off <<= 1) {
+            if (words > 1) words /= 2;
+            const bool upper = (threadIdx.x & off) != 0;
+            const bool halve = off < 8 * kLanes;
+#pragma unroll
+            for (int i = 0; i < words; ++i) {
+                const uint32_t a = halve && upper ? lo[i + words] : lo[i], b = halve && upper ? hi[i + words] : hi[i];
+                const uint32_t give_a = halve && !upper ? lo[i + words] : lo[i], give_b = halve && !upper ? hi[i + words] : hi[i];
+                lo[i] = bits(__hmin2(widen(a), widen(__shfl_xor_sync(0xffffffffu, give_a, off))));
+                hi[i] = bits(__hmax2(widen(b), widen(__shfl_xor_sync(0xffffffffu, give_b, off))));
+            }
+            if (halve && upper) *w += words;
+        }
+        const float power = kHalf ? __uint_as_float(top << 23) : 1.f;
+#pragma unroll
+        for (int i = 0; i < (kLanes == 8 ? 2 : 1); ++i) {
+            const float2 x = floats<kPairBf16>(lo[i]), y = floats<kPairBf16>(hi[i]);
+            l[2 * i] = x.x * power, l[2 * i + 1] = x.y * power, u[2 * i] = y.x * power, u[2 * i + 1] = y.y * power;
+        }
+    }
+};
+
+// A warp takes one page of one sequence and one head: groups of kLanes lanes read slots in turn, 16 channels a lane.
 template <bool kBf16, int kForm, int kLanes>
 __global__ void __launch_bounds__(kWarps * 32) kv_bounds_kernel(const KvBoundsParams p) {
     const PagedParams& c = p.c;
-    constexpr bool kPairBf16 = kBf16 || kForm != kRows16;
-    using T = typename Pair<kPairBf16>::T;
-    constexpr int kGroups = 32 / kLanes, kUnroll = 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t w = (int64_t)blockIdx.x * kWarps + warp;
     const int h = blockIdx.y;
@@ -69,10 +185,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv_bounds_kernel(const KvBoundsPa
         auto start = [&](int i) { return (int64_t)page_of(c, max(p.cu_new[i], 0)) + 2 * i; };
         int lo = 0, hi = (int)c.batch;
         if (w >= start(hi)) return;
-        while (hi - lo > 1) {
-            const int mid = (lo + hi) >> 1;
-            if (start(mid) <= w) lo = mid;
-            else hi = mid;
+        while (hi - lo > 1) {  // a lane a place
+            const int apart = (hi - lo + 31) / 32, at = lo + lane * apart;
+            const int before = __popc(__ballot_sync(0xffffffffu, at < hi && start(at < hi ? at : lo) <= w));
+            lo += max(before - 1, 0) * apart;
+            hi = min(lo + apart, hi);
         }
         b = lo;
         nth = w - start(b);
@@ -92,120 +209,76 @@ __global__ void __launch_bounds__(kWarps * 32) kv_bounds_kernel(const KvBoundsPa
     if (first >= len) return;
     const int64_t j = page_of(c, first) + nth;
     if (j * c.page_size >= len) return;
-    const Slot at = slot_of(c, c.table[b * c.table_stride + j], 0);
+    const int32_t page = c.table[b * c.table_stride + j];
+    const Slot at = slot_of(c, page, 0);
     if (at.off < 0) return;
     const int live = (int)min((int64_t)c.page_size, len - j * c.page_size);
-    // ---- lowest and highest of the lane's channels
     const int li = lane % kLanes, gr = lane / kLanes;
-    const bool on = 8 * li < c.d;
-    constexpr uint32_t kInf2 = kPairBf16 ? 0x7f807f80u : 0x7c007c00u;
-    uint32_t lo[4], hi[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) lo[i] = kInf2, hi[i] = kInf2 | 0x80008000u;
-    auto widen = [&](uint32_t word) { return *reinterpret_cast<T*>(&word); };
-    auto bits = [&](T x) { return *reinterpret_cast<uint32_t*>(&x); };
-    const char* base = c.k + at.off + h * c.head_stride;
-    const int64_t exp0 = at.exp + (int64_t)h * c.page_size;
-    for (int s0 = gr; s0 < live; s0 += kGroups * kUnroll) {
-        uint32_t k[kUnroll][4];
-        uint32_t byte[kUnroll], scale[kUnroll];
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const int s = s0 + u * kGroups;
-            if (s >= live || !on) continue;
-            const char* row = base + s * c.slot_stride;
-            if constexpr (kForm == kRows16) {
-                const uint4 x = *reinterpret_cast<const uint4*>(row + 16 * li);
-                k[u][0] = x.x, k[u][1] = x.y, k[u][2] = x.z, k[u][3] = x.w;
-            } else if constexpr (kForm == kRowsE4m3) {
-                const uint2 x = *reinterpret_cast<const uint2*>(row + 8 * li);
-                k[u][0] = x.x, k[u][1] = x.y;
-                byte[u] = c.k_exp[exp0 + s];
-            } else {
-                k[u][0] = *reinterpret_cast<const uint32_t*>(row + 4 * li);
-                byte[u] = c.k_exp[exp0 + s];
-                scale[u] = c.k_scale[(exp0 + s) * (c.d / 16) + li / 2];
-            }
+    constexpr int kRowBits = kForm == kRows16 ? 16 : (kForm == kRowsE4m3 ? 8 : 4);
+    const int pack = min(2 * li, c.d / 8 - 1), part = min(li, c.d / 16 - 1);  // (codes: whole 16)
+    const char* row0 = c.k + at.off + h * c.head_stride;
+    PageKeys<kForm, kLanes> keys{c, row0 + (kForm == kRows16 ? 16 * pack : 2 * kRowBits * part), row0 + 16 * min(2 * li + 1, c.d / 8 - 1),
+                                 at.exp + (int64_t)h * c.page_size, live, gr, part};
+    keys.load(0);
+    constexpr int kOwn = kLanes == 8 ? 4 : 2;  // channels a lane ends with
+    float l[kOwn], u[kOwn];
+    int w0;
+    if constexpr (kForm == kRows16) {
+        keys.template compare<kBf16, false>(0, &w0, l, u);
+    } else {
+        // Below the largest byte of the page's rows by no more than 14, a row's codes (4 bits: times their scales), which are
+        // multiples of 2^-9 (2^-10) of no more than 6 bits, are exact in half at the largest one's power.
+        uint32_t top = 0, low = 255;
+        for (int s = lane; s < live; s += 32) {
+            const uint32_t x = c.k_exp[keys.exp0 + s];
+            top = max(top, x);
+            low = min(low, x);
         }
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            if (s0 + u * kGroups >= live || !on) continue;
-            uint32_t x[4];
-            if constexpr (kForm == kRows16) {
-#pragma unroll
-                for (int i = 0; i < 4; ++i) x[i] = k[u][i];
-            } else {
-                uint32_t f[4];
-                if constexpr (kForm == kRowsE4m3) {
-                    e4m3x4_to_f16x4(k[u][0], f[0], f[1]);
-                    e4m3x4_to_f16x4(k[u][1], f[2], f[3]);
-                } else {
-                    e2m1x8_to_f16x8(k[u][0], f);
-                    const uint32_t s = e4m3x2_to_f16x2(scale[u] * 0x101u);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) f[i] = hmul2(f[i], s);
-                }
-                const float two = __uint_as_float(byte[u] << 23);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&f[i]));
-                    x[i] = pack2<true>(y.x * two, y.y * two);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {  // (a NaN is not taken)
-                lo[i] = bits(__hmin2(widen(lo[i]), widen(x[i])));
-                hi[i] = bits(__hmax2(widen(hi[i]), widen(x[i])));
-            }
-        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        low = __reduce_min_sync(0xffffffffu, low);
+        if (top - low <= 14) keys.template compare<true, true>(top, &w0, l, u);
+        else keys.template compare<true, false>(top, &w0, l, u);
     }
-#pragma unroll
-    for (int off = kLanes; off < 32; off <<= 1)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            lo[i] = bits(__hmin2(widen(lo[i]), widen(__shfl_xor_sync(0xffffffffu, lo[i], off))));
-            hi[i] = bits(__hmax2(widen(hi[i]), widen(__shfl_xor_sync(0xffffffffu, hi[i], off))));
-        }
     // ---- codes
-    float l[8], u[8], a = 0.f;
+    float a = 0.f;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 x = floats<kPairBf16>(lo[i]), y = floats<kPairBf16>(hi[i]);
-        l[2 * i] = x.x, l[2 * i + 1] = x.y, u[2 * i] = y.x, u[2 * i + 1] = y.y;
-    }
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < kOwn; ++i) {
         if (l[i] > u[i]) l[i] = u[i] = 0.f;  // nothing but NaN
         const float x = fabsf(l[i]), y = fabsf(u[i]);
         a = fmaxf(a, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
     }
-    if (!on) a = 0.f;
-#pragma unroll
-    for (int off = kLanes / 2; off > 0; off >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, off));
-    const int e = bound_exp(a);
-    if (gr != 0 || !on) return;
+    const int e = bound_exp(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a))));
+    const int channel = 16 * li + 2 * w0;
+    if (channel >= c.d || gr >= 8) return;  // (16 groups end with the same twice)
     const float inv = exp2_of(-e);
-    uint32_t out[2][2] = {};
+    auto limited = [&](float x) { return fmaxf(fminf(x * inv, 127.f), -127.f); };  // (infinities)
+    uint32_t low[kOwn], high[kOwn];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int low = (int)fmaxf(fminf(floorf(l[i] * inv), 127.f), -127.f), high = (int)fmaxf(fminf(ceilf(u[i] * inv), 127.f), -127.f);
-        out[0][i / 4] |= (uint32_t)(low & 0xff) << (8 * (i % 4));
-        out[1][i / 4] |= (uint32_t)(high & 0xff) << (8 * (i % 4));
+    for (int i = 0; i < kOwn; ++i) low[i] = (uint32_t)__float2int_rd(limited(l[i])), high[i] = (uint32_t)__float2int_ru(limited(u[i]));
+    uint32_t out[2] = {__byte_perm(low[0], low[1], 0x0040), __byte_perm(high[0], high[1], 0x0040)};
+    if constexpr (kOwn == 4) {
+        out[0] = __byte_perm(out[0], __byte_perm(low[2], low[3], 0x0040), 0x5410);
+        out[1] = __byte_perm(out[1], __byte_perm(high[2], high[3], 0x0040), 0x5410);
     }
-    const int64_t row = at.exp / c.page_size + h;  // page * hkv + h
-    int8_t* dst = p.bounds + row * 2 * c.d + 8 * li;
-    *reinterpret_cast<uint2*>(dst) = make_uint2(out[0][0], out[0][1]);
-    *reinterpret_cast<uint2*>(dst + c.d) = make_uint2(out[1][0], out[1][1]);
-    if (li == 0) p.bounds_exp[row] = (uint8_t)(e + 127);
+    const int64_t row = (int64_t)page * c.hkv + h;
+    int8_t* dst = p.bounds + row * 2 * c.d + channel;
+    if constexpr (kOwn == 4) {
+        *reinterpret_cast<uint32_t*>(dst) = out[0];
+        *reinterpret_cast<uint32_t*>(dst + c.d) = out[1];
+    } else {
+        *reinterpret_cast<uint16_t*>(dst) = (uint16_t)out[0];
+        *reinterpret_cast<uint16_t*>(dst + c.d) = (uint16_t)out[1];
+    }
+    if (lane == 0) p.bounds_exp[row] = (uint8_t)(e + 127);
 }
 
 template <bool kBf16, int kForm>
 cudaError_t launch_bounds_form(const KvBoundsParams& p, cudaStream_t stream) {
     const int64_t pages = p.cu_new ? p.tokens / p.c.page_size + 2 * p.c.batch : p.c.batch;
     const dim3 grid((unsigned)((pages + kWarps - 1) / kWarps), (unsigned)p.c.hkv);
-    if (p.c.d <= 32) return launch_early(kv_bounds_kernel<kBf16, kForm, 4>, grid, dim3(kWarps * 32), 0, stream, p);
-    if (p.c.d <= 64) return launch_early(kv_bounds_kernel<kBf16, kForm, 8>, grid, dim3(kWarps * 32), 0, stream, p);
-    return launch_early(kv_bounds_kernel<kBf16, kForm, 16>, grid, dim3(kWarps * 32), 0, stream, p);
+    if (p.c.d <= 32) return launch_early(kv_bounds_kernel<kBf16, kForm, 2>, grid, dim3(kWarps * 32), 0, stream, p);
+    if (p.c.d <= 64) return launch_early(kv_bounds_kernel<kBf16, kForm, 4>, grid, dim3(kWarps * 32), 0, stream, p);
+    return launch_early(kv_bounds_kernel<kBf16, kForm, 8>, grid, dim3(kWarps * 32), 0, stream, p);
 }
 
 // ---------------------------------------------------------------------------- scores

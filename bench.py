@@ -820,17 +820,40 @@ def serving_cases(ops):
     ]
 
 
+def more_serving_cases(ops):
+    """The cases of perf/more_operators.py, and what they leave out of the 4-bit decode and the selection."""
+    listed = ops.listed()
+    batch, long, sparse = ({c["name"]: c for c in listed}[n] for n in ("decode batch", "decode long", "sparse batch"))
+    return listed + [
+        dict(batch, name="decode batch, 16 heads", group=16),
+        dict(batch, name="decode batch, 20 heads", group=20),
+        dict(batch, name="decode batch, pages of 1", page=1),
+        dict(batch, name="decode batch, pages of 8", page=8),
+        dict(batch, name="decode batch, pages of 24", page=24),
+        dict(batch, name="decode batch, d 32", d=32),
+        dict(batch, name="decode batch, d 64", d=64),
+        dict(batch, name="decode batch, d 96", d=96),
+        dict(batch, name="decode batch, fp16", dtype="f16"),
+        dict(long, name="decode long, d 128", d=128),
+        dict(sparse, name="sparse batch, 16-bit", cache="same"),
+        dict(sparse, name="sparse batch, 8-bit", cache="e4m3"),
+        dict(sparse, name="sparse batch, pages of 8", page=8, budget=256),
+    ]
+
+
 def run_serving(args):
     """The rotary, cache and decode calls: device time of a call among others of its kind (three sets of tensors in turn,
     the median of 9 timings between two events), one JSON line."""
     import torch
 
     from attention_fa2_forward_02_gb300 import binding as B
-    from perf import operators as ops
-    pk, out = peaks(), {}
+    from perf import more_operators, operators
+    pk, first, more = peaks(), {}, {}
     sampler = ClockSampler(str(torch.cuda.current_device()))
     sampler.begin()
-    for case in serving_cases(ops):
+    cases = [(operators, first, c) for c in serving_cases(operators)]
+    cases += [(more_operators, more, c) for c in more_serving_cases(more_operators)]
+    for ops, out, case in cases:
         ops.own = True
         states = [ops.prepare(case, seed) for seed in range(3)]
         if "table_pages" in case:
@@ -858,7 +881,7 @@ def run_serving(args):
         del states
     B.fa2_device_status()
     sampler.end()
-    print(json.dumps({"serving": out, "clocks": sampler.stop(), "hbm_gbs": pk["hbm_gbs"], "data": "synthetic"}))
+    print(json.dumps({"serving": first, "more_serving": more, "clocks": sampler.stop(), "hbm_gbs": pk["hbm_gbs"], "data": "synthetic"}))
     return 0
 
 

@@ -89,6 +89,28 @@ def test_bounds_of_special_keys(dtype):
     assert torch.isnan(c.dev["k"][t[1], 1, 0, 2])
 
 
+@pytest.mark.parametrize("form", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("spread", [1, 13, 14, 15, 60])
+def test_bounds_of_rows_of_different_powers(spread, form):
+    """Rows whose powers of two lie up to so far apart in a page: the smallest codes of the smallest rows count, where a page has no others."""
+    torch = G.require_gpu()
+    c = cache_of(form, "bounds/powers", [200, 31], 16, 2, 64, stale=False)
+    exps = c.exps()["k_exp"]
+    up = (synth.counter_u16(f"bounds/powers/{spread}", tuple(exps.shape)) % (spread + 1)).astype(np.int64)
+    up[:, :, 0], up[:, :, 1] = 0, spread  # the whole spread in each page
+    exps += torch.from_numpy(up.astype(np.uint8)).cuda()
+    c.host["k"] = c.host["k"] * 2.0 ** up[..., None]
+    # a channel that is 0 but in the row of the lowest power, whose smallest code it has
+    small = 2.0 ** (exps[:, :, 0].cpu().numpy().astype(np.float64) - 127)
+    if form == "e4m3":
+        codes = c.dev["k"].view(torch.uint8)
+        codes[..., 5] = 0
+        codes[:, :, 0, 5] = 1
+        c.host["k"][..., 5], c.host["k"][:, :, 0, 5] = 0.0, 2.0 ** -9 * small
+    check_bounds(c, *make_bounds(c))
+    binding.fa2_device_status()
+
+
 def test_bounds_skip_bad_pages_and_positions():
     torch = G.require_gpu()
     c = Cache("bounds/bad", [40, 40, 20], 16, 2, 32)

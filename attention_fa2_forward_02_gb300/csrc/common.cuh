@@ -124,9 +124,11 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
 
 // Every thread of every CTA in the cluster, at the same point of the program: shared-memory
 // writes before it (to any CTA of the cluster) are visible after it.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_sync_all() {
-    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+    cluster_arrive();
+    cluster_wait();
 }
 
 __device__ __forceinline__ void mbar_arrive(uint32_t bar) {

@@ -384,19 +384,21 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, const Queries
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const uint32_t q_at = smem_u32(q.rows), my = smem_u32(ring) + (threadIdx.x >> 5) * (kDepth * 16 * kRow);
     const int per_row = p.d / 8;  // pieces
+    const int8_t* const bounds = p.bounds + (int64_t)hk * 2 * p.d;
+    const uint32_t page_bytes = (uint32_t)(p.hkv * 2 * p.d);
     auto look = [&](int64_t tile) { return lane < 16 && tile * 16 + lane < pages ? table[tile * 16 + lane] : -1; };
     // a tile's copies, one group of them; lane r has page r's power of two, or -1
     auto fetch = [&](int64_t tile, int page, uint32_t at) {
         float scale = -1.f;
         if (tile * 16 < pages) {
-            const int64_t row = page >= 0 && page < p.num_pages ? (int64_t)page * p.hkv + hk : -1;
-            if (row >= 0) scale = __uint_as_float((uint32_t)p.bounds_exp[row] << 23);
+            const int good = page >= 0 && page < p.num_pages ? page : -1;
+            if (good >= 0) scale = __uint_as_float((uint32_t)p.bounds_exp[(int64_t)good * p.hkv + hk] << 23);
 #pragma unroll
             for (int i = 0; i < 2 * kPieces; ++i) {  // 32 pieces at a time, row by row
                 const int n = 32 * i + lane, r = n / (4 * kPieces), piece = n % (4 * kPieces);
-                const int64_t here = __shfl_sync(0xffffffffu, row, r);
+                const int here = __shfl_sync(0xffffffffu, good, r);
                 const bool on = here >= 0 && piece < per_row;
-                copy16(at + r * kRow + (piece ^ (r % 2 * kFlip)) * 16, p.bounds + (on ? here * 2 * p.d + 16 * piece : 0), on);
+                copy16(at + r * kRow + (piece ^ (r % 2 * kFlip)) * 16, bounds + (on ? (uint64_t)(uint32_t)here * page_bytes + 16 * piece : 0), on);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
@@ -405,7 +407,7 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, const Queries
     auto finish = [&](int64_t tile, uint32_t at, float scale) {
         float best[2] = {-INFINITY, -INFINITY};
         for (int h0 = 0; h0 < p.group; h0 += 8) {
-            float c[4] = {};
+            float c2[2][4] = {};  // two chains of products
 #pragma unroll
             for (int i = 0; i < kPieces; ++i) {
                 const uint32_t b = q_at + (uint32_t)(h0 + g) * Queries<kPieces>::kRow + 128 * i + 32 * t;
@@ -417,10 +419,11 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, const Queries
 #pragma unroll
                 for (int w = 0; w < 4; ++w) {
                     const uint32_t y = u[w] ^ 0x80808080u, z = v[w] ^ 0x80808080u;
-                    mma_f16(c, __byte_perm(y, 0, 0x4140), __byte_perm(z, 0, 0x4140), __byte_perm(y, 0, 0x4342), __byte_perm(z, 0, 0x4342), bs[2 * w],
+                    mma_f16(c2[w % 2], __byte_perm(y, 0, 0x4140), __byte_perm(z, 0, 0x4140), __byte_perm(y, 0, 0x4342), __byte_perm(z, 0, 0x4342), bs[2 * w],
                             bs[2 * w + 1]);
                 }
             }
+            const float c[4] = {c2[0][0] + c2[1][0], c2[0][1] + c2[1][1], c2[0][2] + c2[1][2], c2[0][3] + c2[1][3]};
 #pragma unroll
             for (int n = 0; n < 2; ++n) {  // heads 2t, 2t+1
                 if (h0 + 2 * t + n >= p.group) continue;
@@ -496,6 +499,21 @@ struct SelectSmem {
     uint32_t bins[kBins];
     uint32_t found[3];
     uint32_t few, list[32];
+    __device__ __forceinline__ void begin() { found[0] = 0xffffffffu, found[1] = found[2] = few = 0; }
+};
+
+// The range of the scores that are not forced, and how many are.
+struct Range {
+    uint32_t lo = 0xffffffffu, hi = 0, forced = 0;
+    __device__ __forceinline__ void add(uint32_t key) {
+        if (key == kForced) ++forced;
+        else lo = min(lo, key), hi = max(hi, key);
+    }
+    __device__ __forceinline__ void reduce() {  // over the warp
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        forced = __reduce_add_sync(0xffffffffu, forced);
+    }
 };
 
 // All pages of row `row` (a sequence and head): there are no more than the budget.
@@ -513,31 +531,29 @@ __device__ __forceinline__ void take_all(const SelectParams& p, int row, const i
 // into kBins equal parts of the range that holds it, three times at the most (for 32 bits), mostly twice: the range
 // begins as that of the scores there are.
 // T: two counts of pages in one, 16 bits each (n < 2^16) or 32.
-template <int kThreads, typename T, typename Key>
+// kRanged: sm.found has the range and the number forced already, sm.few is 0.
+template <int kThreads, typename T, bool kRanged, typename Key>
 __device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm, int row, const int32_t* table, int n, int len, Key key) {
     constexpr int kHalf = 4 * sizeof(T);  // bits of a count
     constexpr T kOne = (T)1 << kHalf, kLow = kOne - 1;
     T* const sums = reinterpret_cast<T*>(sm.sums);
     const int lane = threadIdx.x & 31;
     // ---- the range of the scores that are not forced, and how many to take of those
-    uint32_t lo = 0xffffffffu, hi = 0, forced = 0;
+    uint32_t lo, hi;
+    if constexpr (!kRanged) {
+        Range range;
 #pragma unroll 1
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const uint32_t k = key(i);
-        if (k == kForced) ++forced;
-        else lo = min(lo, k), hi = max(hi, k);
+        for (int i = threadIdx.x; i < n; i += kThreads) range.add(key(i));
+        if (threadIdx.x == 0) sm.begin();
+        range.reduce();
+        __syncthreads();
+        if (lane == 0) {
+            atomicMin(&sm.found[0], range.lo);
+            atomicMax(&sm.found[1], range.hi);
+            if (range.forced) atomicAdd(&sm.found[2], range.forced);
+        }
+        __syncthreads();
     }
-    if (threadIdx.x == 0) sm.found[0] = 0xffffffffu, sm.found[1] = 0u, sm.found[2] = 0u, sm.few = 0;
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    forced = __reduce_add_sync(0xffffffffu, forced);
-    __syncthreads();
-    if (lane == 0) {
-        atomicMin(&sm.found[0], lo);
-        atomicMax(&sm.found[1], hi);
-        if (forced) atomicAdd(&sm.found[2], forced);
-    }
-    __syncthreads();
     lo = sm.found[0], hi = sm.found[1];
     uint32_t need = (uint32_t)p.budget - sm.found[2];
     uint32_t least = kForced - 1, equal = 0;  // all above `least` are taken and the earliest `equal` of those equal to it
@@ -635,19 +651,36 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) select_kernel(const Se
     Queries<kPieces> q(smem, padded);
     uint8_t* const ring = smem + Queries<kPieces>::bytes(p.group);
     uint32_t* scores = reinterpret_cast<uint32_t*>(ring + ring_bytes(kPieces));
+    if (threadIdx.x == 0) sm.begin();
+    cluster_arrive();  // all have started, the first one's counts are there: waited for before the first score
     grid_begin();
     const int len = bounded_len(p.lens[b], p.per_seq * p.page_size, p.status), n = pages_of(p, len);
     const int32_t* table = p.table + b * p.table_stride;
     if (n <= p.budget) {  // of the whole cluster
+        cluster_wait();
         if (rank == 0) take_all(p, row, table, n, len);
         return;
     }
-    const uint32_t to = cluster_map(smem_u32(scores), 0);
+    const uint32_t to = cluster_map(smem_u32(scores), 0), found = cluster_map(smem_u32(sm.found), 0);
+    Range range;
     score_tiles<kPieces>(
-        p, q, ring, table, hk, n, rank * kSelWarps + (int)(threadIdx.x >> 5), ranks * kSelWarps, [&] { q.template make<kBf16>(p, b, hk); },
-        [&](int j, uint32_t key) { asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 4 * j), "r"(key) : "memory"); });
+        p, q, ring, table, hk, n, rank * kSelWarps + (int)(threadIdx.x >> 5), ranks * kSelWarps,
+        [&] {
+            q.template make<kBf16>(p, b, hk);
+            cluster_wait();
+        },
+        [&](int j, uint32_t key) {
+            asm volatile("st.shared::cluster.u32 [%0], %1;" ::"r"(to + 4 * j), "r"(key) : "memory");
+            range.add(key);
+        });
+    range.reduce();
+    if (threadIdx.x % 32 == 0) {
+        asm volatile("red.relaxed.cluster.shared::cluster.min.u32 [%0], %1;" ::"r"(found), "r"(range.lo) : "memory");
+        asm volatile("red.relaxed.cluster.shared::cluster.max.u32 [%0], %1;" ::"r"(found + 4), "r"(range.hi) : "memory");
+        if (range.forced) asm volatile("red.relaxed.cluster.shared::cluster.add.u32 [%0], %1;" ::"r"(found + 8), "r"(range.forced) : "memory");
+    }
     cluster_sync_all();
-    if (rank == 0) select_row<kSelThreads, uint32_t>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
+    if (rank == 0) select_row<kSelThreads, uint32_t, true>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
 }
 
 // The same for tables too wide for that, in two launches through the workspace.
@@ -672,7 +705,7 @@ __global__ void __launch_bounds__(kWideThreads) wide_select_kernel(const SelectP
     const int32_t* table = p.table + b * p.table_stride;
     if (n <= p.budget) return take_all(p, row, table, n, len);
     const uint32_t* scores = p.scores + (int64_t)row * p.per_seq;
-    select_row<kWideThreads, unsigned long long>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
+    select_row<kWideThreads, unsigned long long, false>(p, sm, row, table, n, len, [&](int i) { return scores[i]; });
 }
 // Tables no wider than the budget: every page is taken, without a look at the bounds.
 __global__ void __launch_bounds__(kSelThreads) take_all_kernel(const SelectParams p) {

@@ -317,18 +317,20 @@ struct Queries {
     float2* stats;  // a head's -128 times the sum of its integers, and 2^e (0: no such head)
     __device__ Queries(uint8_t* smem, int padded) : rows(smem), stats(reinterpret_cast<float2*>(smem + (size_t)padded * kRow)) {}
 
-    // A warp a head, 4 channels a lane (d <= 128); every thread of the CTA calls it.
+    // A warp a head, 4 channels a lane (d <= 128).
+    static __device__ __forceinline__ uint2 load(const SelectParams& p, int b, int hk, int h) {
+        const int lane = threadIdx.x & 31;
+        if (h >= p.group || 4 * lane >= p.d) return make_uint2(0, 0);
+        return *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + b * p.q_batch + ((int64_t)hk * p.group + h) * p.q_head + 4 * lane);
+    }
+    // `first`: what load gave for this warp's first head. Every thread of the CTA calls it.
     template <bool kBf16>
-    __device__ __forceinline__ void make(const SelectParams& p, int b, int hk) {
+    __device__ __forceinline__ void make(const SelectParams& p, int b, int hk, uint2 first) {
         const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, padded = (p.group + 7) / 8 * 8;
         for (int h = warp; h < padded; h += kSelWarps) {
-            float x[4] = {}, a = 0.f;
-            if (h < p.group && 4 * lane < p.d) {
-                const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p.q) + b * p.q_batch +
-                                                                ((int64_t)hk * p.group + h) * p.q_head + 4 * lane);
-                const float2 f = floats<kBf16>(w.x), g = floats<kBf16>(w.y);
-                x[0] = f.x, x[1] = f.y, x[2] = g.x, x[3] = g.y;
-            }
+            const uint2 w = h == warp ? first : load(p, b, hk, h);
+            const float2 f = floats<kBf16>(w.x), g = floats<kBf16>(w.y);
+            float x[4] = {f.x, f.y, g.x, g.y}, a = 0.f;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 if (x[i] != x[i]) x[i] = 0.f;
@@ -374,7 +376,7 @@ __device__ __forceinline__ uint4 load16(uint32_t addr) {
 // exact. (GB300, products a quarter of an SM can begin: one of 8-bit integers, 32 terms, every 63 cycles, one of halves,
 // 16 terms, every 8; sums of four products 2 cycles for a 512th of either's 8192.)
 // A page's number and its bounds follow one another from far away, 2 us and more: kDepth tiles are on their way or in
-// use a warp, the first ones while `meanwhile` runs. (In registers they would not fit, and a register that is spilled
+// use a warp; `meanwhile` runs while the first page numbers come. (In registers they would not fit, and a register that is spilled
 // waits for its load: 35 us for 42 MB that way.)
 constexpr int kDepth = 3;
 template <int kPieces, typename Meanwhile, typename Put>
@@ -453,10 +455,10 @@ __device__ __forceinline__ void score_tiles(const SelectParams& p, const Queries
     int ahead[kDepth];
 #pragma unroll
     for (int i = 0; i < kDepth; ++i) ahead[i] = look(tile + i * (int64_t)step);
+    meanwhile();
 #pragma unroll
     for (int i = 0; i < kDepth - 1; ++i) scales[i] = fetch(tile + i * (int64_t)step, ahead[i], my + i * 16 * kRow);
     int next = ahead[kDepth - 1];
-    meanwhile();
     int use = 0, fill = kDepth - 1;
     for (; tile * 16 < pages; tile += step) {  // (no warp waits for another in here)
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 2) : "memory");
@@ -654,6 +656,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) select_kernel(const Se
     if (threadIdx.x == 0) sm.begin();
     cluster_arrive();  // all have started, the first one's counts are there: waited for before the first score
     grid_begin();
+    const uint2 first_head = q.load(p, b, hk, threadIdx.x >> 5);
     const int len = bounded_len(p.lens[b], p.per_seq * p.page_size, p.status), n = pages_of(p, len);
     const int32_t* table = p.table + b * p.table_stride;
     if (n <= p.budget) {  // of the whole cluster
@@ -666,7 +669,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) select_kernel(const Se
     score_tiles<kPieces>(
         p, q, ring, table, hk, n, rank * kSelWarps + (int)(threadIdx.x >> 5), ranks * kSelWarps,
         [&] {
-            q.template make<kBf16>(p, b, hk);
+            q.template make<kBf16>(p, b, hk, first_head);
             cluster_wait();
         },
         [&](int j, uint32_t key) {
@@ -690,12 +693,13 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) wide_scores_kernel(con
     const int padded = (p.group + 7) / 8 * 8, row = blockIdx.x / row_ctas, cta = blockIdx.x % row_ctas, b = row / p.hkv, hk = row % p.hkv;
     Queries<kPieces> q(smem, padded);
     grid_begin();
+    const uint2 first_head = q.load(p, b, hk, threadIdx.x >> 5);
     const int n = pages_of(p, bounded_len(p.lens[b], p.per_seq * p.page_size, p.status));
     if (n <= p.budget || (int64_t)cta * kSelWarps * 16 >= n) return;
     uint32_t* out = p.scores + (int64_t)row * p.per_seq;
     score_tiles<kPieces>(
         p, q, smem + Queries<kPieces>::bytes(p.group), p.table + b * p.table_stride, hk, n, cta * kSelWarps + (int)(threadIdx.x >> 5), row_ctas * kSelWarps,
-        [&] { q.template make<kBf16>(p, b, hk); }, [&](int j, uint32_t key) { out[j] = key; });
+        [&] { q.template make<kBf16>(p, b, hk, first_head); }, [&](int j, uint32_t key) { out[j] = key; });
 }
 __global__ void __launch_bounds__(kWideThreads) wide_select_kernel(const SelectParams p) {
     __shared__ SelectSmem sm;

@@ -491,8 +491,12 @@ __device__ __forceinline__ T scan(T v, T* sums) {
     if (lane == 31) sums[warp] = upto;
     __syncthreads();
     T before = 0;
+    if constexpr (sizeof(T) == 4) {
+        before = __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0);
+    } else {
 #pragma unroll 1  // (a kernel that runs once waits for its instructions: few of them)
-    for (int w = 0; w < warp; ++w) before += sums[w];
+        for (int w = 0; w < warp; ++w) before += sums[w];
+    }
     return before + upto - v;
 }
 
@@ -500,7 +504,8 @@ struct SelectSmem {
     unsigned long long sums[32];
     uint32_t bins[kBins];
     uint32_t found[3];
-    uint32_t few, list[32];
+    uint32_t few;
+    __align__(16) uint32_t list[32];
     __device__ __forceinline__ void begin() { found[0] = 0xffffffffu, found[1] = found[2] = few = 0; }
 };
 
@@ -606,7 +611,12 @@ __device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm
             const uint32_t mine = lane < (int)left ? sm.list[lane] : 0u;
             uint32_t above_it = 0, alike = 0;
 #pragma unroll 1
-            for (uint32_t i = 0; i < left; ++i) above_it += sm.list[i] > mine, alike += sm.list[i] == mine;
+            for (uint32_t i = 0; i < left; i += 4) {
+                const uint4 four = *reinterpret_cast<const uint4*>(&sm.list[i]);
+                const uint32_t x[4] = {four.x, four.y, four.z, four.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) above_it += i + j < left && x[j] > mine, alike += i + j < left && x[j] == mine;
+            }
             const uint32_t who = __ballot_sync(0xffffffffu, lane < (int)left && above_it < need && need <= above_it + alike);
             least = __shfl_sync(0xffffffffu, mine, __ffs(who) - 1);
             equal = need - __shfl_sync(0xffffffffu, above_it, __ffs(who) - 1);

@@ -33,8 +33,8 @@
 // operands are made in registers (a byte of two codes to a pair of halves, times the group's scale; the lanes' pieces
 // of a row are permuted alike on both sides of a product, so no element moves between lanes). That and the products
 // bound it, not its 73 bytes a row: about 350 instructions for 16 keys of 128, issued in 57 of 100 cycles. GB300, 32
-// sequences of up to 8192 (d 128, 8 heads on each of 8, 193 MB): 57 us, 3.4 TB/s; 21 of up to 65536 (d 64, half, 507
-// MB): 170 us, 3.0 TB/s, where each weight takes two products.
+// sequences of up to 8192 (d 128, 8 heads on each of 8, 193 MB): 56 us, 3.5 TB/s; 21 of up to 65536 (d 64, half, 507
+// MB): 168 us, 3.0 TB/s, where each weight takes two products.
 //
 // Contexts that can only be short (by the block table's width, or the window) take one launch: the
 // CTAs of a thread-block cluster share an item and join their results in distributed shared
@@ -139,13 +139,6 @@ __device__ __forceinline__ void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
 
-__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t (&r)[4]) {  // lanes 0 .. 15 give addresses
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-}
-__device__ __forceinline__ void ldsm2_t(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.trans.shared.b16 {%0, %1}, [%2];" : "=r"(r[0]), "=r"(r[1]) : "r"(addr) : "memory");
-}
-
 // kBytes: 4 or 8, read where `on`, else zeros
 template <int kBytes>
 __device__ __forceinline__ void cp_async_small(uint32_t dst, const void* src, bool on) {
@@ -157,6 +150,11 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint32_t v) {
 __device__ __forceinline__ void st_shared_u32(uint32_t addr, uint32_t v) { asm volatile("st.shared.u32 [%0], %1;" ::"r"(addr), "r"(v) : "memory"); }
 __device__ __forceinline__ void st_shared_v2(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
+}
+__device__ __forceinline__ uint32_t ld_shared_u8(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ uint32_t ld_shared_u16(uint32_t addr) {
     uint16_t v;
@@ -179,46 +177,45 @@ __device__ __forceinline__ uint4 ld_shared_v4(uint32_t addr) {
     return v;
 }
 
-// The lower or the upper half of a pair, twice.
-__device__ __forceinline__ uint32_t twice(uint32_t pair, bool upper) {
-    const __half2 x = *reinterpret_cast<const __half2*>(&pair), y = upper ? __high2half2(x) : __low2half2(x);
-    return *reinterpret_cast<const uint32_t*>(&y);
+// 4-bit rows. Which 16 keys and which of their codes are a product's rows and terms is free, as long as the other operand has
+// the same order, so each lane takes codes that lie together: for the scores, of a key, the D / 4 from D / 4 t on (a piece of
+// 16, 8 or 4 bytes, one or two scales), for O, of four keys, the D / 8 from D / 8 g on (8, 4 or 2 bytes, a scale a key).
+// Row r of eight is key key_of(r), an order in which neither reads a bank twice: D = 128 0 3 4 7 1 2 5 6, 64 0 6 1 7 2 4 3 5.
+// (As matrix loads bring them, with 4 scales a key and side and pairs of keys made after the conversion: batch of 32 57.3 us,
+// 55.8 so; in half 62.7 and 59.5; 21 contexts of up to 65536 at d 128 257 and 242; d 32 27.6 and 28.2.)
+template <int D>
+__device__ __forceinline__ int key_of(int r) {
+    return D == 128 ? (0x65217430u >> (4 * r)) & 7 : (D == 64 ? (0x53427160u >> (4 * r)) & 7 : r);
 }
 
-// A key's scales of groups `half`, half + 2, ... as pairs of the same half number; `row`: its D / 16 bytes.
+// A key's scales for each 8 of this lane's codes, as pairs of the same half; `row`: the key's D / 16 bytes.
 template <int D>
-__device__ __forceinline__ void key_scales(uint32_t row, int half, uint32_t (&s)[D / 32]) {
-    if constexpr (D == 32) {
-        s[0] = twice(e4m3x2_to_f16x2(ld_shared_u16(row)), half);
+__device__ __forceinline__ void key_scales(uint32_t row, int t, uint32_t (&s)[D / 32]) {
+    if constexpr (D == 128) {
+        const uint32_t two = e4m3x2_to_f16x2(ld_shared_u16(row + 2 * t));
+        s[0] = s[1] = __byte_perm(two, 0, 0x1010);
+        s[2] = s[3] = __byte_perm(two, 0, 0x3232);
     } else {
-        uint32_t w;
-        if constexpr (D == 128) {
-            const uint2 b = ld_shared_v2(row);
-            w = __byte_perm(b.x, b.y, half ? 0x7531 : 0x6420);
-        } else {
-            w = __byte_perm(ld_shared_u32(row), 0, half ? 0x4431 : 0x4420);
-        }
-        uint32_t f[2];
-        e4m3x4_to_f16x4(w, f[0], f[1]);
+        const uint32_t one = e4m3x2_to_f16x2(ld_shared_u8(row + (D == 64 ? t : t / 2)) * 0x101u);
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) s[i] = twice(f[i / 2], i % 2);
+        for (int i = 0; i < D / 32; ++i) s[i] = one;
     }
 }
 
-// Two keys' scales of groups `half`, half + 2, ..., the first key's in the lower half; `rows`: their 2 D / 16 bytes.
-template <int D>
-__device__ __forceinline__ void value_scales(uint32_t rows, int half, uint32_t (&s)[D / 32]) {
-    if constexpr (D == 32) {
-        const uint32_t w = ld_shared_u32(rows);
-        s[0] = e4m3x2_to_f16x2(__byte_perm(w, 0, half ? 0x4431 : 0x4420));
-    } else if constexpr (D == 64) {
-        const uint2 w = ld_shared_v2(rows);
-        e4m3x4_to_f16x4(__byte_perm(w.x, w.y, half ? 0x7351 : 0x6240), s[0], s[1]);
+// A lane's codes of a key: D / 8 bytes (kHalf: D / 16), in words.
+template <int D, bool kHalf>
+__device__ __forceinline__ void lane_codes(uint32_t addr, uint32_t (&w)[kHalf ? (D + 63) / 64 : D / 32]) {
+    constexpr int kBytes = kHalf ? D / 16 : D / 8;
+    if constexpr (kBytes == 16) {
+        const uint4 x = ld_shared_v4(addr);
+        w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+    } else if constexpr (kBytes == 8) {
+        const uint2 x = ld_shared_v2(addr);
+        w[0] = x.x, w[1] = x.y;
+    } else if constexpr (kBytes == 4) {
+        w[0] = ld_shared_u32(addr);
     } else {
-        const uint4 w = ld_shared_v4(rows);
-        const uint32_t a = __byte_perm(w.x, w.y, half ? 0x7531 : 0x6420), b = __byte_perm(w.z, w.w, half ? 0x7531 : 0x6420);
-        e4m3x4_to_f16x4(__byte_perm(a, b, 0x5140), s[0], s[1]);
-        e4m3x4_to_f16x4(__byte_perm(a, b, 0x7362), s[2], s[3]);
+        w[0] = ld_shared_u16(addr);
     }
 }
 
@@ -845,6 +842,18 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     int number = 0, use = 0;                // the segment's number, the stage to use next
     bool first_item = true;
     Torn ends_later{0, 0, 0, 0};
+    // e2m1: where a lane's codes of K's row g and V's rows 2t, 2t+1 lie in a tile, V's scales (rows 8 and 16 further the same)
+    const int row_key = kE2m1 ? key_of<D>(g) : g;
+    uint32_t k_at = 0, v_at[2] = {0, 0}, vs_at[2] = {0, 0};
+    if constexpr (kE2m1) {
+        k_at = swizzle<C::kChunks>(row_key, D / 8 * t / 16) * 16 + D / 8 * t % 16;
+#pragma unroll
+        for (int n = 0; n < 2; ++n) {
+            const int key = key_of<D>(2 * t + n);
+            v_at[n] = swizzle<C::kChunks>(key, D / 16 * g / 16) * 16 + D / 16 * g % 16;
+            vs_at[n] = key * C::kScaleRow + D / 8 * g / 16;
+        }
+    }
 
     for (; live; ++number) {
         const int hk = seg.item / hblocks, hb = seg.item % hblocks;
@@ -873,21 +882,11 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                 for (int i = 0; i < 8; ++i)
                     w[i] = pack2<false>(__uint_as_float(w[i] << 16) * up, __uint_as_float(w[i] & 0xffff0000u) * up);
             }
-            // 8-bit cache: elements 4t .. 4t+3 of 16 as columns 2t, 2t+1, 2t+8, 2t+9, the order its codes come in;
-            // 4-bit cache: the same of elements 8t .. 8t+3, and 8t+4 .. 8t+7, of 32 for its two steps of 16
+            // 8-bit cache: elements 4t .. 4t+3 of 16 as columns 2t, 2t+1, 2t+8, 2t+9, the order its codes come in
             if (r < kRows) {
                 uint4* row = reinterpret_cast<uint4*>(q_smem);
-                if constexpr (kE2m1) {
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int e = 0; e < 2; ++e)
-                            reinterpret_cast<uint2*>(row + swizzle<D / 8>(r, 4 * (part / 2) + 2 * m + e))[part % 2] =
-                                make_uint2(w[2 * m + e], w[4 + 2 * m + e]);
-                } else {
                 row[swizzle<D / 8>(r, 2 * part)] = kE4m3 ? make_uint4(w[0], w[2], w[4], w[6]) : make_uint4(w[0], w[1], w[2], w[3]);
                 row[swizzle<D / 8>(r, 2 * part + 1)] = kE4m3 ? make_uint4(w[1], w[3], w[5], w[7]) : make_uint4(w[4], w[5], w[6], w[7]);
-                }
                 if (part == 0) q_scale[r] = scale;
             }
         }
@@ -900,7 +899,12 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
 #pragma unroll
             for (int kk = 0; kk < D / 16; kk += 2) {
                 uint32_t q4[4];
-                ldsm4(q_addr + swizzle<D / 8>(8 * h + (lane & 7), 2 * kk + (lane >> 3)) * 16, q4);
+                if constexpr (kE2m1) {  // 8 elements for each 8 of the lane's codes, 4 of them a step
+                    const uint4 x = ld_shared_v4(q_addr + swizzle<D / 8>(8 * h + g, D / 32 * t + kk / 2) * 16);
+                    q4[0] = x.x, q4[1] = x.y, q4[2] = x.z, q4[3] = x.w;
+                } else {
+                    ldsm4(q_addr + swizzle<D / 8>(8 * h + (lane & 7), 2 * kk + (lane >> 3)) * 16, q4);
+                }
                 qf[h][kk][0] = q4[0];
                 qf[h][kk][1] = q4[1];
                 qf[h][kk + 1][0] = q4[2];
@@ -968,30 +972,24 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
             } else if constexpr (kE2m1) {
 #pragma unroll
                 for (int j = 0; j < kMt; ++j) {
-                    // the scales of keys g, g + 8 (in half, twice) for this lane's half t / 2 of each 32 codes
-                    uint32_t ks[2][D / 32];
+                    uint32_t ks[2][D / 32], kw[2][D / 32];  // of the keys of rows g, g + 8
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        key_scales<D>(vt + C::kTile + C::kInfo + (16 * j + 8 * e + g) * C::kScaleRow, t >> 1, ks[e]);
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = 16 * j + 8 * e;
+                        key_scales<D>(vt + C::kTile + C::kInfo + (key + row_key) * C::kScaleRow, t, ks[e]);
+                        lane_codes<D, false>(kt + key * C::kRowBytes + k_at, kw[e]);
+                    }
 #pragma unroll
-                    for (int cc = 0; cc < D / 32; cc += 2) {
-                        uint32_t k4[4];  // (keys 0-7, 8-15) of 32 codes, of the next 32: codes 8t .. 8t+7
-                        const uint32_t at = kt + swizzle<C::kChunks>(16 * j + (lane & 15), C::kChunks > 1 ? cc + (lane >> 4) : 0) * 16;
-                        if constexpr (C::kChunks > 1) ldsm4(at, k4);
-                        else ldsm2(at, k4);
+                    for (int w = 0; w < D / 32; ++w) {
+                        uint32_t a[4], b[4];
+                        e2m1x8_to_f16x8(kw[0][w], a);
+                        e2m1x8_to_f16x8(kw[1][w], b);
 #pragma unroll
-                        for (int e = 0; e < 2 && cc + e < D / 32; ++e) {
-                            uint32_t a[4], b[4];  // pairs of codes of key g, of key g + 8
-                            e2m1x8_to_f16x8(k4[2 * e], a);
-                            e2m1x8_to_f16x8(k4[2 * e + 1], b);
+                        for (int m = 0; m < 2; ++m) {
+                            const uint32_t a4[4] = {hmul2(a[2 * m], ks[0][w]), hmul2(b[2 * m], ks[1][w]), hmul2(a[2 * m + 1], ks[0][w]),
+                                                    hmul2(b[2 * m + 1], ks[1][w])};
 #pragma unroll
-                            for (int m = 0; m < 2; ++m) {
-                                const uint32_t a4[4] = {hmul2(a[2 * m], ks[0][cc + e]), hmul2(b[2 * m], ks[1][cc + e]),
-                                                        hmul2(a[2 * m + 1], ks[0][cc + e]), hmul2(b[2 * m + 1], ks[1][cc + e])};
-#pragma unroll
-                                for (int h = 0; h < kTiles; ++h)
-                                    mma16816<false>(sc[j][h], a4, qf[h][2 * (cc + e) + m][0], qf[h][2 * (cc + e) + m][1]);
-                            }
+                            for (int h = 0; h < kTiles; ++h) mma16816<false>(sc[j][h], a4, qf[h][2 * w + m][0], qf[h][2 * w + m][1]);
                         }
                     }
                 }
@@ -1019,7 +1017,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                 for (int j = 0; j < kMt; ++j)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const float2 f = reinterpret_cast<const float2*>(info)[16 * j + 8 * e + g];
+                        const float2 f = reinterpret_cast<const float2*>(info)[16 * j + 8 * e + row_key];
                         ev[j][e] = f.y;
                         const float off = f.y == -INFINITY ? -INFINITY : 0.f;
 #pragma unroll
@@ -1120,7 +1118,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                         for (int j = 0; j < kMt; ++j)
 #pragma unroll
                             for (int e = 0; e < 2; ++e)
-                                if ((zeros[j / 2] >> (16 * (j % 2) + 8 * e + g)) & 1u) {
+                                if ((zeros[j / 2] >> (16 * (j % 2) + 8 * e + row_key)) & 1u) {
 #pragma unroll
                                     for (int h = 0; h < kTiles; ++h) sc[j][h][2 * e] = sc[j][h][2 * e + 1] = -INFINITY;
                                 }
@@ -1181,31 +1179,38 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                         }
                     }
                 } else if constexpr (kE2m1) {
-                    // the scales of keys 2t, 2t+1 (and + 8) for this lane's half g / 4 of each 32 codes
-                    uint32_t vs[2][D / 32];
+                    // rows 2t, 2t+1 (and + 8): the keys' scale as a pair, the codes as bytes of one key's and the other's
+                    const uint32_t sc_at = vt + C::kTile + C::kInfo + C::kScales + 16 * j * C::kScaleRow;
+                    constexpr int kVw = (D + 63) / 64;
+                    uint32_t vs[2], even[2][kVw], odd[2][kVw];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        value_scales<D>(vt + C::kTile + C::kInfo + C::kScales + (16 * j + 8 * e + 2 * t) * C::kScaleRow, g >> 2, vs[e]);
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t s = sc_at + 8 * e * C::kScaleRow;
+                        vs[e] = e4m3x2_to_f16x2(ld_shared_u8(s + vs_at[0]) + ld_shared_u8(s + vs_at[1]) * 256u);
+                        uint32_t a[kVw], b[kVw];
+                        lane_codes<D, true>(vt + (16 * j + 8 * e) * C::kRowBytes + v_at[0], a);
+                        lane_codes<D, true>(vt + (16 * j + 8 * e) * C::kRowBytes + v_at[1], b);
 #pragma unroll
-                    for (int cc = 0; cc < D / 32; cc += 2) {
-                        uint32_t v4[4];  // (keys 0-7, 8-15) of 32 codes, of the next 32: keys 2t, 2t+1 x codes 4g .. 4g+3
-                        const uint32_t at = vt + swizzle<C::kChunks>(16 * j + (lane & 15), C::kChunks > 1 ? cc + (lane >> 4) : 0) * 16;
-                        if constexpr (C::kChunks > 1) ldsm4_t(at, v4);
-                        else ldsm2_t(at, v4);
+                        for (int w = 0; w < kVw; ++w) {
+                            even[e][w] = (a[w] & 0x0f0f0f0fu) | ((b[w] << 4) & 0xf0f0f0f0u);
+                            odd[e][w] = ((a[w] >> 4) & 0x0f0f0f0fu) | (b[w] & 0xf0f0f0f0u);
+                        }
+                    }
 #pragma unroll
-                        for (int e = 0; e < 2 && cc + e < D / 32; ++e) {
-                            uint32_t lo[4], hi[4];  // code 4g + i of keys 2t, 2t+1; of keys 2t+8, 2t+9
-                            e2m1_2x4_to_f16(v4[2 * e], lo);
-                            e2m1_2x4_to_f16(v4[2 * e + 1], hi);
+                    for (int w = 0; w < kVw; ++w) {  // rows g: the even codes, rows g + 8: the odd ones
+                        uint32_t x[2][4], y[2][4];
 #pragma unroll
-                            for (int m = 0; m < 2; ++m) {  // rows g: codes 4g + 2m, rows g + 8: 4g + 2m + 1
-                                const uint32_t a4[4] = {hmul2(lo[2 * m], vs[0][cc + e]), hmul2(lo[2 * m + 1], vs[0][cc + e]),
-                                                        hmul2(hi[2 * m], vs[1][cc + e]), hmul2(hi[2 * m + 1], vs[1][cc + e])};
+                        for (int e = 0; e < 2; ++e) {
+                            e2m1x8_to_f16x8(even[e][w], x[e]);
+                            e2m1x8_to_f16x8(odd[e][w], y[e]);
+                        }
 #pragma unroll
-                                for (int h = 0; h < kTiles; ++h) {
-                                    mma16816<false>(o[2 * (cc + e) + m][h], a4, pf[h][0], pf[h][1]);
-                                    if constexpr (kRest) mma16816<false>(o[2 * (cc + e) + m][h], a4, pl[h][0], pl[h][1]);
-                                }
+                        for (int i = 0; i < 4 && 4 * w + i < D / 16; ++i) {
+                            const uint32_t a4[4] = {hmul2(x[0][i], vs[0]), hmul2(y[0][i], vs[0]), hmul2(x[1][i], vs[1]), hmul2(y[1][i], vs[1])};
+#pragma unroll
+                            for (int h = 0; h < kTiles; ++h) {
+                                mma16816<false>(o[4 * w + i][h], a4, pf[h][0], pf[h][1]);
+                                if constexpr (kRest) mma16816<false>(o[4 * w + i][h], a4, pl[h][0], pl[h][1]);
                             }
                         }
                     }
@@ -1268,7 +1273,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                             row[16 * d + g] = o[d][h][n];
                             row[16 * d + 8 + g] = o[d][h][2 + n];
                         } else if constexpr (kE2m1) {
-                            *reinterpret_cast<float2*>(row + 32 * (d / 2) + 4 * g + 2 * (d % 2)) = make_float2(o[d][h][n], o[d][h][2 + n]);
+                            *reinterpret_cast<float2*>(row + D / 8 * g + 2 * d) = make_float2(o[d][h][n], o[d][h][2 + n]);
                         } else {
                             *reinterpret_cast<float2*>(row + 16 * d + 2 * g) = make_float2(o[d][h][n], o[d][h][2 + n]);
                         }

@@ -85,18 +85,6 @@ __device__ __forceinline__ void e2m1x8_to_f16x8(uint32_t codes, uint32_t (&r)[4]
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(codes));
 }
 
-// Four codes of each of two rows, the first row's in the lower half of the word -> four pairs of halves, code i
-// of the first and of the second row in pair i. (Converted first, paired after: 8 instructions; pairs of codes made of
-// nibbles first take 11, and the unit that does them is the decode's busiest.)
-__device__ __forceinline__ void e2m1_2x4_to_f16(uint32_t codes, uint32_t (&r)[4]) {
-    uint32_t x[4];
-    e2m1x8_to_f16x8(codes, x);
-    r[0] = __byte_perm(x[0], x[2], 0x5410);
-    r[1] = __byte_perm(x[0], x[2], 0x7632);
-    r[2] = __byte_perm(x[1], x[3], 0x5410);
-    r[3] = __byte_perm(x[1], x[3], 0x7632);
-}
-
 __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
     const __half2 x = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
     return *reinterpret_cast<const uint32_t*>(&x);

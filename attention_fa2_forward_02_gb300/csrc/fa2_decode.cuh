@@ -575,7 +575,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
     // a page, and copy them: no address crosses lanes. (One key a lane, as below, took 390 instructions a block of 32
     // keys, more than its products.)
     const bool sixteens = c.page_size % 16 == 0;
-    constexpr bool by_sixteens = C::kSixteens;
+    const bool by_sixteens = C::kSixteens;
     constexpr int kTeam = kE2m1 ? 512 / kKeys : 32;
     int page[C::kLooks], slot[C::kLooks];  // slot -1: no such key
     int64_t head_off = 0, head_exp = 0;    // and the block's head

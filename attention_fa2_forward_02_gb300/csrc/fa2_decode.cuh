@@ -32,7 +32,7 @@
 // The 4-bit cache is the same with code * scale, 6 bits and exact in half, in the place of the code: K's and V's
 // operands are made in registers (a byte of two codes to a pair of halves, times the group's scale; the lanes' pieces
 // of a row are permuted alike on both sides of a product, so no element moves between lanes). That and the products
-// bound it, not its 73 bytes a row: about 350 instructions for 16 keys of 128, issued in 57 of 100 cycles. GB300, 32
+// bound it, not its 73 bytes a row: 420 instructions for 16 keys of 128, issued in 57 of 100 cycles. GB300, 32
 // sequences of up to 8192 (d 128, 8 heads on each of 8, 193 MB): 56 us, 3.5 TB/s; 21 of up to 65536 (d 64, half, 507
 // MB): 168 us, 3.0 TB/s, where each weight takes two products.
 //

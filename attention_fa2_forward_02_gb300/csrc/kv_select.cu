@@ -17,7 +17,8 @@
 //
 // Latency bounds it: each step of the chain length - table - bounds - scores - counts - pages waits 1 to 3 us, so it is one
 // launch where it can be (with the attention, 16 sequences: 43.5 us, 48.8 in two). GB300, 128 of 1876 pages for each of 8
-// heads of one sequence: 9.5 us; 64 of up to 2048 pages for each of 8 heads of 16 sequences, 42 MB of bounds: 23 us.
+// heads of one sequence: 8.2 us; 64 of up to 2048 pages for each of 8 heads of 16 sequences, 42 MB of bounds: 21 us, 12 of
+// them the scores of the longest row, whose tiles and queries pass through shared memory at half its rate.
 #include <algorithm>
 
 #include "paged.cuh"

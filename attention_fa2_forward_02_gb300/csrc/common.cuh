@@ -122,10 +122,11 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return v;
 }
 
-// Every thread of every CTA in the cluster, at the same point of the program: shared-memory
-// writes before it (to any CTA of the cluster) are visible after it.
+// The halves of cluster_sync_all, with work between them.
 __device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// Every thread of every CTA in the cluster, at the same point of the program: shared-memory
+// writes before it (to any CTA of the cluster) are visible after it.
 __device__ __forceinline__ void cluster_sync_all() {
     cluster_arrive();
     cluster_wait();

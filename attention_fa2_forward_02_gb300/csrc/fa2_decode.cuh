@@ -753,8 +753,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
         fill = fill + 1 == S ? 0 : fill + 1;
     };
     // e2m1, by sixteens, before a block of keys key0 .. of the range is used: its info from the bytes of its powers of two (0:
-    // the page is not there); rows of d / 16 scale bytes to kScaleRow; and zeros for the scales of keys that do not count, so
-    // that whatever lies there (a NaN) times any code is zero.
+    // the page is not there); rows of d / 16 scale bytes to kScaleRow; and zeros for the scales and the power of two of keys that do
+    // not count, so that whatever lies there (a NaN, a byte of 255) leaves them a product of zero and a score of -infinity.
     auto tidy = [&](uint8_t* stage, int key0, const Range& range) {
         if constexpr (kE2m1) {
             if (!by_sixteens) return;
@@ -766,7 +766,8 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                 const uint32_t k = stage[C::kExps + r], v = stage[C::kExps + kKeys + r];
                 counts[j] = v != 0 && key >= range.first && key < range.len;
                 all = all && counts[j];
-                reinterpret_cast<float2*>(stage + 2 * C::kTile)[r] = make_float2(__uint_as_float(k << 23), counts[j] ? (float)((int)v - 127) : -INFINITY);
+                reinterpret_cast<float2*>(stage + 2 * C::kTile)[r] =
+                    counts[j] ? make_float2(__uint_as_float(k << 23), (float)((int)v - 127)) : make_float2(0.f, -INFINITY);
             }
             if (widen || __any_sync(0xffffffffu, !all)) {
                 const uint32_t scales = smem_u32(stage) + 2 * C::kTile + C::kInfo;

@@ -1107,6 +1107,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                         uint32_t any = 0;
 #pragma unroll
                         for (int i = 0; i < C::kChunks; ++i) {
+                            if (C::kSixteens && 32 * i >= c.d) break;  // (pieces past the head's size were not copied)
                             const uint4 w = *reinterpret_cast<const uint4*>(info - C::kTile + swizzle<C::kChunks>(r, i) * 16);
                             any |= w.x | w.y | w.z | w.w;
                         }

@@ -169,6 +169,41 @@ struct PageKeys {
             l[2 * i] = x.x * power, l[2 * i + 1] = x.y * power, u[2 * i] = y.x * power, u[2 * i + 1] = y.y * power;
         }
     }
+
+    // The largest finite magnitude in the lane's channels, which the lowest and the highest do not tell where they are infinite.
+    // (Rare: a row at a time.)
+    template <bool kBf16>
+    __device__ __forceinline__ float largest() const {
+        float a = 0.f;
+#pragma unroll 1
+        for (int s = gr; s < live; s += kGroups) {
+            const float two = kForm == kRows16 ? 1.f : __uint_as_float((uint32_t)c.k_exp[exp0 + s] << 23);
+            uint32_t of16 = 0;
+            if constexpr (kForm == kRowsE2m1) of16 = e4m3x2_to_f16x2(c.k_scale[(exp0 + s) * (c.d / 16) + part] * 0x101u);
+#pragma unroll 1
+            for (int i = 0; i < 2; ++i) {  // 8 channels
+                const char* at = (kForm == kRows16 && i ? second : base + i * kWords / 2 * 4) + s * c.slot_stride;
+                uint32_t x[4];
+                if constexpr (kForm == kRows16) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(at);
+                    x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w;
+                } else if constexpr (kForm == kRowsE4m3) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(at);
+                    e4m3x4_to_f16x4(w.x, x[0], x[1]);
+                    e4m3x4_to_f16x4(w.y, x[2], x[3]);
+                } else {
+                    e2m1x8_to_f16x8(*reinterpret_cast<const uint32_t*>(at), x);
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 y = floats<kForm == kRows16 && kBf16>(kForm == kRowsE2m1 ? hmul2(x[j], of16) : x[j]);
+                    const float p = fabsf(y.x * two), q = fabsf(y.y * two);
+                    a = fmaxf(a, fmaxf(p < INFINITY ? p : 0.f, q < INFINITY ? q : 0.f));
+                }
+            }
+        }
+        return a;
+    }
 };
 
 // A warp takes one page of one sequence and one head: groups of kLanes lanes read slots in turn, 16 channels a lane.
@@ -245,10 +280,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv_bounds_kernel(const KvBoundsPa
 #pragma unroll
     for (int i = 0; i < kOwn; ++i) {
         if (l[i] > u[i]) l[i] = u[i] = 0.f;  // nothing but NaN
-        const float x = fabsf(l[i]), y = fabsf(u[i]);
-        a = fmaxf(a, fmaxf(x < INFINITY ? x : 0.f, y < INFINITY ? y : 0.f));
+        a = fmaxf(a, fmaxf(fabsf(l[i]), fabsf(u[i])));
     }
-    const int e = bound_exp(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(a))));
+    auto of_all = [](float x) { return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(x))); };
+    a = of_all(a);
+    if (a == INFINITY) a = of_all(keys.template largest<kBf16>());
+    const int e = bound_exp(a);
     const int channel = 16 * li + 2 * w0;
     if (channel >= c.d || gr >= 8) return;  // (16 groups end with the same twice)
     const float inv = exp2_of(-e);

@@ -615,8 +615,8 @@ fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_ca
  * fa2_rope_append, with the same cu_new and seq_lens (tokens: the rows of k and v there).
  *   2^e, e = byte - 127 is the smallest power of two with every finite |key| <= 127 * 2^e, e no
  *   less than -60 (0 for keys of zeros); the lowest is rounded down, the highest up, so that
- *   low * 2^e <= key <= high * 2^e for every live key; infinities count as 127 * 2^e with their
- *   sign, NaN not at all.
+ *   low * 2^e <= key <= high * 2^e for every finite live key; infinities count as 127 * 2^e with
+ *   their sign (as do codes that stand for 2^128 and more), NaN not at all.
  * Any type of cache; only k (with k_exp and k_scale) is read (v may be NULL).  A page outside the cache is
  * skipped and sets the status FA2_ERR_BAD_INDEX, as does a token without a valid position.
  * Two sequences may share a page only if neither has new tokens in it.

@@ -174,8 +174,8 @@ def page_bounds(keys):
     none = np.isnan(k).all(0)
     low = np.where(none, 0.0, np.min(np.where(np.isnan(k), np.inf, k), 0))
     high = np.where(none, 0.0, np.max(np.where(np.isnan(k), -np.inf, k), 0))
-    both = np.abs(np.stack([low, high]))
-    e = smallest_exp(both[np.isfinite(both)].max() if np.isfinite(both).any() else 0.0, 127.0)
+    finite = np.abs(k[np.isfinite(k)])
+    e = smallest_exp(finite.max() if finite.size else 0.0, 127.0)
     return np.clip(np.stack([np.floor(low * 2.0 ** -e), np.ceil(high * 2.0 ** -e)]), -127, 127).astype(np.int64), e + 127
 
 

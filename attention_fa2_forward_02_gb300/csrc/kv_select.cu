@@ -131,7 +131,8 @@ struct PageKeys {
                         for (int i = 0; i < 8; ++i) x[i] = hmul2(x[i], s);
                     }
                     if constexpr (!kHalf) {
-                        const float two = __uint_as_float(byte[n] << 23);
+                        // (bfloat16 ends at 2^-133, a byte of 1 at 2^-136: any key below 2^-60 has bounds of -1, 0 or 1)
+                        const float two = __uint_as_float(max(byte[n], 4u) << 23);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
                             const float2 y = __half22float2(*reinterpret_cast<const __half2*>(&x[i]));

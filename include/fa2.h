@@ -608,7 +608,7 @@ fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_ca
  *   bounds      int8 [num_pages, n_kv_heads, 2, head_dim], contiguous, 16-byte aligned: the
  *               lowest, then the highest keys' codes
  *   bounds_exp  uint8 [num_pages, n_kv_heads], contiguous: a code stands for code * 2^(byte - 127),
- *               bytes 1 to 254
+ *               bytes 67 to 254 (fa2_kv_bounds writes 67 to 249)
  *
  * fa2_kv_bounds - makes the bounds of the pages that new tokens lie in, from all of the page's
  * live keys (those before the sequence's length): call it after fa2_kv_append or
@@ -626,7 +626,8 @@ fa2_status fa2_decode(const void* q, const int64_t q_strides[2], const fa2_kv_ca
  *   two, e_h >= -60, with every finite |q| <= 127 * 2^e_h; rounded to nearest even; NaN counts as 0,
  *   infinities as 127 * 2^e_h), page p has the score
  *     max_h (2^e_h sum_c max(Q_hc low_pc, Q_hc high_pc)) * 2^e_p,
- *   a float32 that no rounding enters (it may overflow to infinity).  The `first` first pages
+ *   a float32 that no rounding enters (it may overflow to infinity; with bytes below 67 scores
+ *   below float32's smallest numbers would be rounded).  The `first` first pages
  *   of the sequence and the `recent` last ones are taken before all others, then those of the
  *   largest scores, the earlier of two alike, up to `budget` pages.
  *   q           element (b, h, d) as for fa2_decode;  n_heads / n_kv_heads <= 128

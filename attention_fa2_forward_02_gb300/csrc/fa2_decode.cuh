@@ -766,8 +766,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                 const uint32_t k = stage[C::kExps + r], v = stage[C::kExps + kKeys + r];
                 counts[j] = v != 0 && key >= range.first && key < range.len;
                 all = all && counts[j];
-                reinterpret_cast<float2*>(stage + 2 * C::kTile)[r] =
-                    counts[j] ? make_float2(__uint_as_float(k << 23), (float)((int)v - 127)) : make_float2(0.f, -INFINITY);
+                reinterpret_cast<float2*>(stage + 2 * C::kTile)[r] = make_float2(__uint_as_float(k << 23), counts[j] ? (float)((int)v - 127) : -INFINITY);
             }
             if (widen || __any_sync(0xffffffffu, !all)) {
                 const uint32_t scales = smem_u32(stage) + 2 * C::kTile + C::kInfo;
@@ -788,6 +787,7 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
 #pragma unroll
                 for (int j = 0; j < C::kLooks; ++j) {
                     if (!widen && counts[j]) continue;
+                    if (!counts[j]) reinterpret_cast<float2*>(stage + 2 * C::kTile)[lane + 32 * j].x = 0.f;
 #pragma unroll
                     for (int side = 0; side < 2; ++side) {
                         const uint32_t to = scales + side * C::kScales + (lane + 32 * j) * C::kScaleRow;

@@ -824,6 +824,12 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
         if (on && 16 * q_part < c.d) q_lo = *reinterpret_cast<const uint4*>(src);
         if (on && 16 * q_part + 8 < c.d) q_hi = *reinterpret_cast<const uint4*>(src + 8);
     };
+    if constexpr (C::kSixteens && D == 128) {
+        // d = 96: load_sixteens leaves V's last pieces out, which the look for rows of zeros takes as they are
+        if (c.d < D)
+            for (int i = lane; i < S * kKeys; i += 32)
+                *reinterpret_cast<uint4*>(my + i / kKeys * C::kStage + C::kTile + swizzle<C::kChunks>(i % kKeys, C::kChunks - 1) * 16) = make_uint4(0, 0, 0, 0);
+    }
     look();
     if (live) fetch_q(seg);
 #pragma unroll
@@ -1107,7 +1113,6 @@ __global__ void __launch_bounds__(kThreads, kCluster ? Cfg<D, kForm, kTiles>::kS
                         uint32_t any = 0;
 #pragma unroll
                         for (int i = 0; i < C::kChunks; ++i) {
-                            if (C::kSixteens && 32 * i >= c.d) break;  // (pieces past the head's size were not copied)
                             const uint4 w = *reinterpret_cast<const uint4*>(info - C::kTile + swizzle<C::kChunks>(r, i) * 16);
                             any |= w.x | w.y | w.z | w.w;
                         }

@@ -31,10 +31,11 @@
 //
 // The 4-bit cache is the same with code * scale, 6 bits and exact in half, in the place of the code: K's and V's
 // operands are made in registers (a byte of two codes to a pair of halves, times the group's scale; the lanes' pieces
-// of a row are permuted alike on both sides of a product, so no element moves between lanes). That and the products
-// bound it, not its 73 bytes a row: 420 instructions for 16 keys of 128, issued in 57 of 100 cycles. GB300, 32
+// of a row are permuted alike on both sides of a product, so no element moves between lanes). Not its 73 bytes a row bound
+// it but the chain of a block: conversion, product, maximum, exponential, second product, 420 instructions for 16 keys of 128
+// by three warps a scheduler, issued in 58 of 100 cycles; no unit is busy for more than 47. GB300, 32
 // sequences of up to 8192 (d 128, 8 heads on each of 8, 193 MB): 56 us, 3.5 TB/s; 21 of up to 65536 (d 64, half, 507
-// MB): 168 us, 3.0 TB/s, where each weight takes two products.
+// MB): 159 to 168 us, 3.0 to 3.2 TB/s, where each weight takes two products.
 //
 // Contexts that can only be short (by the block table's width, or the window) take one launch: the
 // CTAs of a thread-block cluster share an item and join their results in distributed shared

@@ -8,7 +8,7 @@ constexpr int kWarps = 4;
 
 // 4-bit rows back to 16 bits: as kv_rows_kernel of kv_cache.cu, a lane's 16 elements as packs of 8 that lie kLanes
 // packs apart, so that both sides of a row's lanes are one after another in memory. Every element is exact in bfloat16. GB300,
-// 9 sequences of up to 16384, 8 heads of 128 (372 MB, 7 bytes written for 2 read): 69.5 us, 5.4 TB/s; a step's 2.9 us.
+// 9 sequences of up to 16384, 8 heads of 128 (425 MB, 7 bytes written for 2 read): 70 us, 6.1 TB/s; a step's 2.9 us.
 template <bool kBf16, int kLanes, int kRows, int kTok>
 __global__ void __launch_bounds__(kWarps * 32) kv_read_e2m1_kernel(const KvRowsParams p, int rows_per_warp) {
     const PagedParams& c = p.c;

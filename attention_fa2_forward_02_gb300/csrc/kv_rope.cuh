@@ -5,13 +5,14 @@
 // pays two launches. Here each row is read once and written once: bytes set the pace of prompts, the chain
 // length - page - row - store that of a step. GB300: 16-bit prompts (6 of up to 6100, 32 and 8 heads of 128, 334 MB)
 // 57.8 us, 5.8 TB/s; into e4m3 (11 of up to 16384, 16 and 16 heads of 64, half of each turned, 937 MB) 163 us, 5.7 TB/s:
-// memory, as far as the rounds on their way reach. Into 4 bits (9 of up to 16384, 8 heads of 128, 372 MB) 93 us, 4.0 TB/s:
-// maxima, quotients and conversions. A step of 33 sequences into e4m3 4.3 us.
+// memory, as far as the rounds on their way reach. Into 4 bits (9 of up to 16384, 8 heads of 128, 319 MB) 94 us, 3.4 TB/s,
+// keys turned on the way 120 (interleaved pairs 110): maxima, quotients and conversions. A step of 33 sequences into e4m3 4.4 us.
 //
 // A warp takes a token (and a share of its rows); kLanes lanes hold a row, 16 elements each, as two packs of 8:
 // i .. i + 7 and i + rot / 2 .. in the half layout, any two in the interleaved one, so that every pair lies in one
 // lane whichever the layout, accesses are whole 16-byte vectors, and the 8 sines and cosines a lane needs are
-// the same for all rows of the token (rope.cuh makes them from the position in fixed point).
+// the same for all rows of the token (rope.cuh makes them from the position in fixed point). Hence rot a multiple of 16: whole
+// packs turn with whole packs. (fa2_rope, which has narrower accesses, takes any even one.)
 //
 // The 8- and 4-bit forms take a row's power of two from the row as it came (the magnitudes of 16-bit floats are
 // ordered as their bits are): a rotation by any angle makes an element no more than sqrt(2) |magnitude| times the
@@ -34,7 +35,8 @@ namespace fa2 {
 namespace {
 
 constexpr int kWarps = 4;
-// CTAs an SM: 102 registers a thread, room for the rounds on their way (launch_lanes).
+// CTAs an SM: 96 registers a thread, room for the rounds on their way (launch_lanes). With pairs in halves and two rounds ahead
+// 4-bit rows spill 16 to 24 bytes, with three ahead e4m3 rows of up to 64 spill 16.
 constexpr int kPerSm = 5;
 constexpr int kMinExp = -60, kMaxExp = 120;
 

@@ -2,14 +2,15 @@
 //
 // Bounds: the lowest and the highest key of every channel, as 8-bit integers at a power of two of the page and
 // head, rounded outwards: for 16 tokens of 128 channels in 16 bits 257 bytes for 8192 of keys and values. From 16-bit
-// keys memory sets the pace (GB300, 9 prompts of up to 16384 tokens, 8 heads, 132 MB, 27 us, 4.9 TB/s); codes have to be
+// keys memory sets the pace (GB300, 9 prompts of up to 16384 tokens, 8 heads, 128 MB, 24 us, 5.3 TB/s); codes have to be
 // widened and are compared two at a time, which does (60 of 100 cycles of the integer and comparison unit): e4m3, 66 MB,
-// 19 us, 3.5 TB/s; 24 when they were compared as bfloat16, by way of float32. Half of a page's 930 instructions find
-// it and make its codes, as many as 32 rows of 128 take; larger pages have fewer. The pages of a step of 33 sequences take 3.5 us: a launch and four reads one after another.
+// 18.7 us, 3.6 TB/s (24 when they were compared as bfloat16, by way of float32); 4 bits, 39 MB, 18.6 us. Half of a page's 910
+// instructions find it and make its codes, as many as 32 rows of 128 take; larger pages have fewer, and for pages of a few keys
+// that is the time (16 bits, pages of 8 39 us, of 1 263). The pages of a step of 33 sequences take 3.3 us: a launch and four reads one after another.
 //
-// Scores: sum_c max(q_c low_c, q_c high_c) is no less than q . k for any key within the bounds. The query's
-// 8-bit integers, split into those above zero (which meet the highest keys) and those below (the lowest), make it
-// a sum of integer products: exact, so that which pages are taken does not depend on the order of sums, and a
+// Scores: sum_c max(q_c low_c, q_c high_c) is no less than q . k for any key within the bounds, with the query's 8-bit
+// integers for q; for the query itself, which they round, it is an estimate that can lie below q . k. The integers, split
+// into those above zero (which meet the highest keys) and those below (the lowest), make it a sum of integer products: exact, so that which pages are taken does not depend on the order of sums, and a
 // float32 holds the result (below 2^21) times powers of two.
 //
 // Selection: the budget-th largest score by counting, the earlier page first among equals, pages in the order of
@@ -574,7 +575,7 @@ __device__ __forceinline__ void take_all(const SelectParams& p, int row, const i
 }
 
 // The budget of row `row` out of n > budget pages with keys key(0) .. key(n - 1). The budget-th largest is found by counting
-// into kBins equal parts of the range that holds it, three times at the most (for 32 bits), mostly twice: the range
+// into kBins equal parts of the range that holds it, four times at the most (32 bits, 10 a time), mostly twice: the range
 // begins as that of the scores there are.
 // T: two counts of pages in one, 16 bits each (n < 2^16) or 32.
 // kRanged: sm.found has the range and the number forced already, sm.few is 0.
@@ -604,7 +605,7 @@ __device__ __forceinline__ void select_row(const SelectParams& p, SelectSmem& sm
     uint32_t need = (uint32_t)p.budget - sm.found[2];
     uint32_t least = kForced - 1, equal = 0;  // all above `least` are taken and the earliest `equal` of those equal to it
 #pragma unroll 1
-    for (int round = 0; need && round < 4; ++round) {  // (three are enough)
+    for (int round = 0; need && round < 4; ++round) {  // (four are enough)
         const int shift = max(0, 22 - __clz(hi - lo));  // (hi - lo) >> shift < kBins
         for (int i = threadIdx.x; i < kBins; i += kThreads) sm.bins[i] = 0;
         __syncthreads();  // (found is read)

@@ -449,7 +449,8 @@ fa2_status fa2_rope_backward(const void* dy, void* dx, const int32_t* positions,
  * of sequences through a block table (int32 [batch, pages_per_seq], rows table_stride entries
  * apart): token `pos` of sequence b lies in slot pos % page_size of page
  * block_table[b * table_stride + pos / page_size].  Entries past a sequence's length are never
- * read.  Sequences may share pages that are only read.
+ * read.  Sequences may share pages that are only read.  Pools need no clearing: whatever lies in
+ * slots that hold no key of a sequence enters none of its results.
  *
  *   k, v       element (page, head, slot, d) at page * page_stride + head * head_stride +
  *              slot * slot_stride + d, strides in elements and whole 16-byte units: pages as

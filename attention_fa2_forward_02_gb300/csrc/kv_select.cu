@@ -291,12 +291,12 @@ __global__ void __launch_bounds__(kWarps * 32) kv_bounds_kernel(const KvBoundsPa
     const int channel = 16 * li + 2 * w0;
     if (channel >= c.d || gr >= 8) return;  // (16 groups end with the same twice)
     const float inv = exp2_of(-e);
-    auto limited = [&](float x) { return fmaxf(fminf(x * inv, 127.f), -127.f); };  // (infinities)
+    auto limited = [](float x) { return fmaxf(fminf(x, 127.f), -127.f); };  // (infinities)
     uint32_t low[kOwn], high[kOwn];
 #pragma unroll
-    for (int i = 0; i < kOwn; ++i) {  // (a key far below the page's largest can be 0 times inv, and is no 0)
-        low[i] = (uint32_t)min(__float2int_rd(limited(l[i])), l[i] < 0.f ? -1 : 127);
-        high[i] = (uint32_t)max(__float2int_ru(limited(u[i])), u[i] > 0.f ? 1 : -127);
+    for (int i = 0; i < kOwn; ++i) {  // (the products round outwards too: a key far below the page's largest does not become 0)
+        low[i] = (uint32_t)__float2int_rd(limited(__fmul_rd(l[i], inv)));
+        high[i] = (uint32_t)__float2int_ru(limited(__fmul_ru(u[i], inv)));
     }
     uint32_t out[2] = {__byte_perm(low[0], low[1], 0x0040), __byte_perm(high[0], high[1], 0x0040)};
     if constexpr (kOwn == 4) {

@@ -6,7 +6,7 @@
 // widened and are compared two at a time, which does (60 of 100 cycles of the integer and comparison unit): e4m3, 66 MB,
 // 18.7 us, 3.6 TB/s (24 when they were compared as bfloat16, by way of float32); 4 bits, 39 MB, 18.6 us. Half of a page's 910
 // instructions find it and make its codes, as many as 32 rows of 128 take; larger pages have fewer, and for pages of a few keys
-// that is the time (16 bits, pages of 8 39 us, of 1 263). The pages of a step of 33 sequences take 3.3 us: a launch and four reads one after another.
+// that is the time (16 bits, pages of 8 39 us, of 1 265). The pages of a step of 33 sequences take 3.3 us: a launch and four reads one after another.
 //
 // Scores: sum_c max(q_c low_c, q_c high_c) is no less than q . k for any key within the bounds, with the query's 8-bit
 // integers for q; for the query itself, which they round, it is an estimate that can lie below q . k. The integers, split
